@@ -499,6 +499,162 @@ kvq_status kvq_decode_attn_packed_noalloc(const kvq_request* reqs, int n_request
                                           int head_dim, int depth, const uint16_t* q, float softmax_scale,
                                           float* out, kvq_cuda_stream stream);
 
+/*
+ * Paged cache: keys and values that are not packed yet. New tokens are written
+ * to 16-bit (or 8-bit) pages with the position rotation applied (RFC §3.3:
+ * stored keys are post-RoPE), the pages are attended where they lie, and a full
+ * 64-token page of a token-major BF16 cache is what kvq_append_tile and
+ * kvq_append_tile_batch read ([64][H][D]) and what the BF16 tail of a request
+ * points at.
+ *
+ *   dtype  of the stored keys, values and bounds: BF16, FP16, or E4M3 with one
+ *          FP32 scale per KV head (value = stored * scale[h]).
+ *   k, v   element (page p, place s, head h, channel d) at
+ *          p * page_stride + s * token_stride + h * head_stride + d, in
+ *          elements; the strides are multiples of 16 bytes and describe places
+ *          that do not overlap (token-major, head-major, K and V interleaved
+ *          in one allocation ...); k and v 16-byte aligned, same strides.
+ *   key_bounds  [n_pages][n_heads][2][head_dim], contiguous: the smallest (0)
+ *          and largest (1) stored key of a page per head and channel, kept by
+ *          kvq_paged_append; NULL: none are kept (kvq_paged_select needs them).
+ *   k_scale, v_scale  FP32 [n_heads], positive, E4M3 only (NULL: 1).
+ *   error  DEVICE int32 or NULL: KVQ_PAGED_ERR_* bits are OR-ed in by the
+ *          kernels and never cleared; the caller zeroes it.
+ *
+ * A request's pages are row b of page_table, int32 [n_requests][max_pages]
+ * (device): token t lies on page page_table[b][t / page_size], place t %
+ * page_size. Entries behind a request's last page are not read. Table contents
+ * and lengths are checked on the device: a request whose length is negative or
+ * beyond its table row, or whose pages are outside the pool, is refused (see
+ * each call) and sets an error bit; nothing outside the pool is read or written.
+ *
+ * head_dim is 128 and Hq / H is 1..16 (any integer). Workspaces may be shared
+ * by calls that follow one another on one stream; calls that may overlap need
+ * one each. Every call can be captured into a CUDA graph; lengths, tables and
+ * offsets are then read at replay.
+ */
+#define KVQ_DT_BF16 0
+#define KVQ_DT_FP16 1
+#define KVQ_DT_E4M3 2
+
+#define KVQ_PAGED_ERR_LENGTH 1     /* a length, start or offset outside its range */
+#define KVQ_PAGED_ERR_SELECTION 32 /* a selection that is not ascending page numbers of its request */
+#define KVQ_PAGED_ERR_PAGE 128     /* a page number outside the pool */
+#define KVQ_PAGED_ERR_POSITION 256 /* a position outside the rotation table */
+
+#define KVQ_PAGED_MAX_PAGE 1024 /* largest page_size */
+#define KVQ_PAGED_MAX_G 16      /* query heads per KV head */
+
+typedef struct kvq_paged_cache {
+  uint32_t version;   /* KVQ_FORMAT_VERSION */
+  int32_t dtype;      /* KVQ_DT_* */
+  int32_t n_pages;    /* pages in the pool */
+  int32_t page_size;  /* tokens per page, 1..KVQ_PAGED_MAX_PAGE */
+  int32_t n_heads;    /* KV heads H */
+  int32_t head_dim;   /* 128 */
+  int64_t page_stride;  /* elements */
+  int64_t token_stride;
+  int64_t head_stride;
+  void* k;
+  void* v;
+  void* key_bounds;
+  const float* k_scale;
+  const float* v_scale;
+  int32_t* error;
+} kvq_paged_cache;
+
+/* Fill the fields of a token-major pool [n_pages][page_size][H][D] and clear the pointers. */
+kvq_status kvq_paged_cache_init(kvq_paged_cache* c, int dtype, int n_pages, int page_size, int n_heads, int head_dim);
+
+/* The rows that kvq_paged_append brings (host struct of device pointers). */
+typedef struct kvq_paged_rows {
+  const int32_t* start;   /* [n_requests]: tokens already cached = position of the first new one */
+  const int32_t* offsets; /* [n_requests + 1]: rows offsets[b] .. offsets[b+1]-1 belong to request b, ascending;
+                             NULL: one row per request (n_rows == n_requests) */
+  int32_t n_rows;         /* rows of k, v and q; rows behind offsets[n_requests] are padding and left alone */
+  int32_t dtype;          /* KVQ_DT_BF16 or KVQ_DT_FP16 of k, v, q and q_out */
+  const void* k;          /* row r at r * k_stride elements, [H][D] within a row; 16-byte aligned, as v, q, q_out */
+  const void* v;
+  int64_t k_stride;       /* multiples of 8 elements */
+  int64_t v_stride;
+  const void* q;          /* rotated into q_out with the keys' angles; NULL: no queries */
+  void* q_out;            /* may be q itself */
+  int64_t q_stride;
+  int64_t q_out_stride;
+  int32_t n_q_heads;
+  int32_t rotary_dim;     /* R channels are rotated, the rest passes; 0 or a multiple of 8 up to head_dim */
+  const float* rope;      /* FP32 [rope_positions][R]: R/2 cosines, then R/2 sines; NULL when R is 0 */
+  int32_t rope_positions;
+  int32_t interleaved;    /* 0: pairs (d, d + R/2); 1: pairs (2d, 2d + 1) */
+  const int32_t* positions; /* [n_rows] row of `rope` of each row; NULL: the token's place in its request */
+} kvq_paged_rows;
+
+/*
+ * Append: row i of request b is token start[b] + i. Its key is rotated (x' =
+ * x cos - y sin, y' = y cos + x sin in FP32, one rounding at the end), its value
+ * copied, both stored on the token's page (E4M3: divided by the head's scale,
+ * rounded to nearest, saturated at 448); the page's key bounds take in the new
+ * keys, and start afresh on a page whose first place is written. Queries are
+ * rotated the same way into q_out. start is not changed.
+ * No two requests may append to the same page in one call. Not written are the
+ * rows of a refused request (bad start or offsets), rows whose page is outside
+ * the pool and rows whose position is outside the rotation table; their queries
+ * are not written either.
+ */
+kvq_status kvq_paged_append(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages, int n_requests,
+                            const kvq_paged_rows* rows, kvq_cuda_stream stream);
+
+/* Workspace bytes that satisfy kvq_paged_decode_attn, kvq_paged_select and
+ * kvq_paged_sparse_attn on the current device. 0 for invalid sizes. */
+size_t kvq_paged_workspace_bytes(int n_requests, int n_heads, int n_q_heads, int max_pages);
+
+/*
+ * Decode attention of one query per request over its first seq_lens[b] cached
+ * tokens.
+ *   q     BF16 or FP16 (the cache's type unless it is E4M3), request b at b *
+ *         q_stride elements, [Hq][D] within; 16-byte aligned, q_stride a multiple of 8.
+ *   out   FP32 [n_requests][Hq][D], 16-byte aligned.
+ *   lse   FP32 [n_requests][Hq] or NULL: ln of the sum of exp(scale q.k), by which
+ *         results over disjoint tokens can be joined.
+ * Query head hq reads KV head hq / (Hq/H); softmax and sums are FP32. A request
+ * without tokens gets out 0 and lse -inf, a refused one NaN in both.
+ */
+kvq_status kvq_paged_decode_attn(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages,
+                                 int n_requests, const int32_t* seq_lens, const void* q, int q_dtype,
+                                 int64_t q_stride, int n_q_heads, float softmax_scale, float* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, kvq_cuda_stream stream);
+
+/*
+ * Page selection: for every request and KV head the pages that the query most
+ * likely finds something on, from the key bounds alone. The score of a page is
+ * the sum over the group's query heads of the largest q.k that its bounds allow,
+ *     sum_j sum_d (q_jd < 0 ? q_jd lo_d : q_jd hi_d).
+ * The first n_first and the last n_last pages are always taken (n_first + n_last
+ * <= n_select), the others by score, equal scores by page number; a page whose
+ * score is not finite counts as the largest. The order is that of the exact
+ * scores: values too near the border for FP32 are computed in FP64.
+ *   sel   int32 [n_requests][n_heads][n_select]: page numbers within the request
+ *         (not the pool), ascending, -1 behind the request's last; a refused
+ *         request gets -1 throughout. A page outside the pool counts as the
+ *         smallest and sets the error bit.
+ */
+kvq_status kvq_paged_select(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages, int n_requests,
+                            const int32_t* seq_lens, const void* q, int q_dtype, int64_t q_stride, int n_q_heads,
+                            int n_select, int n_first, int n_last, int32_t* sel, void* workspace,
+                            size_t workspace_bytes, kvq_cuda_stream stream);
+
+/*
+ * kvq_paged_decode_attn over the tokens of the selected pages only; sel as
+ * kvq_paged_select writes it (ascending, -1 behind the last). A selection of one
+ * KV head that is not of that form gives NaN to that head's queries and sets
+ * KVQ_PAGED_ERR_SELECTION; one that holds no page gives out 0 and lse -inf.
+ */
+kvq_status kvq_paged_sparse_attn(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages,
+                                 int n_requests, const int32_t* seq_lens, const void* q, int q_dtype,
+                                 int64_t q_stride, int n_q_heads, const int32_t* sel, int n_select,
+                                 float softmax_scale, float* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, kvq_cuda_stream stream);
+
 /* Human-readable name of a status code. */
 const char* kvq_status_string(kvq_status s);
 

@@ -29,6 +29,7 @@ ATTN_AUTO, ATTN_SIMT, ATTN_MMA, ATTN_MMA_GENERAL, ATTN_TCGEN05 = 0, 1, 2, 3, 4
 ATTN_NVFP4 = 8  # OR-ed into algo: the table may hold NVFP4 residual loops
 KVQ_KGROUP_COMPACT, KVQ_KGROUP_TILE = 0, 1  # K groups: 64 stored rows / the stored rows of one 64-token tile
 KVQ_LOOP_K_TILE, KVQ_LOOP_K_NVFP4, KVQ_LOOP_V_NVFP4 = 1, 2, 4
+PAGED_ERR_LENGTH, PAGED_ERR_SELECTION, PAGED_ERR_PAGE, PAGED_ERR_POSITION = 1, 32, 128, 256
 KVQ_FMT_INT4, KVQ_FMT_NVFP4 = 0, 1  # residual formats: affine INT4 / E2M1 + E4M3 per 16 + FP32 per stream
 
 EXPORTED = (
@@ -40,7 +41,8 @@ EXPORTED = (
     "kvq_sparse_decode_attn", "kvq_stream_payload_bytes_ex", "kvq_stream_set_format", "kvq_encode_batch_ex",
     "kvq_reconstruct_batch_ex", "kvq_stream_set_capacity", "kvq_append_workspace_bytes", "kvq_append_tile",
     "kvq_append_batch_workspace_bytes", "kvq_append_tile_batch", "kvq_sparse_decode_workspace_bytes",
-    "kvq_sparse_decode_attn_ex",
+    "kvq_sparse_decode_attn_ex", "kvq_paged_cache_init", "kvq_paged_append", "kvq_paged_workspace_bytes",
+    "kvq_paged_decode_attn", "kvq_paged_select", "kvq_paged_sparse_attn",
 )
 
 
@@ -100,6 +102,49 @@ class kvq_request(ctypes.Structure):
         ("sink_v", ctypes.c_void_p),
         ("tail_k", ctypes.c_void_p),
         ("tail_v", ctypes.c_void_p),
+    ]
+
+
+class kvq_paged_cache(ctypes.Structure):
+    _fields_ = [
+        ("version", ctypes.c_uint32),
+        ("dtype", ctypes.c_int32),
+        ("n_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("n_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("key_bounds", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("error", ctypes.c_void_p),
+    ]
+
+
+class kvq_paged_rows(ctypes.Structure):
+    _fields_ = [
+        ("start", ctypes.c_void_p),
+        ("offsets", ctypes.c_void_p),
+        ("n_rows", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64),
+        ("n_q_heads", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("rope", ctypes.c_void_p),
+        ("rope_positions", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("positions", ctypes.c_void_p),
     ]
 
 
@@ -163,11 +208,24 @@ def lib():
             L.kvq_reconstruct_batch.argtypes = [vp, i32, i32, i32, i32, i32, vp, vp, sz, vp]
             L.kvq_encode_batch_ex.argtypes = [vp, i32, i32, i32, i32, i32, vp, ctypes.c_uint32, vp, sz, vp]
             L.kvq_reconstruct_batch_ex.argtypes = [vp, i32, i32, i32, i32, i32, vp, ctypes.c_uint32, vp, sz, vp]
+            i64, f32 = ctypes.c_int64, ctypes.c_float
+            L.kvq_paged_cache_init.argtypes = [P(kvq_paged_cache), i32, i32, i32, i32, i32]
+            L.kvq_paged_append.argtypes = [P(kvq_paged_cache), vp, i32, i32, P(kvq_paged_rows), vp]
+            L.kvq_paged_workspace_bytes.argtypes = [i32, i32, i32, i32]
+            L.kvq_paged_workspace_bytes.restype = sz
+            L.kvq_paged_decode_attn.argtypes = [P(kvq_paged_cache), vp, i32, i32, vp, vp, i32, i64, i32, f32, vp, vp,
+                                                vp, sz, vp]
+            L.kvq_paged_select.argtypes = [P(kvq_paged_cache), vp, i32, i32, vp, vp, i32, i64, i32, i32, i32, i32, vp,
+                                           vp, sz, vp]
+            L.kvq_paged_sparse_attn.argtypes = [P(kvq_paged_cache), vp, i32, i32, vp, vp, i32, i64, i32, vp, i32, f32,
+                                                vp, vp, vp, sz, vp]
             for name in ("kvq_stream_init", "kvq_encode_base", "kvq_encode_residual", "kvq_build_tile_dir",
                          "kvq_reconstruct", "kvq_request_fill", "kvq_decode_attn_packed",
                          "kvq_decode_attn_packed_ex", "kvq_encode_batch", "kvq_reconstruct_batch",
                          "kvq_stream_set_format", "kvq_encode_batch_ex", "kvq_reconstruct_batch_ex",
-                         "kvq_stream_set_capacity", "kvq_append_tile", "kvq_append_tile_batch"):
+                         "kvq_stream_set_capacity", "kvq_append_tile", "kvq_append_tile_batch",
+                         "kvq_paged_cache_init", "kvq_paged_append", "kvq_paged_decode_attn", "kvq_paged_select",
+                         "kvq_paged_sparse_attn"):
                 getattr(L, name).restype = ctypes.c_int32
             _lib = L
     return _lib
@@ -726,3 +784,277 @@ def kvq_sparse_decode_attn(table: RequestTable, q: torch.Tensor, depth: int, n_h
                                            _stream_handle(stream)),
            "kvq_sparse_decode_attn")
     return out
+
+
+# --------------------------------------------------------------------------- paged cache
+
+_PAGED_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+
+
+class PagedCache:
+    """Pages of keys and values that are not packed yet, and what the library
+    keeps about them. Wraps the caller's tensors:
+
+    k, v        [n_pages, page_size, n_heads, 128] of BF16, FP16 or E4M3 with the
+                same strides; any layout in memory whose rows of 128 channels are
+                contiguous and whose strides are multiples of 16 bytes (a
+                head-major pool is passed as its transposed view).
+    key_bounds  [n_pages, n_heads, 2, 128], contiguous, of the same type: smallest
+                and largest key per page, head and channel, kept by
+                kvq_paged_append and read by kvq_paged_select; None: none.
+    k_scale, v_scale  FP32 [n_heads], positive, for E4M3: value = stored * scale.
+
+    The kernels OR what they refuse into an error word of the cache
+    (PAGED_ERR_*): error_word() reads it, clear_error() zeroes it. A page of 64
+    tokens of a token-major BF16 cache (cache.k[page]) is a tile for
+    kvq_append_tile."""
+
+    def __init__(self, page_size: int, n_heads: int, k: torch.Tensor | None = None, v: torch.Tensor | None = None,
+                 key_bounds: torch.Tensor | None = None, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        first = k if k is not None else key_bounds
+        if first is None:
+            raise KvqError("a paged cache needs k and v, or key_bounds")
+        if (k is None) != (v is None):
+            raise KvqError("k and v come together")
+        if first.dtype not in _PAGED_DTYPES:
+            raise KvqError(f"paged cache of {first.dtype}: bfloat16, float16 or float8_e4m3fn")
+        n_pages = first.shape[0]
+        for name, t in (("k", k), ("v", v), ("key_bounds", key_bounds), ("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None:
+                continue
+            if not t.is_cuda or t.device != first.device:
+                raise KvqError(f"{name} must be a CUDA tensor on {first.device}")
+            if name in ("k", "v"):
+                if tuple(t.shape) != (n_pages, page_size, n_heads, 128) or t.dtype != first.dtype:
+                    raise KvqError(f"{name} must be {first.dtype} [{n_pages}, {page_size}, {n_heads}, 128], got "
+                                   f"{t.dtype} {list(t.shape)}")
+                if t.stride(3) != 1 or t.stride() != k.stride():
+                    raise KvqError("k and v need contiguous channels and the same strides")
+            elif name == "key_bounds":
+                if tuple(t.shape) != (n_pages, n_heads, 2, 128) or t.dtype != first.dtype or not t.is_contiguous():
+                    raise KvqError(f"key_bounds must be contiguous {first.dtype} [{n_pages}, {n_heads}, 2, 128]")
+            elif t.dtype != torch.float32 or tuple(t.shape) != (n_heads,) or not t.is_contiguous():
+                raise KvqError(f"{name} must be contiguous float32 [{n_heads}]")
+        self.page_size, self.n_heads, self.n_pages = page_size, n_heads, n_pages
+        self.dtype, self.device = first.dtype, first.device
+        self.k, self.v, self.key_bounds, self.k_scale, self.v_scale = k, v, key_bounds, k_scale, v_scale
+        self.desc = kvq_paged_cache()
+        _check(lib().kvq_paged_cache_init(ctypes.byref(self.desc), _PAGED_DTYPES[self.dtype], n_pages, page_size,
+                                          n_heads, 128), "kvq_paged_cache_init")
+        if k is not None:
+            self.desc.page_stride, self.desc.token_stride, self.desc.head_stride = k.stride()[:3]
+        self._error = torch.zeros(4, dtype=torch.int32, device=self.device)
+        for name in ("k", "v", "key_bounds", "k_scale", "v_scale"):
+            t = getattr(self, name)
+            setattr(self.desc, name, None if t is None else t.data_ptr())
+        self.desc.error = self._error.data_ptr()
+        self._ref = ctypes.byref(self.desc)
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_heads: int, dtype=torch.bfloat16, device="cuda",
+              key_bounds: bool = False, k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):
+        """A token-major cache with storage of its own."""
+        k, v = (torch.empty((n_pages, page_size, n_heads, 128), dtype=dtype, device=device) for _ in range(2))
+        bounds = torch.empty((n_pages, n_heads, 2, 128), dtype=dtype, device=device) if key_bounds else None
+        return cls(page_size, n_heads, k, v, bounds, k_scale, v_scale)
+
+    def workspace_bytes(self, n_requests: int, n_q_heads: int, max_pages: int) -> int:
+        """Workspace of the attention and selection calls for these sizes (kvq_paged_workspace_bytes)."""
+        with torch.cuda.device(self.device):
+            return int(lib().kvq_paged_workspace_bytes(n_requests, self.n_heads, n_q_heads, max_pages))
+
+    def error_word(self) -> int:
+        """PAGED_ERR_* bits since the last clear_error() (reads the device)."""
+        return int(self._error[0].item())
+
+    def clear_error(self):
+        self._error.zero_()
+
+
+def _on_stream(cache: PagedCache, stream, call):
+    """call(raw stream) with the cache's device current. Buffers that the call allocates belong to the stream they
+    are used on."""
+    if stream is None and torch.cuda.current_device() == cache.device.index:
+        return call(torch.cuda.current_stream(cache.device).cuda_stream)
+    if stream is not None and stream.device != cache.device:
+        raise KvqError(f"stream of {stream.device} for a cache on {cache.device}")
+    with torch.cuda.device(cache.device):
+        if stream is None:
+            return call(torch.cuda.current_stream(cache.device).cuda_stream)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _int32(cache: PagedCache, t: torch.Tensor, name: str, shape: tuple):
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != cache.device or not t.is_contiguous():
+        raise KvqError(f"{name} must be contiguous int32 {list(shape)} on {cache.device}, got {t.dtype} "
+                       f"{list(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _head_rows(cache: PagedCache, t: torch.Tensor, name: str, dtype, rows: int | None = None, heads: int | None = None):
+    """A [rows, heads, 128] view whose rows may be strided; returns its row stride."""
+    if t.device != cache.device or t.dtype != dtype or t.dim() != 3 or t.shape[2] != 128:
+        raise KvqError(f"{name} must be {dtype} [rows, heads, 128] on {cache.device}, got {t.dtype} {list(t.shape)} "
+                       f"on {t.device}")
+    n, h, _ = t.shape
+    if (rows is not None and n != rows) or (heads is not None and h != heads):
+        raise KvqError(f"{name} must be [{rows}, {heads}, 128], got {list(t.shape)}")
+    s = t.stride()
+    if n and h and (s[2] != 1 or (h > 1 and s[1] != 128)):
+        raise KvqError(f"{name}: the heads of a row must be contiguous")
+    return s[0] if n > 1 else h * 128
+
+
+def _paged_table(cache: PagedCache, table: torch.Tensor):
+    if table.dim() != 2:
+        raise KvqError("page_table must be [n_requests, max_pages]")
+    B, W = table.shape
+    return _int32(cache, table, "page_table", (B, W)), B, W
+
+
+def kvq_paged_append(cache: PagedCache, page_table: torch.Tensor, start: torch.Tensor, k: torch.Tensor,
+                     v: torch.Tensor, offsets: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                     q_out: torch.Tensor | None = None, rope: torch.Tensor | None = None, interleaved: bool = False,
+                     positions: torch.Tensor | None = None, stream=None):
+    """Append new keys and values to the cache, rotating keys (and queries) by
+    their position. page_table int32 [B, max_pages]; start int32 [B], tokens
+    already cached; k, v BF16 or FP16 [n, H, 128] (rows may be strided, as a
+    slice of a fused projection is); offsets int32 [B + 1], rows of each request
+    (None: one row per request); rope FP32 [positions, R], R/2 cosines then R/2
+    sines (None: no rotation); positions int32 [n], rows of `rope` (None: the
+    token's place). With q [n, Hq, 128] its rotation goes to q_out (allocated
+    when None; may be q) and is returned. start is not changed. Rows behind
+    offsets[B] are padding: neither they nor their q_out rows are touched."""
+    tab, B, W = _paged_table(cache, page_table)
+    if cache.k is None:
+        raise KvqError("a cache of key bounds alone cannot be appended to")
+    r = kvq_paged_rows()
+    dtype = k.dtype
+    if dtype not in (torch.bfloat16, torch.float16):
+        raise KvqError(f"k must be bfloat16 or float16, got {dtype}")
+    r.dtype = _PAGED_DTYPES[dtype]
+    n = k.shape[0]
+    r.n_rows = n
+    r.start = _int32(cache, start, "start", (B,))
+    r.k_stride = _head_rows(cache, k, "k", dtype, n, cache.n_heads)
+    r.v_stride = _head_rows(cache, v, "v", dtype, n, cache.n_heads)
+    r.k, r.v = k.data_ptr(), v.data_ptr()
+    if offsets is not None:
+        r.offsets = _int32(cache, offsets, "offsets", (B + 1,))
+    if positions is not None:
+        r.positions = _int32(cache, positions, "positions", (n,))
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 2 or rope.device != cache.device or not rope.is_contiguous():
+            raise KvqError(f"rope must be contiguous float32 [positions, R] on {cache.device}")
+        r.rope, r.rope_positions, r.rotary_dim = rope.data_ptr(), rope.shape[0], rope.shape[1]
+        r.interleaved = int(interleaved)
+    if q is None and q_out is not None:
+        raise KvqError("q_out without q")
+
+    def call(raw):
+        out = q_out
+        if q is not None:
+            if out is None:
+                out = torch.empty((n, q.shape[1], 128), dtype=q.dtype, device=q.device)
+            r.q_stride = _head_rows(cache, q, "q", dtype, n)
+            r.q_out_stride = _head_rows(cache, out, "q_out", dtype, n, q.shape[1])
+            r.q, r.q_out, r.n_q_heads = q.data_ptr(), out.data_ptr(), q.shape[1]
+        _check(lib().kvq_paged_append(cache._ref, tab, W, B, ctypes.byref(r), raw), "kvq_paged_append")
+        return out
+
+    return _on_stream(cache, stream, call)
+
+
+def _paged_query(cache: PagedCache, page_table, seq_lens, q):
+    tab, B, W = _paged_table(cache, page_table)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise KvqError(f"q must be bfloat16 or float16, got {q.dtype}")
+    stride = _head_rows(cache, q, "q", q.dtype, B)
+    return tab, B, W, _int32(cache, seq_lens, "seq_lens", (B,)), _PAGED_DTYPES[q.dtype], stride
+
+
+def _paged_workspace(cache: PagedCache, workspace, B, Hq, W):
+    if workspace is None:
+        need = int(lib().kvq_paged_workspace_bytes(B, cache.n_heads, Hq, W))
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
+    _require_cuda(workspace, "workspace", torch.uint8)
+    if workspace.device != cache.device:
+        raise KvqError(f"workspace must be on {cache.device}")
+    return workspace
+
+
+def _paged_attend(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, workspace, stream, what):
+    tab, B, W, lens, qdt, stride = _paged_query(cache, page_table, seq_lens, q)
+    Hq = q.shape[1]
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(128)
+    for name, t, shape in (("out", out, (B, Hq, 128)), ("lse", lse, (B, Hq))):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or t.device != cache.device
+                              or not t.is_contiguous()):
+            raise KvqError(f"{name} must be contiguous float32 {list(shape)} on {cache.device}")
+    if sel is not None:
+        if sel.dim() != 3:
+            raise KvqError("sel must be [n_requests, n_heads, n_select]")
+        sel_ptr = _int32(cache, sel, "sel", (B, cache.n_heads, sel.shape[2]))
+
+    def call(raw):
+        o = torch.empty((B, Hq, 128), dtype=torch.float32, device=cache.device) if out is None else out
+        ws = _paged_workspace(cache, workspace, B, Hq, W)
+        lse_ptr = None if lse is None else lse.data_ptr()
+        if sel is None:
+            st = lib().kvq_paged_decode_attn(cache._ref, tab, W, B, lens, q.data_ptr(), qdt, stride, Hq,
+                                             softmax_scale, o.data_ptr(), lse_ptr, ws.data_ptr(), ws.numel(), raw)
+        else:
+            st = lib().kvq_paged_sparse_attn(cache._ref, tab, W, B, lens, q.data_ptr(), qdt, stride, Hq, sel_ptr,
+                                             sel.shape[2], softmax_scale, o.data_ptr(), lse_ptr, ws.data_ptr(),
+                                             ws.numel(), raw)
+        _check(st, what)
+        return o
+
+    return _on_stream(cache, stream, call)
+
+
+def kvq_paged_decode_attn(cache: PagedCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor,
+                          softmax_scale: float | None = None, out: torch.Tensor | None = None,
+                          lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """FP32 [B, Hq, 128] attention of q [B, Hq, 128] (rows may be strided) over
+    the first seq_lens[b] cached tokens of each request; lse, FP32 [B, Hq], takes
+    the natural log of the softmax's sum. workspace: cache.workspace_bytes(...)
+    bytes, allocated when None; calls that may overlap need one each."""
+    return _paged_attend(cache, page_table, seq_lens, q, None, softmax_scale, out, lse, workspace, stream,
+                         "kvq_paged_decode_attn")
+
+
+def kvq_paged_select(cache: PagedCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor,
+                     n_select: int, n_first: int = 1, n_last: int = 1, sel: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """int32 [B, H, n_select]: the pages of each request on which the query can
+    find the largest q.k by the cache's key bounds (summed over the query heads
+    of a KV head), the first n_first and last n_last among them; ascending page
+    numbers of the request, -1 behind the last."""
+    tab, B, W, lens, qdt, stride = _paged_query(cache, page_table, seq_lens, q)
+    Hq = q.shape[1]
+    shape = (B, cache.n_heads, n_select)
+    if sel is not None:
+        _int32(cache, sel, "sel", shape)
+
+    def call(raw):
+        s = torch.empty(shape, dtype=torch.int32, device=cache.device) if sel is None else sel
+        ws = _paged_workspace(cache, workspace, B, Hq, W)
+        _check(lib().kvq_paged_select(cache._ref, tab, W, B, lens, q.data_ptr(), qdt, stride, Hq, n_select, n_first,
+                                      n_last, s.data_ptr(), ws.data_ptr(), ws.numel(), raw), "kvq_paged_select")
+        return s
+
+    return _on_stream(cache, stream, call)
+
+
+def kvq_paged_sparse_attn(cache: PagedCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor,
+                          sel: torch.Tensor, softmax_scale: float | None = None, out: torch.Tensor | None = None,
+                          lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """kvq_paged_decode_attn over the tokens of the pages `sel` (kvq_paged_select) only."""
+    return _paged_attend(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, workspace, stream,
+                         "kvq_paged_sparse_attn")
