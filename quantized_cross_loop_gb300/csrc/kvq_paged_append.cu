@@ -8,14 +8,20 @@
 // row is read and written once); a decode step is too small for that and bound by
 // the chain of dependent loads start -> page table and rotation table -> store.
 //
-// A unit of work is (request, touched page, head), heads fastest: the H KV heads
-// (K and V together) and then the query heads. A warp has every new token of its
-// page and head, so the bounds need no atomics. Lane l holds channels 4l .. 4l+3.
-// Two kernels, the host choosing by the rows a request brings on average:
-//   few (up to 8)  a warp takes any units in turn, everything by plain loads;
-//   many           a block takes a page and eight heads at a time, one per warp: the
-//                  rotation table's rows of the page are staged once in shared
-//                  memory for the eight, and a warp keeps eight rows in flight.
+// Sixteen lanes (a team) hold a row of a head, eight channels each: four of the
+// first half of the rotated channels and their four partners of the second, so that
+// a pair never crosses lanes and a lane needs four angles; channels behind the
+// rotated ones are shared out eight a lane. All new tokens of a page and head are
+// one unit of work, so the bounds need no atomics.
+// The host chooses by the rows that a request brings on average:
+//   few (up to 8)  one launch; a team takes any units (request, page, head) in
+//                  turn, KV heads (K and V together) and query heads alike;
+//   many           one launch for the keys and values, in which a block (pages of
+//                  more than 32 tokens) or a warp has a unit, and one for the
+//                  queries, in which a team takes four heads of a row.
+// Rows in flight and resident warps bound these; staging the rotation table in
+// shared memory for eight heads, and fetching the next rows into registers ahead of
+// the arithmetic, were slower (a table's row is in L1 for the heads that follow).
 #include "kvq_paged.cuh"
 
 namespace kvq {
@@ -23,29 +29,11 @@ namespace paged {
 namespace {
 
 constexpr int kFewThreads = 128;
-constexpr int kFewRows = 2;        // rows in flight per warp
+constexpr int kTeam = 16;          // lanes of a row
 constexpr int kManyThreads = 256;
 constexpr int kManyWarps = kManyThreads / 32;
-constexpr int kManyRows = 8;
-constexpr int kSlice = 64;         // rows of the rotation table staged at a time
-constexpr int kManyBlocksPerSm = 3;
-
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float4 min_nan(float4 a, float4 b) {
-  return make_float4(min_nan(a.x, b.x), min_nan(a.y, b.y), min_nan(a.z, b.z), min_nan(a.w, b.w));
-}
-__device__ __forceinline__ float4 max_nan(float4 a, float4 b) {
-  return make_float4(max_nan(a.x, b.x), max_nan(a.y, b.y), max_nan(a.z, b.z), max_nan(a.w, b.w));
-}
+constexpr int kKeyRows = 2;        // rows a team has in flight
+constexpr int kQueryHeads = 4;     // heads a team has in flight
 
 // New rows of request b, or -1 when its start or offsets are outside their range.
 __device__ __forceinline__ int rows_of(const AppendArgs& a, int b, int& start, int& row0) {
@@ -69,76 +57,123 @@ __device__ __forceinline__ int pages_of(const AppendArgs& a, int b) {
   return n <= 0 ? 0 : a.c.ps.div(start + n - 1) - a.c.ps.div(start) + 1;
 }
 
-// A lane's share of the rotation.
+// A lane's channels: a .. a + 3 and b .. b + 3.
 struct Lane {
-  int d;         // first channel
-  int partner;   // lane that holds the partners (split pairing)
-  int angle;     // first angle
-  float sign;    // -1: first of its pair, +1: second
+  int a, b;
   bool rotated;
-  __device__ __forceinline__ Lane(const AppendArgs& a, int lane) {
-    d = 4 * lane;
-    rotated = d < a.R;
-    const bool second = d >= a.R / 2;
-    partner = rotated ? (second ? lane - a.R / 8 : lane + a.R / 8) : lane;
-    angle = a.interleaved ? d / 2 : (second ? d - a.R / 2 : d);
-    sign = second ? 1.0f : -1.0f;
+  __device__ __forceinline__ Lane(const AppendArgs& g, int lane) {
+    rotated = lane < g.R / 8;
+    a = rotated ? 4 * lane : 8 * lane;
+    b = rotated ? g.R / 2 + 4 * lane : 8 * lane + 4;
   }
 };
 
 struct Angles {
-  float4 cs, sn;
+  float4 c, s;  // of the lane's four pairs
   // t: the position's row of the rotation table (global or shared memory)
-  __device__ __forceinline__ void load(const AppendArgs& a, const Lane& L, const float* t) {
+  template <bool INTER>
+  __device__ __forceinline__ void load(const AppendArgs& g, const Lane& L, const float* t) {
     if (!L.rotated) return;
-    if (a.interleaved) {
-      const float2 c = *reinterpret_cast<const float2*>(t + L.angle);
-      const float2 s = *reinterpret_cast<const float2*>(t + a.R / 2 + L.angle);
-      cs = make_float4(c.x, c.x, c.y, c.y);
-      sn = make_float4(-s.x, s.x, -s.y, s.y);
+    if constexpr (INTER) {
+      const float2 c0 = *reinterpret_cast<const float2*>(t + L.a / 2), c1 = *reinterpret_cast<const float2*>(t + L.b / 2);
+      t += g.R / 2;
+      const float2 s0 = *reinterpret_cast<const float2*>(t + L.a / 2), s1 = *reinterpret_cast<const float2*>(t + L.b / 2);
+      c = make_float4(c0.x, c0.y, c1.x, c1.y);
+      s = make_float4(s0.x, s0.y, s1.x, s1.y);
     } else {
-      cs = *reinterpret_cast<const float4*>(t + L.angle);
-      sn = *reinterpret_cast<const float4*>(t + a.R / 2 + L.angle);
-      sn = make_float4(L.sign * sn.x, L.sign * sn.y, L.sign * sn.z, L.sign * sn.w);
+      c = *reinterpret_cast<const float4*>(t + L.a);
+      s = *reinterpret_cast<const float4*>(t + L.b);  // (b = R / 2 + a: the sines lie there)
     }
   }
 };
 
-template <int IN>
-__device__ __forceinline__ float4 floats(uint2 w) {
-  return load4<IN>(&w);
+struct Raw {  // eight 16-bit channels as they come
+  uint2 a, b;
+};
+struct Wide {
+  float4 a, b;
+};
+
+__device__ __forceinline__ Raw load_raw(const char* p, const Lane& L) {
+  return Raw{*reinterpret_cast<const uint2*>(p + 2 * L.a), *reinterpret_cast<const uint2*>(p + 2 * L.b)};
 }
 
-// The lane's four channels `w` rotated; all lanes of the warp take part.
-template <int IN>
-__device__ __forceinline__ float4 rotate(const AppendArgs& a, const Lane& L, const Angles& t, uint2 w) {
-  const float4 x = floats<IN>(w);
-  float4 y;
-  if (a.interleaved) {
-    y = make_float4(x.y, x.x, x.w, x.z);
-  } else {
-    uint2 o;
-    o.x = __shfl_sync(0xFFFFFFFFu, w.x, L.partner);
-    o.y = __shfl_sync(0xFFFFFFFFu, w.y, L.partner);
-    y = floats<IN>(o);
-  }
+// x c - y s and y c + x s.
+__device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
+  const float u = x;
+  x = x * c - y * s;
+  y = y * c + u * s;
+}
+
+template <int IN, bool INTER>
+__device__ __forceinline__ Wide rotate(const Lane& L, const Angles& t, const Raw& w) {
+  Wide x{load4<IN>(&w.a), load4<IN>(&w.b)};
   if (!L.rotated) return x;
-  return make_float4(x.x * t.cs.x + y.x * t.sn.x, x.y * t.cs.y + y.y * t.sn.y, x.z * t.cs.z + y.z * t.sn.z,
-                     x.w * t.cs.w + y.w * t.sn.w);
+  if constexpr (INTER) {
+    turn(x.a.x, x.a.y, t.c.x, t.s.x);
+    turn(x.a.z, x.a.w, t.c.y, t.s.y);
+    turn(x.b.x, x.b.y, t.c.z, t.s.z);
+    turn(x.b.z, x.b.w, t.c.w, t.s.w);
+  } else {
+    turn(x.a.x, x.b.x, t.c.x, t.s.x);
+    turn(x.a.y, x.b.y, t.c.y, t.s.y);
+    turn(x.a.z, x.b.z, t.c.z, t.s.z);
+    turn(x.a.w, x.b.w, t.c.w, t.s.w);
+  }
+  return x;
 }
 
 __device__ __forceinline__ float4 div4(float4 x, float s) {
   return make_float4(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s), __fdiv_rn(x.z, s), __fdiv_rn(x.w, s));
 }
 
-// What a warp does to one (page, head): where rows come from and go to.
+// Four stored keys as two words of 16-bit pairs (E4M3 as FP16, exact), and their
+// smaller and larger ones; NaN stays.
+template <int DT>
+__device__ __forceinline__ uint2 pairs_of(const char* p) {
+  if constexpr (DT == kE4m3) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    return make_uint2(e4m3x2_to_f16x2(w & 0xFFFFu), e4m3x2_to_f16x2(w >> 16));
+  } else {
+    return *reinterpret_cast<const uint2*>(p);
+  }
+}
+template <int DT>
+__device__ __forceinline__ void put_pairs(char* p, uint2 x) {
+  if constexpr (DT == kE4m3) store4<kE4m3>(p, load4<kFp16>(&x));
+  else *reinterpret_cast<uint2*>(p) = x;
+}
+template <int DT>
+__device__ __forceinline__ uint32_t smaller(uint32_t x, uint32_t y) {
+  if constexpr (DT == kBf16) {
+    const __nv_bfloat162 r =
+        __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 r = __hmin2_nan(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) {
+  if constexpr (DT == kBf16) {
+    const __nv_bfloat162 r =
+        __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+// What a team does to one (page, head): where rows come from and go to.
 template <int DT, int IN>
 struct Unit {
   bool is_q, live;  // live: the page is in the pool
+  bool any;
   int h, page, place0, first, last, start, row0;
   float ks, vs;
-  float4 lo, hi;
-  bool any;
+  uint32_t lo[4], hi[4];  // bounds of the lane's channels, 16-bit pairs
 
   __device__ __forceinline__ void open(const AppendArgs& a, int b, int page_of_request, int hh, int s, int r0, int n) {
     const int ps = int(a.c.ps.d);
@@ -152,52 +187,89 @@ struct Unit {
     h = is_q ? hh - a.c.H : hh;
     ks = DT == kE4m3 && !is_q && a.c.k_scale != nullptr ? a.c.k_scale[h] : 1.0f;
     vs = DT == kE4m3 && !is_q && a.c.v_scale != nullptr ? a.c.v_scale[h] : 1.0f;
-    lo = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
-    hi = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     any = false;
+    constexpr uint32_t kInf = DT == kBf16 ? 0x7F807F80u : 0x7C007C00u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = kInf;
+      hi[i] = kInf | 0x80008000u;
+    }
   }
   __device__ __forceinline__ void check(const AppendArgs& a) {  // (apart from open: the loads in between need no page)
     live = page >= 0 && page < a.c.n_pages;
     if (!live) flag(a.c, KVQ_PAGED_ERR_PAGE);
   }
-  __device__ __forceinline__ uint2 key(const AppendArgs& a, const Lane& L, int t) const {
+  // Where token t's row of this head is, read and (queries) written.
+  __device__ __forceinline__ const char* source(const AppendArgs& a, int t) const {
     const long long row = row0 + (t - start);
-    const char* p = is_q ? a.q + row * a.q_stride : a.k + row * a.k_stride;
-    return *reinterpret_cast<const uint2*>(p + (h * kD + L.d) * 2);
+    return (is_q ? a.q + row * a.q_stride : a.k + row * a.k_stride) + h * (kD * 2);
   }
-  __device__ __forceinline__ uint2 value(const AppendArgs& a, const Lane& L, int t) const {
-    const long long row = row0 + (t - start);
-    return *reinterpret_cast<const uint2*>(a.v + row * a.v_stride + (h * kD + L.d) * 2);
+  __device__ __forceinline__ const char* value(const AppendArgs& a, int t) const {
+    return a.v + (row0 + (t - start)) * a.v_stride + h * (kD * 2);
   }
-  __device__ __forceinline__ void put(const AppendArgs& a, const Lane& L, int t, float4 x, uint2 v) {
-    if (is_q) {
-      store4<IN>(a.q_out + (long long)(row0 + (t - start)) * a.q_out_stride + (h * kD + L.d) * 2, x);
-      return;
-    }
-    const long long place = (long long)page * a.c.page_stride + (long long)(t - place0) * a.c.token_stride +
-                            (long long)h * a.c.head_stride + L.d * elem_bytes<DT>();
+  __device__ __forceinline__ char* query_out(const AppendArgs& a, int t) const {
+    return a.q_out + (row0 + (t - start)) * a.q_out_stride + h * (kD * 2);
+  }
+  __device__ __forceinline__ long long place(const AppendArgs& a, int t) const {  // in k and v
+    return (long long)page * a.c.page_stride + (long long)(t - place0) * a.c.token_stride +
+           (long long)h * a.c.head_stride;
+  }
+  __device__ __forceinline__ static void put_query(const Lane& L, char* p, const Wide& x) {
+    store4<IN>(p + 2 * L.a, x.a);
+    store4<IN>(p + 2 * L.b, x.b);
+  }
+  __device__ __forceinline__ void put(const Lane& L, char* k, char* w, Wide x, const Raw& v) {
+    constexpr int kE = elem_bytes<DT>();
     if constexpr (DT == kE4m3) {
-      x = div4(x, ks);
-      store4<DT>(a.c.v + place, div4(floats<IN>(v), vs));
+      x.a = div4(x.a, ks);
+      x.b = div4(x.b, ks);
+      store4<DT>(w + L.a, div4(load4<IN>(&v.a), vs));
+      store4<DT>(w + L.b, div4(load4<IN>(&v.b), vs));
     } else {
-      *reinterpret_cast<uint2*>(a.c.v + place) = v;
+      *reinterpret_cast<uint2*>(w + kE * L.a) = v.a;
+      *reinterpret_cast<uint2*>(w + kE * L.b) = v.b;
     }
-    store4<DT>(a.c.k + place, x);
-    const float4 s = rounded4<DT>(x);
-    lo = min_nan(lo, s);
-    hi = max_nan(hi, s);
+    alignas(8) char stored[2][4 * kE];
+    store4<DT>(stored[0], x.a);
+    store4<DT>(stored[1], x.b);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      char* to = k + kE * (i == 0 ? L.a : L.b);
+      if constexpr (DT == kE4m3) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(stored[i]);
+      else *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(stored[i]);
+      const uint2 y = pairs_of<DT>(stored[i]);
+      lo[2 * i] = smaller<DT>(lo[2 * i], y.x);
+      lo[2 * i + 1] = smaller<DT>(lo[2 * i + 1], y.y);
+      hi[2 * i] = larger<DT>(hi[2 * i], y.x);
+      hi[2 * i + 1] = larger<DT>(hi[2 * i + 1], y.y);
+    }
     any = true;
+  }
+  // The bounds of the two teams of a warp joined.
+  __device__ __forceinline__ void join() {
+    any = __any_sync(0xFFFFFFFFu, any);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = smaller<DT>(lo[i], __shfl_xor_sync(0xFFFFFFFFu, lo[i], kTeam));
+      hi[i] = larger<DT>(hi[i], __shfl_xor_sync(0xFFFFFFFFu, hi[i], kTeam));
+    }
   }
   __device__ __forceinline__ void close(const AppendArgs& a, const Lane& L) const {
     if (is_q || !any || a.c.bounds == nullptr) return;
-    char* p = a.c.bounds + (((long long)page * a.c.H + h) * 2 * kD + L.d) * elem_bytes<DT>();
-    float4 l = lo, u = hi;
-    if (first > place0) {  // the page held tokens before
-      l = min_nan(l, load4<DT>(p));
-      u = max_nan(u, load4<DT>(p + kD * elem_bytes<DT>()));
+    constexpr int kE = elem_bytes<DT>();
+    char* p = a.c.bounds + ((long long)page * a.c.H + h) * (2 * kD * kE);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      char* to = p + kE * (i == 0 ? L.a : L.b);
+      uint2 l = make_uint2(lo[2 * i], lo[2 * i + 1]), u = make_uint2(hi[2 * i], hi[2 * i + 1]);
+      if (first > place0) {  // the page held tokens before
+        const uint2 l0 = pairs_of<DT>(to), u0 = pairs_of<DT>(to + kD * kE);
+        l = make_uint2(smaller<DT>(l.x, l0.x), smaller<DT>(l.y, l0.y));
+        u = make_uint2(larger<DT>(u.x, u0.x), larger<DT>(u.y, u0.y));
+      }
+      put_pairs<DT>(to, l);
+      put_pairs<DT>(to + kD * kE, u);
     }
-    store4<DT>(p, l);
-    store4<DT>(p + kD * elem_bytes<DT>(), u);
   }
 };
 
@@ -216,10 +288,9 @@ __device__ __forceinline__ void flag_lengths(const AppendArgs& a) {
   }
 }
 
-template <int DT, int IN>
+template <int DT, int IN, bool INTER>
 __global__ void __launch_bounds__(kFewThreads) append_few_kernel(AppendArgs a) {
   __shared__ Prefix<kFewThreads> S;
-  const int lane = threadIdx.x & 31;
   const int heads = a.c.H + (a.q != nullptr ? a.Hq : 0);
   auto count = [&](int b) { return (long long)pages_of(a, b) * heads; };
   long long total = (long long)a.B * heads;
@@ -228,11 +299,11 @@ __global__ void __launch_bounds__(kFewThreads) append_few_kernel(AppendArgs a) {
     total = S.pre[kFewThreads];
   }
   flag_lengths(a);
-  const long long warps = (long long)gridDim.x * (kFewThreads / 32);
-  const long long me = (long long)blockIdx.x * (kFewThreads / 32) + threadIdx.x / 32;
-  const long long u0 = me * total / warps, u1 = (me + 1) * total / warps;
+  const long long teams = (long long)gridDim.x * (kFewThreads / kTeam);
+  const long long me = (long long)blockIdx.x * (kFewThreads / kTeam) + threadIdx.x / kTeam;
+  const long long u0 = me * total / teams, u1 = (me + 1) * total / teams;
   if (u0 >= u1) return;
-  const Lane L(a, lane);
+  const Lane L(a, threadIdx.x % kTeam);
   long long at = u0;
   int b, hh, page_i;
   if (a.offsets == nullptr) {
@@ -254,29 +325,19 @@ __global__ void __launch_bounds__(kFewThreads) append_few_kernel(AppendArgs a) {
     if (n > 0) {
       Unit<DT, IN> u;
       u.open(a, b, a.c.ps.div(start) + page_i, hh, start, row0, n);
-      for (int t0 = u.first; t0 < u.last; t0 += kFewRows) {
-        uint2 x[kFewRows], v[kFewRows];
-        Angles g[kFewRows];
-        bool ok[kFewRows];
-#pragma unroll
-        for (int i = 0; i < kFewRows; ++i) {
-          const int t = t0 + i;
-          ok[i] = t < u.last;
-          x[i] = v[i] = make_uint2(0, 0);
-          if (!ok[i]) continue;
-          x[i] = u.key(a, L, t);
-          if (!u.is_q) v[i] = u.value(a, L, t);
-          const int pos = position(a, u, t);
-          ok[i] = pos >= 0;
-          if (ok[i]) g[i].load(a, L, a.rope + (long long)pos * a.R);
-          else flag(a.c, KVQ_PAGED_ERR_POSITION);
-        }
+      for (int t = u.first; t < u.last; ++t) {
+        const Raw x = load_raw(u.source(a, t), L);
+        Raw v{};
+        if (!u.is_q) v = load_raw(u.value(a, t), L);
+        const int pos = position(a, u, t);
+        Angles g;
+        if (pos >= 0) g.load<INTER>(a, L, a.rope + (long long)pos * a.R);
+        else flag(a.c, KVQ_PAGED_ERR_POSITION);
         u.check(a);
-#pragma unroll
-        for (int i = 0; i < kFewRows; ++i) {
-          const float4 r = rotate<IN>(a, L, g[i], x[i]);
-          if (ok[i] && u.live) u.put(a, L, t0 + i, r, v[i]);
-        }
+        if (pos < 0 || !u.live) continue;
+        const Wide y = rotate<IN, INTER>(L, g, x);
+        if (u.is_q) u.put_query(L, u.query_out(a, t), y);
+        else u.put(L, a.c.k + u.place(a, t), a.c.v + u.place(a, t), y, v);
       }
       u.close(a, L);
     }
@@ -293,77 +354,88 @@ __global__ void __launch_bounds__(kFewThreads) append_few_kernel(AppendArgs a) {
   }
 }
 
-template <int DT, int IN>
-__global__ void __launch_bounds__(kManyThreads, kManyBlocksPerSm) append_many_kernel(AppendArgs a) {
+// Keys and values: WARPS warps have a unit (1 or all of the block).
+template <int DT, int IN, bool INTER, int WARPS>
+__global__ void __launch_bounds__(kManyThreads, 3) append_keys_kernel(AppendArgs a) {
+  constexpr int kTeams = 2 * WARPS;  // of a unit
   __shared__ Prefix<kManyThreads> S;
-  __shared__ int s_pos[kSlice];  // table row of each staged row, -1: none
-  extern __shared__ __align__(16) float s_rope[];  // [kSlice][R]
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int heads = a.c.H + (a.q != nullptr ? a.Hq : 0), groups = (heads + kManyWarps - 1) / kManyWarps;
-  auto count = [&](int b) { return (long long)pages_of(a, b) * groups; };
+  __shared__ uint32_t s_bound[WARPS > 1 ? kManyWarps : 1][8][kTeam];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x % kTeam;
+  const int team = WARPS > 1 ? threadIdx.x / kTeam : (threadIdx.x / kTeam) & 1;
+  auto count = [&](int b) { return (long long)pages_of(a, b) * a.c.H; };
   build_prefix<kManyThreads>(S, a.B, count);
   flag_lengths(a);
-  const long long total = S.pre[kManyThreads];
-  const long long u0 = blockIdx.x * total / gridDim.x, u1 = (blockIdx.x + 1) * total / gridDim.x;
+  const long long total = S.pre[kManyThreads], groups = (long long)gridDim.x * (kManyWarps / WARPS);
+  const long long me = (long long)blockIdx.x * (kManyWarps / WARPS) + (WARPS > 1 ? 0 : warp);
+  const long long u0 = me * total / groups, u1 = (me + 1) * total / groups;
   if (u0 >= u1) return;
   const Lane L(a, lane);
   long long at = u0;
   int b = find_request<kManyThreads>(S, a.B, count, at);
-  int page_i = int(at / groups), grp = int(at % groups);
+  int page_i = int(at / a.c.H), h = int(at % a.c.H);
   int start = 0, row0 = 0, n = rows_of(a, b, start, row0), pages = pages_of(a, b);
   for (long long w = u0; w < u1; ++w) {
-    while (pages == 0 && b < a.B - 1) {
+    while (pages == 0 && b < a.B - 1) {  // requests that bring nothing hold no unit
       ++b;
       n = rows_of(a, b, start, row0);
       pages = pages_of(a, b);
     }
-    if (n > 0) {  // (the same for the whole block)
-      const int hh = grp * kManyWarps + warp;
-      const bool active = hh < heads;
-      Unit<DT, IN> u;
-      u.open(a, b, a.c.ps.div(start) + page_i, active ? hh : 0, start, row0, n);
-      for (int s0 = u.first; s0 < u.last; s0 += kSlice) {
-        const int rows = min(kSlice, u.last - s0), per = a.R / 4;  // 16-byte chunks of a table row
-        __syncthreads();  // the slice before is done with
-        if (threadIdx.x < rows) {
-          const int pos = position(a, u, s0 + threadIdx.x);
-          s_pos[threadIdx.x] = pos;
-          if (pos < 0) flag(a.c, KVQ_PAGED_ERR_POSITION);
-        }
-        for (int i = threadIdx.x; i < rows * per; i += kManyThreads) {
-          const int r = i / per, c = i - r * per, pos = position(a, u, s0 + r);
-          if (pos >= 0)
-            *reinterpret_cast<float4*>(s_rope + r * a.R + 4 * c) =
-                *reinterpret_cast<const float4*>(a.rope + (long long)pos * a.R + 4 * c);
-        }
-        __syncthreads();
-        if (s0 == u.first) u.check(a);
-        if (!active || !u.live) continue;
-        for (int r0 = 0; r0 < rows; r0 += kManyRows) {
-          uint2 x[kManyRows], v[kManyRows];
+    Unit<DT, IN> u;
+    u.open(a, b, a.c.ps.div(start) + page_i, h, start, row0, max(n, 0));
+    u.check(a);
+    if (u.live) {
+      for (int t0 = u.first + team; t0 < u.last; t0 += kTeams * kKeyRows) {
+        Raw x[kKeyRows], y[kKeyRows];
+        Angles g[kKeyRows];
+        bool ok[kKeyRows];
 #pragma unroll
-          for (int i = 0; i < kManyRows; ++i) {
-            x[i] = v[i] = make_uint2(0, 0);
-            if (r0 + i < rows) {
-              x[i] = u.key(a, L, s0 + r0 + i);
-              if (!u.is_q) v[i] = u.value(a, L, s0 + r0 + i);
-            }
-          }
+        for (int i = 0; i < kKeyRows; ++i) {
+          const int t = t0 + i * kTeams;
+          ok[i] = t < u.last;
+          if (!ok[i]) continue;
+          x[i] = load_raw(u.source(a, t), L);
+          y[i] = load_raw(u.value(a, t), L);
+          const int pos = position(a, u, t);
+          ok[i] = pos >= 0;
+          if (ok[i]) g[i].load<INTER>(a, L, a.rope + (long long)pos * a.R);
+          else flag(a.c, KVQ_PAGED_ERR_POSITION);
+        }
 #pragma unroll
-          for (int i = 0; i < kManyRows; ++i) {
-            const int r = r0 + i;
-            if (r >= rows) break;
-            Angles g;
-            g.load(a, L, s_rope + r * a.R);
-            const float4 y = rotate<IN>(a, L, g, x[i]);
-            if (s_pos[r] >= 0) u.put(a, L, s0 + r, y, v[i]);
-          }
+        for (int i = 0; i < kKeyRows; ++i) {
+          if (!ok[i]) continue;
+          const long long place = u.place(a, t0 + i * kTeams);
+          u.put(L, a.c.k + place, a.c.v + place, rotate<IN, INTER>(L, g[i], x[i]), y[i]);
         }
       }
-      if (active) u.close(a, L);
     }
-    if (++grp == groups) {
-      grp = 0;
+    if (a.c.bounds != nullptr) {
+      __syncwarp();
+      u.join();
+      if constexpr (WARPS > 1) {
+        if ((threadIdx.x & 31) < kTeam) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s_bound[warp][i][lane] = u.lo[i];
+            s_bound[warp][4 + i][lane] = u.hi[i];
+          }
+        }
+        u.any = __syncthreads_or(u.any);
+        if (threadIdx.x < kTeam) {
+          for (int v = 1; v < WARPS; ++v)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              u.lo[i] = smaller<DT>(u.lo[i], s_bound[v][i][lane]);
+              u.hi[i] = larger<DT>(u.hi[i], s_bound[v][4 + i][lane]);
+            }
+          u.close(a, L);
+        }
+        __syncthreads();  // s_bound is free again
+      } else if (team == 0) {
+        u.close(a, L);
+      }
+    }
+    if (++h == a.c.H) {
+      h = 0;
       if (++page_i == pages) {
         page_i = 0;
         if (++b < a.B) {
@@ -375,20 +447,88 @@ __global__ void __launch_bounds__(kManyThreads, kManyBlocksPerSm) append_many_ke
   }
 }
 
+// Queries: the new rows of all requests, concatenated and cut into equal ranges,
+// one per block; a team takes four heads of a row at a time.
+template <int IN, bool INTER>
+__global__ void __launch_bounds__(kManyThreads, 4) append_queries_kernel(AppendArgs a) {
+  __shared__ Prefix<kManyThreads> S;
+  const int team = threadIdx.x / kTeam, quads = (a.Hq + kQueryHeads - 1) / kQueryHeads;
+  auto count = [&](int b) {
+    int start, row0;
+    return (long long)max(0, rows_of(a, b, start, row0)) * quads;
+  };
+  build_prefix<kManyThreads>(S, a.B, count);
+  const long long total = S.pre[kManyThreads];
+  const long long i0 = blockIdx.x * total / gridDim.x, i1 = (blockIdx.x + 1) * total / gridDim.x;
+  long long at = i0 + team;
+  if (at >= i1) return;
+  const Lane L(a, threadIdx.x % kTeam);
+  const long long left = i1 - at;
+  int b = find_request<kManyThreads>(S, a.B, count, at);
+  int start = 0, row0 = 0, n = rows_of(a, b, start, row0);
+  int row = int(at / quads), quad = int(at % quads);  // of the request
+  for (long long i = 0; i < left; i += kManyThreads / kTeam) {
+    while (row >= n && b < a.B - 1) {
+      row -= max(n, 0);
+      ++b;
+      n = rows_of(a, b, start, row0);
+    }
+    const int t = start + row, page = a.table[(long long)b * a.max_pages + a.c.ps.div(t)];
+    const int pos = a.positions != nullptr ? a.positions[row0 + row] : t;
+    const bool ok = a.R == 0 || (pos >= 0 && pos < a.rope_positions);
+    const char* from = a.q + (long long)(row0 + row) * a.q_stride + quad * (kQueryHeads * kD * 2);
+    const int heads = min(kQueryHeads, a.Hq - quad * kQueryHeads);
+    Raw x[kQueryHeads];
+#pragma unroll
+    for (int h = 0; h < kQueryHeads; ++h)
+      if (h < heads) x[h] = load_raw(from + h * (kD * 2), L);
+    Angles g;
+    if (ok) g.load<INTER>(a, L, a.rope + (long long)pos * a.R);
+    if (ok && page >= 0 && page < a.c.n_pages) {  // (the keys' kernel flags the others)
+      char* to = a.q_out + (long long)(row0 + row) * a.q_out_stride + quad * (kQueryHeads * kD * 2);
+#pragma unroll
+      for (int h = 0; h < kQueryHeads; ++h) {
+        if (h >= heads) continue;
+        const Wide y = rotate<IN, INTER>(L, g, x[h]);
+        store4<IN>(to + h * (kD * 2) + 2 * L.a, y.a);
+        store4<IN>(to + h * (kD * 2) + 2 * L.b, y.b);
+      }
+    }
+    quad += kManyThreads / kTeam;
+    while (quad >= quads) {
+      quad -= quads;
+      ++row;
+    }
+  }
+}
+
+template <int DT, int IN, bool INTER>
+cudaError_t launch_form(const AppendArgs& a, int sms, cudaStream_t stream) {
+  const long long pages = a.offsets == nullptr ? a.B : a.n_rows / a.c.ps.d + 2 * (long long)a.B;  // at most
+  auto grid = [&](long long need, int per_sm) { return int(need < (long long)per_sm * sms ? need : (long long)per_sm * sms); };
+  count_launch();
+  if (a.offsets == nullptr || a.n_rows <= 8LL * a.B) {
+    const long long teams = pages * (a.c.H + (a.q != nullptr ? a.Hq : 0));
+    append_few_kernel<DT, IN, INTER>
+        <<<grid((teams * kTeam + kFewThreads - 1) / kFewThreads, 8), kFewThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+  if (a.c.ps.d > 32)
+    append_keys_kernel<DT, IN, INTER, kManyWarps><<<grid(pages * a.c.H, 3), kManyThreads, 0, stream>>>(a);
+  else
+    append_keys_kernel<DT, IN, INTER, 1>
+        <<<grid((pages * a.c.H + kManyWarps - 1) / kManyWarps, 3), kManyThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.q == nullptr) return e;
+  count_launch();
+  append_queries_kernel<IN, INTER>
+      <<<grid((a.n_rows * (long long)a.Hq + 63) / 64, 4), kManyThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
 template <int DT, int IN>
 cudaError_t launch_types(const AppendArgs& a, int sms, cudaStream_t stream) {
-  const long long heads = a.c.H + (a.q != nullptr ? a.Hq : 0);
-  const long long pages = a.offsets == nullptr ? a.B : a.n_rows / a.c.ps.d + 2 * (long long)a.B;  // at most
-  count_launch();
-  if (a.offsets != nullptr && a.n_rows > 8LL * a.B) {
-    const long long need = pages * ((heads + kManyWarps - 1) / kManyWarps), fit = (long long)kManyBlocksPerSm * sms;
-    append_many_kernel<DT, IN>
-        <<<int(need < fit ? need : fit), kManyThreads, size_t(kSlice) * a.R * 4, stream>>>(a);
-  } else {
-    const long long need = (pages * heads + 3) / 4, fit = 8LL * sms;
-    append_few_kernel<DT, IN><<<int(need < fit ? need : fit), kFewThreads, 0, stream>>>(a);
-  }
-  return cudaGetLastError();
+  return a.interleaved ? launch_form<DT, IN, true>(a, sms, stream) : launch_form<DT, IN, false>(a, sms, stream);
 }
 
 }  // namespace
