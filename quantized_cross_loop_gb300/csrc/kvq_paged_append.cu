@@ -22,6 +22,7 @@
 // Rows in flight and resident warps bound these; staging the rotation table in
 // shared memory for eight heads, and fetching the next rows into registers ahead of
 // the arithmetic, were slower (a table's row is in L1 for the heads that follow).
+#include "kvq_attn_common.cuh"
 #include "kvq_paged.cuh"
 
 namespace kvq {
@@ -29,6 +30,7 @@ namespace paged {
 namespace {
 
 constexpr int kFewThreads = 128;
+constexpr int kFewBlocksPerSm = 5;
 constexpr int kTeam = 16;          // lanes of a row
 constexpr int kManyThreads = 256;
 constexpr int kManyWarps = kManyThreads / 32;
@@ -289,7 +291,9 @@ __device__ __forceinline__ void flag_lengths(const AppendArgs& a) {
 }
 
 template <int DT, int IN, bool INTER>
-__global__ void __launch_bounds__(kFewThreads) append_few_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) append_few_kernel(AppendArgs a) {
+  wait_prior_grid();
+  allow_dependents();
   __shared__ Prefix<kFewThreads> S;
   const int heads = a.c.H + (a.q != nullptr ? a.Hq : 0);
   auto count = [&](int b) { return (long long)pages_of(a, b) * heads; };
@@ -357,6 +361,8 @@ __global__ void __launch_bounds__(kFewThreads) append_few_kernel(AppendArgs a) {
 // Keys and values: WARPS warps have a unit (1 or all of the block).
 template <int DT, int IN, bool INTER, int WARPS>
 __global__ void __launch_bounds__(kManyThreads, 3) append_keys_kernel(AppendArgs a) {
+  wait_prior_grid();
+  allow_dependents();
   constexpr int kTeams = 2 * WARPS;  // of a unit
   __shared__ Prefix<kManyThreads> S;
   __shared__ uint32_t s_bound[WARPS > 1 ? kManyWarps : 1][8][kTeam];
@@ -451,6 +457,8 @@ __global__ void __launch_bounds__(kManyThreads, 3) append_keys_kernel(AppendArgs
 // one per block; a team takes four heads of a row at a time.
 template <int IN, bool INTER>
 __global__ void __launch_bounds__(kManyThreads, 4) append_queries_kernel(AppendArgs a) {
+  wait_prior_grid();
+  allow_dependents();
   __shared__ Prefix<kManyThreads> S;
   const int team = threadIdx.x / kTeam, quads = (a.Hq + kQueryHeads - 1) / kQueryHeads;
   auto count = [&](int b) {
@@ -509,21 +517,20 @@ cudaError_t launch_form(const AppendArgs& a, int sms, cudaStream_t stream) {
   count_launch();
   if (a.offsets == nullptr || a.n_rows <= 8LL * a.B) {
     const long long teams = pages * (a.c.H + (a.q != nullptr ? a.Hq : 0));
-    append_few_kernel<DT, IN, INTER>
-        <<<grid((teams * kTeam + kFewThreads - 1) / kFewThreads, 8), kFewThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(append_few_kernel<DT, IN, INTER>,
+                            dim3(grid((teams * kTeam + kFewThreads - 1) / kFewThreads, kFewBlocksPerSm)),
+                            dim3(kFewThreads), 0, stream, a);
   }
-  if (a.c.ps.d > 32)
-    append_keys_kernel<DT, IN, INTER, kManyWarps><<<grid(pages * a.c.H, 3), kManyThreads, 0, stream>>>(a);
-  else
-    append_keys_kernel<DT, IN, INTER, 1>
-        <<<grid((pages * a.c.H + kManyWarps - 1) / kManyWarps, 3), kManyThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      a.c.ps.d > 32 ? launch_dependent(append_keys_kernel<DT, IN, INTER, kManyWarps>, dim3(grid(pages * a.c.H, 3)),
+                                       dim3(kManyThreads), 0, stream, a)
+                    : launch_dependent(append_keys_kernel<DT, IN, INTER, 1>,
+                                       dim3(grid((pages * a.c.H + kManyWarps - 1) / kManyWarps, 3)),
+                                       dim3(kManyThreads), 0, stream, a);
   if (e != cudaSuccess || a.q == nullptr) return e;
   count_launch();
-  append_queries_kernel<IN, INTER>
-      <<<grid((a.n_rows * (long long)a.Hq + 63) / 64, 4), kManyThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(append_queries_kernel<IN, INTER>, dim3(grid((a.n_rows * (long long)a.Hq + 63) / 64, 4)),
+                          dim3(kManyThreads), 0, stream, a);
 }
 
 template <int DT, int IN>

@@ -7,11 +7,15 @@
 // Bound: HBM. A token and KV head bring 4 D bytes (16-bit) for 4 D g flops, so a
 // block must keep loads in flight and spend few instructions a byte.
 //
-// Work: the tiles of 64 tokens of all (request, KV head) units, concatenated and
-// cut into equal ranges, one per block (two blocks an SM); lengths are read on
+// Work: the tiles (64 or 128 tokens) of all (request, KV head) units, concatenated
+// and cut into equal ranges, one per block (two blocks an SM); lengths are read on
 // the device, so a captured call follows them. A unit that lies in one block's
 // range is finished there; of the others each block leaves (m, l, sum) in one of
-// its two slots, and the combine kernel joins them.
+// its two slots, and the combine kernel joins them. (Joined in the same launch, by the
+// block that finds the flags of all parts set, they took longer in every case:
+// 10.1 against 8.7 us for one request of 256 tokens, 97.8 against 90.2 us for
+// 4 x 32768 and eight query heads: the fences and flags come to more than a second
+// launch that is already waiting.)
 //
 // A warp owns 16 tokens of every tile and a ring of its own in shared memory,
 // filled by 16-byte asynchronous copies, so that the main loop has no block
@@ -29,7 +33,6 @@
 // E4M3: keys and values become FP16 in registers (exact); a BF16 query is scaled
 // by a power of two into FP16's range (exact down to 2^-31 of its largest).
 #include <atomic>
-#include <cstddef>
 
 #include "kvq_attn_common.cuh"
 #include "kvq_paged.cuh"
@@ -40,24 +43,28 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = 4;
-constexpr int kTile = 64;          // tokens per tile, 16 per warp
 constexpr int kBufStride = 132;    // floats per head of the merge buffers: the lanes' columns hit distinct banks
 constexpr int kBlocksPerSm = 2;
-constexpr int kCombineThreads = 512;
+constexpr int kCombineThreads = 1024;
+constexpr int kCombineWarps = kCombineThreads / 32;
+constexpr int kMinTiles = 2;       // tiles of a block's range, once every SM has one
 
 struct Rec {  // of a block: the unit that starts in its range and ends in block `last`'s (u < 0: none)
   int32_t u, last;
 };
 
-// Workspace: Rec[n], then 2 n slots of g heads x (sum[128], m, l).
-__host__ __device__ constexpr size_t recs_bytes(int n) { return (size_t(n) * sizeof(Rec) + 15) / 16 * 16; }
-__host__ __device__ constexpr size_t slot_floats(int g) { return size_t(g) * (kD + 2); }
+// Workspace: Rec[n], then 2 n slots of g heads x sum[128] and g x (m, l).
+__host__ __device__ constexpr size_t slots_offset(int n) { return (size_t(n) * sizeof(Rec) + 15) / 16 * 16; }
+__host__ __device__ constexpr size_t slot_floats(int g) { return size_t(g) * kD + (size_t(g) + 1) / 2 * 4; }  // (16-byte steps)
 
 template <int DT>
 struct Form {
   static constexpr int kRow = kD * elem_bytes<DT>();       // bytes of a row
-  static constexpr int kStages = DT == kE4m3 ? 5 : 3;      // 96 KB (16-bit) or 80 KB of ring per block
-  static constexpr int kSlice = 2 * 16 * kRow;             // a warp's K and V rows of a tile
+  static constexpr int kSteps = DT == kE4m3 ? 2 : 1;       // blocks of 16 tokens in a warp's slice of a tile: 8 KB
+  static constexpr int kRows = 16 * kSteps;
+  static constexpr int kTile = kRows * kWarps;             // tokens per tile
+  static constexpr int kStages = 3;                        // 96 KB of ring per block
+  static constexpr int kSlice = 2 * kRows * kRow;          // a warp's K and V rows of a tile
   static constexpr int kRing = kStages * kSlice;
   static constexpr bool kHalf = DT != kBf16;               // operands are FP16
   static constexpr float kShift = kHalf ? 14.0f : 0.0f;    // weights up to 2^14: FP16 parts of small ones stay normal
@@ -66,16 +73,12 @@ struct Form {
 template <int DT>
 struct Smem {
   char ring[kWarps][Form<DT>::kRing];
-  int mask[Form<DT>::kStages][kWarps];  // bits 0..15: rows that hold a token; bit 16: a refused row
+  uint32_t mask[Form<DT>::kStages][kWarps];  // bit i: row i of the slice holds a token
+  int refused[Form<DT>::kStages][kWarps];    // a row that the request or selection does not allow
   Prefix<kThreads> prefix;
   float m[kWarps][kMaxGroup], l[kWarps][kMaxGroup];
-  float buf[2][1];  // [2][heads][kBufStride], sized at launch
+  float buf[2 * 8 * kBufStride];  // sums of two warps, eight heads
 };
-
-template <int DT>
-constexpr size_t smem_bytes(int nt) {
-  return offsetof(Smem<DT>, buf) + size_t(2) * nt * 8 * kBufStride * 4;
-}
 
 __device__ __forceinline__ void copy16(uint32_t dst, const char* src, bool live) {
   const int n = live ? 16 : 0;  // 0: zeros
@@ -118,6 +121,21 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 2^x; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Four E4M3 values as two FP16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
 __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -142,7 +160,7 @@ __device__ __forceinline__ void split(float a, float b, uint32_t (&part)[3]) {
 }
 
 // Tokens (of the whole cache, or of the selected pages) that a call visits of a
-// request: its work is ceil(tokens / 64) tiles per KV head.
+// request: its work is ceil(tokens / tile) tiles per KV head.
 template <bool SEL>
 __device__ __forceinline__ int span_of(const AttnArgs& a, int T) {
   if (T <= 0) return 0;
@@ -151,13 +169,13 @@ __device__ __forceinline__ int span_of(const AttnArgs& a, int T) {
 }
 
 // A position in the concatenated tiles.
-template <bool SEL>
+template <bool SEL, int TILE>
 struct Cursor {
   int b, h, tile, T, span, tiles;
   __device__ __forceinline__ void load(const AttnArgs& a) {
     T = b < a.B ? checked_len(a.lens, b, a.max_pages, a.c.ps) : 0;
     span = span_of<SEL>(a, T);
-    tiles = (span + kTile - 1) / kTile;
+    tiles = (span + TILE - 1) / TILE;
   }
   __device__ __forceinline__ void next(const AttnArgs& a) {
     if (++tile < tiles) return;
@@ -171,7 +189,7 @@ struct Cursor {
   }
 };
 
-// Where a lane's row (token lane % 16 of the warp's slice) comes from, looked up in two steps.
+// Where a lane's row (of the warp's slice) comes from, looked up in two steps.
 struct Row {
   int page;     // step one: page of the request; step two: page of the pool
   int before;   // selection: the entry before
@@ -180,8 +198,8 @@ struct Row {
   int bad;      // KVQ_PAGED_ERR_* bits
 };
 
-template <bool SEL>
-__device__ __forceinline__ void look_up_entry(const AttnArgs& a, const Cursor<SEL>& at, int v, Row& r) {
+template <bool SEL, int TILE>
+__device__ __forceinline__ void look_up_entry(const AttnArgs& a, const Cursor<SEL, TILE>& at, int v, Row& r) {
   const int e = a.c.ps.div(v);
   r.place = v - e * int(a.c.ps.d);
   r.h = at.h;
@@ -292,10 +310,13 @@ struct Block {
     const bool in_pool = r.page >= 0 && r.page < a.c.n_pages;
     const bool live = r.live && in_pool;
     const int bad = r.bad | (r.live && !in_pool ? KVQ_PAGED_ERR_PAGE : 0);
-    const uint32_t rows = __ballot_sync(0xFFFFFFFFu, live) & 0xFFFFu;
+    const uint32_t rows = __ballot_sync(0xFFFFFFFFu, live) & (0xFFFFFFFFu >> (32 - F::kRows));
     const uint32_t refused = __ballot_sync(0xFFFFFFFFu, bad != 0);
     if (refused && bad) flag(a.c, bad);
-    if (lane == 0) S.mask[stage][warp] = int(rows | (refused ? 0x10000u : 0u));
+    if (lane == 0) {
+      S.mask[stage][warp] = rows;
+      S.refused[stage][warp] = refused != 0;
+    }
     const long long off = live ? (long long)r.page * a.c.page_stride + (long long)r.place * a.c.token_stride +
                                      (long long)r.h * a.c.head_stride
                                : -1;
@@ -303,31 +324,31 @@ struct Block {
     const uint32_t base = ring + stage * F::kSlice;
     const int chunk = lane % kChunks;
 #pragma unroll
-    for (int i = 0; i < 16 / kPer; ++i) {
+    for (int i = 0; i < F::kRows / kPer; ++i) {
       const int row = i * kPer + lane / kChunks;
       const long long x = __shfl_sync(0xFFFFFFFFu, off, row);
       const long long src = (x < 0 ? 0 : x) + chunk * 16;
       const int kc = DT == kE4m3 ? chunk ^ ((row & 1) << 2) : chunk ^ (row & 7);
       const int vc = DT == kE4m3 ? chunk ^ (((row >> 1) & 3) << 1) : chunk ^ (row & 7);
       copy16(base + row * F::kRow + kc * 16, a.c.k + src, x >= 0);
-      copy16(base + 16 * F::kRow + row * F::kRow + vc * 16, a.c.v + src, x >= 0);
+      copy16(base + F::kRows * F::kRow + row * F::kRow + vc * 16, a.c.v + src, x >= 0);
     }
   }
 
   __device__ __forceinline__ void attend(int stage) {
-    const uint32_t kb = ring + stage * F::kSlice, vb = kb + 16 * F::kRow;
-    const int mask = S.mask[stage][warp];
-    // logits: two blocks of eight tokens, even and odd k-steps apart (independent chains)
-    float s[2][2][4];
+    constexpr int kBlocks = 2 * F::kSteps;            // of eight tokens
+    constexpr int kChains = F::kSteps == 1 ? 2 : 1;   // even and odd k-steps apart, so that four chains run at once
+    const uint32_t kb = ring + stage * F::kSlice, vb = kb + F::kRows * F::kRow;
+    float s[kBlocks][kChains][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < kBlocks; ++t)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < kChains; ++e)
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[t][e][i] = 0.0f;
     auto qk = [&](int j, int t, uint32_t b0, uint32_t b1) {
-      if constexpr (NT == 2) mma<F::kHalf>(s[t][j & 1], qa[j][0], qa[j][2], qa[j][1], qa[j][3], b0, b1);
-      else mma<F::kHalf>(s[t][j & 1], qa[j][0], 0u, qa[j][1], 0u, b0, b1);
+      if constexpr (NT == 2) mma<F::kHalf>(s[t][j % kChains], qa[j][0], qa[j][2], qa[j][1], qa[j][3], b0, b1);
+      else mma<F::kHalf>(s[t][j % kChains], qa[j][0], 0u, qa[j][1], 0u, b0, b1);
     };
     const int mr = (lane & 7) + (lane >> 4) * 8, mc = (lane >> 3) & 1;  // the lane's row and chunk of an ldmatrix
     if constexpr (DT != kE4m3) {
@@ -342,87 +363,114 @@ struct Block {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
+        for (int t = 0; t < kBlocks; ++t) {
           const int row = t * 8 + lane / 4;
           const uint4 x = lds16(kb + row * 128 + ((((lane & 3) + 4 * i) ^ ((row & 1) << 2)) << 4));
           const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) qk(4 * i + j, t, e4m3x2_to_f16x2(w[j] & 0xFFFFu), e4m3x2_to_f16x2(w[j] >> 16));
+          for (int j = 0; j < 4; ++j) {
+            uint32_t b0, b1;
+            e4m3x4_to_f16(w[j], b0, b1);
+            qk(4 * i + j, t, b0, b1);
+          }
         }
     }
-    uint32_t part[2][NT][3];  // weights of the two token blocks, split
+    const uint32_t mask = S.mask[stage][warp];
+    if (mask != (0xFFFFFFFFu >> (32 - F::kRows))) {  // some rows hold no token
+#pragma unroll
+      for (int t = 0; t < kBlocks; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!((mask >> (8 * t + 2 * (lane & 3) + (i & 1))) & 1)) s[t][0][i] = -INFINITY;
+    }
+    uint32_t part[kBlocks][NT][3];  // the weights, split
     float alpha[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      float x[2][2];
+      float mx = -INFINITY;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < kBlocks; ++t)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          x[t][i] = (s[t][0][2 * n + i] + s[t][1][2 * n + i]) * scale[n];
-          const int row = 8 * t + 2 * (lane & 3) + i;
-          if (!((mask >> row) & 1)) x[t][i] = -INFINITY;
+          if constexpr (kChains == 2) s[t][0][2 * n + i] += s[t][1][2 * n + i];
+          mx = fmaxf(mx, s[t][0][2 * n + i]);
         }
-      float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 1));
       mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 2));
-      mx = fmaxf(m[n], mx);
+      mx = fmaxf(m[n], mx * scale[n]);  // (scale > 0)
       const float base = mx == -INFINITY ? 0.0f : mx;
-      alpha[n] = exp2f(m[n] - base);
+      alpha[n] = exp2_ftz(m[n] - base);
       m[n] = mx;
       float sum = 0.0f;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const float p0 = exp2f(x[t][0] - base + F::kShift), p1 = exp2f(x[t][1] - base + F::kShift);
+      for (int t = 0; t < kBlocks; ++t) {
+        const float p0 = exp2_ftz(fmaf(s[t][0][2 * n], scale[n], F::kShift - base));
+        const float p1 = exp2_ftz(fmaf(s[t][0][2 * n + 1], scale[n], F::kShift - base));
         sum += p0 + p1;
         split<F::kHalf>(p0, p1, part[t][n]);
       }
-      l[n] = l[n] * alpha[n] + sum;
-      if (mask & 0x10000) l[n] = NAN;  // a refused row: the whole unit's result is NaN
+      l[n] = fmaf(l[n], alpha[n], sum);
+      if (S.refused[stage][warp]) l[n] = NAN;  // the whole unit's result is NaN
     }
     float f[NT][2];  // rescaling of the heads whose sums this lane holds
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) f[n][i] = __shfl_sync(0xFFFFFFFFu, alpha[n], (2 * (lane & 3) + i) * 4);
-    auto pv = [&](int j, const uint32_t (&v)[4]) {
+    // products of values and weights of 16 tokens (step k), the small parts first
+    auto pv = [&](float (&c)[4], int k, int n, const uint32_t (&v)[4]) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int i = F::kHalf ? 1 : 2; i >= 0; --i)
+        mma<F::kHalf>(c, v[0], v[1], v[2], v[3], part[2 * k][n][i], part[2 * k + 1][n][i]);
+    };
+    auto add = [&](int j, int n, const float (&c)[4]) {
 #pragma unroll
-        for (int i = F::kHalf ? 1 : 2; i >= 0; --i)
-          mma<F::kHalf>(c, v[0], v[1], v[2], v[3], part[0][n][i], part[1][n][i]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[j][4 * n + i] = o[j][4 * n + i] * f[n][i & 1] + c[i];
-      }
+      for (int i = 0; i < 4; ++i) o[j][4 * n + i] = fmaf(o[j][4 * n + i], f[n][i & 1], c[i]);
     };
     if constexpr (DT != kE4m3) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         uint32_t v[4];
         ldmatrix4_trans(v, vb + mr * 256 + (((2 * j + mc) ^ (mr & 7)) << 4));
-        pv(j, v);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          pv(c, 0, n, v);
+          add(j, n, c);
+        }
       }
     } else {
-      // the lane's 16 channels (chunk lane / 4) of its four tokens 2q, 2q + 1, 2q + 8, 2q + 9; the operand of step j
-      // takes channels 2j and 2j + 1 of them as its rows lane / 4 and lane / 4 + 8
-      uint4 x[4];
+      // the lane's 16 channels (chunk lane / 4) of its four tokens 2q, 2q + 1, 2q + 8, 2q + 9 of a step; the operand
+      // of product j takes channels 2j and 2j + 1 of them as its rows lane / 4 and lane / 4 + 8
+      uint4 x[F::kSteps][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = 2 * (lane & 3) + (i & 1) + 8 * (i >> 1);
-        x[i] = lds16(vb + row * 128 + (((lane >> 2) ^ (((row >> 1) & 3) << 1)) << 4));
-      }
+      for (int k = 0; k < F::kSteps; ++k)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t w[4] = {(&x[0].x)[k], (&x[1].x)[k], (&x[2].x)[k], (&x[3].x)[k]};
-        const uint32_t lo0 = __byte_perm(w[0], w[1], 0x5140), hi0 = __byte_perm(w[0], w[1], 0x7362);
-        const uint32_t lo1 = __byte_perm(w[2], w[3], 0x5140), hi1 = __byte_perm(w[2], w[3], 0x7362);
-        const uint32_t even[4] = {e4m3x2_to_f16x2(lo0 & 0xFFFFu), e4m3x2_to_f16x2(lo0 >> 16),
-                                  e4m3x2_to_f16x2(lo1 & 0xFFFFu), e4m3x2_to_f16x2(lo1 >> 16)};
-        const uint32_t odd[4] = {e4m3x2_to_f16x2(hi0 & 0xFFFFu), e4m3x2_to_f16x2(hi0 >> 16),
-                                 e4m3x2_to_f16x2(hi1 & 0xFFFFu), e4m3x2_to_f16x2(hi1 >> 16)};
-        pv(2 * k, even);
-        pv(2 * k + 1, odd);
+        for (int i = 0; i < 4; ++i) {
+          const int row = 16 * k + 2 * (lane & 3) + (i & 1) + 8 * (i >> 1);
+          x[k][i] = lds16(vb + row * 128 + (((lane >> 2) ^ (((row >> 1) & 3) << 1)) << 4));
+        }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {  // four channels: products 2 w and 2 w + 1
+        uint32_t v[F::kSteps][2][4];
+#pragma unroll
+        for (int k = 0; k < F::kSteps; ++k) {
+          const uint32_t y[4] = {(&x[k][0].x)[w], (&x[k][1].x)[w], (&x[k][2].x)[w], (&x[k][3].x)[w]};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {  // tokens 2q, 2q + 1 and 2q + 8, 2q + 9
+            e4m3x4_to_f16(__byte_perm(y[2 * i], y[2 * i + 1], 0x5140), v[k][0][2 * i], v[k][0][2 * i + 1]);
+            e4m3x4_to_f16(__byte_perm(y[2 * i], y[2 * i + 1], 0x7362), v[k][1][2 * i], v[k][1][2 * i + 1]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < F::kSteps; ++k) pv(c, k, n, v[k][i]);
+            add(2 * w + i, n, c);
+          }
       }
     }
   }
@@ -434,7 +482,7 @@ struct Block {
 
   // The block's four warps joined; the result goes to out and lse, or to `slot`.
   __device__ __forceinline__ void finish(int b, int h, float* slot) {
-    float* buf = reinterpret_cast<float*>(reinterpret_cast<char*>(&S) + offsetof(Smem<DT>, buf));
+    float* buf = S.buf;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 1);
@@ -449,72 +497,77 @@ struct Block {
       const float x = fmaxf(fmaxf(S.m[0][head], S.m[1][head]), fmaxf(S.m[2][head], S.m[3][head]));
       return x == -INFINITY ? 0.0f : x;
     };
-    constexpr int kHeads = 8 * NT;
-    float f[NT][2];
+    float* mine = buf + (warp & 1) * 8 * kBufStride;
+    const float vs = DT == kE4m3 && a.c.v_scale != nullptr ? a.c.v_scale[h] : 1.0f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {  // eight heads at a time
+      float f[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int head = 2 * (lane & 3) + i + 8 * n;
-        f[n][i] = exp2f(S.m[warp][head] - top(head));
+        f[i] = exp2f(S.m[warp][head] - top(head));
       }
-    float* mine = buf + (warp & 1) * kHeads * kBufStride;
-    auto at = [&](int j, int i) -> float& {  // i = 4 n + 2 c + head bit
-      return mine[(2 * (lane & 3) + (i & 1) + 8 * (i >> 2)) * kBufStride + channel(j, (i >> 1) & 1)];
-    };
-    if (warp >= 2) {
+      auto at = [&](int j, int i) -> float& {  // i = 2 c + head bit
+        return mine[(2 * (lane & 3) + (i & 1)) * kBufStride + channel(j, i >> 1)];
+      };
+      if (n > 0) __syncthreads();
+      if (warp >= 2) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int i = 0; i < 4 * NT; ++i) at(j, i) = o[j][i] * f[i >> 2][i & 1];
-    }
-    __syncthreads();
-    if (warp < 2) {
+          for (int i = 0; i < 4; ++i) at(j, i) = o[j][4 * n + i] * f[i & 1];
+      }
+      __syncthreads();
+      if (warp < 2) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int i = 0; i < 4 * NT; ++i) at(j, i) += o[j][i] * f[i >> 2][i & 1];
-    }
-    __syncthreads();
-    const int c = threadIdx.x;
-    const float vs = DT == kE4m3 && a.c.v_scale != nullptr ? a.c.v_scale[h] : 1.0f;
-    for (int j = 0; j < a.g; ++j) {
-      const float mx = top(j);
-      float sum = 0.0f;
+          for (int i = 0; i < 4; ++i) at(j, i) += o[j][4 * n + i] * f[i & 1];
+      }
+      __syncthreads();
+      const int c = threadIdx.x;
+      for (int i = 0; i < min(8, a.g - 8 * n); ++i) {
+        const int j = 8 * n + i;
+        const float mx = top(j);
+        float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += S.l[w][j] * exp2f(S.m[w][j] - mx);
-      const float x = buf[j * kBufStride + c] + buf[(kHeads + j) * kBufStride + c];
-      const bool none = fmaxf(fmaxf(S.m[0][j], S.m[1][j]), fmaxf(S.m[2][j], S.m[3][j])) == -INFINITY;
-      const float at_m = none ? -INFINITY : mx - F::kShift;
-      if (slot != nullptr) {
-        slot[j * kD + c] = x * vs;
-        if (c == 0) {
-          slot[a.g * kD + 2 * j] = at_m;
-          slot[a.g * kD + 2 * j + 1] = sum;
+        for (int w = 0; w < kWarps; ++w) sum += S.l[w][j] * exp2f(S.m[w][j] - mx);
+        const float x = buf[i * kBufStride + c] + buf[(8 + i) * kBufStride + c];
+        const bool none = fmaxf(fmaxf(S.m[0][j], S.m[1][j]), fmaxf(S.m[2][j], S.m[3][j])) == -INFINITY;
+        const float at_m = none ? -INFINITY : mx - F::kShift;
+        if (slot != nullptr) {
+          slot[j * kD + c] = x * vs;
+          if (c == 0) {
+            slot[a.g * kD + 2 * j] = at_m;
+            slot[a.g * kD + 2 * j + 1] = sum;
+          }
+        } else {
+          const long long hq = (long long)b * a.Hq + h * a.g + j;
+          a.out[hq * kD + c] = sum == 0.0f ? 0.0f : x * vs / sum;
+          if (a.lse != nullptr && c == 0) a.lse[hq] = (at_m + log2f(sum)) * 0.6931471805599453f;
         }
-      } else {
-        const long long hq = (long long)b * a.Hq + h * a.g + j;
-        a.out[hq * kD + c] = sum == 0.0f ? 0.0f : x * vs / sum;
-        if (a.lse != nullptr && c == 0) a.lse[hq] = (at_m + log2f(sum)) * 0.6931471805599453f;
       }
     }
     __syncthreads();  // m, l and buf are free again
   }
 };
 
+int blocks_of(int sms) { return sms * kBlocksPerSm; }
+
 template <int DT, int QT, int NT, bool SEL>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a) {
   using F = Form<DT>;
   extern __shared__ __align__(16) char smem[];
   Smem<DT>& S = *reinterpret_cast<Smem<DT>*>(smem);
+  wait_prior_grid();
   allow_dependents();
   const int c = blockIdx.x, n_ctas = gridDim.x;
   Rec* recs = reinterpret_cast<Rec*>(a.ws);
-  float* slots = reinterpret_cast<float*>(a.ws + recs_bytes(n_ctas));
+  float* slots = reinterpret_cast<float*>(a.ws + slots_offset(n_ctas));
   if (threadIdx.x == 0) recs[c] = Rec{-1, 0};
 
   auto tiles_of = [&](int b) {
-    return (long long)a.c.H * ((span_of<SEL>(a, checked_len(a.lens, b, a.max_pages, a.c.ps)) + kTile - 1) / kTile);
+    return (long long)a.c.H * ((span_of<SEL>(a, checked_len(a.lens, b, a.max_pages, a.c.ps)) + F::kTile - 1) / F::kTile);
   };
   build_prefix<kThreads>(S.prefix, a.B, tiles_of);
   // requests without tokens, and refused ones: no block's range holds them
@@ -528,11 +581,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
     if (T < 0 && threadIdx.x == 0) flag(a.c, KVQ_PAGED_ERR_LENGTH);
   }
   const long long W = S.prefix.pre[kThreads];
-  const int C = int(W < n_ctas ? W : n_ctas);  // ranges: none is empty, so the parts of a unit are those of adjacent blocks
+  // ranges: none is empty, so the parts of a unit are those of adjacent blocks
+  const long long sms = n_ctas / kBlocksPerSm, most = W <= sms ? W : max(sms, W / kMinTiles);
+  const int C = int(most < n_ctas ? most : n_ctas);
   if (c >= C) return;
   const long long s0 = cta_start(c, W, C), e0 = cta_start(c + 1, W, C);
 
-  Cursor<SEL> at, ahead;
+  Cursor<SEL, F::kTile> at, ahead;
   long long in_request = s0;
   at.b = find_request<kThreads>(S.prefix, a.B, tiles_of, in_request);
   at.load(a);
@@ -541,10 +596,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
   ahead = at;
 
   Block<DT, QT, NT, SEL> K(a, S);
-  const int row = K.warp * 16 + (K.lane & 15);
+  const int row = K.warp * F::kRows + (K.lane & (F::kRows - 1));
   const int n = int(e0 - s0);
   Row entry, page;  // looked up one step, and both
-  bool fresh = true;
+  K.load_query(at.b, at.h);
+  K.clear();
   // tile i: its selection entry is looked up at i - kStages - 1, its page at i - kStages, its copies issued at
   // i - kStages + 1
   for (int i = -F::kStages - 1; i < n; ++i) {
@@ -562,76 +618,110 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
       look_up_page<SEL>(a, page);
     }
     if (filled + 2 < n) {
-      look_up_entry<SEL>(a, ahead, ahead.tile * kTile + row, entry);
+      look_up_entry<SEL>(a, ahead, ahead.tile * F::kTile + row, entry);
       ahead.next(a);
     }
     if (i < 0) continue;
-    if (fresh) {
-      K.load_query(at.b, at.h);
-      K.clear();
-      fresh = false;
-    }
     __syncwarp();  // the stage's mask
     K.attend(i % F::kStages);
     if (at.tile + 1 == at.tiles || i + 1 == n) {
       const long long ue = s0 + i + (at.tiles - at.tile), us = ue - at.tiles;  // the unit's tiles
       float* slot = nullptr;
       if (us < s0 || ue > e0) {
-        slot = slots + size_t(2 * c + (us < s0 ? 0 : 1)) * slot_floats(a.g);
-        if (us >= s0 && threadIdx.x == 0) recs[c] = Rec{at.b * a.c.H + at.h, cta_of(ue - 1, W, C)};
+        const int k = us < s0 ? 0 : 1;
+        slot = slots + size_t(2 * c + k) * slot_floats(a.g);
+        if (k == 1 && threadIdx.x == 0) recs[c] = Rec{at.b * a.c.H + at.h, cta_of(ue - 1, W, C)};
       }
       K.finish(at.b, at.h, slot);
-      fresh = true;
+      at.next(a);
+      if (i + 1 < n) {
+        K.load_query(at.b, at.h);
+        K.clear();
+      }
+    } else {
+      ++at.tile;
     }
-    at.next(a);
   }
 }
 
-// Joins the parts of a unit that several blocks' ranges share; block (c, j): the
-// unit that starts in range c, query head j of its group. Four groups of 128
-// threads take every fourth part.
+// Joins the parts of a unit that several blocks' ranges share; block (c, y): the
+// unit that starts in range c, eight of its group's query heads. A head has
+// 32 / heads warps, each with every so many parts, four channels a lane; a part is
+// read once, with a running maximum.
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, int n_ctas) {
-  __shared__ float s_top[kCombineThreads / 32], s_l[4], s_x[4][kD];
+  __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
+  __shared__ float4 s_x[kCombineWarps][32];
   wait_prior_grid();
-  const int c = blockIdx.x, j = blockIdx.y, ch = threadIdx.x & 127, grp = threadIdx.x >> 7;
+  allow_dependents();
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Rec r = reinterpret_cast<const Rec*>(a.ws)[c];
   if (r.u < 0) return;
-  const float* slots = reinterpret_cast<const float*>(a.ws + recs_bytes(n_ctas));
+  const int j0 = blockIdx.y * 8, heads = min(8, a.g - j0), per = kCombineWarps / heads;  // warps of a head
+  const int j = j0 + warp / per, mine = warp % per;
+  const float* slots = reinterpret_cast<const float*>(a.ws + slots_offset(n_ctas));
+  const size_t stride = slot_floats(a.g);
   const int parts = r.last - c + 1;  // slot 2 c + 1 of block c, slot 2 c' of the following
-  auto part = [&](int i) { return slots + size_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * slot_floats(a.g); };
-  float top = -INFINITY;
-  for (int i = threadIdx.x; i < parts; i += kCombineThreads) top = fmaxf(top, part(i)[a.g * kD + 2 * j]);
+  float m = -INFINITY, l = 0.0f;
+  float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (warp < per * heads) {
+    for (int i0 = mine; i0 < parts; i0 += 4 * per) {
+      float2 ml[4];
+      float4 y[4];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
-  __syncthreads();
-  for (int w = 0; w < kCombineThreads / 32; ++w) top = fmaxf(top, s_top[w]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  float l = 0.0f, x = 0.0f;
-#pragma unroll 4
-  for (int i = grp; i < parts; i += 4) {
-    const float* p = part(i);
-    const float f = exp2f(p[a.g * kD + 2 * j] - base);
-    l += p[a.g * kD + 2 * j + 1] * f;
-    x += p[j * kD + ch] * f;
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + e * per;
+        ml[e] = make_float2(-INFINITY, 0.0f);
+        y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < parts) {
+          const float* p = slots + size_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * stride;
+          ml[e] = *reinterpret_cast<const float2*>(p + a.g * kD + 2 * j);
+          y[e] = reinterpret_cast<const float4*>(p + j * kD)[lane];
+        }
+      }
+      float top = m;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top = fmaxf(top, ml[e].x);
+      const float base = top == -INFINITY ? 0.0f : top, f = exp2f(m - base);
+      m = top;
+      l *= f;
+      x = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = exp2f(ml[e].x - base);
+        l += ml[e].y * w;
+        x = make_float4(fmaf(w, y[e].x, x.x), fmaf(w, y[e].y, x.y), fmaf(w, y[e].z, x.z), fmaf(w, y[e].w, x.w));
+      }
+    }
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_l[warp] = l;
+    }
+    s_x[warp][lane] = x;
   }
-  s_x[grp][ch] = x;
-  if (ch == 0) s_l[grp] = l;
   __syncthreads();
-  if (grp != 0) return;
-  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-  x = (s_x[0][ch] + s_x[1][ch]) + (s_x[2][ch] + s_x[3][ch]);
+  if (mine != 0 || warp >= per * heads) return;
+  float top = m;
+  for (int w = 1; w < per; ++w) top = fmaxf(top, s_m[warp + w]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  l = 0.0f;
+  x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int w = 0; w < per; ++w) {
+    const float f = exp2f(s_m[warp + w] - base);
+    const float4 y = s_x[warp + w][lane];
+    l += s_l[warp + w] * f;
+    x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
+  }
   const int b = r.u / a.c.H, h = r.u % a.c.H;
   const long long hq = (long long)b * a.Hq + h * a.g + j;
-  a.out[hq * kD + ch] = l == 0.0f ? 0.0f : x / l;
-  if (a.lse != nullptr && ch == 0) a.lse[hq] = (top + log2f(l)) * 0.6931471805599453f;
+  if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  else x = make_float4(x.x / l, x.y / l, x.z / l, x.w / l);
+  reinterpret_cast<float4*>(a.out + hq * kD)[lane] = x;
+  if (a.lse != nullptr && lane == 0) a.lse[hq] = (top + log2f(l)) * 0.6931471805599453f;
 }
-
-int blocks_of(int sms) { return sms * kBlocksPerSm; }
 
 template <int DT, int QT, int NT, bool SEL>
 cudaError_t launch_form(const AttnArgs& a, cudaStream_t stream) {
-  const int smem = int(smem_bytes<DT>(NT)), n = blocks_of(a.sms);
+  const int smem = int(sizeof(Smem<DT>)), n = blocks_of(a.sms);
   static std::atomic<uint64_t> configured{0};  // bit: device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -641,12 +731,11 @@ cudaError_t launch_form(const AttnArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  attn_kernel<DT, QT, NT, SEL><<<n, kThreads, smem, stream>>>(a);
   count_launch();
-  e = cudaGetLastError();
+  e = launch_dependent(attn_kernel<DT, QT, NT, SEL>, dim3(n), dim3(kThreads), size_t(smem), stream, a);
   if (e != cudaSuccess) return e;
   count_launch();
-  return launch_dependent(combine_kernel, dim3(n, a.g), dim3(kCombineThreads), 0, stream, a, n);
+  return launch_dependent(combine_kernel, dim3(n, (a.g + 7) / 8), dim3(kCombineThreads), 0, stream, a, n);
 }
 
 template <int DT, int QT>
@@ -658,7 +747,7 @@ cudaError_t launch_types(const AttnArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t attn_workspace(int B, int H, int Hq, int sms) {
-  return recs_bytes(blocks_of(sms)) + 2 * size_t(blocks_of(sms)) * slot_floats(Hq / H) * 4;
+  return slots_offset(blocks_of(sms)) + 2 * size_t(blocks_of(sms)) * slot_floats(Hq / H) * 4;
 }
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {

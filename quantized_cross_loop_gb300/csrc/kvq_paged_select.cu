@@ -26,7 +26,9 @@ namespace paged {
 namespace {
 
 constexpr int kScoreThreads = 256;
-constexpr int kChunk = 32;           // pages a warp scores at a time
+constexpr int kChunk = 16;           // pages a warp scores at a time
+constexpr int kInFlight = 8;         // loads a lane has in flight
+constexpr int kScoreBlocksPerSm = 4;
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
 constexpr int kBins = 2048;
@@ -96,7 +98,7 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&x)[DT == kE4m3 ? 
   }
 }
 
-// A warp scores 32 pages: a page's bounds are 32 (16-bit) or 16 (E4M3) loads of 16
+// A warp scores 16 pages: a page's bounds are 32 (16-bit) or 16 (E4M3) loads of 16
 // bytes, so a lane holds the weights of its own 8 or 16 channels of lo or hi, and
 // one load instruction covers one or two pages.
 template <int DT, int QT>
@@ -105,6 +107,7 @@ struct Scorer {
   static constexpr int kLanes = 2 * kD / kPer;           // lanes of a page
   static constexpr int kAtOnce = 32 / kLanes;            // pages per load
   static constexpr int kLoads = kChunk / kAtOnce;
+  static constexpr int kBatch = kLoads < kInFlight ? kLoads : kInFlight;
   float w[kPer];
 
   __device__ __forceinline__ void weights(const SelectArgs& a, int b, int h, int lane) {
@@ -125,27 +128,30 @@ struct Scorer {
     }
   }
 
-  // Scores of pages p0 .. p0 + 31 (those below `pages`): the key of page p0 + index in each lane; `index` and the
-  // chunk's A are returned too.
-  __device__ __forceinline__ uint32_t score(const SelectArgs& a, int b, int h, int p0, int pages, int lane, int& index,
-                                            float& largest) {
-    int page = p0 + lane < pages ? a.table[(long long)b * a.max_pages + p0 + lane] : 0;
-    const bool ok = page >= 0 && page < a.c.n_pages;
-    if (!ok) {
+  // Page numbers of the chunk from page p0 on, one in each lane of a half warp (0 behind the last).
+  __device__ __forceinline__ static int ids(const SelectArgs& a, int b, int p0, int pages, int lane) {
+    const int p = p0 + (lane & (kChunk - 1));
+    return p < pages ? a.table[(long long)b * a.max_pages + p] : 0;
+  }
+
+  // Scores of the chunk whose page numbers are `page`: the key of its page `index` in each lane. The chunk's A, a
+  // lane's largest sums added over the lanes, joins `largest`.
+  __device__ __forceinline__ uint32_t score(const SelectArgs& a, int h, int page, int lane, int& index, float& largest) {
+    if (page < 0 || page >= a.c.n_pages) {
       flag(a.c, KVQ_PAGED_ERR_PAGE);
       page = -1;
     }
     float v[kLoads], top = 0.0f;
 #pragma unroll
-    for (int i0 = 0; i0 < kLoads; i0 += 8) {
-      uint4 r[8];
+    for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
+      uint4 r[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kBatch; ++i) {
         const int id = __shfl_sync(0xFFFFFFFFu, page, (i0 + i) * kAtOnce + lane / kLanes);
         r[i] = __ldg(reinterpret_cast<const uint4*>(bounds_of<DT>(a, id < 0 ? 0 : id, h)) + lane % kLanes);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < kBatch; ++i) {
         float x[kPer], s = 0.0f, t = 0.0f;
         unpack<DT>(r[i], x);
 #pragma unroll
@@ -157,26 +163,36 @@ struct Scorer {
         if (t <= 3.4e38f) top = fmaxf(top, t);  // (infinite and NaN bounds set no E: their pages' keys are exact)
       }
     }
-    // lane i keeps the sum of load i: halves of the values change sides with halves of the lanes
+    // sums over the lanes of a page: halves of the values change sides with halves of the lanes while there are any
+    int n = kLoads, load = 0;
 #pragma unroll
-    for (int o = kLoads / 2; o >= 1; o >>= 1)
+    for (int o = kLanes / 2; o >= 1; o >>= 1) {
+      const bool hi = (lane & o) != 0;
+      if (n > 1) {
+        n /= 2;
 #pragma unroll
-      for (int k = 0; k < o; ++k) {
-        const bool hi = (lane & o) != 0;
-        const float send = hi ? v[k] : v[k + o], keep = hi ? v[k + o] : v[k];
-        v[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+        for (int k = 0; k < kLoads / 2; ++k) {
+          if (k >= n) break;
+          const float send = hi ? v[k] : v[k + n], keep = hi ? v[k + n] : v[k];
+          v[k] = keep + __shfl_xor_sync(0xFFFFFFFFu, send, o);
+        }
+        load += hi ? n : 0;
+      } else {
+        v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
       }
-    index = kAtOnce == 1 ? lane : 2 * (lane & 15) + (lane >> 4);
+    }
+    index = load * kAtOnce + lane / kLanes;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top += __shfl_xor_sync(0xFFFFFFFFu, top, o);
-    largest = top;
+    largest = fmaxf(largest, top);
     return __shfl_sync(0xFFFFFFFFu, page, index) < 0 ? kLastKey : key_of(v[0]);
   }
 };
 
 template <int DT, int QT>
-__global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, Workspace ws) {
+__global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm) score_kernel(SelectArgs a, Workspace ws) {
   __shared__ Prefix<kScoreThreads> S;
+  wait_prior_grid();
   allow_dependents();
   auto count = [&](int b) {
     const int pages = pages_of(a, checked_len(a.lens, b, a.max_pages, a.c.ps));
@@ -198,12 +214,13 @@ __global__ void __launch_bounds__(kScoreThreads) score_kernel(SelectArgs a, Work
   Scorer<DT, QT> K;
   bool fresh = true;
   for (long long c = c0; c < c1; ++c) {
+    const int ids = K.ids(a, b, chunk * kChunk, pages, lane);
     if (fresh) K.weights(a, b, h, lane);
     fresh = false;
     const long long unit = (long long)b * a.c.H + h;
     int index;
-    float largest;
-    const uint32_t key = K.score(a, b, h, chunk * kChunk, pages, lane, index, largest);
+    float largest = 0.0f;
+    const uint32_t key = K.score(a, h, ids, lane, index, largest);
     const int p = chunk * kChunk + index;
     if (p < pages) ws.keys[unit * a.max_pages + p] = key;
     if (lane == 0) ws.largest[unit * chunks_of(a.max_pages) + chunk] = largest;
@@ -261,6 +278,22 @@ __device__ __forceinline__ uint64_t exact_key(const SelectArgs& a, const Pick& S
   return key_of(x);
 }
 
+// The `left`-th largest of up to kPickThreads keys: the one with fewer than `left` above it and enough not below.
+__device__ __forceinline__ uint32_t ranked(Pick& S, const uint32_t* keys, int n, int left) {
+  if (threadIdx.x < n) {
+    const uint32_t x = keys[threadIdx.x];
+    int more = 0, same = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      more += keys[i] > x;
+      same += keys[i] == x;
+    }
+    if (more < left && left <= more + same) S.t = x;
+  }
+  __syncthreads();
+  return S.t;
+}
+
 // Picks a unit's pages from its keys (`keys` is scratch: written, too); the block's threads together.
 template <int DT, int QT>
 __device__ __forceinline__ void pick(const SelectArgs& a, Pick& S, int b, int h, int pages, uint32_t* keys,
@@ -274,25 +307,28 @@ __device__ __forceinline__ void pick(const SelectArgs& a, Pick& S, int b, int h,
     for (int p = f0 + tid; p < f1; p += kPickThreads) keys[p] = kLastKey;  // none but those
     __syncthreads();
   } else {
-    for (int p = f0 + tid; p < f1; p += kPickThreads) {
-      lo = min(lo, keys[p]);
-      hi = max(hi, keys[p]);
-    }
-    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-    if (lane == 0) {
-      S.warp_lo[warp] = lo;
-      S.warp_hi[warp] = hi;
-    }
-    __syncthreads();
-    for (int w = 0; w < kPickWarps; ++w) {
-      lo = min(lo, S.warp_lo[w]);
-      hi = max(hi, S.warp_hi[w]);
+    const bool few = f1 - f0 <= kPickThreads;
+    if (!few) {  // the keys' range
+      for (int p = f0 + tid; p < f1; p += kPickThreads) {
+        lo = min(lo, keys[p]);
+        hi = max(hi, keys[p]);
+      }
+      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+      hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+      if (lane == 0) {
+        S.warp_lo[warp] = lo;
+        S.warp_hi[warp] = hi;
+      }
+      __syncthreads();
+      for (int w = 0; w < kPickWarps; ++w) {
+        lo = min(lo, S.warp_lo[w]);
+        hi = max(hi, S.warp_hi[w]);
+      }
     }
     // the k-th largest key
     int left = k;
     uint32_t t = lo;
-    while (lo < hi) {
+    while (lo < hi && !few) {
       const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
       for (int i = tid; i < kBins; i += kPickThreads) S.hist[i] = 0;
       if (tid == 0) S.n_list = 0;
@@ -336,27 +372,18 @@ __device__ __forceinline__ void pick(const SelectArgs& a, Pick& S, int b, int h,
       else hi = min(hi, lo + ((1u << shift) - 1u));
       t = lo;
       const int members = S.members;
-      if (lo < hi && members <= kPickThreads) {  // few: the key with fewer than `left` above and enough not below
+      if (lo < hi && members <= kPickThreads) {
         for (int p = f0 + tid; p < f1; p += kPickThreads) {
           const uint32_t x = keys[p];
           if (x >= lo && x <= hi) S.list_key[atomicAdd(&S.n_list, 1)] = x;
         }
         __syncthreads();
-        if (tid < members) {
-          const uint32_t x = S.list_key[tid];
-          int more = 0, same = 0;
-          for (int i = 0; i < members; ++i) {
-            more += S.list_key[i] > x;
-            same += S.list_key[i] == x;
-          }
-          if (more < left && left <= more + same) S.t = x;
-        }
-        __syncthreads();
-        t = S.t;
+        t = ranked(S, S.list_key, members, left);
         break;
       }
       __syncthreads();  // hist, bin and list are free again
     }
+    if (few) t = ranked(S, keys + f0, f1 - f0, k);
     // pages in doubt
     lo = hi = t;
     if (t != kFirstKey && t != kLastKey) {
@@ -485,6 +512,8 @@ template <int DT, int QT>
 __global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a, Workspace ws, int staged) {
   __shared__ Pick S;
   extern __shared__ __align__(16) uint32_t s_keys[];
+  wait_prior_grid();
+  allow_dependents();
   const long long unit = blockIdx.x;
   const int b = int(unit / a.c.H), h = int(unit % a.c.H), tid = threadIdx.x;
   const int pages = pages_of(a, checked_len(a.lens, b, a.max_pages, a.c.ps));
@@ -493,7 +522,6 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a, Worksp
     for (int i = tid; i < a.n_select; i += kPickThreads) sel[i] = i < pages ? i : -1;
     return;
   }
-  wait_prior_grid();
   uint32_t* keys = ws.keys + unit * a.max_pages;
   if (staged) {
     for (int p = tid; p < pages; p += kPickThreads) s_keys[p] = keys[p];
@@ -510,19 +538,61 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a, Worksp
   pick<DT, QT>(a, S, b, h, pages, keys, largest, ws.exact + unit * a.max_pages, sel);
 }
 
+// Both in one: a block scores and picks a unit's pages, the keys in shared memory.
+template <int DT, int QT>
+__global__ void __launch_bounds__(kPickThreads, 2) select_kernel(SelectArgs a, Workspace ws) {
+  __shared__ Pick S;
+  extern __shared__ __align__(16) uint32_t s_keys[];
+  wait_prior_grid();
+  allow_dependents();
+  const long long unit = blockIdx.x;
+  const int b = int(unit / a.c.H), h = int(unit % a.c.H), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int T = checked_len(a.lens, b, a.max_pages, a.c.ps), pages = pages_of(a, T);
+  if (T < 0 && tid == 0) flag(a.c, KVQ_PAGED_ERR_LENGTH);
+  int32_t* sel = a.sel + unit * a.n_select;
+  if (pages <= a.n_select) {  // all of them, and -1 behind
+    for (int i = tid; i < a.n_select; i += kPickThreads) sel[i] = i < pages ? i : -1;
+    return;
+  }
+  Scorer<DT, QT> K;
+  float largest = 0.0f;
+  int ids = K.ids(a, b, warp * kChunk, pages, lane);
+  K.weights(a, b, h, lane);
+  for (int p0 = warp * kChunk; p0 < pages; p0 += kPickWarps * kChunk) {
+    const int next = K.ids(a, b, p0 + kPickWarps * kChunk, pages, lane);
+    int index;
+    const uint32_t key = K.score(a, h, ids, lane, index, largest);
+    if (p0 + index < pages) s_keys[p0 + index] = key;
+    ids = next;
+  }
+  if (lane == 0) S.warp_a[warp] = largest;
+  __syncthreads();
+  for (int w = 0; w < kPickWarps; ++w) largest = fmaxf(largest, S.warp_a[w]);
+  pick<DT, QT>(a, S, b, h, pages, s_keys, largest, ws.exact + unit * a.max_pages, sel);
+}
+
+// One launch where a unit's pages keep a block busy for no longer than the second
+// launch would take, or where there are units for all SMs; else the pages are
+// scored by all warps of the device and picked by a second kernel.
+constexpr int kFusedPages = 256;      // any number of units
+constexpr int kFusedManyPages = 2048; // at least one unit per SM
+
 template <int DT, int QT>
 cudaError_t launch_types(const SelectArgs& a, cudaStream_t stream) {
   const int units = a.B * a.c.H;
   const Workspace ws = workspace_of(a.ws, units, a.max_pages);
-  const long long warps = (long long)units * chunks_of(a.max_pages);  // at most
-  const long long need = (warps + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
-  const int blocks = int(need < 1 ? 1 : need < 4LL * a.sms ? need : 4LL * a.sms);
-  score_kernel<DT, QT><<<blocks, kScoreThreads, 0, stream>>>(a, ws);
-  count_launch();
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   const int staged = a.max_pages <= kStagedMax;
   const size_t smem = staged ? size_t(a.max_pages) * 4 : 0;
+  if (a.max_pages <= kFusedPages || (a.max_pages <= kFusedManyPages && units >= a.sms)) {
+    count_launch();
+    return launch_dependent(select_kernel<DT, QT>, dim3(units), dim3(kPickThreads), smem, stream, a, ws);
+  }
+  const long long warps = (long long)units * chunks_of(a.max_pages);  // at most
+  const long long need = (warps + kScoreThreads / 32 - 1) / (kScoreThreads / 32);
+  const int blocks = int(need < 1 ? 1 : need < (long long)kScoreBlocksPerSm * a.sms ? need : (long long)kScoreBlocksPerSm * a.sms);
+  count_launch();
+  cudaError_t e = launch_dependent(score_kernel<DT, QT>, dim3(blocks), dim3(kScoreThreads), 0, stream, a, ws);
+  if (e != cudaSuccess) return e;
   if (smem > 16384) {
     e = cudaFuncSetAttribute(pick_kernel<DT, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedMax * 4);
     if (e != cudaSuccess) return e;

@@ -837,7 +837,7 @@ class PagedCache:
             elif t.dtype != torch.float32 or tuple(t.shape) != (n_heads,) or not t.is_contiguous():
                 raise KvqError(f"{name} must be contiguous float32 [{n_heads}]")
         self.page_size, self.n_heads, self.n_pages = page_size, n_heads, n_pages
-        self.dtype, self.device = first.dtype, first.device
+        self.dtype, self.device, self.index = first.dtype, first.device, first.get_device()
         self.k, self.v, self.key_bounds, self.k_scale, self.v_scale = k, v, key_bounds, k_scale, v_scale
         self.desc = kvq_paged_cache()
         _check(lib().kvq_paged_cache_init(ctypes.byref(self.desc), _PAGED_DTYPES[self.dtype], n_pages, page_size,
@@ -872,22 +872,29 @@ class PagedCache:
         self._error.zero_()
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream of a device (the Stream object's construction costs more than a launch)."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 def _on_stream(cache: PagedCache, stream, call):
     """call(raw stream) with the cache's device current. Buffers that the call allocates belong to the stream they
     are used on."""
-    if stream is None and torch.cuda.current_device() == cache.device.index:
-        return call(torch.cuda.current_stream(cache.device).cuda_stream)
+    index = cache.index
+    if stream is None and torch.cuda.current_device() == index:
+        return call(_raw_stream(index))
     if stream is not None and stream.device != cache.device:
         raise KvqError(f"stream of {stream.device} for a cache on {cache.device}")
     with torch.cuda.device(cache.device):
         if stream is None:
-            return call(torch.cuda.current_stream(cache.device).cuda_stream)
+            return call(_raw_stream(index))
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
 
 
 def _int32(cache: PagedCache, t: torch.Tensor, name: str, shape: tuple):
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or t.device != cache.device or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != cache.index or not t.is_contiguous():
         raise KvqError(f"{name} must be contiguous int32 {list(shape)} on {cache.device}, got {t.dtype} "
                        f"{list(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -895,12 +902,13 @@ def _int32(cache: PagedCache, t: torch.Tensor, name: str, shape: tuple):
 
 def _head_rows(cache: PagedCache, t: torch.Tensor, name: str, dtype, rows: int | None = None, heads: int | None = None):
     """A [rows, heads, 128] view whose rows may be strided; returns its row stride."""
-    if t.device != cache.device or t.dtype != dtype or t.dim() != 3 or t.shape[2] != 128:
-        raise KvqError(f"{name} must be {dtype} [rows, heads, 128] on {cache.device}, got {t.dtype} {list(t.shape)} "
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 3 or shape[2] != 128 or t.get_device() != cache.index:
+        raise KvqError(f"{name} must be {dtype} [rows, heads, 128] on {cache.device}, got {t.dtype} {list(shape)} "
                        f"on {t.device}")
-    n, h, _ = t.shape
+    n, h, _ = shape
     if (rows is not None and n != rows) or (heads is not None and h != heads):
-        raise KvqError(f"{name} must be [{rows}, {heads}, 128], got {list(t.shape)}")
+        raise KvqError(f"{name} must be [{rows}, {heads}, 128], got {list(shape)}")
     s = t.stride()
     if n and h and (s[2] != 1 or (h > 1 and s[1] != 128)):
         raise KvqError(f"{name}: the heads of a row must be contiguous")
@@ -908,10 +916,10 @@ def _head_rows(cache: PagedCache, t: torch.Tensor, name: str, dtype, rows: int |
 
 
 def _paged_table(cache: PagedCache, table: torch.Tensor):
-    if table.dim() != 2:
+    shape = table.shape
+    if len(shape) != 2:
         raise KvqError("page_table must be [n_requests, max_pages]")
-    B, W = table.shape
-    return _int32(cache, table, "page_table", (B, W)), B, W
+    return _int32(cache, table, "page_table", shape), shape[0], shape[1]
 
 
 def kvq_paged_append(cache: PagedCache, page_table: torch.Tensor, start: torch.Tensor, k: torch.Tensor,
@@ -957,7 +965,7 @@ def kvq_paged_append(cache: PagedCache, page_table: torch.Tensor, start: torch.T
         out = q_out
         if q is not None:
             if out is None:
-                out = torch.empty((n, q.shape[1], 128), dtype=q.dtype, device=q.device)
+                out = torch.empty((n, q.shape[1], 128), dtype=dtype, device=cache.device)
             r.q_stride = _head_rows(cache, q, "q", dtype, n)
             r.q_out_stride = _head_rows(cache, out, "q_out", dtype, n, q.shape[1])
             r.q, r.q_out, r.n_q_heads = q.data_ptr(), out.data_ptr(), q.shape[1]
@@ -979,9 +987,8 @@ def _paged_workspace(cache: PagedCache, workspace, B, Hq, W):
     if workspace is None:
         need = int(lib().kvq_paged_workspace_bytes(B, cache.n_heads, Hq, W))
         return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
-    _require_cuda(workspace, "workspace", torch.uint8)
-    if workspace.device != cache.device:
-        raise KvqError(f"workspace must be on {cache.device}")
+    if workspace.get_device() != cache.index or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise KvqError(f"workspace must be contiguous uint8 on {cache.device}")
     return workspace
 
 
@@ -991,7 +998,7 @@ def _paged_attend(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, 
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(128)
     for name, t, shape in (("out", out, (B, Hq, 128)), ("lse", lse, (B, Hq))):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != shape or t.device != cache.device
+        if t is not None and (t.dtype is not torch.float32 or t.shape != shape or t.get_device() != cache.index
                               or not t.is_contiguous()):
             raise KvqError(f"{name} must be contiguous float32 {list(shape)} on {cache.device}")
     if sel is not None:
