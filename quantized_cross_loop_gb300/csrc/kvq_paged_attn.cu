@@ -45,7 +45,7 @@ constexpr int kThreads = 128;
 constexpr int kWarps = 4;
 constexpr int kBufStride = 132;    // floats per head of the merge buffers: the lanes' columns hit distinct banks
 constexpr int kBlocksPerSm = 2;
-constexpr int kCombineThreads = 1024;
+constexpr int kCombineThreads = 512;
 constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kMinTiles = 2;       // tiles of a block's range, once every SM has one
 
@@ -77,6 +77,7 @@ struct Smem {
   int refused[Form<DT>::kStages][kWarps];    // a row that the request or selection does not allow
   Prefix<kThreads> prefix;
   float m[kWarps][kMaxGroup], l[kWarps][kMaxGroup];
+  float top[kMaxGroup], sum[kMaxGroup], factor[kMaxGroup];
   float buf[2 * 8 * kBufStride];  // sums of two warps, eight heads
 };
 
@@ -259,8 +260,15 @@ struct Block {
   // numbers them; for E4M3, where a lane converts 16 consecutive key channels,
   // 16 (q + 4 (j / 4)) + 4 (j % 4) + {0 .. 3}: any order of the sum will do if
   // both operands have it.
-  __device__ __forceinline__ void load_query(int b, int h) {
+  __device__ __forceinline__ uint2 query_words(const char* p, int j) const {
     const int q = lane & 3;
+    if constexpr (DT == kE4m3)
+      return *reinterpret_cast<const uint2*>(p + (16 * (q + 4 * (j / 4)) + 4 * (j % 4)) * 2);
+    else
+      return make_uint2(*reinterpret_cast<const uint32_t*>(p + (16 * j + 2 * q) * 2),
+                        *reinterpret_cast<const uint32_t*>(p + (16 * j + 2 * q + 8) * 2));
+  }
+  __device__ __forceinline__ void load_query(int b, int h) {
     const float ks = DT == kE4m3 && a.c.k_scale != nullptr ? a.c.k_scale[h] : 1.0f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -270,15 +278,7 @@ struct Block {
       float top = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        uint2 w = make_uint2(0, 0);
-        if (head < a.g) {
-          if constexpr (DT == kE4m3) {
-            w = *reinterpret_cast<const uint2*>(p + (16 * (q + 4 * (j / 4)) + 4 * (j % 4)) * 2);
-          } else {
-            w.x = *reinterpret_cast<const uint32_t*>(p + (16 * j + 2 * q) * 2);
-            w.y = *reinterpret_cast<const uint32_t*>(p + (16 * j + 2 * q + 8) * 2);
-          }
-        }
+        const uint2 w = head < a.g ? query_words(p, j) : make_uint2(0, 0);
         qa[j][2 * n] = w.x;
         qa[j][2 * n + 1] = w.y;
         if constexpr (DT == kE4m3 && QT == kBf16) {
@@ -298,8 +298,7 @@ struct Block {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t w = qa[j][2 * n + i];
-            qa[j][2 * n + i] =
-                pack_half(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
+            qa[j][2 * n + i] = pack_half(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
           }
       }
     }
@@ -481,8 +480,9 @@ struct Block {
   }
 
   // The block's four warps joined; the result goes to out and lse, or to `slot`.
+  // (Three barriers: what a slow thread still reads of one call is written in the
+  // next only behind that one's first barrier.)
   __device__ __forceinline__ void finish(int b, int h, float* slot) {
-    float* buf = S.buf;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       l[n] += __shfl_xor_sync(0xFFFFFFFFu, l[n], 1);
@@ -494,18 +494,27 @@ struct Block {
     }
     __syncthreads();
     auto top = [&](int head) {
-      const float x = fmaxf(fmaxf(S.m[0][head], S.m[1][head]), fmaxf(S.m[2][head], S.m[3][head]));
-      return x == -INFINITY ? 0.0f : x;
+      return fmaxf(fmaxf(S.m[0][head], S.m[1][head]), fmaxf(S.m[2][head], S.m[3][head]));
     };
-    float* mine = buf + (warp & 1) * 8 * kBufStride;
+    float* mine = S.buf + (warp & 1) * 8 * kBufStride;
     const float vs = DT == kE4m3 && a.c.v_scale != nullptr ? a.c.v_scale[h] : 1.0f;
+    if (threadIdx.x < a.g) {
+      const float mx = top(threadIdx.x), base = mx == -INFINITY ? 0.0f : mx;
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += S.l[w][threadIdx.x] * exp2_ftz(S.m[w][threadIdx.x] - base);
+      S.top[threadIdx.x] = mx - F::kShift;
+      S.sum[threadIdx.x] = sum;
+      S.factor[threadIdx.x] = slot != nullptr ? vs : (sum == 0.0f ? 0.0f : vs / sum);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {  // eight heads at a time
       float f[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int head = 2 * (lane & 3) + i + 8 * n;
-        f[i] = exp2f(S.m[warp][head] - top(head));
+        const float mx = top(head);
+        f[i] = exp2_ftz(S.m[warp][head] - (mx == -INFINITY ? 0.0f : mx));
       }
       auto at = [&](int j, int i) -> float& {  // i = 2 c + head bit
         return mine[(2 * (lane & 3) + (i & 1)) * kBufStride + channel(j, i >> 1)];
@@ -525,30 +534,22 @@ struct Block {
           for (int i = 0; i < 4; ++i) at(j, i) += o[j][4 * n + i] * f[i & 1];
       }
       __syncthreads();
-      const int c = threadIdx.x;
-      for (int i = 0; i < min(8, a.g - 8 * n); ++i) {
-        const int j = 8 * n + i;
-        const float mx = top(j);
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) sum += S.l[w][j] * exp2f(S.m[w][j] - mx);
-        const float x = buf[i * kBufStride + c] + buf[(8 + i) * kBufStride + c];
-        const bool none = fmaxf(fmaxf(S.m[0][j], S.m[1][j]), fmaxf(S.m[2][j], S.m[3][j])) == -INFINITY;
-        const float at_m = none ? -INFINITY : mx - F::kShift;
-        if (slot != nullptr) {
-          slot[j * kD + c] = x * vs;
-          if (c == 0) {
-            slot[a.g * kD + 2 * j] = at_m;
-            slot[a.g * kD + 2 * j + 1] = sum;
-          }
-        } else {
-          const long long hq = (long long)b * a.Hq + h * a.g + j;
-          a.out[hq * kD + c] = sum == 0.0f ? 0.0f : x * vs / sum;
-          if (a.lse != nullptr && c == 0) a.lse[hq] = (at_m + log2f(sum)) * 0.6931471805599453f;
-        }
+      const int c = threadIdx.x, heads = min(8, a.g - 8 * n);
+      float* to = slot != nullptr ? slot + 8 * n * kD + c
+                                  : a.out + ((long long)b * a.Hq + h * a.g + 8 * n) * kD + c;
+#pragma unroll 4
+      for (int i = 0; i < heads; ++i) {
+        const float x = S.buf[i * kBufStride + c] + S.buf[(8 + i) * kBufStride + c];
+        to[i * kD] = S.sum[8 * n + i] == 0.0f ? 0.0f : x * S.factor[8 * n + i];
       }
     }
-    __syncthreads();  // m, l and buf are free again
+    if (threadIdx.x < a.g) {
+      const int j = threadIdx.x;
+      if (slot != nullptr)
+        *reinterpret_cast<float2*>(slot + a.g * kD + 2 * j) = make_float2(S.top[j], S.sum[j]);
+      else if (a.lse != nullptr)
+        a.lse[(long long)b * a.Hq + h * a.g + j] = (S.top[j] + log2f(S.sum[j])) * 0.6931471805599453f;
+    }
   }
 };
 
@@ -646,29 +647,30 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
 
 // Joins the parts of a unit that several blocks' ranges share; block (c, y): the
 // unit that starts in range c, eight of its group's query heads. A head has
-// 32 / heads warps, each with every so many parts, four channels a lane; a part is
+// 16 / heads warps, each with every so many parts, four channels a lane; a part is
 // read once, with a running maximum.
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, int n_ctas) {
   __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
   __shared__ float4 s_x[kCombineWarps][32];
-  wait_prior_grid();
-  allow_dependents();
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const Rec r = reinterpret_cast<const Rec*>(a.ws)[c];
-  if (r.u < 0) return;
   const int j0 = blockIdx.y * 8, heads = min(8, a.g - j0), per = kCombineWarps / heads;  // warps of a head
   const int j = j0 + warp / per, mine = warp % per;
   const float* slots = reinterpret_cast<const float*>(a.ws + slots_offset(n_ctas));
   const size_t stride = slot_floats(a.g);
+  wait_prior_grid();
+  allow_dependents();
+  const Rec r = reinterpret_cast<const Rec*>(a.ws)[c];
+  if (r.u < 0) return;
   const int parts = r.last - c + 1;  // slot 2 c + 1 of block c, slot 2 c' of the following
   float m = -INFINITY, l = 0.0f;
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (warp < per * heads) {
-    for (int i0 = mine; i0 < parts; i0 += 4 * per) {
-      float2 ml[4];
-      float4 y[4];
+    constexpr int kUnroll = 4;
+    for (int i0 = mine; i0 < parts; i0 += kUnroll * per) {
+      float2 ml[kUnroll];
+      float4 y[kUnroll];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kUnroll; ++e) {
         const int i = i0 + e * per;
         ml[e] = make_float2(-INFINITY, 0.0f);
         y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -680,13 +682,13 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, in
       }
       float top = m;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) top = fmaxf(top, ml[e].x);
+      for (int e = 0; e < kUnroll; ++e) top = fmaxf(top, ml[e].x);
       const float base = top == -INFINITY ? 0.0f : top, f = exp2f(m - base);
       m = top;
       l *= f;
       x = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < kUnroll; ++e) {
         const float w = exp2f(ml[e].x - base);
         l += ml[e].y * w;
         x = make_float4(fmaf(w, y[e].x, x.x), fmaf(w, y[e].y, x.y), fmaf(w, y[e].z, x.z), fmaf(w, y[e].w, x.w));
