@@ -47,11 +47,16 @@ constexpr int kBufStride = 132;    // floats per head of the merge buffers: the 
 constexpr int kBlocksPerSm = 2;
 constexpr int kCombineThreads = 512;
 constexpr int kCombineWarps = kCombineThreads / 32;
+constexpr int kUnitCost = 2;       // tiles that the end of a unit takes as long as
 constexpr int kMinTiles = 2;       // tiles of a block's range, once every SM has one
 
-struct Rec {  // of a block: the unit that starts in its range and ends in block `last`'s (u < 0: none)
-  int32_t u, last;
+// A unit whose parts lie in the ranges of blocks first .. last (u < 0: no such
+// unit). Where there are no more units than blocks, unit u's is number u, else the
+// one of the unit that starts in block c's range and goes on behind it number c.
+struct Rec {
+  int32_t u, first, last, pad;
 };
+__host__ __device__ constexpr bool rec_per_unit(long long units, int n_ctas) { return units <= n_ctas; }
 
 // Workspace: Rec[n], then 2 n slots of g heads x sum[128] and g x (m, l).
 __host__ __device__ constexpr size_t slots_offset(int n) { return (size_t(n) * sizeof(Rec) + 15) / 16 * 16; }
@@ -169,17 +174,20 @@ __device__ __forceinline__ int span_of(const AttnArgs& a, int T) {
   return min(a.n_select, a.c.ps.div(T - 1) + 1) * int(a.c.ps.d);
 }
 
-// A position in the concatenated tiles.
+// A position in the concatenated work: a unit is its tiles and kUnitCost more
+// positions that stand for its merge and its query's load, so that a range of many
+// short units is not longer than one of few long ones.
 template <bool SEL, int TILE>
 struct Cursor {
   int b, h, tile, T, span, tiles;
+  long long pos;
   __device__ __forceinline__ void load(const AttnArgs& a) {
     T = b < a.B ? checked_len(a.lens, b, a.max_pages, a.c.ps) : 0;
     span = span_of<SEL>(a, T);
     tiles = (span + TILE - 1) / TILE;
   }
-  __device__ __forceinline__ void next(const AttnArgs& a) {
-    if (++tile < tiles) return;
+  __device__ __forceinline__ void next_unit(const AttnArgs& a) {
+    pos += tiles + kUnitCost - tile;
     tile = 0;
     if (++h < a.c.H) return;
     h = 0;
@@ -188,6 +196,15 @@ struct Cursor {
       load(a);
     } while (b < a.B && tiles == 0);
   }
+  __device__ __forceinline__ void next(const AttnArgs& a) {
+    if (tile + 1 == tiles) {
+      next_unit(a);
+    } else {
+      ++tile;
+      ++pos;
+    }
+  }
+  __device__ __forceinline__ bool before(const AttnArgs& a, long long end) const { return b < a.B && pos < end; }
 };
 
 // Where a lane's row (of the warp's slice) comes from, looked up in two steps.
@@ -565,12 +582,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
   const int c = blockIdx.x, n_ctas = gridDim.x;
   Rec* recs = reinterpret_cast<Rec*>(a.ws);
   float* slots = reinterpret_cast<float*>(a.ws + slots_offset(n_ctas));
-  if (threadIdx.x == 0) recs[c] = Rec{-1, 0};
+  const bool per_unit = rec_per_unit((long long)a.B * a.c.H, n_ctas);
+  if (!per_unit && threadIdx.x == 0) recs[c].u = -1;
 
-  auto tiles_of = [&](int b) {
-    return (long long)a.c.H * ((span_of<SEL>(a, checked_len(a.lens, b, a.max_pages, a.c.ps)) + F::kTile - 1) / F::kTile);
+  auto work_of = [&](int b) {
+    const int tiles = (span_of<SEL>(a, checked_len(a.lens, b, a.max_pages, a.c.ps)) + F::kTile - 1) / F::kTile;
+    return tiles > 0 ? (long long)a.c.H * (tiles + kUnitCost) : 0LL;
   };
-  build_prefix<kThreads>(S.prefix, a.B, tiles_of);
+  build_prefix<kThreads>(S.prefix, a.B, work_of);
   // requests without tokens, and refused ones: no block's range holds them
   for (int b = c; b < a.B; b += n_ctas) {
     const int T = checked_len(a.lens, b, a.max_pages, a.c.ps);
@@ -580,6 +599,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
     if (a.lse != nullptr)
       for (int i = threadIdx.x; i < a.Hq; i += kThreads) a.lse[(long long)b * a.Hq + i] = T < 0 ? NAN : -INFINITY;
     if (T < 0 && threadIdx.x == 0) flag(a.c, KVQ_PAGED_ERR_LENGTH);
+    if (per_unit)
+      for (int h = threadIdx.x; h < a.c.H; h += kThreads) recs[b * a.c.H + h].u = -1;
   }
   const long long W = S.prefix.pre[kThreads];
   // ranges: none is empty, so the parts of a unit are those of adjacent blocks
@@ -590,78 +611,89 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
 
   Cursor<SEL, F::kTile> at, ahead;
   long long in_request = s0;
-  at.b = find_request<kThreads>(S.prefix, a.B, tiles_of, in_request);
+  at.b = find_request<kThreads>(S.prefix, a.B, work_of, in_request);
   at.load(a);
-  at.h = int(in_request / at.tiles);
-  at.tile = int(in_request % at.tiles);
+  at.h = int(in_request / (at.tiles + kUnitCost));
+  at.tile = int(in_request % (at.tiles + kUnitCost));
+  at.pos = s0;
+  if (at.tile >= at.tiles) at.next_unit(a);  // the range begins behind the unit's last tile
+  if (at.h >= a.c.H || !at.before(a, e0)) return;  // (and may hold no tile)
   ahead = at;
 
   Block<DT, QT, NT, SEL> K(a, S);
   const int row = K.warp * F::kRows + (K.lane & (F::kRows - 1));
-  const int n = int(e0 - s0);
   Row entry, page;  // looked up one step, and both
+  bool have_entry = false, have_page = false;
   K.load_query(at.b, at.h);
   K.clear();
   // tile i: its selection entry is looked up at i - kStages - 1, its page at i - kStages, its copies issued at
   // i - kStages + 1
-  for (int i = -F::kStages - 1; i < n; ++i) {
+  for (int i = -F::kStages - 1; i < 0 || at.before(a, e0); ++i) {
     if (i >= 0) {
       wait_groups<F::kStages - 2>();
       __syncwarp();  // every lane's copies have landed, and every lane has left the stage that is filled next
     }
     const int filled = i + F::kStages - 1;
     if (filled >= 0) {
-      if (filled < n) K.issue(filled % F::kStages, page);
+      if (have_page) K.issue(filled % F::kStages, page);
       commit();
     }
-    if (filled + 1 >= 0 && filled + 1 < n) {
+    have_page = have_entry;
+    if (have_entry) {
       page = entry;
       look_up_page<SEL>(a, page);
     }
-    if (filled + 2 < n) {
+    have_entry = ahead.before(a, e0);
+    if (have_entry) {
       look_up_entry<SEL>(a, ahead, ahead.tile * F::kTile + row, entry);
       ahead.next(a);
     }
     if (i < 0) continue;
     __syncwarp();  // the stage's mask
     K.attend(i % F::kStages);
-    if (at.tile + 1 == at.tiles || i + 1 == n) {
-      const long long ue = s0 + i + (at.tiles - at.tile), us = ue - at.tiles;  // the unit's tiles
-      float* slot = nullptr;
-      if (us < s0 || ue > e0) {
-        const int k = us < s0 ? 0 : 1;
-        slot = slots + size_t(2 * c + k) * slot_floats(a.g);
-        if (k == 1 && threadIdx.x == 0) recs[c] = Rec{at.b * a.c.H + at.h, cta_of(ue - 1, W, C)};
-      }
-      K.finish(at.b, at.h, slot);
-      at.next(a);
-      if (i + 1 < n) {
-        K.load_query(at.b, at.h);
-        K.clear();
-      }
-    } else {
+    if (at.tile + 1 < at.tiles && at.pos + 1 < e0) {
       ++at.tile;
+      ++at.pos;
+      continue;
+    }
+    const long long us = at.pos - at.tile, ue = us + at.tiles;  // the unit's tiles
+    float* slot = nullptr;
+    if (us < s0 || ue > e0) {
+      slot = slots + size_t(2 * c + (us < s0 ? 0 : 1)) * slot_floats(a.g);
+    }
+    if (us >= s0 && threadIdx.x == 0) {  // it starts here
+      const int u = at.b * a.c.H + at.h;
+      if (slot != nullptr) recs[per_unit ? u : c] = Rec{u, c, cta_of(ue - 1, W, C), 0};
+      else if (per_unit) recs[u].u = -1;
+    }
+    K.finish(at.b, at.h, slot);
+    at.next(a);
+    if (at.before(a, e0)) {
+      K.load_query(at.b, at.h);
+      K.clear();
     }
   }
 }
 
-// Joins the parts of a unit that several blocks' ranges share; block (c, y): the
-// unit that starts in range c, eight of its group's query heads. A head has
-// 16 / heads warps, each with every so many parts, four channels a lane; a part is
-// read once, with a running maximum.
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, int n_ctas) {
+// Joins the parts of a unit that several blocks' ranges share; block (r, y): the
+// unit of record r, `most` of its group's query heads. A head has 16 / heads warps,
+// each with every so many parts, four channels a lane; a part is read once, with a
+// running maximum.
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, int n_ctas, int most) {
   __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
   __shared__ float4 s_x[kCombineWarps][32];
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int j0 = blockIdx.y * 8, heads = min(8, a.g - j0), per = kCombineWarps / heads;  // warps of a head
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int j0 = blockIdx.y * most, heads = min(most, a.g - j0), per = kCombineWarps / heads;  // warps of a head
   const int j = j0 + warp / per, mine = warp % per;
   const float* slots = reinterpret_cast<const float*>(a.ws + slots_offset(n_ctas));
   const size_t stride = slot_floats(a.g);
   wait_prior_grid();
   allow_dependents();
-  const Rec r = reinterpret_cast<const Rec*>(a.ws)[c];
-  if (r.u < 0) return;
-  const int parts = r.last - c + 1;  // slot 2 c + 1 of block c, slot 2 c' of the following
+  const Rec r = reinterpret_cast<const Rec*>(a.ws)[blockIdx.x];
+  // (the bounds hold for every record of the attention kernel; a workspace that something else writes meanwhile
+  // must not lead outside of it)
+  if (r.u < 0 || r.u >= a.B * a.c.H || r.first < 0 || r.last < r.first || r.last >= n_ctas) return;
+  const int c = r.first, parts = r.last - c + 1;  // slot 2 c + 1 of block c, slot 2 c' of the following
   float m = -INFINITY, l = 0.0f;
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (warp < per * heads) {
@@ -736,8 +768,14 @@ cudaError_t launch_form(const AttnArgs& a, cudaStream_t stream) {
   count_launch();
   e = launch_dependent(attn_kernel<DT, QT, NT, SEL>, dim3(n), dim3(kThreads), size_t(smem), stream, a);
   if (e != cudaSuccess) return e;
+  // one head per block where that makes no more blocks than run at once (parts are many then), up to eight else
+  const long long units = (long long)a.B * a.c.H;
+  const int recs = rec_per_unit(units, n) ? int(units) : n;
+  int most = 1;
+  while (most < 8 && (long long)recs * ((a.g + most - 1) / most) > 4LL * a.sms) most *= 2;
   count_launch();
-  return launch_dependent(combine_kernel, dim3(n, (a.g + 7) / 8), dim3(kCombineThreads), 0, stream, a, n);
+  return launch_dependent(combine_kernel, dim3(recs, (a.g + most - 1) / most), dim3(kCombineThreads), 0, stream, a, n,
+                          most);
 }
 
 template <int DT, int QT>
