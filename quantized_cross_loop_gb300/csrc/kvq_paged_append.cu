@@ -14,11 +14,13 @@
 // rotated ones are shared out eight a lane. All new tokens of a page and head are
 // one unit of work, so the bounds need no atomics.
 // The host chooses by the rows that a request brings on average:
-//   few (up to 8)  one launch; a team takes any units (request, page, head) in
-//                  turn, KV heads (K and V together) and query heads alike;
-//   many           one launch for the keys and values, in which a block (pages of
-//                  more than 32 tokens) or a warp has a unit, and one for the
-//                  queries, in which a team takes four heads of a row.
+//   few (up to 8)  a team takes any units (request, page, head) in turn, KV heads (K
+//                  and V together) and query heads alike;
+//   many           one launch for the keys and values, in which a block (pages of more
+//                  than 32 tokens) or a warp has a unit, and one for the queries, in
+//                  which a team takes four heads of a row. (Both in one launch, some
+//                  blocks for each, was slower: 264 against 223 us for four prompts of
+//                  8192 tokens, the blocks of an SM getting unequal shares.)
 // Rows in flight and resident warps bound these; staging the rotation table in
 // shared memory for eight heads, and fetching the next rows into registers ahead of
 // the arithmetic, were slower (a table's row is in L1 for the heads that follow).
@@ -34,6 +36,8 @@ constexpr int kFewBlocksPerSm = 5;
 constexpr int kTeam = 16;          // lanes of a row
 constexpr int kManyThreads = 256;
 constexpr int kManyWarps = kManyThreads / 32;
+constexpr int kKeyBlocksPerSm = 3;
+constexpr int kQueryBlocksPerSm = 4;
 constexpr int kKeyRows = 2;        // rows a team has in flight
 constexpr int kQueryHeads = 4;     // heads a team has in flight
 
@@ -125,8 +129,8 @@ __device__ __forceinline__ Wide rotate(const Lane& L, const Angles& t, const Raw
   return x;
 }
 
-__device__ __forceinline__ float4 div4(float4 x, float s) {
-  return make_float4(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s), __fdiv_rn(x.z, s), __fdiv_rn(x.w, s));
+__device__ __forceinline__ float4 times(float4 x, float s) {
+  return make_float4(x.x * s, x.y * s, x.z * s, x.w * s);
 }
 
 // Four stored keys as two words of 16-bit pairs (E4M3 as FP16, exact), and their
@@ -174,7 +178,7 @@ struct Unit {
   bool is_q, live;  // live: the page is in the pool
   bool any;
   int h, page, place0, first, last, start, row0;
-  float ks, vs;
+  float ks, vs;           // E4M3: reciprocals of the scales (two roundings of 2^-24 instead of one, before one of 2^-4)
   uint32_t lo[4], hi[4];  // bounds of the lane's channels, 16-bit pairs
 
   __device__ __forceinline__ void open(const AppendArgs& a, int b, int page_of_request, int hh, int s, int r0, int n) {
@@ -187,8 +191,8 @@ struct Unit {
     page = a.table[(long long)b * a.max_pages + page_of_request];
     is_q = hh >= a.c.H;
     h = is_q ? hh - a.c.H : hh;
-    ks = DT == kE4m3 && !is_q && a.c.k_scale != nullptr ? a.c.k_scale[h] : 1.0f;
-    vs = DT == kE4m3 && !is_q && a.c.v_scale != nullptr ? a.c.v_scale[h] : 1.0f;
+    ks = DT == kE4m3 && !is_q && a.c.k_scale != nullptr ? __frcp_rn(a.c.k_scale[h]) : 1.0f;
+    vs = DT == kE4m3 && !is_q && a.c.v_scale != nullptr ? __frcp_rn(a.c.v_scale[h]) : 1.0f;
     any = false;
     constexpr uint32_t kInf = DT == kBf16 ? 0x7F807F80u : 0x7C007C00u;
 #pragma unroll
@@ -223,10 +227,10 @@ struct Unit {
   __device__ __forceinline__ void put(const Lane& L, char* k, char* w, Wide x, const Raw& v) {
     constexpr int kE = elem_bytes<DT>();
     if constexpr (DT == kE4m3) {
-      x.a = div4(x.a, ks);
-      x.b = div4(x.b, ks);
-      store4<DT>(w + L.a, div4(load4<IN>(&v.a), vs));
-      store4<DT>(w + L.b, div4(load4<IN>(&v.b), vs));
+      x.a = times(x.a, ks);
+      x.b = times(x.b, ks);
+      store4<DT>(w + L.a, times(load4<IN>(&v.a), vs));
+      store4<DT>(w + L.b, times(load4<IN>(&v.b), vs));
     } else {
       *reinterpret_cast<uint2*>(w + kE * L.a) = v.a;
       *reinterpret_cast<uint2*>(w + kE * L.b) = v.b;
@@ -360,12 +364,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) append_few_kerne
 
 // Keys and values: WARPS warps have a unit (1 or all of the block).
 template <int DT, int IN, bool INTER, int WARPS>
-__global__ void __launch_bounds__(kManyThreads, 3) append_keys_kernel(AppendArgs a) {
-  wait_prior_grid();
-  allow_dependents();
+__global__ void __launch_bounds__(kManyThreads, kKeyBlocksPerSm) append_keys_kernel(AppendArgs a) {
   constexpr int kTeams = 2 * WARPS;  // of a unit
   __shared__ Prefix<kManyThreads> S;
   __shared__ uint32_t s_bound[WARPS > 1 ? kManyWarps : 1][8][kTeam];
+  wait_prior_grid();
+  allow_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x % kTeam;
   const int team = WARPS > 1 ? threadIdx.x / kTeam : (threadIdx.x / kTeam) & 1;
   auto count = [&](int b) { return (long long)pages_of(a, b) * a.c.H; };
@@ -453,12 +457,10 @@ __global__ void __launch_bounds__(kManyThreads, 3) append_keys_kernel(AppendArgs
   }
 }
 
-// Queries: the new rows of all requests, concatenated and cut into equal ranges,
-// one per block; a team takes four heads of a row at a time.
+// Queries: the new rows of all requests, concatenated and cut into equal ranges, one
+// per block; a team takes four heads of a row at a time.
 template <int IN, bool INTER>
-__global__ void __launch_bounds__(kManyThreads, 4) append_queries_kernel(AppendArgs a) {
-  wait_prior_grid();
-  allow_dependents();
+__device__ __forceinline__ void append_queries(const AppendArgs& a) {
   __shared__ Prefix<kManyThreads> S;
   const int team = threadIdx.x / kTeam, quads = (a.Hq + kQueryHeads - 1) / kQueryHeads;
   auto count = [&](int b) {
@@ -510,27 +512,39 @@ __global__ void __launch_bounds__(kManyThreads, 4) append_queries_kernel(AppendA
   }
 }
 
+// Launched behind the keys' kernel, whose results it does not need: it starts once
+// that one's blocks all run (which they do once what came before them is complete),
+// and waits for it at its end, so that whoever waits for this kernel waits for both.
+template <int IN, bool INTER>
+__global__ void __launch_bounds__(kManyThreads, kQueryBlocksPerSm) append_queries_kernel(AppendArgs a) {
+  allow_dependents();
+  append_queries<IN, INTER>(a);
+  wait_prior_grid();
+}
+
 template <int DT, int IN, bool INTER>
 cudaError_t launch_form(const AppendArgs& a, int sms, cudaStream_t stream) {
   const long long pages = a.offsets == nullptr ? a.B : a.n_rows / a.c.ps.d + 2 * (long long)a.B;  // at most
-  auto grid = [&](long long need, int per_sm) { return int(need < (long long)per_sm * sms ? need : (long long)per_sm * sms); };
+  const int Hq = a.q != nullptr ? a.Hq : 0;
   count_launch();
   if (a.offsets == nullptr || a.n_rows <= 8LL * a.B) {
-    const long long teams = pages * (a.c.H + (a.q != nullptr ? a.Hq : 0));
-    return launch_dependent(append_few_kernel<DT, IN, INTER>,
-                            dim3(grid((teams * kTeam + kFewThreads - 1) / kFewThreads, kFewBlocksPerSm)),
-                            dim3(kFewThreads), 0, stream, a);
+    const long long need = (pages * (a.c.H + Hq) * kTeam + kFewThreads - 1) / kFewThreads, fit = (long long)kFewBlocksPerSm * sms;
+    return launch_dependent(append_few_kernel<DT, IN, INTER>, dim3(int(need < fit ? need : fit)), dim3(kFewThreads), 0,
+                            stream, a);
   }
+  const long long units = pages * a.c.H, fit = (long long)kKeyBlocksPerSm * sms;
+  const bool whole = a.c.ps.d > 32;  // a block per unit, else a warp
+  const long long need = whole ? units : (units + kManyWarps - 1) / kManyWarps;
+  const dim3 grid(int(need < fit ? need : fit));
   const cudaError_t e =
-      a.c.ps.d > 32 ? launch_dependent(append_keys_kernel<DT, IN, INTER, kManyWarps>, dim3(grid(pages * a.c.H, 3)),
-                                       dim3(kManyThreads), 0, stream, a)
-                    : launch_dependent(append_keys_kernel<DT, IN, INTER, 1>,
-                                       dim3(grid((pages * a.c.H + kManyWarps - 1) / kManyWarps, 3)),
-                                       dim3(kManyThreads), 0, stream, a);
-  if (e != cudaSuccess || a.q == nullptr) return e;
+      whole ? launch_dependent(append_keys_kernel<DT, IN, INTER, kManyWarps>, grid, dim3(kManyThreads), 0, stream, a)
+            : launch_dependent(append_keys_kernel<DT, IN, INTER, 1>, grid, dim3(kManyThreads), 0, stream, a);
+  if (e != cudaSuccess || Hq == 0) return e;
   count_launch();
-  return launch_dependent(append_queries_kernel<IN, INTER>, dim3(grid((a.n_rows * (long long)a.Hq + 63) / 64, 4)),
-                          dim3(kManyThreads), 0, stream, a);
+  const long long teams = a.n_rows * (long long)((Hq + kQueryHeads - 1) / kQueryHeads), per = kManyThreads / kTeam;
+  const long long blocks = (teams + per - 1) / per, most = (long long)kQueryBlocksPerSm * sms;
+  return launch_dependent(append_queries_kernel<IN, INTER>, dim3(int(blocks < most ? blocks : most)), dim3(kManyThreads),
+                          0, stream, a);
 }
 
 template <int DT, int IN>

@@ -739,10 +739,12 @@ __global__ void __launch_bounds__(kFusedThreads, 2) select_kernel(SelectArgs a, 
 }
 
 // One launch where a unit's pages keep a block busy for no longer than the second
-// launch would take, or where there are units for all SMs; else the pages are
-// scored by all warps of the device and picked by a second kernel.
-constexpr int kFusedPages = 256;      // any number of units
-constexpr int kFusedManyPages = 2048; // at least one unit per SM
+// launch takes, or where there are units for half of the SMs; else the pages are
+// scored by all warps of the device and picked by a second kernel. Measured (fused,
+// split): 8 units of 256 pages 7.4, 9.4 us; 8 of 512 10.9, 10.8; 64 of 1024 20.5,
+// 20.5; 64 of 2048 33.8, 27.6; 128 of 1024 22.3, 25.9; 256 of 2048 51, 71.
+constexpr int kFusedPages = 512;       // any number of units
+constexpr int kFusedManyPages = 2048;  // half as many units as SMs at least
 
 template <int DT, int QT>
 cudaError_t launch_types(const SelectArgs& a, cudaStream_t stream) {
@@ -763,7 +765,7 @@ cudaError_t launch_types(const SelectArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
-  if (a.max_pages <= kFusedPages || (a.max_pages <= kFusedManyPages && units >= a.sms)) {
+  if (a.max_pages <= kFusedPages || (a.max_pages <= kFusedManyPages && 2 * units >= a.sms)) {
     count_launch();
     return launch_dependent(select_kernel<DT, QT>, dim3(units), dim3(kFusedThreads), ring + smem, stream, a, ws);
   }
