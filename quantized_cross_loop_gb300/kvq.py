@@ -8,6 +8,7 @@ There is no CPU fallback.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -789,6 +790,7 @@ def kvq_sparse_decode_attn(table: RequestTable, q: torch.Tensor, depth: int, n_h
 # --------------------------------------------------------------------------- paged cache
 
 _PAGED_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+_SCALE_128 = 1.0 / math.sqrt(128)
 
 
 class PagedCache:
@@ -849,7 +851,7 @@ class PagedCache:
             t = getattr(self, name)
             setattr(self.desc, name, None if t is None else t.data_ptr())
         self.desc.error = self._error.data_ptr()
-        self._ref = ctypes.byref(self.desc)
+        self.lib, self.ref = lib(), ctypes.byref(self.desc)
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_heads: int, dtype=torch.bfloat16, device="cuda",
@@ -878,30 +880,30 @@ def _raw_stream(index: int) -> int:
     return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
 
 
-def _on_stream(cache: PagedCache, stream, call):
-    """call(raw stream) with the cache's device current. Buffers that the call allocates belong to the stream they
-    are used on."""
-    index = cache.index
-    if stream is None and torch.cuda.current_device() == index:
-        return call(_raw_stream(index))
+@contextlib.contextmanager
+def _made_current(cache: PagedCache, stream):
+    """The cache's device and the given stream made current, so that buffers allocated inside belong to the stream
+    they are used on."""
     if stream is not None and stream.device != cache.device:
         raise KvqError(f"stream of {stream.device} for a cache on {cache.device}")
-    with torch.cuda.device(cache.device):
-        if stream is None:
-            return call(_raw_stream(index))
-        with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+    with torch.cuda.device(cache.device), torch.cuda.stream(stream):
+        yield
 
 
-def _int32(cache: PagedCache, t: torch.Tensor, name: str, shape: tuple):
-    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != cache.index or not t.is_contiguous():
-        raise KvqError(f"{name} must be contiguous int32 {list(shape)} on {cache.device}, got {t.dtype} "
+def _elsewhere(cache: PagedCache, stream) -> bool:
+    return stream is not None or torch.cuda.current_device() != cache.index
+
+
+def _ptr(cache: PagedCache, t: torch.Tensor, name: str, dtype, shape) -> int:
+    """The address of a contiguous tensor of this type and shape on the cache's device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != cache.index or not t.is_contiguous():
+        raise KvqError(f"{name} must be contiguous {dtype} {list(shape)} on {cache.device}, got {t.dtype} "
                        f"{list(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
 def _head_rows(cache: PagedCache, t: torch.Tensor, name: str, dtype, rows: int | None = None, heads: int | None = None):
-    """A [rows, heads, 128] view whose rows may be strided; returns its row stride."""
+    """The heads and the row stride of a [rows, heads, 128] view whose rows may be strided."""
     shape = t.shape
     if t.dtype is not dtype or len(shape) != 3 or shape[2] != 128 or t.get_device() != cache.index:
         raise KvqError(f"{name} must be {dtype} [rows, heads, 128] on {cache.device}, got {t.dtype} {list(shape)} "
@@ -912,14 +914,14 @@ def _head_rows(cache: PagedCache, t: torch.Tensor, name: str, dtype, rows: int |
     s = t.stride()
     if n and h and (s[2] != 1 or (h > 1 and s[1] != 128)):
         raise KvqError(f"{name}: the heads of a row must be contiguous")
-    return s[0] if n > 1 else h * 128
+    return h, s[0] if n > 1 else h * 128
 
 
-def _paged_table(cache: PagedCache, table: torch.Tensor):
+def _table_shape(table: torch.Tensor):
     shape = table.shape
     if len(shape) != 2:
         raise KvqError("page_table must be [n_requests, max_pages]")
-    return _int32(cache, table, "page_table", shape), shape[0], shape[1]
+    return shape
 
 
 def kvq_paged_append(cache: PagedCache, page_table: torch.Tensor, start: torch.Tensor, k: torch.Tensor,
@@ -935,92 +937,94 @@ def kvq_paged_append(cache: PagedCache, page_table: torch.Tensor, start: torch.T
     token's place). With q [n, Hq, 128] its rotation goes to q_out (allocated
     when None; may be q) and is returned. start is not changed. Rows behind
     offsets[B] are padding: neither they nor their q_out rows are touched."""
-    tab, B, W = _paged_table(cache, page_table)
+    if _elsewhere(cache, stream):
+        with _made_current(cache, stream):
+            return kvq_paged_append(cache, page_table, start, k, v, offsets, q, q_out, rope, interleaved, positions)
     if cache.k is None:
         raise KvqError("a cache of key bounds alone cannot be appended to")
-    r = kvq_paged_rows()
+    shape = _table_shape(page_table)
+    B, W = shape
+    tab = _ptr(cache, page_table, "page_table", torch.int32, shape)
     dtype = k.dtype
-    if dtype not in (torch.bfloat16, torch.float16):
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
         raise KvqError(f"k must be bfloat16 or float16, got {dtype}")
-    r.dtype = _PAGED_DTYPES[dtype]
     n = k.shape[0]
-    r.n_rows = n
-    r.start = _int32(cache, start, "start", (B,))
-    r.k_stride = _head_rows(cache, k, "k", dtype, n, cache.n_heads)
-    r.v_stride = _head_rows(cache, v, "v", dtype, n, cache.n_heads)
+    r = kvq_paged_rows()
+    r.dtype, r.n_rows = _PAGED_DTYPES[dtype], n
+    r.start = _ptr(cache, start, "start", torch.int32, (B,))
+    r.k_stride = _head_rows(cache, k, "k", dtype, n, cache.n_heads)[1]
+    r.v_stride = _head_rows(cache, v, "v", dtype, n, cache.n_heads)[1]
     r.k, r.v = k.data_ptr(), v.data_ptr()
     if offsets is not None:
-        r.offsets = _int32(cache, offsets, "offsets", (B + 1,))
+        r.offsets = _ptr(cache, offsets, "offsets", torch.int32, (B + 1,))
     if positions is not None:
-        r.positions = _int32(cache, positions, "positions", (n,))
+        r.positions = _ptr(cache, positions, "positions", torch.int32, (n,))
     if rope is not None:
-        if rope.dtype != torch.float32 or rope.dim() != 2 or rope.device != cache.device or not rope.is_contiguous():
-            raise KvqError(f"rope must be contiguous float32 [positions, R] on {cache.device}")
-        r.rope, r.rope_positions, r.rotary_dim = rope.data_ptr(), rope.shape[0], rope.shape[1]
+        shape = rope.shape
+        if len(shape) != 2:
+            raise KvqError("rope must be [positions, R]")
+        r.rope = _ptr(cache, rope, "rope", torch.float32, shape)
+        r.rope_positions, r.rotary_dim = shape
         r.interleaved = int(interleaved)
-    if q is None and q_out is not None:
+    if q is not None:
+        r.n_q_heads, r.q_stride = _head_rows(cache, q, "q", dtype, n)
+        if q_out is None:
+            q_out = torch.empty((n, r.n_q_heads, 128), dtype=dtype, device=cache.device)
+        r.q_out_stride = _head_rows(cache, q_out, "q_out", dtype, n, r.n_q_heads)[1]
+        r.q, r.q_out = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
         raise KvqError("q_out without q")
-
-    def call(raw):
-        out = q_out
-        if q is not None:
-            if out is None:
-                out = torch.empty((n, q.shape[1], 128), dtype=dtype, device=cache.device)
-            r.q_stride = _head_rows(cache, q, "q", dtype, n)
-            r.q_out_stride = _head_rows(cache, out, "q_out", dtype, n, q.shape[1])
-            r.q, r.q_out, r.n_q_heads = q.data_ptr(), out.data_ptr(), q.shape[1]
-        _check(lib().kvq_paged_append(cache._ref, tab, W, B, ctypes.byref(r), raw), "kvq_paged_append")
-        return out
-
-    return _on_stream(cache, stream, call)
+    st = cache.lib.kvq_paged_append(cache.ref, tab, W, B, ctypes.byref(r), _raw_stream(cache.index))
+    if st:
+        _check(st, "kvq_paged_append")
+    return q_out
 
 
-def _paged_query(cache: PagedCache, page_table, seq_lens, q):
-    tab, B, W = _paged_table(cache, page_table)
-    if q.dtype not in (torch.bfloat16, torch.float16):
+def _query_type(q: torch.Tensor) -> int:
+    if q.dtype is not torch.bfloat16 and q.dtype is not torch.float16:
         raise KvqError(f"q must be bfloat16 or float16, got {q.dtype}")
-    stride = _head_rows(cache, q, "q", q.dtype, B)
-    return tab, B, W, _int32(cache, seq_lens, "seq_lens", (B,)), _PAGED_DTYPES[q.dtype], stride
+    return _PAGED_DTYPES[q.dtype]
 
 
 def _paged_workspace(cache: PagedCache, workspace, B, Hq, W):
     if workspace is None:
-        need = int(lib().kvq_paged_workspace_bytes(B, cache.n_heads, Hq, W))
+        need = int(cache.lib.kvq_paged_workspace_bytes(B, cache.n_heads, Hq, W))
         return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
     if workspace.get_device() != cache.index or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise KvqError(f"workspace must be contiguous uint8 on {cache.device}")
     return workspace
 
 
-def _paged_attend(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, workspace, stream, what):
-    tab, B, W, lens, qdt, stride = _paged_query(cache, page_table, seq_lens, q)
-    Hq = q.shape[1]
+def _paged_attend(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, workspace, what):
+    shape = _table_shape(page_table)
+    B, W = shape
+    tab = _ptr(cache, page_table, "page_table", torch.int32, shape)
+    qdt = _query_type(q)
+    Hq, stride = _head_rows(cache, q, "q", q.dtype, B)
+    lens = _ptr(cache, seq_lens, "seq_lens", torch.int32, (B,))
     if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(128)
-    for name, t, shape in (("out", out, (B, Hq, 128)), ("lse", lse, (B, Hq))):
-        if t is not None and (t.dtype is not torch.float32 or t.shape != shape or t.get_device() != cache.index
-                              or not t.is_contiguous()):
-            raise KvqError(f"{name} must be contiguous float32 {list(shape)} on {cache.device}")
-    if sel is not None:
+        softmax_scale = _SCALE_128
+    if out is None:
+        out = torch.empty((B, Hq, 128), dtype=torch.float32, device=cache.device)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _ptr(cache, out, "out", torch.float32, (B, Hq, 128))
+    lse_ptr = None if lse is None else _ptr(cache, lse, "lse", torch.float32, (B, Hq))
+    ws = _paged_workspace(cache, workspace, B, Hq, W)
+    raw = _raw_stream(cache.index)
+    if sel is None:
+        st = cache.lib.kvq_paged_decode_attn(cache.ref, tab, W, B, lens, q.data_ptr(), qdt, stride, Hq, softmax_scale,
+                                             out_ptr, lse_ptr, ws.data_ptr(), ws.numel(), raw)
+    else:
         if sel.dim() != 3:
             raise KvqError("sel must be [n_requests, n_heads, n_select]")
-        sel_ptr = _int32(cache, sel, "sel", (B, cache.n_heads, sel.shape[2]))
-
-    def call(raw):
-        o = torch.empty((B, Hq, 128), dtype=torch.float32, device=cache.device) if out is None else out
-        ws = _paged_workspace(cache, workspace, B, Hq, W)
-        lse_ptr = None if lse is None else lse.data_ptr()
-        if sel is None:
-            st = lib().kvq_paged_decode_attn(cache._ref, tab, W, B, lens, q.data_ptr(), qdt, stride, Hq,
-                                             softmax_scale, o.data_ptr(), lse_ptr, ws.data_ptr(), ws.numel(), raw)
-        else:
-            st = lib().kvq_paged_sparse_attn(cache._ref, tab, W, B, lens, q.data_ptr(), qdt, stride, Hq, sel_ptr,
-                                             sel.shape[2], softmax_scale, o.data_ptr(), lse_ptr, ws.data_ptr(),
-                                             ws.numel(), raw)
+        n = sel.shape[2]
+        sel_ptr = _ptr(cache, sel, "sel", torch.int32, (B, cache.n_heads, n))
+        st = cache.lib.kvq_paged_sparse_attn(cache.ref, tab, W, B, lens, q.data_ptr(), qdt, stride, Hq, sel_ptr, n,
+                                             softmax_scale, out_ptr, lse_ptr, ws.data_ptr(), ws.numel(), raw)
+    if st:
         _check(st, what)
-        return o
-
-    return _on_stream(cache, stream, call)
+    return out
 
 
 def kvq_paged_decode_attn(cache: PagedCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor,
@@ -1031,7 +1035,10 @@ def kvq_paged_decode_attn(cache: PagedCache, page_table: torch.Tensor, seq_lens:
     the first seq_lens[b] cached tokens of each request; lse, FP32 [B, Hq], takes
     the natural log of the softmax's sum. workspace: cache.workspace_bytes(...)
     bytes, allocated when None; calls that may overlap need one each."""
-    return _paged_attend(cache, page_table, seq_lens, q, None, softmax_scale, out, lse, workspace, stream,
+    if _elsewhere(cache, stream):
+        with _made_current(cache, stream):
+            return kvq_paged_decode_attn(cache, page_table, seq_lens, q, softmax_scale, out, lse, workspace)
+    return _paged_attend(cache, page_table, seq_lens, q, None, softmax_scale, out, lse, workspace,
                          "kvq_paged_decode_attn")
 
 
@@ -1042,20 +1049,26 @@ def kvq_paged_select(cache: PagedCache, page_table: torch.Tensor, seq_lens: torc
     find the largest q.k by the cache's key bounds (summed over the query heads
     of a KV head), the first n_first and last n_last among them; ascending page
     numbers of the request, -1 behind the last."""
-    tab, B, W, lens, qdt, stride = _paged_query(cache, page_table, seq_lens, q)
-    Hq = q.shape[1]
-    shape = (B, cache.n_heads, n_select)
-    if sel is not None:
-        _int32(cache, sel, "sel", shape)
-
-    def call(raw):
-        s = torch.empty(shape, dtype=torch.int32, device=cache.device) if sel is None else sel
-        ws = _paged_workspace(cache, workspace, B, Hq, W)
-        _check(lib().kvq_paged_select(cache._ref, tab, W, B, lens, q.data_ptr(), qdt, stride, Hq, n_select, n_first,
-                                      n_last, s.data_ptr(), ws.data_ptr(), ws.numel(), raw), "kvq_paged_select")
-        return s
-
-    return _on_stream(cache, stream, call)
+    if _elsewhere(cache, stream):
+        with _made_current(cache, stream):
+            return kvq_paged_select(cache, page_table, seq_lens, q, n_select, n_first, n_last, sel, workspace)
+    shape = _table_shape(page_table)
+    B, W = shape
+    tab = _ptr(cache, page_table, "page_table", torch.int32, shape)
+    qdt = _query_type(q)
+    Hq, stride = _head_rows(cache, q, "q", q.dtype, B)
+    lens = _ptr(cache, seq_lens, "seq_lens", torch.int32, (B,))
+    if sel is None:
+        sel = torch.empty((B, cache.n_heads, max(n_select, 0)), dtype=torch.int32, device=cache.device)
+        sel_ptr = sel.data_ptr()
+    else:
+        sel_ptr = _ptr(cache, sel, "sel", torch.int32, (B, cache.n_heads, n_select))
+    ws = _paged_workspace(cache, workspace, B, Hq, W)
+    st = cache.lib.kvq_paged_select(cache.ref, tab, W, B, lens, q.data_ptr(), qdt, stride, Hq, n_select, n_first,
+                                    n_last, sel_ptr, ws.data_ptr(), ws.numel(), _raw_stream(cache.index))
+    if st:
+        _check(st, "kvq_paged_select")
+    return sel
 
 
 def kvq_paged_sparse_attn(cache: PagedCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor,
@@ -1063,5 +1076,8 @@ def kvq_paged_sparse_attn(cache: PagedCache, page_table: torch.Tensor, seq_lens:
                           lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
                           stream=None) -> torch.Tensor:
     """kvq_paged_decode_attn over the tokens of the pages `sel` (kvq_paged_select) only."""
-    return _paged_attend(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, workspace, stream,
+    if _elsewhere(cache, stream):
+        with _made_current(cache, stream):
+            return kvq_paged_sparse_attn(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, workspace)
+    return _paged_attend(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, workspace,
                          "kvq_paged_sparse_attn")
