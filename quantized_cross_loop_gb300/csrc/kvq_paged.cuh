@@ -154,6 +154,24 @@ __device__ __forceinline__ int find_request(const Prefix<NT>& S, int B, const F&
   return b;
 }
 
+// Start of part c of `total` cut into n equal parts: floor(c total / n). By 32-bit
+// arithmetic where that holds (64-bit divisions at the head of a kernel add up to a
+// microsecond, a seventh of the shortest calls). c <= n <= 8192.
+__device__ __forceinline__ long long part_start(int c, long long total, int n) {
+  if (total < (1 << 19)) return uint32_t(c) * uint32_t(total) / uint32_t(n);
+  return (long long)c * total / n;
+}
+// q = x / d and r = x % d, the same way.
+__device__ __forceinline__ void divide(long long x, int d, int& q, int& r) {
+  if (x <= 0x7FFFFFFF) {
+    q = int(x) / d;
+    r = int(x) - q * d;
+  } else {
+    q = int(x / d);
+    r = int(x - (long long)q * d);
+  }
+}
+
 struct AppendArgs {
   View c;
   const int32_t* table;

@@ -307,21 +307,19 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) append_few_kerne
     total = S.pre[kFewThreads];
   }
   flag_lengths(a);
-  const long long teams = (long long)gridDim.x * (kFewThreads / kTeam);
-  const long long me = (long long)blockIdx.x * (kFewThreads / kTeam) + threadIdx.x / kTeam;
-  const long long u0 = me * total / teams, u1 = (me + 1) * total / teams;
+  const int teams = int(gridDim.x) * (kFewThreads / kTeam);  // at most kFewBlocksPerSm x 8 an SM
+  const int me = int(blockIdx.x) * (kFewThreads / kTeam) + threadIdx.x / kTeam;
+  const long long u0 = part_start(me, total, teams), u1 = part_start(me + 1, total, teams);
   if (u0 >= u1) return;
   const Lane L(a, threadIdx.x % kTeam);
   long long at = u0;
   int b, hh, page_i;
   if (a.offsets == nullptr) {
-    b = int(u0 / heads);
-    hh = int(u0 % heads);
+    divide(u0, heads, b, hh);
     page_i = 0;
   } else {
     b = find_request<kFewThreads>(S, a.B, count, at);
-    page_i = int(at / heads);
-    hh = int(at % heads);
+    divide(at, heads, page_i, hh);
   }
   int start = 0, row0 = 0, n = rows_of(a, b, start, row0), pages = pages_of(a, b);
   for (long long w = u0; w < u1; ++w) {
@@ -375,14 +373,15 @@ __global__ void __launch_bounds__(kManyThreads, kKeyBlocksPerSm) append_keys_ker
   auto count = [&](int b) { return (long long)pages_of(a, b) * a.c.H; };
   build_prefix<kManyThreads>(S, a.B, count);
   flag_lengths(a);
-  const long long total = S.pre[kManyThreads], groups = (long long)gridDim.x * (kManyWarps / WARPS);
-  const long long me = (long long)blockIdx.x * (kManyWarps / WARPS) + (WARPS > 1 ? 0 : warp);
-  const long long u0 = me * total / groups, u1 = (me + 1) * total / groups;
+  const long long total = S.pre[kManyThreads];
+  const int groups = int(gridDim.x) * (kManyWarps / WARPS), me = int(blockIdx.x) * (kManyWarps / WARPS) + (WARPS > 1 ? 0 : warp);
+  const long long u0 = part_start(me, total, groups), u1 = part_start(me + 1, total, groups);
   if (u0 >= u1) return;
   const Lane L(a, lane);
   long long at = u0;
   int b = find_request<kManyThreads>(S, a.B, count, at);
-  int page_i = int(at / a.c.H), h = int(at % a.c.H);
+  int page_i, h;
+  divide(at, a.c.H, page_i, h);
   int start = 0, row0 = 0, n = rows_of(a, b, start, row0), pages = pages_of(a, b);
   for (long long w = u0; w < u1; ++w) {
     while (pages == 0 && b < a.B - 1) {  // requests that bring nothing hold no unit
@@ -469,14 +468,15 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a) {
   };
   build_prefix<kManyThreads>(S, a.B, count);
   const long long total = S.pre[kManyThreads];
-  const long long i0 = blockIdx.x * total / gridDim.x, i1 = (blockIdx.x + 1) * total / gridDim.x;
+  const long long i0 = part_start(blockIdx.x, total, gridDim.x), i1 = part_start(blockIdx.x + 1, total, gridDim.x);
   long long at = i0 + team;
   if (at >= i1) return;
   const Lane L(a, threadIdx.x % kTeam);
   const long long left = i1 - at;
   int b = find_request<kManyThreads>(S, a.B, count, at);
   int start = 0, row0 = 0, n = rows_of(a, b, start, row0);
-  int row = int(at / quads), quad = int(at % quads);  // of the request
+  int row, quad;  // of the request
+  divide(at, quads, row, quad);
   for (long long i = 0; i < left; i += kManyThreads / kTeam) {
     while (row >= n && b < a.B - 1) {
       row -= max(n, 0);

@@ -572,6 +572,12 @@ struct Block {
 
 int blocks_of(int sms) { return sms * kBlocksPerSm; }
 
+// The range that holds position x (cta_of), by 32-bit arithmetic where that holds.
+__device__ __forceinline__ int range_of(long long x, long long W, int C) {
+  if (W < (1 << 20)) return int((uint32_t(x + 1) * uint32_t(C) + uint32_t(W) - 1) / uint32_t(W)) - 1;
+  return cta_of(x, W, C);
+}
+
 template <int DT, int QT, int NT, bool SEL>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a) {
   using F = Form<DT>;
@@ -589,7 +595,21 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
     const int tiles = (span_of<SEL>(a, checked_len(a.lens, b, a.max_pages, a.c.ps)) + F::kTile - 1) / F::kTile;
     return tiles > 0 ? (long long)a.c.H * (tiles + kUnitCost) : 0LL;
   };
-  build_prefix<kThreads>(S.prefix, a.B, work_of);
+  // all work W, by a warp's own scan where a lane can have a request (no barriers in the shortest calls)
+  long long W, up_to = 0;  // up_to: work of the requests up to the lane's
+  if (a.B <= 32) {
+    const int lane = threadIdx.x & 31;
+    up_to = lane < a.B ? work_of(lane) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xFFFFFFFFu, up_to, o);
+      if (lane >= o) up_to += x;
+    }
+    W = __shfl_sync(0xFFFFFFFFu, up_to, 31);
+  } else {
+    build_prefix<kThreads>(S.prefix, a.B, work_of);
+    W = S.prefix.pre[kThreads];
+  }
   // requests without tokens, and refused ones: no block's range holds them
   for (int b = c; b < a.B; b += n_ctas) {
     const int T = checked_len(a.lens, b, a.max_pages, a.c.ps);
@@ -602,19 +622,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
     if (per_unit)
       for (int h = threadIdx.x; h < a.c.H; h += kThreads) recs[b * a.c.H + h].u = -1;
   }
-  const long long W = S.prefix.pre[kThreads];
   // ranges: none is empty, so the parts of a unit are those of adjacent blocks
   const long long sms = n_ctas / kBlocksPerSm, most = W <= sms ? W : max(sms, W / kMinTiles);
   const int C = int(most < n_ctas ? most : n_ctas);
   if (c >= C) return;
-  const long long s0 = cta_start(c, W, C), e0 = cta_start(c + 1, W, C);
+  const long long s0 = part_start(c, W, C), e0 = part_start(c + 1, W, C);
 
   Cursor<SEL, F::kTile> at, ahead;
   long long in_request = s0;
-  at.b = find_request<kThreads>(S.prefix, a.B, work_of, in_request);
+  if (a.B <= 32) {
+    at.b = min(__popc(__ballot_sync(0xFFFFFFFFu, up_to <= s0)), a.B - 1);
+    if (at.b > 0) in_request -= __shfl_sync(0xFFFFFFFFu, up_to, at.b - 1);
+  } else {
+    at.b = find_request<kThreads>(S.prefix, a.B, work_of, in_request);
+  }
   at.load(a);
-  at.h = int(in_request / (at.tiles + kUnitCost));
-  at.tile = int(in_request % (at.tiles + kUnitCost));
+  divide(in_request, at.tiles + kUnitCost, at.h, at.tile);
   at.pos = s0;
   if (at.tile >= at.tiles) at.next_unit(a);  // the range begins behind the unit's last tile
   if (at.h >= a.c.H || !at.before(a, e0)) return;  // (and may hold no tile)
@@ -624,8 +647,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
   const int row = K.warp * F::kRows + (K.lane & (F::kRows - 1));
   Row entry, page;  // looked up one step, and both
   bool have_entry = false, have_page = false;
-  K.load_query(at.b, at.h);
-  K.clear();
   // tile i: its selection entry is looked up at i - kStages - 1, its page at i - kStages, its copies issued at
   // i - kStages + 1
   for (int i = -F::kStages - 1; i < 0 || at.before(a, e0); ++i) {
@@ -648,6 +669,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
       look_up_entry<SEL>(a, ahead, ahead.tile * F::kTile + row, entry);
       ahead.next(a);
     }
+    if (i == -1) {  // (the first tiles' copies are on their way)
+      K.load_query(at.b, at.h);
+      K.clear();
+    }
     if (i < 0) continue;
     __syncwarp();  // the stage's mask
     K.attend(i % F::kStages);
@@ -663,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
     }
     if (us >= s0 && threadIdx.x == 0) {  // it starts here
       const int u = at.b * a.c.H + at.h;
-      if (slot != nullptr) recs[per_unit ? u : c] = Rec{u, c, cta_of(ue - 1, W, C), 0};
+      if (slot != nullptr) recs[per_unit ? u : c] = Rec{u, c, range_of(ue - 1, W, C), 0};
       else if (per_unit) recs[u].u = -1;
     }
     K.finish(at.b, at.h, slot);

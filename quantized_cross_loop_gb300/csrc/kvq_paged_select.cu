@@ -264,11 +264,11 @@ __global__ void __launch_bounds__(kScoreThreads, kScoreBlocksPerSm) score_kernel
   // H warps side by side take the heads of the same pages, whose bounds lie side by side: a group of H warps has a
   // range of the chunks of all requests
   const int lane = threadIdx.x & 31;
-  const long long total = S.pre[kScoreThreads], groups = (long long)gridDim.x * (kScoreThreads / 32) / a.c.H;
-  const long long me = (long long)blockIdx.x * (kScoreThreads / 32) + threadIdx.x / 32, group = me / a.c.H;
-  const int h = int(me % a.c.H);
+  const long long total = S.pre[kScoreThreads];
+  const int groups = int(gridDim.x) * kScoreWarps / a.c.H;
+  const int me = int(blockIdx.x) * kScoreWarps + threadIdx.x / 32, group = me / a.c.H, h = me % a.c.H;
   if (group >= groups) return;
-  const long long c0 = group * total / groups, c1 = (group + 1) * total / groups;
+  const long long c0 = part_start(group, total, groups), c1 = part_start(group + 1, total, groups);
   if (c0 >= c1) return;
   long long at = c0;
   const int b = find_request<kScoreThreads>(S, a.B, count, at);
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a, Worksp
   wait_prior_grid();
   allow_dependents();
   const long long unit = blockIdx.x;
-  const int b = int(unit / a.c.H), h = int(unit % a.c.H), tid = threadIdx.x;
+  const int b = int(blockIdx.x) / a.c.H, h = int(blockIdx.x) % a.c.H, tid = threadIdx.x;
   const int pages = pages_of(a, checked_len(a.lens, b, a.max_pages, a.c.ps));
   int32_t* sel = a.sel + unit * a.n_select;
   if (pages <= a.n_select) {  // all of them, and -1 behind
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kFusedThreads, 2) select_kernel(SelectArgs a, 
   wait_prior_grid();
   allow_dependents();
   const long long unit = blockIdx.x;
-  const int b = int(unit / a.c.H), h = int(unit % a.c.H), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = int(blockIdx.x) / a.c.H, h = int(blockIdx.x) % a.c.H, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int T = checked_len(a.lens, b, a.max_pages, a.c.ps), pages = pages_of(a, T);
   if (T < 0 && tid == 0) flag(a.c, KVQ_PAGED_ERR_LENGTH);
   int32_t* sel = a.sel + unit * a.n_select;
