@@ -530,39 +530,41 @@ __device__ __forceinline__ void pick(const SelectArgs& a, Pick& S, int b, int h,
     // as a rule the pages from the window's lower end on are as many as are wanted: written in order at once
     if (pages <= 32 * kWords && emit<THREADS>(a, S, pages, sel, [&](int p) { return p < f0 || p >= f1 || keys[p] >= lo; }))
       return;
-    int n_above = 0, n_in = 0;
+    // the others: counted, the pages in doubt listed
+    if (tid == 0) S.n_list = S.left = 0;
+    __syncthreads();
+    int n_above = 0;
     for (int p = f0 + tid; p < f1; p += THREADS) {
-      n_above += keys[p] > hi;
-      n_in += keys[p] >= lo && keys[p] <= hi;
+      const uint32_t x = keys[p];
+      n_above += x > hi;
+      if (x >= lo && x <= hi) {
+        const int i = atomicAdd(&S.n_list, 1);
+        if (i < kList) S.list_page[i] = p;
+      }
     }
-    int before;
-    n_above = block_prefix<THREADS>(S, n_above, before);
-    n_in = block_prefix<THREADS>(S, n_in, before);
-    const int want = k - n_above;
-    if (want == n_in) {  // (beyond the bit map)
-      __syncthreads();
+    n_above = __reduce_add_sync(0xFFFFFFFFu, n_above);
+    if (lane == 0 && n_above != 0) atomicAdd(&S.left, n_above);
+    if (tid < kD) {
+      double up = 0.0, down = 0.0;
+#pragma unroll 8
+      for (int j = 0; j < a.g; ++j) {
+        const uint16_t v = *reinterpret_cast<const uint16_t*>(a.q + (long long)b * a.q_stride +
+                                                              ((long long)(h * a.g + j) * kD + tid) * 2);
+        const float x = QT == kBf16 ? bf16_bits_to_f32(v) : f16_bits_to_f32(v);
+        if (x < 0.0f) down += x;
+        else up += x;
+      }
+      S.up[tid] = up;
+      S.down[tid] = down;
+    }
+    __syncthreads();
+    const int want = k - S.left, n_in = S.n_list;
+    if (want == n_in) {  // (pages beyond the bit map)
       for (int p = f0 + tid; p < f1; p += THREADS)
         if (keys[p] >= lo && keys[p] <= hi) keys[p] = kFirstKey;
       __syncthreads();
     } else {
-      if (tid < kD) {
-        double up = 0.0, down = 0.0;
-        for (int j = 0; j < a.g; ++j) {
-          const uint16_t v = *reinterpret_cast<const uint16_t*>(a.q + (long long)b * a.q_stride +
-                                                                ((long long)(h * a.g + j) * kD + tid) * 2);
-          const float x = QT == kBf16 ? bf16_bits_to_f32(v) : f16_bits_to_f32(v);
-          if (x < 0.0f) down += x;
-          else up += x;
-        }
-        S.up[tid] = up;
-        S.down[tid] = down;
-      }
-      if (tid == 0) S.n_list = 0;
-      __syncthreads();
       if (n_in <= kList) {
-        for (int p = f0 + tid; p < f1; p += THREADS)
-          if (keys[p] >= lo && keys[p] <= hi) S.list_page[atomicAdd(&S.n_list, 1)] = p;
-        __syncthreads();
         for (int i = warp; i < n_in; i += (THREADS / 32)) {
           const uint64_t x = exact_key<DT>(a, S, b, h, S.list_page[i], lane);
           if (lane == 0) S.list_exact[i] = x;

@@ -818,3 +818,94 @@ def test_binding_refusals():
     with pytest.raises(E, match="scales belong"):
         s = torch.ones(2, device="cuda")
         kvq.kvq_paged_decode_attn(kvq.PagedCache(16, 2, b.k, b.v, None, s, s), b.table, b.seq, q)
+
+
+def _bounds_only(lens, ps, H, dtype, seed=0):
+    """A cache of key bounds alone, finite random bounds lo <= hi, for selections over more pages than a pool would hold."""
+    g = _gen(seed)
+    b = Batch.__new__(Batch)
+    b.lens, b.ps, b.H, b.dt = lens, ps, H, DT[dtype]
+    pages = [-(-t // ps) for t in lens]
+    n, W = sum(pages) + 1, max(pages)
+    mid = torch.randn((n, H, D), generator=g, device="cuda")
+    w = torch.rand((n, H, D), generator=g, device="cuda") + 1
+    b.bounds = torch.stack([mid - w, mid + w], 2).to(b.dt)
+    perm = torch.randperm(n, generator=g, device="cuda").int()
+    b.table = torch.full((len(lens), W), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for i, m in enumerate(pages):
+        b.table[i, :m] = perm[at:at + m]
+        at += m
+    b.seq = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    b.cache = kvq.PagedCache(ps, H, key_bounds=b.bounds)
+    return b
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,H,n,first,last", [
+    ([1500] * 12, 8, 40, 1, 1),        # a launch in which a block has a unit, more than 512 pages
+    ([300, 12, 4000, 90], 3, 12, 6, 6),  # nothing but the forced pages of the long ones
+    ([3000], 1, 2999, 0, 0),
+    ([40000, 700], 1, 100, 1, 1),      # more pages than the bit map and the staged keys hold
+])
+def test_selection_over_many_pages(cache, lens, H, n, first, last):
+    b = _bounds_only(lens, 1, H, cache, seed=n)
+    _check_selection(b, _query(len(lens), 4 * H), n, first, last)
+
+
+@pytest.mark.parametrize("lens,H", [([3000], 1), ([1800] * 12, 7), ([40000], 1)])
+@pytest.mark.parametrize("differing", [0, 5])
+def test_selection_ties_beyond_the_list(lens, H, differing):
+    """More pages of the same score than are ranked in shared memory."""
+    b = _bounds_only(lens, 1, H, "bf16")
+    one = b.bounds[:1].clone()
+    b.bounds.copy_(one.expand_as(b.bounds))
+    up = _raw(b.bounds)
+    for i in range(differing):
+        up[b.table[0, 700 + 211 * i].long(), :, :, 3 * i] += 1 + i
+    _check_selection(b, _query(len(lens), 2 * H), 1300, 0, 0)
+    _check_selection(b, _query(len(lens), 2 * H, seed=7), 60, 2, 3)
+
+
+@pytest.mark.parametrize("g", [3, 12])
+def test_attention_many_units(g):
+    """More (request, KV head) pairs than blocks, for either width of the query operand."""
+    lens = [(37 * i) % 300 for i in range(170)] + [5000]
+    b = Batch(lens, 16, 2, "bf16", seed=g, bounds=False)
+    q = _query(len(lens), 2 * g)
+    out, lse = _attend(b, q)
+    _compare(b, q, out, lse, 1 / math.sqrt(D))
+
+
+def test_attention_of_keys_that_are_minus_infinity():
+    """Logits of -inf weigh nothing; a request of nothing else has no sum."""
+    b = Batch([40, 20], 16, 1, "bf16")
+    q = _query(2, 4).abs()  # every product with -inf is -inf
+    for i in range(2):
+        n = 30 if i == 0 else 20  # request 0 keeps ten tokens
+        t = torch.arange(n, device="cuda")
+        b.k[b.table[i].long()[t // 16], t % 16] = -math.inf
+    out, lse = _attend(b, q)
+    o, l, to, tl = _exact(q[0], b.K[0][:, 0], b.V[0][:, 0], 1 / math.sqrt(D), torch.arange(30, 40, device="cuda"))
+    assert (out[0] - o).abs().le(to).all() and (lse[0] - l).abs().le(tl).all()
+    assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()
+
+
+def test_more_requests_than_lanes_and_threads():
+    """Batches around the sizes at which a block finds its range another way (32 requests, 128 threads)."""
+    for n in (31, 32, 33, 127, 128, 129, 400):
+        lens = [(13 * i) % 61 for i in range(n)]
+        b = Batch(lens, 8, 1, "bf16", seed=n, room=2)
+        q = _query(n, 2)
+        out, lse = _attend(b, q)
+        _compare(b, q, out, lse, 1 / math.sqrt(D))
+        _check_selection(b, q, 3, 1, 1)
+        per = [(i % 3) for i in range(n)]
+        kn = torch.randn((sum(per), 1, D), generator=_gen(n), device="cuda").bfloat16()
+        off = torch.tensor([0] + per).cumsum(0)
+        kvq.kvq_paged_append(b.cache, b.table, b.seq, kn, kn, offsets=off.int().cuda())
+        for i in range(0, n, 7):
+            pos = torch.arange(per[i], device="cuda") + lens[i]
+            got = b.k[b.table[i].long()[pos // 8], pos % 8]
+            assert torch.equal(got, kn[off[i]:off[i + 1]])
+        assert b.cache.error_word() == 0
