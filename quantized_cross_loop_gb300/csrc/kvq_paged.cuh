@@ -32,16 +32,16 @@ inline FastDiv fast_div(int d) {
 
 // The cache with strides in bytes (the stride of a dimension of one entry is 0).
 struct View {
+  FastDiv ps;
+  int32_t H;
+  int32_t n_pages;
+  int32_t* err;
   char* k;
   char* v;
-  char* bounds;  // [n_pages][H][2][128] elements, or nullptr
+  long long page_stride, token_stride, head_stride;
   const float* k_scale;
   const float* v_scale;
-  int32_t* err;
-  long long page_stride, token_stride, head_stride;
-  int32_t n_pages;
-  int32_t H;
-  FastDiv ps;
+  char* bounds;  // [n_pages][H][2][128] elements, or nullptr
 };
 
 __device__ __forceinline__ void flag(const View& c, int bits) {
@@ -196,23 +196,24 @@ struct AppendArgs {
 };
 
 struct AttnArgs {
-  View c;
+  const int32_t* lens;
   const int32_t* table;
   int32_t max_pages;
   int32_t B;
-  const int32_t* lens;
+  int32_t lane_heads;  // KV heads of a lane of blocks (launch_attn)
+  int32_t g;
+  int32_t Hq;
+  int32_t n_select;
+  const int32_t* sel;  // [B][H][n_select], or nullptr: every page
+  View c;
   const char* q;
   long long q_stride;  // bytes
-  int32_t q_dtype;
-  int32_t dtype;
-  int32_t Hq;
-  int32_t g;
-  const int32_t* sel;  // [B][H][n_select], or nullptr: every page
-  int32_t n_select;
   float scale;
+  int32_t q_dtype;
   float* out;
   float* lse;
   char* ws;
+  int32_t dtype;
   int32_t sms;
 };
 

@@ -7,15 +7,17 @@
 // Bound: HBM. A token and KV head bring 4 D bytes (16-bit) for 4 D g flops, so a
 // block must keep loads in flight and spend few instructions a byte.
 //
-// Work: the tiles (64 or 128 tokens) of all (request, KV head) units, concatenated
-// and cut into equal ranges, one per block (two blocks an SM); lengths are read on
-// the device, so a captured call follows them. A unit that lies in one block's
-// range is finished there; of the others each block leaves (m, l, sum) in one of
-// its two slots, and the combine kernel joins them. (Joined in the same launch, by the
-// block that finds the flags of all parts set, they took longer in every case:
-// 10.1 against 8.7 us for one request of 256 tokens, 97.8 against 90.2 us for
-// 4 x 32768 and eight query heads: the fences and flags come to more than a second
-// launch that is already waiting.)
+// Work: L blocks side by side have H / L heads each of the same tokens (a token's
+// heads lie side by side in a token-major pool: read at about the same time they
+// are whole DRAM pages). The tiles (64 or 128 tokens) of a lane's (request, KV
+// head) units, concatenated, are cut into equal ranges, one per block of the lane
+// (two blocks an SM); lengths are read on the device, so a captured call follows
+// them. A unit that lies in one block's range is finished there; of the others each
+// block leaves (m, l, sum) in one of its two slots, and the combine kernel joins
+// them. (Joined in the same launch, by the block that finds the flags of all parts
+// set, they took longer in every case: 10.1 against 8.7 us for one request of 256
+// tokens, 97.8 against 90.2 us for 4 x 32768 and eight query heads: the fences and
+// flags come to more than a second launch that is already waiting.)
 //
 // A warp owns 16 tokens of every tile and a ring of its own in shared memory,
 // filled by 16-byte asynchronous copies, so that the main loop has no block
@@ -50,11 +52,12 @@ constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kUnitCost = 2;       // tiles that the end of a unit takes as long as
 constexpr int kMinTiles = 2;       // tiles of a block's range, once every SM has one
 
-// A unit whose parts lie in the ranges of blocks first .. last (u < 0: no such
-// unit). Where there are no more units than blocks, unit u's is number u, else the
-// one of the unit that starts in block c's range and goes on behind it number c.
+// A unit that several blocks share: the first of them and how many, `lanes` apart (u
+// < 0: no such unit). Where there are no more units than blocks, unit u's is number
+// u, else the one of the unit that starts in block c's range and goes on behind it
+// number c.
 struct Rec {
-  int32_t u, first, last, pad;
+  int32_t u, first, parts, pad;
 };
 __host__ __device__ constexpr bool rec_per_unit(long long units, int n_ctas) { return units <= n_ctas; }
 
@@ -186,19 +189,19 @@ struct Cursor {
     span = span_of<SEL>(a, T);
     tiles = (span + TILE - 1) / TILE;
   }
-  __device__ __forceinline__ void next_unit(const AttnArgs& a) {
+  __device__ __forceinline__ void next_unit(const AttnArgs& a, int h0) {  // h0: first of the lane's heads
     pos += tiles + kUnitCost - tile;
     tile = 0;
-    if (++h < a.c.H) return;
-    h = 0;
+    if (++h < h0 + a.lane_heads) return;
+    h = h0;
     do {
       ++b;
       load(a);
     } while (b < a.B && tiles == 0);
   }
-  __device__ __forceinline__ void next(const AttnArgs& a) {
+  __device__ __forceinline__ void next(const AttnArgs& a, int h0) {
     if (tile + 1 == tiles) {
-      next_unit(a);
+      next_unit(a, h0);
     } else {
       ++tile;
       ++pos;
@@ -570,7 +573,7 @@ struct Block {
   }
 };
 
-int blocks_of(int sms) { return sms * kBlocksPerSm; }
+int most_blocks(int sms) { return sms * kBlocksPerSm; }
 
 // The range that holds position x (cta_of), by 32-bit arithmetic where that holds.
 __device__ __forceinline__ int range_of(long long x, long long W, int C) {
@@ -585,7 +588,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
   Smem<DT>& S = *reinterpret_cast<Smem<DT>*>(smem);
   wait_prior_grid();
   allow_dependents();
-  const int c = blockIdx.x, n_ctas = gridDim.x;
+  // grid: (lanes, groups of blocks side by side)
+  const int lanes = gridDim.x, groups = gridDim.y, group = blockIdx.y, c = group * lanes + blockIdx.x, n_ctas = lanes * groups;
+  const int h0 = blockIdx.x * a.lane_heads;  // first of the lane's heads
   Rec* recs = reinterpret_cast<Rec*>(a.ws);
   float* slots = reinterpret_cast<float*>(a.ws + slots_offset(n_ctas));
   const bool per_unit = rec_per_unit((long long)a.B * a.c.H, n_ctas);
@@ -593,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
 
   auto work_of = [&](int b) {
     const int tiles = (span_of<SEL>(a, checked_len(a.lens, b, a.max_pages, a.c.ps)) + F::kTile - 1) / F::kTile;
-    return tiles > 0 ? (long long)a.c.H * (tiles + kUnitCost) : 0LL;
+    return tiles > 0 ? (long long)a.lane_heads * (tiles + kUnitCost) : 0LL;
   };
   // all work W, by a warp's own scan where a lane can have a request (no barriers in the shortest calls)
   long long W, up_to = 0;  // up_to: work of the requests up to the lane's
@@ -622,11 +627,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
     if (per_unit)
       for (int h = threadIdx.x; h < a.c.H; h += kThreads) recs[b * a.c.H + h].u = -1;
   }
-  // ranges: none is empty, so the parts of a unit are those of adjacent blocks
-  const long long sms = n_ctas / kBlocksPerSm, most = W <= sms ? W : max(sms, W / kMinTiles);
-  const int C = int(most < n_ctas ? most : n_ctas);
-  if (c >= C) return;
-  const long long s0 = part_start(c, W, C), e0 = part_start(c + 1, W, C);
+  // ranges: none is empty, so the parts of a unit are those of adjacent groups
+  const int sms = groups / kBlocksPerSm;
+  const long long most = W <= sms ? W : max((long long)sms, W / kMinTiles);
+  const int C = int(most < groups ? most : groups);
+  if (group >= C) return;
+  const long long s0 = part_start(group, W, C), e0 = part_start(group + 1, W, C);
 
   Cursor<SEL, F::kTile> at, ahead;
   long long in_request = s0;
@@ -638,8 +644,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
   }
   at.load(a);
   divide(in_request, at.tiles + kUnitCost, at.h, at.tile);
+  at.h += h0;
   at.pos = s0;
-  if (at.tile >= at.tiles) at.next_unit(a);  // the range begins behind the unit's last tile
+  if (at.tile >= at.tiles) at.next_unit(a, h0);  // the range begins behind the unit's last tile
   if (at.h >= a.c.H || !at.before(a, e0)) return;  // (and may hold no tile)
   ahead = at;
 
@@ -667,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
     have_entry = ahead.before(a, e0);
     if (have_entry) {
       look_up_entry<SEL>(a, ahead, ahead.tile * F::kTile + row, entry);
-      ahead.next(a);
+      ahead.next(a, h0);
     }
     if (i == -1) {  // (the first tiles' copies are on their way)
       K.load_query(at.b, at.h);
@@ -688,11 +695,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
     }
     if (us >= s0 && threadIdx.x == 0) {  // it starts here
       const int u = at.b * a.c.H + at.h;
-      if (slot != nullptr) recs[per_unit ? u : c] = Rec{u, c, range_of(ue - 1, W, C), 0};
+      if (slot != nullptr) recs[per_unit ? u : c] = Rec{u, c, range_of(ue - 1, W, C) - group + 1, 0};
       else if (per_unit) recs[u].u = -1;
     }
     K.finish(at.b, at.h, slot);
-    at.next(a);
+    at.next(a, h0);
     if (at.before(a, e0)) {
       K.load_query(at.b, at.h);
       K.clear();
@@ -704,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
 // unit of record r, `most` of its group's query heads. A head has 16 / heads warps,
 // each with every so many parts, four channels a lane; a part is read once, with a
 // running maximum.
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, int n_ctas, int most) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, int n_ctas, int lanes, int most) {
   __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
   __shared__ float4 s_x[kCombineWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -717,8 +724,10 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, in
   const Rec r = reinterpret_cast<const Rec*>(a.ws)[blockIdx.x];
   // (the bounds hold for every record of the attention kernel; a workspace that something else writes meanwhile
   // must not lead outside of it)
-  if (r.u < 0 || r.u >= a.B * a.c.H || r.first < 0 || r.last < r.first || r.last >= n_ctas) return;
-  const int c = r.first, parts = r.last - c + 1;  // slot 2 c + 1 of block c, slot 2 c' of the following
+  if (r.u < 0 || r.u >= a.B * a.c.H || r.first < 0 || r.first >= n_ctas || r.parts < 1 ||
+      r.parts > n_ctas || r.first + (r.parts - 1) * lanes >= n_ctas)
+    return;
+  const int c = r.first, parts = r.parts;  // slot 2 c + 1 of the first block c, slot 2 c' of the others
   float m = -INFINITY, l = 0.0f;
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (warp < per * heads) {
@@ -732,7 +741,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, in
         ml[e] = make_float2(-INFINITY, 0.0f);
         y[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (i < parts) {
-          const float* p = slots + size_t(i == 0 ? 2 * c + 1 : 2 * (c + i)) * stride;
+          const float* p = slots + size_t(i == 0 ? 2 * c + 1 : 2 * (c + i * lanes)) * stride;
           ml[e] = *reinterpret_cast<const float2*>(p + a.g * kD + 2 * j);
           y[e] = reinterpret_cast<const float4*>(p + j * kD)[lane];
         }
@@ -780,7 +789,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, in
 
 template <int DT, int QT, int NT, bool SEL>
 cudaError_t launch_form(const AttnArgs& a, cudaStream_t stream) {
-  const int smem = int(sizeof(Smem<DT>)), n = blocks_of(a.sms);
+  const int smem = int(sizeof(Smem<DT>)), lanes = a.c.H / a.lane_heads, groups = most_blocks(a.sms) / lanes, n = lanes * groups;
   static std::atomic<uint64_t> configured{0};  // bit: device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -791,7 +800,7 @@ cudaError_t launch_form(const AttnArgs& a, cudaStream_t stream) {
     configured.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
   }
   count_launch();
-  e = launch_dependent(attn_kernel<DT, QT, NT, SEL>, dim3(n), dim3(kThreads), size_t(smem), stream, a);
+  e = launch_dependent(attn_kernel<DT, QT, NT, SEL>, dim3(lanes, groups), dim3(kThreads), size_t(smem), stream, a);
   if (e != cudaSuccess) return e;
   // one head per block where that makes no more blocks than run at once (parts are many then), up to eight else
   const long long units = (long long)a.B * a.c.H;
@@ -800,7 +809,7 @@ cudaError_t launch_form(const AttnArgs& a, cudaStream_t stream) {
   while (most < 8 && (long long)recs * ((a.g + most - 1) / most) > 4LL * a.sms) most *= 2;
   count_launch();
   return launch_dependent(combine_kernel, dim3(recs, (a.g + most - 1) / most), dim3(kCombineThreads), 0, stream, a, n,
-                          most);
+                          lanes, most);
 }
 
 template <int DT, int QT>
@@ -812,10 +821,18 @@ cudaError_t launch_types(const AttnArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t attn_workspace(int B, int H, int Hq, int sms) {
-  return slots_offset(blocks_of(sms)) + 2 * size_t(blocks_of(sms)) * slot_floats(Hq / H) * 4;
+  return slots_offset(most_blocks(sms)) + 2 * size_t(most_blocks(sms)) * slot_floats(Hq / H) * 4;
 }
 
-cudaError_t launch_attn(const AttnArgs& a, cudaStream_t stream) {
+cudaError_t launch_attn(const AttnArgs& args, cudaStream_t stream) {
+  AttnArgs a = args;
+  // as many lanes as leave at most one block in twenty without one (eight lanes against one: 64 x 4000 tokens of
+  // 8-bit keys 94, 102 us; 512 x 1000 of BF16 314, 327 us)
+  const int n = most_blocks(a.sms);
+  int lanes = 1;
+  for (int l = 2; l <= a.c.H && 2 * l <= n; ++l)
+    if (a.c.H % l == 0 && 20 * (n / l * l) >= 19 * n) lanes = l;
+  a.lane_heads = a.c.H / lanes;
   const bool bf = a.q_dtype == kBf16;
   if (a.dtype == kBf16) return launch_types<kBf16, kBf16>(a, stream);
   if (a.dtype == kFp16) return launch_types<kFp16, kFp16>(a, stream);

@@ -877,6 +877,23 @@ def test_attention_many_units(g):
     _compare(b, q, out, lse, 1 / math.sqrt(D))
 
 
+@pytest.mark.parametrize("H,g,cache", [(6, 4, "bf16"), (16, 2, "e4m3"), (64, 1, "fp16"), (160, 1, "bf16"), (7, 16, "bf16")])
+def test_attention_head_counts(H, g, cache):
+    """Head counts that share the device's blocks out in different ways (lanes of one head, of several, or one lane)."""
+    lens = [700, 0, 33, 128, 1, 400]
+    b = Batch(lens, 16, H, cache, seed=H, bounds=False)
+    q = _query(len(lens), H * g, "fp16" if cache == "fp16" else "bf16")
+    out, lse = _attend(b, q)
+    _compare(b, q, out, lse, 1 / math.sqrt(D))
+    sel = torch.full((len(lens), H, 5), -1, dtype=torch.int32, device="cuda")
+    for i, t in enumerate(lens):
+        for h in range(H):
+            n = min(5, -(-t // 16))
+            sel[i, h, :n] = torch.randperm(-(-t // 16), generator=torch.Generator().manual_seed(h))[:n].sort().values.int()
+    out = kvq.kvq_paged_sparse_attn(b.cache, b.table, b.seq, q, sel, lse=lse)
+    _compare(b, q, out, lse, 1 / math.sqrt(D), sel=sel)
+
+
 def test_attention_of_keys_that_are_minus_infinity():
     """Logits of -inf weigh nothing; a request of nothing else has no sum."""
     b = Batch([40, 20], 16, 1, "bf16")
