@@ -586,7 +586,8 @@ typedef struct kvq_paged_rows {
   const float* rope;      /* FP32 [rope_positions][R]: R/2 cosines, then R/2 sines; NULL when R is 0 */
   int32_t rope_positions;
   int32_t interleaved;    /* 0: pairs (d, d + R/2); 1: pairs (2d, 2d + 1) */
-  const int32_t* positions; /* [n_rows] row of `rope` of each row; NULL: the token's place in its request */
+  const int32_t* positions; /* [n_rows] row of `rope` of each row, not read when R is 0; NULL: the token's place in
+                               its request */
 } kvq_paged_rows;
 
 /*

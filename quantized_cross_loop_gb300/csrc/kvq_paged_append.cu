@@ -279,11 +279,12 @@ struct Unit {
   }
 };
 
-// The row of the rotation table of token t, or -1 when it has none.
+// The row of the rotation table of token t, or -1 when it has none (0 without a rotation).
 template <typename U>
 __device__ __forceinline__ int position(const AppendArgs& a, const U& u, int t) {
+  if (a.R == 0) return 0;
   const int pos = a.positions != nullptr ? a.positions[u.row0 + (t - u.start)] : t;
-  return a.R > 0 && (pos < 0 || pos >= a.rope_positions) ? -1 : pos;
+  return pos < 0 || pos >= a.rope_positions ? -1 : pos;
 }
 
 __device__ __forceinline__ void flag_lengths(const AppendArgs& a) {

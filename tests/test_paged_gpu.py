@@ -926,3 +926,18 @@ def test_more_requests_than_lanes_and_threads():
             got = b.k[b.table[i].long()[pos // 8], pos % 8]
             assert torch.equal(got, kn[off[i]:off[i + 1]])
         assert b.cache.error_word() == 0
+
+
+def test_append_without_rotation_has_no_use_for_positions():
+    """Without a rotation table no position can be outside it."""
+    b = Batch([3], 16, 2, "bf16", room=8)
+    kn, vn = (torch.randn((4, 2, D), generator=_gen(s), device="cuda").bfloat16() for s in (1, 2))
+    pos = torch.tensor([-1, -5, 1 << 30, 0], dtype=torch.int32, device="cuda")
+    for off in (None, torch.tensor([0, 4], dtype=torch.int32, device="cuda")):
+        n = 1 if off is None else 4
+        q = torch.randn((n, 4, D), generator=_gen(3), device="cuda").bfloat16()
+        b.k.zero_()
+        got = kvq.kvq_paged_append(b.cache, b.table, b.seq, kn[:n], vn[:n], offsets=off, q=q, positions=pos[:n])
+        assert b.cache.error_word() == 0 and torch.equal(got, q)
+        page = int(b.table[0, 0])
+        assert torch.equal(b.k[page, 3:3 + n], kn[:n]) and torch.equal(b.v[page, 3:3 + n], vn[:n])
