@@ -179,13 +179,13 @@ struct Scorer {
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
-    return t;
+    return t < INFINITY ? t : INFINITY;  // (0 * inf: no bound either, and a NaN would be lost among the others)
   }
 
-  // Page numbers of the chunk from page p0 on, one in each of kPages lanes (0 behind the last).
+  // Page numbers of the chunk from page p0 on, one in each of kPages lanes (behind the last: the last, whose bounds A
+  // has to cover anyway).
   __device__ __forceinline__ static int ids(const SelectArgs& a, int b, int p0, int pages, int lane) {
-    const int p = p0 + (lane & (kPages - 1));
-    return p < pages ? a.table[(long long)b * a.max_pages + p] : 0;
+    return a.table[(long long)b * a.max_pages + min(p0 + (lane & (kPages - 1)), pages - 1)];
   }
 
   // Copies of the bounds of the pages `ids` into the lane's place of a stage. Returns the lanes whose page is outside

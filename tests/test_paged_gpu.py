@@ -941,3 +941,30 @@ def test_append_without_rotation_has_no_use_for_positions():
         assert b.cache.error_word() == 0 and torch.equal(got, q)
         page = int(b.table[0, 0])
         assert torch.equal(b.k[page, 3:3 + n], kn[:n]) and torch.equal(b.v[page, 3:3 + n], vn[:n])
+
+
+@pytest.mark.parametrize("pages", [400, 600])
+def test_selection_of_scores_that_cancel_beside_infinite_bounds(pages):
+    """A page with an infinite bound in a channel where the query is zero (0 * inf: not finite, so it is taken) stands
+    beside pages whose order FP32 loses: theirs is exact all the same."""
+    b = Batch([8 * pages], 8, 1, "bf16")
+    ids = b.table[0, :pages].long()
+    g = _gen(12)
+    q = _query(1, 2)
+    q[..., 7] = 0.0
+    q[..., 3] = q[..., 3].abs()
+    perm = torch.randperm(D // 2, generator=g, device="cuda")
+    q[..., D // 2:] = q[..., perm]
+    b.bounds[ids] = 0.0
+    b.bounds[ids, :, :, 3] = -100.0
+    infinite = [0, 64, 128]
+    near = [p for i in infinite for p in range(i + 1, i + 8)]  # their scores: terms of 2^4 to 2^24, sums below 1
+    x = torch.randn((len(near), 1, 1, D // 2), generator=g, device="cuda")
+    x = (x * 2.0 ** (4 + 20 * torch.rand(x.shape, generator=g, device="cuda"))).bfloat16()
+    b.bounds[ids[near]] = torch.cat([x, -x[..., perm]], 3).expand(-1, 1, 2, -1)
+    for c in (3, 7):
+        b.bounds[ids[near], :, :, c] = 0.0
+        b.bounds[ids[near], :, :, D // 2 + int((perm == c).nonzero())] = 0.0
+    b.bounds[ids[near], :, :, 3] = (torch.randn((len(near), 1, 1), generator=g, device="cuda") / 4).bfloat16()
+    b.bounds[ids[infinite], :, :, 7] = math.inf
+    _check_selection(b, q, 13, 0, 0)
