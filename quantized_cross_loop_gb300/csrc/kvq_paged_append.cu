@@ -13,14 +13,18 @@
 // a pair never crosses lanes and a lane needs four angles; channels behind the
 // rotated ones are shared out eight a lane. All new tokens of a page and head are
 // one unit of work, so the bounds need no atomics.
-// The host chooses by the rows that a request brings on average:
-//   few (up to 8)  a team takes any units (request, page, head) in turn, KV heads (K
-//                  and V together) and query heads alike;
-//   many           one launch for the keys and values, in which a block (pages of more
-//                  than 32 tokens) or a warp has a unit, and one for the queries, in
+//   one row per request  (no offsets) one launch, in which a team takes any units in
+//                  turn, KV heads (K and V together) and query heads alike: 3.1 us for
+//                  64 requests and 8 + 32 heads, 5.5 us by the launches below;
+//   any rows       one launch for the keys and values, and one for the queries, in
 //                  which a team takes four heads of a row. (Both in one launch, some
 //                  blocks for each, was slower: 264 against 223 us for four prompts of
 //                  8192 tokens, the blocks of an SM getting unequal shares.)
+// A unit of up to 32 rows is a warp's, a larger one a block's (4 x 2048 rows, pages of
+// 64: 40 us by blocks, 46 by warps; pages of 16: 50 by blocks, 40 by warps), chosen by
+// each unit's own rows, and the ranges are equal in rows, not units: batches mix
+// prompts with requests of one row (a prompt of 2048 and 499 single rows, pages of 256:
+// 26 us; by equal counts of units, each a team's, 849).
 // Rows in flight and resident warps bound these; staging the rotation table in
 // shared memory for eight heads, and fetching the next rows into registers ahead of
 // the arithmetic, were slower (a table's row is in L1 for the heads that follow).
@@ -31,15 +35,22 @@ namespace kvq {
 namespace paged {
 namespace {
 
-constexpr int kFewThreads = 128;
-constexpr int kFewBlocksPerSm = 5;
+constexpr int kStepThreads = 128;
+constexpr int kStepBlocksPerSm = 5;
 constexpr int kTeam = 16;          // lanes of a row
 constexpr int kManyThreads = 256;
 constexpr int kManyWarps = kManyThreads / 32;
-constexpr int kKeyBlocksPerSm = 3;
+constexpr int kKeyBlocksPerSm = 2;
 constexpr int kQueryBlocksPerSm = 4;
-constexpr int kKeyRows = 2;        // rows a team has in flight
+constexpr int kKeyRows = 4;        // rows a team has in flight
 constexpr int kQueryHeads = 4;     // heads a team has in flight
+constexpr int kWarpRows = 32;      // rows of a unit that a warp takes by itself
+
+// Rows that the beginning and end of a unit count for: pages of up to kWarpRows take
+// a warp much the same time whatever they hold (nine prompts of up to 777 tokens,
+// pages of 16: 24.2 us with 64, 26.9 with 8), larger ones take a block their rows
+// (499 single rows and 2048, pages of 64: 20.7 us with 8, 29 with 32).
+__device__ __forceinline__ int unit_rows(int ps) { return ps <= kWarpRows ? 64 : 8; }
 
 // New rows of request b, or -1 when its start or offsets are outside their range.
 __device__ __forceinline__ int rows_of(const AppendArgs& a, int b, int& start, int& row0) {
@@ -54,13 +65,6 @@ __device__ __forceinline__ int rows_of(const AppendArgs& a, int b, int& start, i
   }
   if (start < 0 || (long long)start + n > (long long)a.max_pages * a.c.ps.d) return -1;
   return n;
-}
-
-// Pages that request b's new rows touch.
-__device__ __forceinline__ int pages_of(const AppendArgs& a, int b) {
-  int start, row0;
-  const int n = rows_of(a, b, start, row0);
-  return n <= 0 ? 0 : a.c.ps.div(start + n - 1) - a.c.ps.div(start) + 1;
 }
 
 // A lane's channels: a .. a + 3 and b .. b + 3.
@@ -295,165 +299,165 @@ __device__ __forceinline__ void flag_lengths(const AppendArgs& a) {
   }
 }
 
+// One row per request, keys, values and queries: a unit is a request's head.
 template <int DT, int IN, bool INTER>
-__global__ void __launch_bounds__(kFewThreads, kFewBlocksPerSm) append_few_kernel(AppendArgs a) {
+__global__ void __launch_bounds__(kStepThreads, kStepBlocksPerSm) append_step_kernel(AppendArgs a) {
   wait_prior_grid();
   allow_dependents();
-  __shared__ Prefix<kFewThreads> S;
   const int heads = a.c.H + (a.q != nullptr ? a.Hq : 0);
-  auto count = [&](int b) { return (long long)pages_of(a, b) * heads; };
-  long long total = (long long)a.B * heads;
-  if (a.offsets != nullptr) {
-    build_prefix<kFewThreads>(S, a.B, count);
-    total = S.pre[kFewThreads];
-  }
+  const long long total = (long long)a.B * heads;
   flag_lengths(a);
-  const int teams = int(gridDim.x) * (kFewThreads / kTeam);  // at most kFewBlocksPerSm x 8 an SM
-  const int me = int(blockIdx.x) * (kFewThreads / kTeam) + threadIdx.x / kTeam;
+  const int teams = int(gridDim.x) * (kStepThreads / kTeam);  // at most kStepBlocksPerSm x 8 an SM
+  const int me = int(blockIdx.x) * (kStepThreads / kTeam) + threadIdx.x / kTeam;
   const long long u0 = part_start(me, total, teams), u1 = part_start(me + 1, total, teams);
   if (u0 >= u1) return;
   const Lane L(a, threadIdx.x % kTeam);
-  long long at = u0;
-  int b, hh, page_i;
-  if (a.offsets == nullptr) {
-    divide(u0, heads, b, hh);
-    page_i = 0;
-  } else {
-    b = find_request<kFewThreads>(S, a.B, count, at);
-    divide(at, heads, page_i, hh);
-  }
-  int start = 0, row0 = 0, n = rows_of(a, b, start, row0), pages = pages_of(a, b);
+  int b, hh;
+  divide(u0, heads, b, hh);
   for (long long w = u0; w < u1; ++w) {
-    while (pages == 0 && a.offsets != nullptr && b < a.B - 1) {  // requests that bring nothing hold no unit
-      ++b;
-      n = rows_of(a, b, start, row0);
-      pages = pages_of(a, b);
-    }
-    if (n > 0) {
+    int start, row0;
+    if (rows_of(a, b, start, row0) > 0) {
       Unit<DT, IN> u;
-      u.open(a, b, a.c.ps.div(start) + page_i, hh, start, row0, n);
-      for (int t = u.first; t < u.last; ++t) {
-        const Raw x = load_raw(u.source(a, t), L);
-        Raw v{};
-        if (!u.is_q) v = load_raw(u.value(a, t), L);
-        const int pos = position(a, u, t);
-        Angles g;
-        if (pos >= 0) g.load<INTER>(a, L, a.rope + (long long)pos * a.R);
-        else flag(a.c, KVQ_PAGED_ERR_POSITION);
-        u.check(a);
-        if (pos < 0 || !u.live) continue;
+      u.open(a, b, a.c.ps.div(start), hh, start, row0, 1);
+      const Raw x = load_raw(u.source(a, start), L);
+      Raw v{};
+      if (!u.is_q) v = load_raw(u.value(a, start), L);
+      const int pos = position(a, u, start);
+      Angles g;
+      if (pos >= 0) g.load<INTER>(a, L, a.rope + (long long)pos * a.R);
+      else flag(a.c, KVQ_PAGED_ERR_POSITION);
+      u.check(a);
+      if (pos >= 0 && u.live) {
         const Wide y = rotate<IN, INTER>(L, g, x);
-        if (u.is_q) u.put_query(L, u.query_out(a, t), y);
-        else u.put(L, a.c.k + u.place(a, t), a.c.v + u.place(a, t), y, v);
+        if (u.is_q) {
+          u.put_query(L, u.query_out(a, start), y);
+        } else {
+          const long long place = u.place(a, start);
+          u.put(L, a.c.k + place, a.c.v + place, y, v);
+          u.close(a, L);
+        }
       }
-      u.close(a, L);
     }
     if (++hh == heads) {
       hh = 0;
-      if (a.offsets == nullptr || ++page_i == pages) {
-        page_i = 0;
-        if (++b < a.B) {
-          n = rows_of(a, b, start, row0);
-          pages = pages_of(a, b);
-        }
-      }
+      ++b;
     }
   }
 }
 
-// Keys and values: WARPS warps have a unit (1 or all of the block).
-template <int DT, int IN, bool INTER, int WARPS>
+// Keys and values of any rows: a block takes the units that start in its range of the
+// work, a row counting one and a unit unit_rows() more. Its warps take the units of up
+// to kWarpRows rows in turn, all of them together the others.
+template <int DT, int IN, bool INTER>
 __global__ void __launch_bounds__(kManyThreads, kKeyBlocksPerSm) append_keys_kernel(AppendArgs a) {
-  constexpr int kTeams = 2 * WARPS;  // of a unit
   __shared__ Prefix<kManyThreads> S;
-  __shared__ uint32_t s_bound[WARPS > 1 ? kManyWarps : 1][8][kTeam];
+  __shared__ uint32_t s_bound[kManyWarps][8][kTeam];
   wait_prior_grid();
   allow_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x % kTeam;
-  const int team = WARPS > 1 ? threadIdx.x / kTeam : (threadIdx.x / kTeam) & 1;
-  auto count = [&](int b) { return (long long)pages_of(a, b) * a.c.H; };
-  build_prefix<kManyThreads>(S, a.B, count);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x % kTeam, ps = int(a.c.ps.d), extra = unit_rows(ps);
+  auto work_of = [&](int b) {
+    int start, row0;
+    const int n = rows_of(a, b, start, row0);
+    return n <= 0 ? 0LL : a.c.H * (n + (long long)extra * (a.c.ps.div(start + n - 1) - a.c.ps.div(start) + 1));
+  };
+  build_prefix<kManyThreads>(S, a.B, work_of);
   flag_lengths(a);
   const long long total = S.pre[kManyThreads];
-  const int groups = int(gridDim.x) * (kManyWarps / WARPS), me = int(blockIdx.x) * (kManyWarps / WARPS) + (WARPS > 1 ? 0 : warp);
-  const long long u0 = part_start(me, total, groups), u1 = part_start(me + 1, total, groups);
-  if (u0 >= u1) return;
+  const bool small = ps <= kWarpRows;  // no unit is for more than a warp: each warp has a range of its own
+  const int ranges = small ? int(gridDim.x) * kManyWarps : int(gridDim.x);
+  const int range = small ? int(blockIdx.x) * kManyWarps + warp : int(blockIdx.x);
+  const long long s0 = part_start(range, total, ranges), s1 = part_start(range + 1, total, ranges);
+  if (s0 >= s1) return;
   const Lane L(a, lane);
-  long long at = u0;
-  int b = find_request<kManyThreads>(S, a.B, count, at);
-  int page_i, h;
-  divide(at, a.c.H, page_i, h);
-  int start = 0, row0 = 0, n = rows_of(a, b, start, row0), pages = pages_of(a, b);
-  for (long long w = u0; w < u1; ++w) {
-    while (pages == 0 && b < a.B - 1) {  // requests that bring nothing hold no unit
-      ++b;
-      n = rows_of(a, b, start, row0);
-      pages = pages_of(a, b);
+  long long at = s0;
+  int b = find_request<kManyThreads>(S, a.B, work_of, at);
+  int start, row0, n, p, pages;  // the request's rows; the unit's page, and the one behind the last
+  auto load = [&] {
+    n = rows_of(a, b, start, row0);
+    p = a.c.ps.div(start);
+    pages = n <= 0 ? 0 : a.c.ps.div(start + n - 1) + 1;
+  };
+  auto rows = [&] { return min(start + n, (p + 1) * ps) - max(start, p * ps); };  // on page p
+  load();
+  const long long first = (long long)a.c.H * (min(n, (p + 1) * ps - start) + extra);  // work of the first page
+  if (at >= first) {
+    int skip, rest;
+    divide(at - first, a.c.H * (ps + extra), skip, rest);
+    p += 1 + skip;
+    at = rest;
+  }
+  int r = rows(), h = (int(at) + r + extra - 1) / (r + extra);  // the first unit that starts here or behind
+  long long pos = s0 - at + (long long)h * (r + extra);
+  int turn = 0;  // the warp that takes the next unit of its own
+  for (;; ++h) {
+    if (h == a.c.H) {
+      h = 0;
+      if (++p >= pages) {
+        do {
+          if (++b == a.B) return;
+          load();
+        } while (n <= 0);
+      }
+      r = rows();
     }
+    if (pos >= s1) return;
+    pos += r + extra;
+    const bool all = r > kWarpRows;
+    if (!all && !small) {
+      const bool mine = turn == warp;
+      turn = (turn + 1) % kManyWarps;
+      if (!mine) continue;
+    }
+    const int team = all ? threadIdx.x / kTeam : (threadIdx.x / kTeam) & 1, step = all ? kManyThreads / kTeam : 2;
     Unit<DT, IN> u;
-    u.open(a, b, a.c.ps.div(start) + page_i, h, start, row0, max(n, 0));
+    u.open(a, b, p, h, start, row0, n);
     u.check(a);
-    if (u.live) {
-      for (int t0 = u.first + team; t0 < u.last; t0 += kTeams * kKeyRows) {
-        Raw x[kKeyRows], y[kKeyRows];
-        Angles g[kKeyRows];
-        bool ok[kKeyRows];
+    for (int t0 = u.live ? u.first + team : u.last; t0 < u.last; t0 += step * kKeyRows) {
+      Raw x[kKeyRows], y[kKeyRows];
+      Angles g[kKeyRows];
+      bool ok[kKeyRows];
 #pragma unroll
-        for (int i = 0; i < kKeyRows; ++i) {
-          const int t = t0 + i * kTeams;
-          ok[i] = t < u.last;
-          if (!ok[i]) continue;
-          x[i] = load_raw(u.source(a, t), L);
-          y[i] = load_raw(u.value(a, t), L);
-          const int pos = position(a, u, t);
-          ok[i] = pos >= 0;
-          if (ok[i]) g[i].load<INTER>(a, L, a.rope + (long long)pos * a.R);
-          else flag(a.c, KVQ_PAGED_ERR_POSITION);
-        }
+      for (int i = 0; i < kKeyRows; ++i) {
+        const int t = t0 + i * step;
+        ok[i] = t < u.last;
+        if (!ok[i]) continue;
+        x[i] = load_raw(u.source(a, t), L);
+        y[i] = load_raw(u.value(a, t), L);
+        const int row = position(a, u, t);
+        ok[i] = row >= 0;
+        if (ok[i]) g[i].load<INTER>(a, L, a.rope + (long long)row * a.R);
+        else flag(a.c, KVQ_PAGED_ERR_POSITION);
+      }
 #pragma unroll
-        for (int i = 0; i < kKeyRows; ++i) {
-          if (!ok[i]) continue;
-          const long long place = u.place(a, t0 + i * kTeams);
-          u.put(L, a.c.k + place, a.c.v + place, rotate<IN, INTER>(L, g[i], x[i]), y[i]);
-        }
+      for (int i = 0; i < kKeyRows; ++i) {
+        if (!ok[i]) continue;
+        const long long place = u.place(a, t0 + i * step);
+        u.put(L, a.c.k + place, a.c.v + place, rotate<IN, INTER>(L, g[i], x[i]), y[i]);
       }
     }
-    if (a.c.bounds != nullptr) {
-      __syncwarp();
-      u.join();
-      if constexpr (WARPS > 1) {
-        if ((threadIdx.x & 31) < kTeam) {
+    if (a.c.bounds == nullptr) continue;
+    __syncwarp();
+    u.join();
+    if (all) {
+      if ((threadIdx.x & 31) < kTeam) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s_bound[warp][i][lane] = u.lo[i];
+          s_bound[warp][4 + i][lane] = u.hi[i];
+        }
+      }
+      u.any = __syncthreads_or(u.any);
+      if (threadIdx.x < kTeam) {
+        for (int v = 1; v < kManyWarps; ++v)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            s_bound[warp][i][lane] = u.lo[i];
-            s_bound[warp][4 + i][lane] = u.hi[i];
+            u.lo[i] = smaller<DT>(u.lo[i], s_bound[v][i][lane]);
+            u.hi[i] = larger<DT>(u.hi[i], s_bound[v][4 + i][lane]);
           }
-        }
-        u.any = __syncthreads_or(u.any);
-        if (threadIdx.x < kTeam) {
-          for (int v = 1; v < WARPS; ++v)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              u.lo[i] = smaller<DT>(u.lo[i], s_bound[v][i][lane]);
-              u.hi[i] = larger<DT>(u.hi[i], s_bound[v][4 + i][lane]);
-            }
-          u.close(a, L);
-        }
-        __syncthreads();  // s_bound is free again
-      } else if (team == 0) {
-        u.close(a, L);
       }
     }
-    if (++h == a.c.H) {
-      h = 0;
-      if (++page_i == pages) {
-        page_i = 0;
-        if (++b < a.B) {
-          n = rows_of(a, b, start, row0);
-          pages = pages_of(a, b);
-        }
-      }
-    }
+    if (team == 0) u.close(a, L);
+    if (all) __syncthreads();  // s_bound is free again
   }
 }
 
@@ -514,7 +518,8 @@ __device__ __forceinline__ void append_queries(const AppendArgs& a) {
 }
 
 // Launched behind the keys' kernel, whose results it does not need: it starts once
-// that one's blocks all run (which they do once what came before them is complete),
+// that one's blocks have all waited for what came before them (whose results are then
+// in memory),
 // and waits for it at its end, so that whoever waits for this kernel waits for both.
 template <int IN, bool INTER>
 __global__ void __launch_bounds__(kManyThreads, kQueryBlocksPerSm) append_queries_kernel(AppendArgs a) {
@@ -525,21 +530,21 @@ __global__ void __launch_bounds__(kManyThreads, kQueryBlocksPerSm) append_querie
 
 template <int DT, int IN, bool INTER>
 cudaError_t launch_form(const AppendArgs& a, int sms, cudaStream_t stream) {
-  const long long pages = a.offsets == nullptr ? a.B : a.n_rows / a.c.ps.d + 2 * (long long)a.B;  // at most
   const int Hq = a.q != nullptr ? a.Hq : 0;
   count_launch();
-  if (a.offsets == nullptr || a.n_rows <= 8LL * a.B) {
-    const long long need = (pages * (a.c.H + Hq) * kTeam + kFewThreads - 1) / kFewThreads, fit = (long long)kFewBlocksPerSm * sms;
-    return launch_dependent(append_few_kernel<DT, IN, INTER>, dim3(int(need < fit ? need : fit)), dim3(kFewThreads), 0,
+  if (a.offsets == nullptr) {
+    const long long need = ((long long)a.B * (a.c.H + Hq) * kTeam + kStepThreads - 1) / kStepThreads;
+    const long long fit = (long long)kStepBlocksPerSm * sms;
+    return launch_dependent(append_step_kernel<DT, IN, INTER>, dim3(int(need < fit ? need : fit)), dim3(kStepThreads), 0,
                             stream, a);
   }
-  const long long units = pages * a.c.H, fit = (long long)kKeyBlocksPerSm * sms;
-  const bool whole = a.c.ps.d > 32;  // a block per unit, else a warp
-  const long long need = whole ? units : (units + kManyWarps - 1) / kManyWarps;
-  const dim3 grid(int(need < fit ? need : fit));
-  const cudaError_t e =
-      whole ? launch_dependent(append_keys_kernel<DT, IN, INTER, kManyWarps>, grid, dim3(kManyThreads), 0, stream, a)
-            : launch_dependent(append_keys_kernel<DT, IN, INTER, 1>, grid, dim3(kManyThreads), 0, stream, a);
+  // blocks: eight units each, or (pages of more rows than a warp takes) one unit of 32 rows
+  const long long units = (a.n_rows / a.c.ps.d + 2 * (long long)a.B) * a.c.H;  // at most
+  const long long by_units = (units + kManyWarps - 1) / kManyWarps;
+  const long long by_rows = a.c.ps.d > kWarpRows ? (long long)a.n_rows * a.c.H / 32 : 0;
+  const long long need = by_units > by_rows ? by_units : by_rows, fit = (long long)kKeyBlocksPerSm * sms;
+  const cudaError_t e = launch_dependent(append_keys_kernel<DT, IN, INTER>, dim3(int(need < fit ? need : fit)),
+                                         dim3(kManyThreads), 0, stream, a);
   if (e != cudaSuccess || Hq == 0) return e;
   count_launch();
   const long long teams = a.n_rows * (long long)((Hq + kQueryHeads - 1) / kQueryHeads), per = kManyThreads / kTeam;

@@ -968,3 +968,14 @@ def test_selection_of_scores_that_cancel_beside_infinite_bounds(pages):
     b.bounds[ids[near], :, :, 3] = (torch.randn((len(near), 1, 1), generator=g, device="cuda") / 4).bfloat16()
     b.bounds[ids[infinite], :, :, 7] = math.inf
     _check_selection(b, q, 13, 0, 0)
+
+
+@pytest.mark.parametrize("cache,inter,layout", [("bf16", False, "token"), ("e4m3", True, "head")])
+@pytest.mark.parametrize("ps", [8, 32, 33, 64, 256, 1024])
+def test_append_of_prompts_among_single_rows(cache, inter, layout, ps):
+    """Units of every size side by side: pages that a warp takes, pages that a block takes, requests without rows."""
+    rng = random.Random(ps)
+    lens = [rng.choice([0, ps - 1, ps, rng.randint(0, 90)]) for _ in range(45)]
+    rows = [rng.choice([0, 1, 1, 1, 2, 31, 32, 33]) for _ in range(45)]
+    rows[7], rows[8], rows[30], rows[44] = 600, 1, 300, 0
+    test_append(cache, "bf16", lens, rows, ps, 3, 2, 128, inter, layout)
