@@ -40,7 +40,7 @@ constexpr int kStepBlocksPerSm = 5;
 constexpr int kTeam = 16;          // lanes of a row
 constexpr int kManyThreads = 256;
 constexpr int kManyWarps = kManyThreads / 32;
-constexpr int kKeyBlocksPerSm = 2;
+constexpr int kKeyBlocksPerSm = 2;    // (as many as an SM's registers hold)
 constexpr int kQueryBlocksPerSm = 4;
 constexpr int kKeyRows = 4;        // rows a team has in flight
 constexpr int kQueryHeads = 4;     // heads a team has in flight
@@ -535,22 +535,27 @@ cudaError_t launch_form(const AppendArgs& a, int sms, cudaStream_t stream) {
   if (a.offsets == nullptr) {
     const long long need = ((long long)a.B * (a.c.H + Hq) * kTeam + kStepThreads - 1) / kStepThreads;
     const long long fit = (long long)kStepBlocksPerSm * sms;
-    return launch_dependent(append_step_kernel<DT, IN, INTER>, dim3(int(need < fit ? need : fit)), dim3(kStepThreads), 0,
-                            stream, a);
+    return launch_dependent(append_step_kernel<DT, IN, INTER>, dim3(int(need < fit ? need : fit)),
+                            dim3(kStepThreads), 0, stream, a);
   }
-  // blocks: eight units each, or (pages of more rows than a warp takes) one unit of 32 rows
+  // More than two query heads per KV head: half as many blocks of each kernel, so that both fit on an SM and run side
+  // by side; else the queries' blocks follow the keys' (4 x 2048 rows, pages of 64, side by side and one after the
+  // other: 8 + 32 heads 38.7, 40.1 us, 8 + 24 35.3, 35.0, 16 + 32 59.2, 52.4, 32 + 32 103, 80; nine prompts of up to
+  // 613 rows into 8-bit pages of 16, 8 + 32 heads 21.1, 24.2).
+  const int part = Hq > 2 * a.c.H ? 2 : 1;
+  // the keys' blocks: eight units each, or (pages of more rows than a warp takes) one unit of 32 rows
   const long long units = (a.n_rows / a.c.ps.d + 2 * (long long)a.B) * a.c.H;  // at most
   const long long by_units = (units + kManyWarps - 1) / kManyWarps;
   const long long by_rows = a.c.ps.d > kWarpRows ? (long long)a.n_rows * a.c.H / 32 : 0;
-  const long long need = by_units > by_rows ? by_units : by_rows, fit = (long long)kKeyBlocksPerSm * sms;
+  const long long need = by_units > by_rows ? by_units : by_rows, fit = (long long)kKeyBlocksPerSm * sms / part;
   const cudaError_t e = launch_dependent(append_keys_kernel<DT, IN, INTER>, dim3(int(need < fit ? need : fit)),
                                          dim3(kManyThreads), 0, stream, a);
   if (e != cudaSuccess || Hq == 0) return e;
   count_launch();
   const long long teams = a.n_rows * (long long)((Hq + kQueryHeads - 1) / kQueryHeads), per = kManyThreads / kTeam;
-  const long long blocks = (teams + per - 1) / per, most = (long long)kQueryBlocksPerSm * sms;
-  return launch_dependent(append_queries_kernel<IN, INTER>, dim3(int(blocks < most ? blocks : most)), dim3(kManyThreads),
-                          0, stream, a);
+  const long long blocks = (teams + per - 1) / per, most = (long long)kQueryBlocksPerSm * sms / part;
+  return launch_dependent(append_queries_kernel<IN, INTER>, dim3(int(blocks < most ? blocks : most)),
+                          dim3(kManyThreads), 0, stream, a);
 }
 
 template <int DT, int IN>
