@@ -513,11 +513,12 @@ kvq_status kvq_decode_attn_packed_noalloc(const kvq_request* reqs, int n_request
  *          p * page_stride + s * token_stride + h * head_stride + d, in
  *          elements; the strides are multiples of 16 bytes and describe places
  *          that do not overlap (token-major, head-major, K and V interleaved
- *          in one allocation ...); k and v 16-byte aligned, same strides.
+ *          in one allocation ...), the pool at most 2^46 elements; k and v
+ *          16-byte aligned, same strides.
  *   key_bounds  [n_pages][n_heads][2][head_dim], contiguous: the smallest (0)
  *          and largest (1) stored key of a page per head and channel, kept by
  *          kvq_paged_append; NULL: none are kept (kvq_paged_select needs them).
- *   k_scale, v_scale  FP32 [n_heads], positive, E4M3 only (NULL: 1).
+ *   k_scale, v_scale  FP32 [n_heads], positive normal numbers, E4M3 only (NULL: 1).
  *   error  DEVICE int32 or NULL: KVQ_PAGED_ERR_* bits are OR-ed in by the
  *          kernels and never cleared; the caller zeroes it.
  *
@@ -597,7 +598,9 @@ typedef struct kvq_paged_rows {
  * rounded to nearest, saturated at 448); the page's key bounds take in the new
  * keys, and start afresh on a page whose first place is written. Queries are
  * rotated the same way into q_out. start is not changed.
- * No two requests may append to the same page in one call. Not written are the
+ * No page may take rows of two requests, or from two table entries, in one call.
+ * After a smaller start than before (tokens taken back) a page's bounds stay as
+ * wide as they were until its first place is written again. Not written are the
  * rows of a refused request (bad start or offsets), rows whose page is outside
  * the pool and rows whose position is outside the rotation table; their queries
  * are not written either.
@@ -617,8 +620,11 @@ size_t kvq_paged_workspace_bytes(int n_requests, int n_heads, int n_q_heads, int
  *   out   FP32 [n_requests][Hq][D], 16-byte aligned.
  *   lse   FP32 [n_requests][Hq] or NULL: ln of the sum of exp(scale q.k), by which
  *         results over disjoint tokens can be joined.
- * Query head hq reads KV head hq / (Hq/H); softmax and sums are FP32. A request
- * without tokens gets out 0 and lse -inf, a refused one NaN in both.
+ * Query head hq reads KV head hq / (Hq/H); softmax and sums are FP32, so that
+ * q.k, and |v| summed over the tokens, have to lie within FP32's range; a value
+ * that is not finite among those attended to makes its channel NaN or infinite
+ * (what lies in other places of a page is not read). A request without tokens, and one whose keys all weigh
+ * nothing (q.k = -inf), gets out 0 and lse -inf, a refused one NaN in both.
  */
 kvq_status kvq_paged_decode_attn(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages,
                                  int n_requests, const int32_t* seq_lens, const void* q, int q_dtype,
@@ -632,8 +638,9 @@ kvq_status kvq_paged_decode_attn(const kvq_paged_cache* cache, const int32_t* pa
  *     sum_j sum_d (q_jd < 0 ? q_jd lo_d : q_jd hi_d).
  * The first n_first and the last n_last pages are always taken (n_first + n_last
  * <= n_select), the others by score, equal scores by page number; a page whose
- * score is not finite counts as the largest. The order is that of the exact
- * scores: values too near the border for FP32 are computed in FP64.
+ * score is not finite in FP32 (a NaN or infinite bound, an overflow) comes before
+ * all others. The order is that of the exact scores: values too near the border
+ * for FP32 are computed in FP64.
  *   sel   int32 [n_requests][n_heads][n_select]: page numbers within the request
  *         (not the pool), ascending, -1 behind the request's last; a refused
  *         request gets -1 throughout. A page outside the pool counts as the
@@ -646,7 +653,8 @@ kvq_status kvq_paged_select(const kvq_paged_cache* cache, const int32_t* page_ta
 
 /*
  * kvq_paged_decode_attn over the tokens of the selected pages only; sel as
- * kvq_paged_select writes it (ascending, -1 behind the last). A selection of one
+ * kvq_paged_select writes it (ascending, -1 behind the last; entries beyond the
+ * number of the request's pages are not looked at). A selection of one
  * KV head that is not of that form gives NaN to that head's queries and sets
  * KVQ_PAGED_ERR_SELECTION; one that holds no page gives out 0 and lse -inf.
  */

@@ -75,7 +75,7 @@ kvq_status check_cache(const kvq_paged_cache* c, int need, paged::View* v) {
         if (dim[j].first < dim[i].first) std::swap(dim[i], dim[j]);
     for (const auto& d : dim) {
       if (d.second == 1) continue;
-      if (d.first < span || d.first > (int64_t(1) << 40))
+      if (d.first < span || d.first > (int64_t(1) << 46) / d.second)
         return fail(KVQ_ERR_BAD_ARG, "cache: strides page %lld token %lld head %lld overlap or are out of range",
                     (long long)c->page_stride, (long long)c->token_stride, (long long)c->head_stride);
       if (d.first * es % 16 != 0) return fail(KVQ_ERR_MISALIGNED, "cache: strides must be multiples of 16 bytes");

@@ -124,6 +124,14 @@ def test_head_major_and_interleaved_strides_are_accepted(L):
     assert _attn(L, one, Hq=4, out=None) == BAD and b"out" in L.kvq_last_error()
 
 
+def test_pools_beyond_any_memory_are_refused(L):
+    """A span whose product would wrap around 64 bits, or that no address reaches, is no layout."""
+    for pages, stride in ((1 << 20, 1 << 39), (2**31 - 1, 1 << 40), (2**31 - 1, 1 << 33), (10, 1 << 62)):
+        assert _attn(L, _cache(L, n_pages=pages, page_stride=stride), out=None) == BAD
+        assert b"strides" in L.kvq_last_error()
+    assert _attn(L, _cache(L, n_pages=1 << 20, page_stride=1 << 26), out=None) == BAD and b"out is" in L.kvq_last_error()
+
+
 def test_sparse_and_selection_refusals(L):
     c = _cache(L)
 
