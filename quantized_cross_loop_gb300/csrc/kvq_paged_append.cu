@@ -47,7 +47,7 @@ constexpr int kQueryHeads = 4;     // heads a team has in flight
 constexpr int kWarpRows = 32;      // rows of a unit that a warp takes by itself
 
 // Rows that the beginning and end of a unit count for: pages of up to kWarpRows take
-// a warp much the same time whatever they hold (nine prompts of up to 777 tokens,
+// a warp much the same time whatever they hold (nine prompts of up to 613 rows, 8-bit
 // pages of 16: 24.2 us with 64, 26.9 with 8), larger ones take a block their rows
 // (499 single rows and 2048, pages of 64: 20.7 us with 8, 29 with 32).
 __device__ __forceinline__ int unit_rows(int ps) { return ps <= kWarpRows ? 64 : 8; }

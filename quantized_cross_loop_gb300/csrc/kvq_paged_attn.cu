@@ -815,7 +815,10 @@ cudaError_t launch_form(const AttnArgs& a, cudaStream_t stream) {
 
 template <int DT, int QT>
 cudaError_t launch_types(const AttnArgs& a, cudaStream_t stream) {
-  if (a.sel != nullptr) return a.g <= 8 ? launch_form<DT, QT, 1, true>(a, stream) : launch_form<DT, QT, 2, true>(a, stream);
+  // up to eight heads fill half of a product's rows: the form for 16 would do, but takes 7.9 us instead of 7.1 (one
+  // request of 256 tokens), 324 instead of 312 (512 x 1000) and 119 instead of 92 (64 ragged ones of 8-bit keys)
+  if (a.sel != nullptr)
+    return a.g <= 8 ? launch_form<DT, QT, 1, true>(a, stream) : launch_form<DT, QT, 2, true>(a, stream);
   return a.g <= 8 ? launch_form<DT, QT, 1, false>(a, stream) : launch_form<DT, QT, 2, false>(a, stream);
 }
 

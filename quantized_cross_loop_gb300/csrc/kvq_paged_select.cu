@@ -68,8 +68,8 @@ __host__ __device__ constexpr size_t key_stride(int max_pages) { return (size_t(
 __host__ __device__ inline int chunks_of(int pages, int of) { return (pages + of - 1) / of; }
 inline Workspace workspace_of(char* ws, int units, int max_pages) {
   Workspace w;
-  w.keys = reinterpret_cast<uint32_t*>(ws + 16);
-  char* p = ws + 16 + size_t(units) * key_stride(max_pages) * 4;
+  w.keys = reinterpret_cast<uint32_t*>(ws);
+  char* p = ws + size_t(units) * key_stride(max_pages) * 4;
   w.largest = reinterpret_cast<float*>(p);
   w.exact = reinterpret_cast<uint64_t*>(p + up16(size_t(units) * chunks_of(max_pages, kChunk) * 4));
   return w;
@@ -786,7 +786,7 @@ cudaError_t launch_types(const SelectArgs& a, cudaStream_t stream) {
 
 size_t select_workspace(int B, int H, int max_pages) {
   const size_t units = size_t(B) * H;
-  return 16 + units * key_stride(max_pages) * 4 + up16(units * chunks_of(max_pages, kChunk) * 4) + up16(units * max_pages * 8);
+  return units * key_stride(max_pages) * 4 + up16(units * chunks_of(max_pages, kChunk) * 4) + up16(units * max_pages * 8);
 }
 
 cudaError_t launch_select(const SelectArgs& a, cudaStream_t stream) {
