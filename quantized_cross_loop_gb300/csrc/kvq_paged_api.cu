@@ -269,7 +269,8 @@ kvq_status kvq_paged_append(const kvq_paged_cache* cache, const int32_t* page_ta
 
 size_t kvq_paged_workspace_bytes(int n_requests, int n_heads, int n_q_heads, int max_pages) {
   const int sms = current_sms();
-  if (n_requests < 0 || n_heads < 1 || n_q_heads < n_heads || n_q_heads % n_heads != 0 || max_pages < 0 || sms == 0)
+  if (n_requests < 0 || n_heads < 1 || n_heads > 1024 || n_q_heads < n_heads || n_q_heads % n_heads != 0 ||
+      n_q_heads / n_heads > KVQ_PAGED_MAX_G || max_pages < 0 || sms == 0)
     return 0;
   const size_t a = paged::attn_workspace(n_requests, n_heads, n_q_heads, sms);
   const size_t b = paged::select_workspace(n_requests, n_heads, max_pages);

@@ -68,7 +68,9 @@ __host__ __device__ constexpr size_t slot_floats(int g) { return size_t(g) * kD 
 template <int DT>
 struct Form {
   static constexpr int kRow = kD * elem_bytes<DT>();       // bytes of a row
-  static constexpr int kSteps = DT == kE4m3 ? 2 : 1;       // blocks of 16 tokens in a warp's slice of a tile: 8 KB
+  // blocks of 16 tokens in a warp's slice of a tile: 8 KB (E4M3 with one: 106 us instead of 89 for 64 ragged requests,
+  // by three blocks an SM too: the softmax's own instructions come twice as often)
+  static constexpr int kSteps = DT == kE4m3 ? 2 : 1;
   static constexpr int kRows = 16 * kSteps;
   static constexpr int kTile = kRows * kWarps;             // tokens per tile
   static constexpr int kStages = 3;                        // 96 KB of ring per block

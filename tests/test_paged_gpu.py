@@ -979,3 +979,10 @@ def test_append_of_prompts_among_single_rows(cache, inter, layout, ps):
     rows = [rng.choice([0, 1, 1, 1, 2, 31, 32, 33]) for _ in range(45)]
     rows[7], rows[8], rows[30], rows[44] = 600, 1, 300, 0
     test_append(cache, "bf16", lens, rows, ps, 3, 2, 128, inter, layout)
+
+
+def test_workspace_bytes_of_sizes_that_no_call_takes():
+    b = Batch([64, 3], 16, 2, "bf16")
+    assert b.cache.workspace_bytes(2, 32, 4) > 0
+    for n, hq, width in ((-1, 8, 4), (2, 7, 4), (2, 1, 4), (2, 34, 4), (2, 8, -1)):
+        assert b.cache.workspace_bytes(n, hq, width) == 0
