@@ -397,6 +397,24 @@ __device__ __forceinline__ bool emit(const SelectArgs& a, Pick& S, int pages, in
     if (lane == 0) S.words[w] = m;
   }
   __syncthreads();
+  if (words <= 32) {  // every warp sums the words' counts by itself and writes the pages of the words it made
+    const int own = lane < words ? __popc(S.words[lane]) : 0;
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const int all = __shfl_sync(0xFFFFFFFFu, sum, 31), first = out != nullptr ? *out : 0;
+    if (out == nullptr && all != a.n_select) return false;
+    for (int w = tid / 32; w < words; w += THREADS / 32) {
+      const uint32_t m = S.words[w];
+      const int i = first + __shfl_sync(0xFFFFFFFFu, sum - own, w) + __popc(m & ((1u << lane) - 1u));
+      if (((m >> lane) & 1) && i < a.n_select) sel[i] = base + 32 * w + lane;
+    }
+    if (out != nullptr) *out += all;
+    return true;
+  }
   constexpr int kOwn = (kWords + THREADS - 1) / THREADS;  // words of a thread
   uint32_t m[kOwn];
   int n = 0, before;
@@ -443,6 +461,34 @@ __device__ __forceinline__ uint32_t warp_ranked(const uint32_t* keys, int n, int
   return __reduce_min_sync(0xFFFFFFFFu, lane < n && more < left ? x : 0xFFFFFFFFu);
 }
 
+// The same of up to kFew keys, by a warp, bit by bit. As many pages need no histogram (the k-th largest of 256 keys
+// this way and the words of emit by each warp: 8 units 6.8 us instead of 7.4, 256 units 12.1 instead of 12.9).
+__device__ __forceinline__ uint32_t bitwise_ranked(const uint32_t* keys, int n, int left) {
+  constexpr int kOwn = kFew / 32;
+  const int lane = threadIdx.x & 31;
+  uint32_t x[kOwn], lo = 0xFFFFFFFFu, hi = 0u;
+#pragma unroll
+  for (int e = 0; e < kOwn; ++e) {
+    const bool in = 32 * e + lane < n;
+    x[e] = in ? keys[32 * e + lane] : 0u;
+    if (in) lo = min(lo, x[e]);
+    hi = max(hi, x[e]);
+  }
+  lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+  hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+#pragma unroll
+  for (int e = 0; e < kOwn; ++e) x[e] = max(x[e], lo) - lo;
+  uint32_t t = 0;  // the largest with `left` keys that are no smaller
+  for (int bit = 31 - __clz(hi - lo); bit >= 0; --bit) {
+    const uint32_t y = t | (1u << bit);
+    int more = 0;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) more += x[e] >= y;
+    if (__reduce_add_sync(0xFFFFFFFFu, more) >= left) t = y;
+  }
+  return lo + t;
+}
+
 // Picks a unit's pages from its keys (`keys` is scratch: written, too); the block's threads together.
 // lo and hi are the range of some of the keys that may be chosen, over the block of all.
 template <int DT, int QT, int THREADS>
@@ -457,67 +503,77 @@ __device__ __forceinline__ void pick(const SelectArgs& a, Pick& S, int b, int h,
     for (int p = f0 + tid; p < f1; p += THREADS) keys[p] = kLastKey;  // none but those
     __syncthreads();
   } else {
-    lo = __reduce_min_sync(0xFFFFFFFFu, lo);
-    hi = __reduce_max_sync(0xFFFFFFFFu, hi);
-    if (lane == 0) {
-      S.warp_lo[warp] = lo;
-      S.warp_hi[warp] = hi;
-    }
-    for (int i = tid; i < kBins; i += THREADS) S.hist[i] = 0;
-    if (tid == 0) S.n_list = 0;
-    __syncthreads();  // (also: the keys are there)
-    lo = __reduce_min_sync(0xFFFFFFFFu, lane < THREADS / 32 ? S.warp_lo[lane] : 0xFFFFFFFFu);
-    hi = __reduce_max_sync(0xFFFFFFFFu, lane < THREADS / 32 ? S.warp_hi[lane] : 0u);
-    // the k-th largest key
-    int left = k;
-    uint32_t t = lo;
-    while (lo < hi) {
-      const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
-#pragma unroll 4
-      for (int p = f0 + tid; p < f1; p += THREADS) {
-        const uint32_t x = keys[p];
-        if (x >= lo && x <= hi) atomicAdd(&S.hist[(x - lo) >> shift], 1);
+    uint32_t t;
+    if (f1 - f0 <= kFew) {
+      if (warp == 0) {
+        t = bitwise_ranked(keys + f0, f1 - f0, k);
+        if (lane == 0) S.t = t;
       }
       __syncthreads();
-      {  // bins from the top: thread i holds the kOwn bins below kBins - kOwn i
-        constexpr int kOwn = kBins / THREADS;
-        int own[kOwn], n = 0, before;
-#pragma unroll
-        for (int e = 0; e < kOwn; ++e) {
-          own[e] = S.hist[kBins - 1 - kOwn * tid - e];
-          n += own[e];
-        }
-        block_prefix<THREADS>(S, n, before);
-#pragma unroll
-        for (int e = 0; e < kOwn; ++e) {
-          if (before < left && left <= before + own[e]) {  // one thread, one bin
-            S.bin = kBins - 1 - kOwn * tid - e;
-            S.above = before;
-            S.members = own[e];
-          }
-          before += own[e];
-        }
-        __syncthreads();
+      t = S.t;
+    } else {
+      lo = __reduce_min_sync(0xFFFFFFFFu, lo);
+      hi = __reduce_max_sync(0xFFFFFFFFu, hi);
+      if (lane == 0) {
+        S.warp_lo[warp] = lo;
+        S.warp_hi[warp] = hi;
       }
-      left -= S.above;
-      lo += uint32_t(S.bin) << shift;
-      if (shift == 0) hi = lo;
-      else hi = min(hi, lo + ((1u << shift) - 1u));
+      for (int i = tid; i < kBins; i += THREADS) S.hist[i] = 0;
+      if (tid == 0) S.n_list = 0;
+      __syncthreads();  // (also: the keys are there)
+      lo = __reduce_min_sync(0xFFFFFFFFu, lane < THREADS / 32 ? S.warp_lo[lane] : 0xFFFFFFFFu);
+      hi = __reduce_max_sync(0xFFFFFFFFu, lane < THREADS / 32 ? S.warp_hi[lane] : 0u);
+      // the k-th largest key
+      int left = k;
       t = lo;
-      const int members = S.members;
-      if (lo < hi && members <= kFew) {
+      while (lo < hi) {
+        const int bits = 32 - __clz(hi - lo), shift = bits > 11 ? bits - 11 : 0;
 #pragma unroll 4
         for (int p = f0 + tid; p < f1; p += THREADS) {
           const uint32_t x = keys[p];
-          if (x >= lo && x <= hi) S.list_key[atomicAdd(&S.n_list, 1)] = x;
+          if (x >= lo && x <= hi) atomicAdd(&S.hist[(x - lo) >> shift], 1);
         }
         __syncthreads();
-        t = members <= 32 ? warp_ranked(S.list_key, members, left) : ranked(S, S.list_key, members, left);
-        break;
+        {  // bins from the top: thread i holds the kOwn bins below kBins - kOwn i
+          constexpr int kOwn = kBins / THREADS;
+          int own[kOwn], n = 0, before;
+#pragma unroll
+          for (int e = 0; e < kOwn; ++e) {
+            own[e] = S.hist[kBins - 1 - kOwn * tid - e];
+            n += own[e];
+          }
+          block_prefix<THREADS>(S, n, before);
+#pragma unroll
+          for (int e = 0; e < kOwn; ++e) {
+            if (before < left && left <= before + own[e]) {  // one thread, one bin
+              S.bin = kBins - 1 - kOwn * tid - e;
+              S.above = before;
+              S.members = own[e];
+            }
+            before += own[e];
+          }
+          __syncthreads();
+        }
+        left -= S.above;
+        lo += uint32_t(S.bin) << shift;
+        if (shift == 0) hi = lo;
+        else hi = min(hi, lo + ((1u << shift) - 1u));
+        t = lo;
+        const int members = S.members;
+        if (lo < hi && members <= kFew) {
+#pragma unroll 4
+          for (int p = f0 + tid; p < f1; p += THREADS) {
+            const uint32_t x = keys[p];
+            if (x >= lo && x <= hi) S.list_key[atomicAdd(&S.n_list, 1)] = x;
+          }
+          __syncthreads();
+          t = members <= 32 ? warp_ranked(S.list_key, members, left) : ranked(S, S.list_key, members, left);
+          break;
+        }
+        __syncthreads();  // hist, bin and list are free again
+        for (int i = tid; i < kBins; i += THREADS) S.hist[i] = 0;
+        __syncthreads();
       }
-      __syncthreads();  // hist, bin and list are free again
-      for (int i = tid; i < kBins; i += THREADS) S.hist[i] = 0;
-      __syncthreads();
     }
     // pages in doubt
     lo = hi = t;
@@ -743,7 +799,7 @@ __global__ void __launch_bounds__(kFusedThreads, 2) select_kernel(SelectArgs a, 
 // One launch where a unit's pages keep a block busy for no longer than the second
 // launch takes, or where there are units for half of the SMs; else the pages are
 // scored by all warps of the device and picked by a second kernel. Measured (fused,
-// split): 8 units of 256 pages 7.4, 9.4 us; 8 of 512 10.9, 10.8; 64 of 1024 20.5,
+// split): 8 units of 256 pages 6.8, 9.4 us; 8 of 512 10.2, 10.8; 64 of 1024 20.5,
 // 20.5; 64 of 2048 33.8, 27.6; 128 of 1024 22.3, 25.9; 256 of 2048 51, 71.
 constexpr int kFusedPages = 512;       // any number of units
 constexpr int kFusedManyPages = 2048;  // half as many units as SMs at least
