@@ -195,6 +195,37 @@ struct AppendArgs {
   const int32_t* positions;
 };
 
+// The arguments of an append from its checked descriptors. Positions choose rows of the
+// rotation table: without one the kernels do not see them.
+inline AppendArgs append_args(const View& c, int dtype, const int32_t* page_table, int max_pages, int n_requests,
+                              const kvq_paged_rows& r) {
+  AppendArgs a{};
+  a.c = c;
+  a.table = page_table;
+  a.max_pages = max_pages;
+  a.B = n_requests;
+  a.start = r.start;
+  a.offsets = r.offsets;
+  a.n_rows = r.n_rows;
+  a.in_dtype = r.dtype;
+  a.dtype = dtype;
+  a.Hq = r.n_q_heads;
+  a.k = static_cast<const char*>(r.k);
+  a.v = static_cast<const char*>(r.v);
+  a.q = static_cast<const char*>(r.q);
+  a.q_out = static_cast<char*>(r.q_out);
+  a.k_stride = r.k_stride * 2;
+  a.v_stride = r.v_stride * 2;
+  a.q_stride = r.q_stride * 2;
+  a.q_out_stride = r.q_out_stride * 2;
+  a.rope = r.rope;
+  a.rope_positions = r.rope_positions;
+  a.R = r.rotary_dim;
+  a.interleaved = r.interleaved != 0;
+  a.positions = r.rotary_dim > 0 ? r.positions : nullptr;
+  return a;
+}
+
 struct AttnArgs {
   const int32_t* lens;
   const int32_t* table;

@@ -204,9 +204,8 @@ kvq_status kvq_paged_cache_init(kvq_paged_cache* c, int dtype, int n_pages, int 
 
 kvq_status kvq_paged_append(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages, int n_requests,
                             const kvq_paged_rows* r, kvq_cuda_stream stream) {
-  paged::AppendArgs a;
-  memset(&a, 0, sizeof a);
-  kvq_status st = check_cache(cache, kNeedKv, &a.c);
+  paged::View view;
+  kvq_status st = check_cache(cache, kNeedKv, &view);
   if (st == KVQ_OK) st = check_batch(cache, page_table, max_pages, n_requests);
   if (st != KVQ_OK) return st;
   if (r == nullptr) return fail(KVQ_ERR_BAD_ARG, "rows is NULL");
@@ -242,28 +241,7 @@ kvq_status kvq_paged_append(const kvq_paged_cache* cache, const int32_t* page_ta
     return fail(KVQ_ERR_BAD_ARG, "q_out_stride %lld: rows overlap", (long long)r->q_out_stride);
   const int sms = current_sms();
   if (sms == 0) return fail(KVQ_ERR_CUDA, "no usable CUDA device");
-  a.table = page_table;
-  a.max_pages = max_pages;
-  a.B = n_requests;
-  a.start = r->start;
-  a.offsets = r->offsets;
-  a.n_rows = r->n_rows;
-  a.in_dtype = r->dtype;
-  a.dtype = cache->dtype;
-  a.Hq = r->n_q_heads;
-  a.k = static_cast<const char*>(r->k);
-  a.v = static_cast<const char*>(r->v);
-  a.q = static_cast<const char*>(r->q);
-  a.q_out = static_cast<char*>(r->q_out);
-  a.k_stride = r->k_stride * 2;
-  a.v_stride = r->v_stride * 2;
-  a.q_stride = r->q_stride * 2;
-  a.q_out_stride = r->q_out_stride * 2;
-  a.rope = r->rope;
-  a.rope_positions = r->rope_positions;
-  a.R = r->rotary_dim;
-  a.interleaved = r->interleaved != 0;
-  a.positions = r->positions;
+  const paged::AppendArgs a = paged::append_args(view, cache->dtype, page_table, max_pages, n_requests, *r);
   return cuda_status(paged::launch_append(a, sms, reinterpret_cast<cudaStream_t>(stream)), "paged append launch");
 }
 
