@@ -99,6 +99,10 @@ __device__ __forceinline__ float4 rounded4(float4 x) {
   return load4<DT>(w);
 }
 
+__device__ __forceinline__ float4 times(float4 x, float s) {
+  return make_float4(x.x * s, x.y * s, x.z * s, x.w * s);
+}
+
 // Tokens of request b, or -1 for a length that its table row cannot hold.
 __device__ __forceinline__ int checked_len(const int32_t* lens, int b, int max_pages, const FastDiv& ps) {
   const int T = lens[b];

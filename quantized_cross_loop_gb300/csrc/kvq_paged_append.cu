@@ -133,10 +133,6 @@ __device__ __forceinline__ Wide rotate(const Lane& L, const Angles& t, const Raw
   return x;
 }
 
-__device__ __forceinline__ float4 times(float4 x, float s) {
-  return make_float4(x.x * s, x.y * s, x.z * s, x.w * s);
-}
-
 // Four stored keys as two words of 16-bit pairs (E4M3 as FP16, exact), and their
 // smaller and larger ones; NaN stays.
 template <int DT>

@@ -32,8 +32,13 @@
 // 2^-12 of the FP32 result. The tensor cores cut their sums off, so every 16
 // tokens' product starts from zero and is added to the running sum by FP32 FMA,
 // which also applies the rescaling.
-// E4M3: keys and values become FP16 in registers (exact); a BF16 query is scaled
-// by a power of two into FP16's range (exact down to 2^-31 of its largest).
+// E4M3: keys and values become FP16 in registers (exact). A BF16 query becomes FP16 by
+// a power of two per head that brings its largest channel into [2^15, 2^16): exact
+// down to 2^-17, where FP16's step of 2^-24 is the last of eight bits. A head with a
+// channel below that, 2^-32 of its largest (beside one that meets zero keys it may be
+// all that counts), is found by the attention kernel (WideHeads) and attended again by
+// FP32 multiply-adds, by the combine kernel: a branch or a call for such heads in the
+// attention kernel's loop cost all others up to 12%, by the registers that it moved.
 #include <atomic>
 
 #include "kvq_attn_common.cuh"
@@ -52,6 +57,10 @@ constexpr int kCombineWarps = kCombineThreads / 32;
 constexpr int kUnitCost = 2;       // tiles that the end of a unit takes as long as
 constexpr int kMinTiles = 2;       // tiles of a block's range, once every SM has one
 
+template <int DT, int QT>
+constexpr bool kNarrow = DT == kE4m3 && QT == kBf16;  // the query becomes narrower: BF16 to FP16
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 // A unit that several blocks share: the first of them and how many, `lanes` apart (u
 // < 0: no such unit). Where there are no more units than blocks, unit u's is number
 // u, else the one of the unit that starts in block c's range and goes on behind it
@@ -61,7 +70,7 @@ struct Rec {
 };
 __host__ __device__ constexpr bool rec_per_unit(long long units, int n_ctas) { return units <= n_ctas; }
 
-// Workspace: Rec[n], then 2 n slots of g heads x sum[128] and g x (m, l).
+// Workspace: Rec[n], then 2 n slots of g heads x sum[128] and g x (m, l), then a byte per unit and head (wide_heads).
 __host__ __device__ constexpr size_t slots_offset(int n) { return (size_t(n) * sizeof(Rec) + 15) / 16 * 16; }
 __host__ __device__ constexpr size_t slot_floats(int g) { return size_t(g) * kD + (size_t(g) + 1) / 2 * 4; }  // (16-byte steps)
 
@@ -250,6 +259,71 @@ __device__ __forceinline__ void look_up_page(const AttnArgs& a, Row& r) {
   r.page = r.live ? a.table[(long long)r.b * a.max_pages + r.page] : 0;
 }
 
+// The power of two that brings a BF16 number of this magnitude into [2^15, 2^16).
+__device__ __forceinline__ int query_shift(float top) {
+  const int e = 127 + 15 - int(__float_as_uint(top) >> 23);
+  return top == 0.0f || isinf(top) ? 0 : max(-120, min(120, e));
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
+
+// Whether FP16 holds the query heads of each unit, a byte per head and kMaxGroup bytes per unit, behind the slots.
+__device__ __forceinline__ uint8_t* wide_heads(const AttnArgs& a, int n) {
+  return reinterpret_cast<uint8_t*>(a.ws + slots_offset(n) + 2 * size_t(n) * slot_floats(a.g) * 4);
+}
+
+// Finds the BF16 query heads that FP16 does not hold whole: those with a channel below 2^-17 by their power of two, or
+// one that is infinite (beside which others may overflow). Block c takes the units c, c + n, ..., eight lanes a head.
+struct WideHeads {
+  static constexpr int kLanes = 8, kOwn = 2, kHeads = kOwn * kThreads / kLanes;
+  uint4 w[kOwn][2];
+  __device__ __forceinline__ static int pairs(const AttnArgs& a, int c, int n) {
+    const int units = a.B * a.c.H;
+    return c < units ? ((units - c + n - 1) / n) * a.g : 0;
+  }
+  __device__ __forceinline__ static void place(const AttnArgs& a, int c, int n, int p, int& u, int& j) {
+    u = p / a.g;
+    j = p - u * a.g;
+    u = c + u * n;
+  }
+  __device__ __forceinline__ void load(const AttnArgs& a, int c, int n, int pairs, int at) {
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      const int p = at + (e * kThreads + threadIdx.x) / kLanes;
+      w[e][0] = w[e][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (p >= pairs) continue;
+      int u, j;
+      place(a, c, n, p, u, j);
+      const int b = u / a.c.H, h = u - b * a.c.H;
+      const char* q = a.q + (long long)b * a.q_stride + (long long)(h * a.g + j) * (kD * 2) + threadIdx.x % kLanes * 16;
+      w[e][0] = *reinterpret_cast<const uint4*>(q);
+      w[e][1] = *reinterpret_cast<const uint4*>(q + kD);
+    }
+  }
+  __device__ __forceinline__ void store(const AttnArgs& a, int c, int n, int pairs, int at) const {
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+      float top = 0.0f, low = INFINITY;  // magnitudes: the largest, and the smallest that is not 0
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t v = (&w[e][i / 8].x)[i / 2 % 4];
+        const float x = fabsf(__uint_as_float(i & 1 ? v & 0xFFFF0000u : v << 16));
+        top = fmaxf(top, x);
+        low = fminf(low, x == 0.0f ? INFINITY : x);
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o *= 2) {
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        low = fminf(low, __shfl_xor_sync(0xFFFFFFFFu, low, o));
+      }
+      const int p = at + (e * kThreads + threadIdx.x) / kLanes;
+      if (p >= pairs || threadIdx.x % kLanes != 0) continue;
+      int u, j;
+      place(a, c, n, p, u, j);
+      wide_heads(a, n)[u * kMaxGroup + j] = isinf(top) || low * power_of_two(query_shift(top)) < 0x1p-17f;
+    }
+  }
+};
+
 template <int DT, int QT, int NT, bool SEL>
 struct Block {
   using F = Form<DT>;
@@ -296,25 +370,24 @@ struct Block {
     for (int n = 0; n < NT; ++n) {
       const int head = lane / 4 + 8 * n;
       const char* p = a.q + (long long)b * a.q_stride + (long long)(h * a.g + head) * (kD * 2);
-      scale[n] = a.scale * ks * 1.4426950408889634f;
+      scale[n] = a.scale * ks * kLog2e;
       float top = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const uint2 w = head < a.g ? query_words(p, j) : make_uint2(0, 0);
         qa[j][2 * n] = w.x;
         qa[j][2 * n + 1] = w.y;
-        if constexpr (DT == kE4m3 && QT == kBf16) {
+        if constexpr (kNarrow<DT, QT>) {
           top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w.x << 16)), fabsf(__uint_as_float(w.x & 0xFFFF0000u))));
           top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w.y << 16)), fabsf(__uint_as_float(w.y & 0xFFFF0000u))));
         }
       }
-      if constexpr (DT == kE4m3 && QT == kBf16) {  // BF16 to FP16 by a power of two: the largest into [2^7, 2^8)
+      if constexpr (kNarrow<DT, QT>) {  // BF16 to FP16 by a power of two
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-        int e = 134 - int(__float_as_uint(top) >> 23);  // 7 - (exponent - 127)
-        e = top == 0.0f || isinf(top) ? 0 : max(-120, min(120, e));
-        const float f = __uint_as_float(uint32_t(127 + e) << 23);
-        scale[n] *= __uint_as_float(uint32_t(127 - e) << 23);
+        const int e = query_shift(top);
+        const float f = power_of_two(e);
+        scale[n] *= power_of_two(-e);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -570,7 +643,7 @@ struct Block {
       if (slot != nullptr)
         *reinterpret_cast<float2*>(slot + a.g * kD + 2 * j) = make_float2(S.top[j], S.sum[j]);
       else if (a.lse != nullptr)
-        a.lse[(long long)b * a.Hq + h * a.g + j] = (S.top[j] + log2f(S.sum[j])) * 0.6931471805599453f;
+        a.lse[(long long)b * a.Hq + h * a.g + j] = (S.top[j] + log2f(S.sum[j])) * kLn2;
     }
   }
 };
@@ -598,6 +671,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
   const bool per_unit = rec_per_unit((long long)a.B * a.c.H, n_ctas);
   if (!per_unit && threadIdx.x == 0) recs[c].u = -1;
 
+  [[maybe_unused]] WideHeads heads;
+  const int looker = n_ctas - 1 - c;  // (where units are few, the blocks that are left without work)
+  const int pairs = kNarrow<DT, QT> ? WideHeads::pairs(a, looker, n_ctas) : 0;
+  if (pairs > 0) heads.load(a, looker, n_ctas, pairs, 0);
+  auto look = [&] {
+    if (pairs > 0) {
+      heads.store(a, looker, n_ctas, pairs, 0);
+      for (int i = WideHeads::kHeads; i < pairs; i += WideHeads::kHeads) {
+        heads.load(a, looker, n_ctas, pairs, i);
+        heads.store(a, looker, n_ctas, pairs, i);
+      }
+    }
+  };
   auto work_of = [&](int b) {
     const int tiles = (span_of<SEL>(a, checked_len(a.lens, b, a.max_pages, a.c.ps)) + F::kTile - 1) / F::kTile;
     return tiles > 0 ? (long long)a.lane_heads * (tiles + kUnitCost) : 0LL;
@@ -617,6 +703,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
     build_prefix<kThreads>(S.prefix, a.B, work_of);
     W = S.prefix.pre[kThreads];
   }
+  // The query heads loaded above are looked at here, or, more than eight a group, behind the first copies: ragged 8-bit
+  // requests, 4 heads 92.7 us here, 93.1 there, 12 heads 126.6, 118.4; 16 selected pages, 4 heads 37.5, 38.2, 16 heads
+  // 61.1, 53.6 (without the look 91.5, 125.8; 36.6, 59.7)
+  constexpr bool kLate = NT == 2;
+  if (!kLate) look();
   // requests without tokens, and refused ones: no block's range holds them
   for (int b = c; b < a.B; b += n_ctas) {
     const int T = checked_len(a.lens, b, a.max_pages, a.c.ps);
@@ -633,7 +724,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
   const int sms = groups / kBlocksPerSm;
   const long long most = W <= sms ? W : max((long long)sms, W / kMinTiles);
   const int C = int(most < groups ? most : groups);
-  if (group >= C) return;
+  if (group >= C) {
+    if (kLate) look();
+    return;
+  }
   const long long s0 = part_start(group, W, C), e0 = part_start(group + 1, W, C);
 
   Cursor<SEL, F::kTile> at, ahead;
@@ -649,7 +743,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
   at.h += h0;
   at.pos = s0;
   if (at.tile >= at.tiles) at.next_unit(a, h0);  // the range begins behind the unit's last tile
-  if (at.h >= a.c.H || !at.before(a, e0)) return;  // (and may hold no tile)
+  if (at.h >= a.c.H || !at.before(a, e0)) {  // (and may hold no tile)
+    if (kLate) look();
+    return;
+  }
   ahead = at;
 
   Block<DT, QT, NT, SEL> K(a, S);
@@ -679,6 +776,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
       ahead.next(a, h0);
     }
     if (i == -1) {  // (the first tiles' copies are on their way)
+      if (kLate) look();
       K.load_query(at.b, at.h);
       K.clear();
     }
@@ -709,27 +807,136 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
   }
 }
 
+struct Joint {  // shared memory of the combine kernel
+  float m[kCombineWarps], l[kCombineWarps];
+  float4 x[kCombineWarps][32];
+  alignas(16) float q[kD];
+};
+
+// Sum, maximum and sum of exponentials of `per` warps from `warp` on, in log2 units; every lane has its four channels of x.
+__device__ __forceinline__ void join_warps(const Joint& S, int warp, int per, int lane, float& top, float& l, float4& x) {
+  top = S.m[warp];
+  for (int w = 1; w < per; ++w) top = fmaxf(top, S.m[warp + w]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  l = 0.0f;
+  x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int w = 0; w < per; ++w) {
+    const float f = exp2f(S.m[warp + w] - base);
+    const float4 y = S.x[warp + w][lane];
+    l += S.l[warp + w] * f;
+    x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
+  }
+}
+// x / l to out and lse of query head j of KV head h.
+__device__ __forceinline__ void put_head(const AttnArgs& a, int b, int h, int j, int lane, float top, float l, float4 x) {
+  const long long hq = (long long)b * a.Hq + h * a.g + j;
+  if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  else x = make_float4(x.x / l, x.y / l, x.z / l, x.w / l);
+  reinterpret_cast<float4*>(a.out + hq * kD)[lane] = x;
+  if (a.lse != nullptr && lane == 0) a.lse[hq] = (top + log2f(l)) * kLn2;
+}
+
+// The attention of one query head to E4M3 keys by FP32 multiply-adds, by a block: a lane has a token of a warp's 32
+// for the scores and four channels for the sums.
+template <bool SEL>
+__device__ __forceinline__ void attend_plainly(const AttnArgs& a, Joint& S, int u, int j) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  Cursor<SEL, kCombineThreads> at;
+  at.b = u / a.c.H;
+  at.h = u % a.c.H;
+  at.load(a);
+  if (at.span == 0) return;  // no tokens, or refused: written by the attention kernel
+  const float ks = a.c.k_scale != nullptr ? a.c.k_scale[at.h] : 1.0f, vs = a.c.v_scale != nullptr ? a.c.v_scale[at.h] : 1.0f;
+  const float scale = a.scale * kLog2e;
+  __syncthreads();  // nobody reads S of the head before
+  if (warp == 0) {
+    const char* q = a.q + (long long)at.b * a.q_stride + ((long long)(at.h * a.g + j) * kD + 4 * lane) * 2;
+    *reinterpret_cast<float4*>(&S.q[4 * lane]) = load4<kBf16>(q);
+  }
+  __syncthreads();
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int v0 = 32 * warp; v0 < at.span; v0 += kCombineThreads) {
+    Row r;
+    look_up_entry<SEL>(a, at, v0 + lane, r);
+    look_up_page<SEL>(a, r);
+    const bool in_pool = r.page >= 0 && r.page < a.c.n_pages, live = r.live && in_pool;
+    const bool refused = __any_sync(0xFFFFFFFFu, r.bad != 0 || (r.live && !in_pool));  // (flagged by the attention kernel)
+    const long long off = live ? (long long)r.page * a.c.page_stride + (long long)r.place * a.c.token_stride +
+                                     (long long)r.h * a.c.head_stride
+                               : -1;
+    float s = 0.0f;
+    if (live)
+#pragma unroll 4
+      for (int c = 0; c < kD; c += 4) {
+        const float4 k = times(load4<kE4m3>(a.c.k + off + c), ks), q = *reinterpret_cast<const float4*>(&S.q[c]);
+        s = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s))));
+      }
+    float mx = live ? s : -INFINITY;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+    mx = fmaxf(m, mx * scale);
+    const float base = mx == -INFINITY ? 0.0f : mx, alpha = exp2_ftz(m - base);
+    const float p = live ? exp2_ftz(fmaf(s, scale, -base)) : 0.0f;
+    m = mx;
+    l = refused ? NAN : fmaf(l, alpha, p);
+    o = times(o, alpha);
+    for (int t = 0; t < 32; ++t) {
+      const long long x = __shfl_sync(0xFFFFFFFFu, off, t);
+      const float w = __shfl_sync(0xFFFFFFFFu, p, t);
+      if (x < 0) continue;
+      const float4 v = load4<kE4m3>(a.c.v + x + 4 * lane);
+      o = make_float4(fmaf(w, v.x, o.x), fmaf(w, v.y, o.y), fmaf(w, v.z, o.z), fmaf(w, v.w, o.w));
+    }
+  }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
+  if (lane == 0) {
+    S.m[warp] = m;
+    S.l[warp] = l;
+  }
+  S.x[warp][lane] = times(o, vs);
+  __syncthreads();
+  if (warp != 0) return;
+  float top;
+  join_warps(S, 0, kCombineWarps, lane, top, l, o);
+  put_head(a, at.b, at.h, j, lane, top, l, o);
+}
+
 // Joins the parts of a unit that several blocks' ranges share; block (r, y): the
 // unit of record r, `most` of its group's query heads. A head has 16 / heads warps,
 // each with every so many parts, four channels a lane; a part is read once, with a
-// running maximum.
+// running maximum. NARROW (BF16 queries of E4M3 keys): the heads that FP16 does not
+// hold are attended again, by block (r, y) those of the units r, r + gridDim.x, ...
+template <bool NARROW, bool SEL>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, int n_ctas, int lanes, int most) {
-  __shared__ float s_m[kCombineWarps], s_l[kCombineWarps];
-  __shared__ float4 s_x[kCombineWarps][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ Joint S;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, units = a.B * a.c.H;
   const int j0 = blockIdx.y * most, heads = min(most, a.g - j0), per = kCombineWarps / heads;  // warps of a head
   const int j = j0 + warp / per, mine = warp % per;
   const float* slots = reinterpret_cast<const float*>(a.ws + slots_offset(n_ctas));
   const size_t stride = slot_floats(a.g);
+  const uint8_t* wide = wide_heads(a, n_ctas);
   wait_prior_grid();
   allow_dependents();
   const Rec r = reinterpret_cast<const Rec*>(a.ws)[blockIdx.x];
   // (the bounds hold for every record of the attention kernel; a workspace that something else writes meanwhile
   // must not lead outside of it)
-  if (r.u < 0 || r.u >= a.B * a.c.H || r.first < 0 || r.first >= n_ctas || r.parts < 1 ||
-      r.parts > n_ctas || r.first + (r.parts - 1) * lanes >= n_ctas)
-    return;
-  const int c = r.first, parts = r.parts;  // slot 2 c + 1 of the first block c, slot 2 c' of the others
+  const bool shared = r.u >= 0 && r.u < units && r.first >= 0 && r.first < n_ctas && r.parts >= 1 && r.parts <= n_ctas &&
+                      r.first + (r.parts - 1) * lanes < n_ctas;
+  // own units x0, x0 + gridDim.x, ...: of as many as a warp has lanes, which have heads to be attended again
+  const int x0 = int(blockIdx.x);
+  auto look = [&](int u0) {
+    const long long u = u0 + (long long)lane * gridDim.x;
+    const uint64_t among = (~0ull >> (64 - 8 * heads)) << (8 * (j0 & 7));  // the block's heads
+    return __ballot_sync(0xFFFFFFFFu, u < units && (*reinterpret_cast<const uint64_t*>(wide + u * kMaxGroup + (j0 & 8)) & among) != 0);
+  };
+  uint32_t again = 0u;
+  if constexpr (NARROW) again = look(x0);
+  if (!shared && again == 0u && (!NARROW || units <= 32 * int(gridDim.x))) return;
+  // (another block attends these heads of this one's unit)
+  const bool others = NARROW && shared && r.u != x0 && warp < per * heads && wide[r.u * kMaxGroup + j] != 0;
+  const int c = r.first, parts = shared ? r.parts : 0;  // slot 2 c + 1 of the first block c, slot 2 c' of the others
   float m = -INFINITY, l = 0.0f;
   float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (warp < per * heads) {
@@ -763,30 +970,29 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, in
       }
     }
     if (lane == 0) {
-      s_m[warp] = m;
-      s_l[warp] = l;
+      S.m[warp] = m;
+      S.l[warp] = l;
     }
-    s_x[warp][lane] = x;
+    S.x[warp][lane] = x;
   }
   __syncthreads();
-  if (mine != 0 || warp >= per * heads) return;
-  float top = m;
-  for (int w = 1; w < per; ++w) top = fmaxf(top, s_m[warp + w]);
-  const float base = top == -INFINITY ? 0.0f : top;
-  l = 0.0f;
-  x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int w = 0; w < per; ++w) {
-    const float f = exp2f(s_m[warp + w] - base);
-    const float4 y = s_x[warp + w][lane];
-    l += s_l[warp + w] * f;
-    x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
+  if (shared && mine == 0 && warp < per * heads && !others) {
+    float top;
+    join_warps(S, warp, per, lane, top, l, x);
+    put_head(a, r.u / a.c.H, r.u % a.c.H, j, lane, top, l, x);
   }
-  const int b = r.u / a.c.H, h = r.u % a.c.H;
-  const long long hq = (long long)b * a.Hq + h * a.g + j;
-  if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  else x = make_float4(x.x / l, x.y / l, x.z / l, x.w / l);
-  reinterpret_cast<float4*>(a.out + hq * kD)[lane] = x;
-  if (a.lse != nullptr && lane == 0) a.lse[hq] = (top + log2f(l)) * 0.6931471805599453f;
+  if constexpr (NARROW) {
+    for (int u0 = x0;;) {
+      for (; again != 0u; again &= again - 1u) {
+        const int u = u0 + (__ffs(again) - 1) * int(gridDim.x);
+        for (int i = j0; i < j0 + heads; ++i)
+          if (wide[u * kMaxGroup + i] != 0) attend_plainly<SEL>(a, S, u, i);
+      }
+      if (units - u0 <= 32 * int(gridDim.x)) break;
+      u0 += 32 * int(gridDim.x);
+      again = look(u0);
+    }
+  }
 }
 
 template <int DT, int QT, int NT, bool SEL>
@@ -811,7 +1017,7 @@ cudaError_t launch_form(const AttnArgs& a, cudaStream_t stream) {
   int most = 1;
   while (most < 8 && (long long)recs * ((a.g + most - 1) / most) > a.sms) most *= 2;
   count_launch();
-  return launch_dependent(combine_kernel, dim3(recs, (a.g + most - 1) / most), dim3(kCombineThreads), 0, stream, a, n,
+  return launch_dependent(combine_kernel<kNarrow<DT, QT>, kNarrow<DT, QT> && SEL>, dim3(recs, (a.g + most - 1) / most), dim3(kCombineThreads), 0, stream, a, n,
                           lanes, most);
 }
 
@@ -827,7 +1033,8 @@ cudaError_t launch_types(const AttnArgs& a, cudaStream_t stream) {
 }  // namespace
 
 size_t attn_workspace(int B, int H, int Hq, int sms) {
-  return slots_offset(most_blocks(sms)) + 2 * size_t(most_blocks(sms)) * slot_floats(Hq / H) * 4;
+  return slots_offset(most_blocks(sms)) + 2 * size_t(most_blocks(sms)) * slot_floats(Hq / H) * 4 +
+         size_t(B) * H * kMaxGroup;
 }
 
 cudaError_t launch_attn(const AttnArgs& args, cudaStream_t stream) {

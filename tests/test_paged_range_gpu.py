@@ -1,0 +1,99 @@
+"""The paged cache's operators at the ends of their types' ranges, against plain
+64-bit implementations: queries and scales of very different sizes, scores in the
+subnormal range, ties of the 8-bit rounding, infinities beside masked places.
+
+Tolerances are those of the arithmetic: a sum of 128 exact products in FP32 is off
+by at most 132 * 2^-23 of the sum of the terms' magnitudes, whatever the query's
+channels that meet zero keys are (their products are zero). Orders and stored
+codes have no tolerance.
+"""
+
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from quantized_cross_loop_gb300 import kvq
+from tests.test_paged_gpu import D, DT, Batch, _attend, _bounds_only, _check_selection, _compare, _gen, _query, _raw
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("g", [4, 12])
+@pytest.mark.parametrize("ratio", [0, 16, 24, 30, 31, 32, 33, 34, 40, 64, 66, 67, 90, 120])
+def test_e4m3_attention_of_queries_with_channels_far_apart(ratio, g):
+    """Channels of 2^ratio and many sizes below, which meet zero keys, leave the logits to ordinary channels: no bit of
+    those may be lost beside them. Heads of one group differ in their channels' spread."""
+    b = Batch([100, 64, 900, 3], 16, 2, "e4m3", seed=ratio)
+    zero = D // 2
+    _raw(b.k)[..., :zero] = 0
+    for k in b.K:
+        k[..., :zero] = 0
+    q = _query(4, 2 * g)
+    steps = torch.arange(zero, 0, -1, device="cuda") * (ratio / zero)
+    large = (torch.randn((4, 2 * g, zero), generator=_gen(ratio), device="cuda").double() * 2.0 ** steps).bfloat16()
+    large[..., 0] = 2.0**ratio
+    q[:, 1:, :zero] = large[:, 1:]  # (head 0 stays as it is)
+    q[1, 2] = 0
+    out, lse = _attend(b, q)
+    _compare(b, q, out, lse, 1 / math.sqrt(D))
+
+
+def test_e4m3_attention_of_queries_over_the_whole_range_of_bf16():
+    """One channel at BF16's end, ordinary ones, and channels down to BF16's smallest subnormal on keys of a large
+    scale: the largest meets zero keys, so that what counts lies up to 2^260 below it."""
+    b = Batch([70, 200], 16, 1, "e4m3", seed=2)
+    _raw(b.k)[..., 0] = 0
+    b.k_scale.fill_(2.0**120)
+    b.K = [k.clone() for k in b.K]
+    for i, t in enumerate(b.lens):
+        at = torch.arange(t, device="cuda")
+        k = _raw(b.k)[b.table[i].long()[at // 16], at % 16].view(b.dt).double()
+        b.K[i] = k * 2.0**120
+    q = torch.zeros((2, 4, D), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 2.0**127
+    q[:, 0, 1:40] = (torch.randn((2, 39), generator=_gen(1), device="cuda").double() * 2.0**-126).bfloat16()
+    q[:, 1, 1:40] = 2.0**-133  # the smallest BF16 number
+    q[:, 2, 1:40] = -(2.0**-130)
+    q[:, 3, 0] = 0
+    q[:, 3, 5:9] = 2.0**-133
+    out, lse = _attend(b, q, softmax_scale=1.0)
+    _compare(b, q, out, lse, 1.0)
+
+
+@pytest.mark.parametrize("g,requests", [(4, 4), (4, 170), (16, 170), (1, 700), (3, 5000)])
+def test_e4m3_attention_of_far_apart_channels_in_some_heads(g, requests):
+    """Heads whose channels need more than FP16, here and there in batches of fewer and of many more units than blocks,
+    over all pages and over selected ones; beside a refused request, one without tokens, and a bad selection."""
+    lens = [(29 * i) % 170 for i in range(requests)]
+    lens[:4] = [3000, 40, 0, 75]
+    b = Batch(lens, 16, 2, "e4m3", seed=g, bounds=False)
+    _raw(b.k)[..., 0] = 0
+    for k in b.K:
+        k[..., 0] = 0
+    q = _query(requests, 2 * g)
+    i = torch.arange(requests * 2 * g, device="cuda").view(requests, 2 * g)
+    q[..., 0] = torch.where(i % 5 == 2, 2.0**60, q[..., 0].float()).bfloat16()
+    check = list(range(4)) + list(range(4, requests, max(1, requests // 40)))
+    some = Batch.__new__(Batch)
+    some.lens, some.ps, some.H = [lens[x] for x in check], 16, 2
+    some.K, some.V = [b.K[x] for x in check], [b.V[x] for x in check]
+    out, lse = _attend(b, q)
+    _compare(some, q[check], out[check], lse[check], 1 / math.sqrt(D))
+    sel = torch.full((requests, 2, 4), -1, dtype=torch.int32, device="cuda")
+    pages = torch.tensor([-(-t // 16) for t in lens], device="cuda")
+    for h in range(2):
+        for e in range(3):
+            sel[:, h, e] = torch.where(pages > 2 * e + h, 2 * e + h, -1)
+    out = kvq.kvq_paged_sparse_attn(b.cache, b.table, b.seq, q, sel, lse=lse)
+    _compare(some, q[check], out[check], lse[check], 1 / math.sqrt(D), sel=sel[check])
+    assert b.cache.error_word() == 0
+    b.seq[1] = -1
+    b.table[3, 2] = b.cache.n_pages
+    out, lse = _attend(b, q)
+    _compare(some, q[check], out[check], lse[check], 1 / math.sqrt(D), skip=(1, 3))
+    b.seq[1], sel[0, 1, 1] = 40, 0
+    out = kvq.kvq_paged_sparse_attn(b.cache, b.table, b.seq, q, sel, lse=lse)
+    assert torch.isnan(out[0, g:]).all() and torch.isfinite(out[0, :g]).all()
