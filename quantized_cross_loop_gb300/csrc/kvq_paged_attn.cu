@@ -364,13 +364,21 @@ struct Block {
       return make_uint2(*reinterpret_cast<const uint32_t*>(p + (16 * j + 2 * q) * 2),
                         *reinterpret_cast<const uint32_t*>(p + (16 * j + 2 * q + 8) * 2));
   }
+  // scale ks 2^shift, whose parts may leave FP32's range where the logits do not (a scale of 0 would make a masked place's
+  // logit NaN; with 2^-149 no logit is off by more than 2^-116).
+  __device__ __forceinline__ static float scaled(float scale, float ks, int shift) {
+    const uint32_t k = __float_as_uint(ks);
+    const float x = ldexpf(scale * __uint_as_float((k & 0x7FFFFFu) | 0x3F800000u), int(k >> 23) - 127 + shift);
+    return fminf(fmaxf(x, 0x1p-149f), 3.402823466e38f);
+  }
   __device__ __forceinline__ void load_query(int b, int h) {
     const float ks = DT == kE4m3 && a.c.k_scale != nullptr ? a.c.k_scale[h] : 1.0f;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int head = lane / 4 + 8 * n;
       const char* p = a.q + (long long)b * a.q_stride + (long long)(h * a.g + head) * (kD * 2);
-      scale[n] = a.scale * ks * kLog2e;
+      scale[n] = a.scale * kLog2e;
+      int shift = 0;
       float top = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -387,7 +395,7 @@ struct Block {
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         const int e = query_shift(top);
         const float f = power_of_two(e);
-        scale[n] *= power_of_two(-e);
+        shift = -e;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -396,6 +404,7 @@ struct Block {
             qa[j][2 * n + i] = pack_half(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xFFFF0000u) * f);
           }
       }
+      if constexpr (DT == kE4m3) scale[n] = scaled(scale[n], ks, shift);
     }
   }
 

@@ -97,3 +97,19 @@ def test_e4m3_attention_of_far_apart_channels_in_some_heads(g, requests):
     b.seq[1], sel[0, 1, 1] = 40, 0
     out = kvq.kvq_paged_sparse_attn(b.cache, b.table, b.seq, q, sel, lse=lse)
     assert torch.isnan(out[0, g:]).all() and torch.isfinite(out[0, :g]).all()
+
+
+@pytest.mark.parametrize("gain,k_scale,softmax_scale", [
+    (2.0**-115, 2.0**-33, 0.1),      # the scales' product is below FP32's smallest number: all tokens weigh the same
+    (2.0**126, 2.0**-78, 2.0**-78),  # ... beside queries of BF16's other end
+    (2.0**-133, 2.0**35, 2.0**95),   # above FP32's largest, and the smallest queries bring the logits back
+])
+def test_e4m3_attention_of_scales_whose_product_leaves_fp32(gain, k_scale, softmax_scale):
+    b = Batch([77, 200, 64], 16, 2, "e4m3", seed=4, spread=20.0)
+    stored = [k / b.k_scale.double()[:, None] for k in b.K]
+    b.k_scale.fill_(k_scale)
+    b.K = [k * k_scale for k in stored]
+    q = (torch.sign(torch.randn((3, 8, D), generator=_gen(3), device="cuda")).double() * gain).bfloat16()
+    assert (q != 0).all()
+    out, lse = _attend(b, q, softmax_scale=softmax_scale)
+    _compare(b, q, out, lse, softmax_scale)
