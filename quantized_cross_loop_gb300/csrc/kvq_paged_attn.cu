@@ -601,7 +601,8 @@ struct Block {
       return fmaxf(fmaxf(S.m[0][head], S.m[1][head]), fmaxf(S.m[2][head], S.m[3][head]));
     };
     float* mine = S.buf + (warp & 1) * 8 * kBufStride;
-    const float vs = DT == kE4m3 && a.c.v_scale != nullptr ? a.c.v_scale[h] : 1.0f;
+    // (a slot's sums stay as they are: times the weights' 2^14, scaled values may leave FP32's range where the mean does not)
+    const float vs = DT == kE4m3 && slot == nullptr && a.c.v_scale != nullptr ? a.c.v_scale[h] : 1.0f;
     if (threadIdx.x < a.g) {
       const float mx = top(threadIdx.x), base = mx == -INFINITY ? 0.0f : mx;
       float sum = 0.0f;
@@ -609,7 +610,7 @@ struct Block {
       for (int w = 0; w < kWarps; ++w) sum += S.l[w][threadIdx.x] * exp2_ftz(S.m[w][threadIdx.x] - base);
       S.top[threadIdx.x] = mx - F::kShift;
       S.sum[threadIdx.x] = sum;
-      S.factor[threadIdx.x] = slot != nullptr ? vs : (sum == 0.0f ? 0.0f : vs / sum);
+      S.factor[threadIdx.x] = slot != nullptr ? 1.0f : (sum == 0.0f ? 0.0f : 1.0f / sum);
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n) {  // eight heads at a time
@@ -644,7 +645,7 @@ struct Block {
 #pragma unroll 4
       for (int i = 0; i < heads; ++i) {
         const float x = S.buf[i * kBufStride + c] + S.buf[(8 + i) * kBufStride + c];
-        to[i * kD] = S.sum[8 * n + i] == 0.0f ? 0.0f : x * S.factor[8 * n + i];
+        to[i * kD] = S.sum[8 * n + i] == 0.0f ? 0.0f : x * S.factor[8 * n + i] * vs;
       }
     }
     if (threadIdx.x < a.g) {
@@ -836,11 +837,12 @@ __device__ __forceinline__ void join_warps(const Joint& S, int warp, int per, in
     x = make_float4(fmaf(f, y.x, x.x), fmaf(f, y.y, x.y), fmaf(f, y.z, x.z), fmaf(f, y.w, x.w));
   }
 }
-// x / l to out and lse of query head j of KV head h.
+// x / l, scaled, to out and lse of query head j of KV head h.
 __device__ __forceinline__ void put_head(const AttnArgs& a, int b, int h, int j, int lane, float top, float l, float4 x) {
   const long long hq = (long long)b * a.Hq + h * a.g + j;
+  const float vs = a.c.v_scale != nullptr ? a.c.v_scale[h] : 1.0f;
   if (l == 0.0f) x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  else x = make_float4(x.x / l, x.y / l, x.z / l, x.w / l);
+  else x = make_float4(x.x / l * vs, x.y / l * vs, x.z / l * vs, x.w / l * vs);
   reinterpret_cast<float4*>(a.out + hq * kD)[lane] = x;
   if (a.lse != nullptr && lane == 0) a.lse[hq] = (top + log2f(l)) * kLn2;
 }
@@ -855,7 +857,7 @@ __device__ __forceinline__ void attend_plainly(const AttnArgs& a, Joint& S, int 
   at.h = u % a.c.H;
   at.load(a);
   if (at.span == 0) return;  // no tokens, or refused: written by the attention kernel
-  const float ks = a.c.k_scale != nullptr ? a.c.k_scale[at.h] : 1.0f, vs = a.c.v_scale != nullptr ? a.c.v_scale[at.h] : 1.0f;
+  const float ks = a.c.k_scale != nullptr ? a.c.k_scale[at.h] : 1.0f;
   const float scale = a.scale * kLog2e;
   __syncthreads();  // nobody reads S of the head before
   if (warp == 0) {
@@ -904,7 +906,7 @@ __device__ __forceinline__ void attend_plainly(const AttnArgs& a, Joint& S, int 
     S.m[warp] = m;
     S.l[warp] = l;
   }
-  S.x[warp][lane] = times(o, vs);
+  S.x[warp][lane] = o;
   __syncthreads();
   if (warp != 0) return;
   float top;

@@ -113,3 +113,15 @@ def test_e4m3_attention_of_scales_whose_product_leaves_fp32(gain, k_scale, softm
     assert (q != 0).all()
     out, lse = _attend(b, q, softmax_scale=softmax_scale)
     _compare(b, q, out, lse, softmax_scale)
+
+
+@pytest.mark.parametrize("v_scale", [2.0**110, 2.0**-126])
+def test_e4m3_attention_of_large_and_small_value_scales(v_scale):
+    """Values whose sum lies within FP32's range, in requests that one block and several blocks attend to."""
+    b = Batch([5000, 40], 16, 1, "e4m3", seed=6)
+    stored = [v / b.v_scale.double()[:, None] for v in b.V]
+    b.v_scale.fill_(v_scale)
+    b.V = stored
+    q = _query(2, 4)
+    out, lse = _attend(b, q)
+    _compare(b, q, out.double() / v_scale, lse, 1 / math.sqrt(D))
