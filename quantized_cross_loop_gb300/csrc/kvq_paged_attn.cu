@@ -484,7 +484,10 @@ struct Block {
       for (int t = 0; t < kBlocks; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (!((mask >> (8 * t + 2 * (lane & 3) + (i & 1))) & 1)) s[t][0][i] = -INFINITY;
+          if (!((mask >> (8 * t + 2 * (lane & 3) + (i & 1))) & 1)) {
+            s[t][0][i] = -INFINITY;
+            if constexpr (kChains == 2) s[t][1][i] = 0.0f;  // (an infinite query times the zeros there is NaN)
+          }
     }
     uint32_t part[kBlocks][NT][3];  // the weights, split
     float alpha[NT];

@@ -125,3 +125,16 @@ def test_e4m3_attention_of_large_and_small_value_scales(v_scale):
     q = _query(2, 4)
     out, lse = _attend(b, q)
     _compare(b, q, out.double() / v_scale, lse, 1 / math.sqrt(D))
+
+
+@pytest.mark.parametrize("cache,act", [("bf16", "bf16"), ("fp16", "fp16"), ("e4m3", "bf16"), ("e4m3", "fp16")])
+@pytest.mark.parametrize("channel", [7, 23])
+def test_infinite_queries_beside_masked_places(cache, act, channel):
+    """A query whose products with all keys are -inf finds nothing, also where the last tile has places without a token."""
+    b = Batch([16, 40, 3, 70], 16, 1, cache)
+    _raw(b.k)[..., channel] = _raw(torch.full((1,), -2.0, device="cuda").to(b.dt))
+    q = _query(4, 4, act)
+    q[:, 1, channel] = math.inf
+    out, lse = _attend(b, q)
+    assert (out[:, 1] == 0).all() and torch.isneginf(lse[:, 1]).all()
+    assert torch.isfinite(out).all() and torch.isfinite(lse[:, [0, 2, 3]]).all()
