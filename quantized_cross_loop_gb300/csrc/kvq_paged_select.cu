@@ -13,6 +13,9 @@
 // sums of g terms of one sign (g - 1 roundings), a lane adds up to 16 products in two
 // chains (9), five additions join the lanes (5); four more cover A's and E's own
 // rounding (A has no more than 30 roundings of 2^-24 each, nothing beside 4 / 33).
+// Products below FP32's normal range are off by up to 2^-150 each whatever their size,
+// 256 of them by 2^-142 (sums there are exact): 2E has 2^-140 more, twice as much as
+// two scores need, which covers A's and E's own steps of 2^-150.
 //
 // The pick kernel finds the key t of the last page that FP32 would take, by
 // histograms over the keys' range. Pages above t + 2E are in, those below t - 2E are
@@ -578,7 +581,7 @@ __device__ __forceinline__ void pick(const SelectArgs& a, Pick& S, int b, int h,
     // pages in doubt
     lo = hi = t;
     if (t != kFirstKey && t != kLastKey) {
-      const float x = float_of(t), e = 2.0f * (float(a.g + 17) * 0x1p-24f) * largest;
+      const float x = float_of(t), e = fmaf(2.0f * (float(a.g + 17) * 0x1p-24f), largest, 0x1p-140f);
       const float x0 = __fsub_rd(x, e), x1 = __fadd_ru(x, e);
       lo = x0 >= -3.4e38f ? key_of(x0) : key_of(-3.402823466e38f);
       hi = x1 <= 3.4e38f ? key_of(x1) : kFirstKey - 1u;

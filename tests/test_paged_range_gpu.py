@@ -138,3 +138,36 @@ def test_infinite_queries_beside_masked_places(cache, act, channel):
     out, lse = _attend(b, q)
     assert (out[:, 1] == 0).all() and torch.isneginf(lse[:, 1]).all()
     assert torch.isfinite(out).all() and torch.isfinite(lse[:, [0, 2, 3]]).all()
+
+
+@pytest.mark.parametrize("lens,H", [([300], 2), ([3000], 1)])  # one launch, two launches
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("size", [-130, -142, -147])
+def test_selection_of_scores_below_fp32s_normal_range(lens, H, cache, size):
+    """Products that FP32 rounds to a few bits or to nothing (FP16's have none such): the order is that of the exact scores all the same."""
+    b = _bounds_only(lens, 1, H, "bf16", seed=-size)
+    g = _gen(-size)
+    n = b.bounds.shape[0]
+    small = torch.rand((n, H, 2, D), generator=g, device="cuda")
+    small[::3, :, :, 5:] = 0  # pages of few large terms beside pages of many small ones
+    small[::3] *= 60
+    e_bounds = size // 2 if cache == "bf16" else -6
+    b.dt = DT[cache]
+    b.bounds = (small.double() * 2.0**e_bounds).to(b.dt)
+    b.cache = kvq.PagedCache(1, H, key_bounds=b.bounds)
+    q = torch.randn((len(lens), 2 * H, D), generator=g, device="cuda").abs()
+    q = (q.double() * 2.0 ** (size - e_bounds)).bfloat16()
+    _check_selection(b, q, 40, 0, 0)
+    _check_selection(b, -q, 41, 1, 1)
+
+
+def test_selection_of_a_page_of_many_terms_below_the_smallest_number():
+    """A score of 51 * 2^-149 whose terms FP32 rounds to zero, beside one of 2^-149 that it does not."""
+    b = _bounds_only([2], 1, 1, "bf16")
+    first, second = (int(b.table[0, i]) for i in (0, 1))
+    b.bounds.zero_()
+    b.bounds[first, 0, 1] = 1.6 * 2.0**-76
+    b.bounds[second, 0, 1, 9] = 2.0**-74
+    q = torch.full((1, 1, D), 2.0**-75, dtype=torch.bfloat16, device="cuda")
+    sel = kvq.kvq_paged_select(b.cache, b.table, b.seq, q, 1, n_first=0, n_last=0)
+    assert sel.flatten().tolist() == [0]
