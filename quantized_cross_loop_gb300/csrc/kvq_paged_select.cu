@@ -61,6 +61,17 @@ __device__ __forceinline__ uint64_t key_of(double x) {
   return (u >> 63) ? ~u : (u | (1ull << 63));
 }
 
+// All pages of a unit with no more than n_select, and -1 behind them; their numbers are looked at for the error bit, by
+// one of the request's units.
+__device__ __forceinline__ void take_all(const SelectArgs& a, int b, int h, int pages, int32_t* sel) {
+  for (int i = threadIdx.x; i < a.n_select; i += blockDim.x) sel[i] = i < pages ? i : -1;
+  if (h != 0 || a.c.err == nullptr) return;
+  for (int i = threadIdx.x; i < pages; i += blockDim.x) {
+    const int page = a.table[(long long)b * a.max_pages + i];
+    if (page < 0 || page >= a.c.n_pages) flag(a.c, KVQ_PAGED_ERR_PAGE);
+  }
+}
+
 struct Workspace {
   uint32_t* keys;   // [units][max_pages rounded up to 4]
   float* largest;   // [units][chunks]: A of the chunk
@@ -704,10 +715,7 @@ __global__ void __launch_bounds__(kPickThreads) pick_kernel(SelectArgs a, Worksp
   const int b = int(blockIdx.x) / a.c.H, h = int(blockIdx.x) % a.c.H, tid = threadIdx.x;
   const int pages = pages_of(a, checked_len(a.lens, b, a.max_pages, a.c.ps));
   int32_t* sel = a.sel + unit * a.n_select;
-  if (pages <= a.n_select) {  // all of them, and -1 behind
-    for (int i = tid; i < a.n_select; i += kPickThreads) sel[i] = i < pages ? i : -1;
-    return;
-  }
+  if (pages <= a.n_select) return take_all(a, b, h, pages, sel);
   uint32_t* keys = ws.keys + unit * key_stride(a.max_pages);
   const float* l = ws.largest + unit * chunks_of(a.max_pages, kChunk);
   const int chunks = chunks_of(pages, Scorer<DT, QT>::kPages);
@@ -748,10 +756,7 @@ __global__ void __launch_bounds__(kFusedThreads, 2) select_kernel(SelectArgs a, 
   const int T = checked_len(a.lens, b, a.max_pages, a.c.ps), pages = pages_of(a, T);
   if (T < 0 && tid == 0) flag(a.c, KVQ_PAGED_ERR_LENGTH);
   int32_t* sel = a.sel + unit * a.n_select;
-  if (pages <= a.n_select) {  // all of them, and -1 behind
-    for (int i = tid; i < a.n_select; i += kFusedThreads) sel[i] = i < pages ? i : -1;
-    return;
-  }
+  if (pages <= a.n_select) return take_all(a, b, h, pages, sel);
   using K = Scorer<DT, QT>;
   K score;
   static_assert(sizeof(Pick) <= kScoreWarps * kRing, "the pick's memory takes the rings' place");

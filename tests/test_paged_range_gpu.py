@@ -171,3 +171,21 @@ def test_selection_of_a_page_of_many_terms_below_the_smallest_number():
     q = torch.full((1, 1, D), 2.0**-75, dtype=torch.bfloat16, device="cuda")
     sel = kvq.kvq_paged_select(b.cache, b.table, b.seq, q, 1, n_first=0, n_last=0)
     assert sel.flatten().tolist() == [0]
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_selection_that_takes_all_pages_checks_them(wide):
+    """A page outside the pool sets the error bit also where no page has to be scored (one launch, two launches)."""
+    b = Batch([100, 90, 1600], 16, 2, "bf16")
+    if wide:
+        pad = torch.full((3, 3000 - b.table.shape[1]), 1 << 30, dtype=torch.int32, device="cuda")
+        b.table = torch.cat([b.table, pad], 1).contiguous()
+    q = _query(3, 8)
+    good = kvq.kvq_paged_select(b.cache, b.table, b.seq, q, 9)
+    assert b.cache.error_word() == 0
+    for bad in (b.cache.n_pages, -1):
+        table = b.table.clone()
+        table[1, 5] = bad  # the last of six
+        sel = kvq.kvq_paged_select(b.cache, table, b.seq, q, 9)
+        assert torch.equal(sel, good) and b.cache.error_word() == kvq.PAGED_ERR_PAGE
+        b.cache.clear_error()
