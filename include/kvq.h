@@ -594,8 +594,8 @@ typedef struct kvq_paged_rows {
 /*
  * Append: row i of request b is token start[b] + i. Its key is rotated (x' =
  * x cos - y sin, y' = y cos + x sin in FP32, one rounding at the end), its value
- * copied, both stored on the token's page (E4M3: divided by the head's scale,
- * rounded to nearest, saturated at 448); the page's key bounds take in the new
+ * copied, both stored on the token's page (E4M3: divided by the head's scale in
+ * FP32, rounded to nearest, ties to even, saturated at 448); the page's key bounds take in the new
  * keys, and start afresh on a page whose first place is written. Queries are
  * rotated the same way into q_out. start is not changed.
  * No page may take rows of two requests, or from two table entries, in one call.

@@ -28,6 +28,8 @@
 // Rows in flight and resident warps bound these; staging the rotation table in
 // shared memory for eight heads, and fetching the next rows into registers ahead of
 // the arithmetic, were slower (a table's row is in L1 for the heads that follow).
+#include <type_traits>
+
 #include "kvq_attn_common.cuh"
 #include "kvq_paged.cuh"
 
@@ -172,13 +174,44 @@ __device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) {
   }
 }
 
+// A head's scale for storing E4M3: the code of the FP32 quotient x / s, rounded to nearest, ties to even. lo and hi are
+// the scale's reciprocal less and more 2^-20, so that x lo and x hi lie on either side of the quotient (all roundings,
+// of a reciprocal below FP32's normal range too, come to less than 2^-20): where both have the same code it is the
+// quotient's, else (one value in some 2^14) the row's values are divided. A power of two has an exact reciprocal: lo and
+// hi are that. (8-bit chunks 21.9 us; one product without the check 20.9, which stored ties wrongly; divisions out of
+// line, or a branch for every four values, 22.8.)
+struct Quotient {
+  float lo, hi, s;
+  __device__ __forceinline__ void open(const float* scale, int h) {
+    s = scale != nullptr ? scale[h] : 1.0f;
+    const float r = __frcp_rn(s);
+    const bool exact = fmaf(r, s, -1.0f) == 0.0f;
+    lo = exact ? r : r * (1.0f - 0x1p-20f);
+    hi = exact ? r : r * (1.0f + 0x1p-20f);
+  }
+  __device__ __forceinline__ static uint32_t codes(const float4& x, float r) {
+    uint32_t c;
+    store4<kE4m3>(&c, times(x, r));
+    return c;
+  }
+};
+__device__ __forceinline__ uint32_t divided(const float4& x, float s) {
+  uint32_t c;
+  store4<kE4m3>(&c, make_float4(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s), __fdiv_rn(x.z, s), __fdiv_rn(x.w, s)));
+  return c;
+}
+
 // What a team does to one (page, head): where rows come from and go to.
 template <int DT, int IN>
 struct Unit {
+  using Word = std::conditional_t<DT == kE4m3, uint32_t, uint2>;  // four stored channels
+  struct Stored {
+    Word k[2], v[2];
+  };
   bool is_q, live;  // live: the page is in the pool
   bool any;
   int h, page, place0, first, last, start, row0;
-  float ks, vs;           // E4M3: reciprocals of the scales (two roundings of 2^-24 instead of one, before one of 2^-4)
+  Quotient ks, vs;        // E4M3
   uint32_t lo[4], hi[4];  // bounds of the lane's channels, 16-bit pairs
 
   __device__ __forceinline__ void open(const AppendArgs& a, int b, int page_of_request, int hh, int s, int r0, int n) {
@@ -191,8 +224,11 @@ struct Unit {
     page = a.table[(long long)b * a.max_pages + page_of_request];
     is_q = hh >= a.c.H;
     h = is_q ? hh - a.c.H : hh;
-    ks = DT == kE4m3 && !is_q && a.c.k_scale != nullptr ? __frcp_rn(a.c.k_scale[h]) : 1.0f;
-    vs = DT == kE4m3 && !is_q && a.c.v_scale != nullptr ? __frcp_rn(a.c.v_scale[h]) : 1.0f;
+    if constexpr (DT == kE4m3)
+      if (!is_q) {
+        ks.open(a.c.k_scale, h);
+        vs.open(a.c.v_scale, h);
+      }
     any = false;
     constexpr uint32_t kInf = DT == kBf16 ? 0x7F807F80u : 0x7C007C00u;
 #pragma unroll
@@ -224,26 +260,38 @@ struct Unit {
     store4<IN>(p + 2 * L.a, x.a);
     store4<IN>(p + 2 * L.b, x.b);
   }
-  __device__ __forceinline__ void put(const Lane& L, char* k, char* w, Wide x, const Raw& v) {
-    constexpr int kE = elem_bytes<DT>();
+  // A row as it is stored.
+  __device__ __forceinline__ Stored stored(const Wide& x, const Raw& v) const {
+    Stored r;
     if constexpr (DT == kE4m3) {
-      x.a = times(x.a, ks);
-      x.b = times(x.b, ks);
-      store4<DT>(w + L.a, times(load4<IN>(&v.a), vs));
-      store4<DT>(w + L.b, times(load4<IN>(&v.b), vs));
+      const Wide y{load4<IN>(&v.a), load4<IN>(&v.b)};
+      r.k[0] = Quotient::codes(x.a, ks.lo);
+      r.k[1] = Quotient::codes(x.b, ks.lo);
+      r.v[0] = Quotient::codes(y.a, vs.lo);
+      r.v[1] = Quotient::codes(y.b, vs.lo);
+      if (((r.k[0] ^ Quotient::codes(x.a, ks.hi)) | (r.k[1] ^ Quotient::codes(x.b, ks.hi)) |
+           (r.v[0] ^ Quotient::codes(y.a, vs.hi)) | (r.v[1] ^ Quotient::codes(y.b, vs.hi))) != 0u) {
+        r.k[0] = divided(x.a, ks.s);
+        r.k[1] = divided(x.b, ks.s);
+        r.v[0] = divided(y.a, vs.s);
+        r.v[1] = divided(y.b, vs.s);
+      }
     } else {
-      *reinterpret_cast<uint2*>(w + kE * L.a) = v.a;
-      *reinterpret_cast<uint2*>(w + kE * L.b) = v.b;
+      r.v[0] = v.a;
+      r.v[1] = v.b;
+      store4<DT>(&r.k[0], x.a);
+      store4<DT>(&r.k[1], x.b);
     }
-    alignas(8) char stored[2][4 * kE];
-    store4<DT>(stored[0], x.a);
-    store4<DT>(stored[1], x.b);
+    return r;
+  }
+  __device__ __forceinline__ void put(const Lane& L, char* k, char* w, const Stored& r) {
+    constexpr int kE = elem_bytes<DT>();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      char* to = k + kE * (i == 0 ? L.a : L.b);
-      if constexpr (DT == kE4m3) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(stored[i]);
-      else *reinterpret_cast<uint2*>(to) = *reinterpret_cast<const uint2*>(stored[i]);
-      const uint2 y = pairs_of<DT>(stored[i]);
+      const int at = kE * (i == 0 ? L.a : L.b);
+      *reinterpret_cast<Word*>(w + at) = r.v[i];
+      *reinterpret_cast<Word*>(k + at) = r.k[i];
+      const uint2 y = pairs_of<DT>(reinterpret_cast<const char*>(&r.k[i]));
       lo[2 * i] = smaller<DT>(lo[2 * i], y.x);
       lo[2 * i + 1] = smaller<DT>(lo[2 * i + 1], y.y);
       hi[2 * i] = larger<DT>(hi[2 * i], y.x);
@@ -329,7 +377,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocksPerSm) append_step_ke
           u.put_query(L, u.query_out(a, start), y);
         } else {
           const long long place = u.place(a, start);
-          u.put(L, a.c.k + place, a.c.v + place, y, v);
+          u.put(L, a.c.k + place, a.c.v + place, u.stored(y, v));
           u.close(a, L);
         }
       }
@@ -428,7 +476,7 @@ __global__ void __launch_bounds__(kManyThreads, kKeyBlocksPerSm) append_keys_ker
       for (int i = 0; i < kKeyRows; ++i) {
         if (!ok[i]) continue;
         const long long place = u.place(a, t0 + i * step);
-        u.put(L, a.c.k + place, a.c.v + place, rotate<IN, INTER>(L, g[i], x[i]), y[i]);
+        u.put(L, a.c.k + place, a.c.v + place, u.stored(rotate<IN, INTER>(L, g[i], x[i]), y[i]));
       }
     }
     if (a.c.bounds == nullptr) continue;

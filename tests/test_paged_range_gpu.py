@@ -189,3 +189,36 @@ def test_selection_that_takes_all_pages_checks_them(wide):
         sel = kvq.kvq_paged_select(b.cache, table, b.seq, q, 9)
         assert torch.equal(sel, good) and b.cache.error_word() == kvq.PAGED_ERR_PAGE
         b.cache.clear_error()
+
+
+SCALES = [7.0, 49.0, 3.0, 5.0, 9.0, 11.0, 13.0, 1.0, 0.5, 0.1, 0.3, 1e-30, 3.1e30, 3.0e38, 1.2e-38, 2.0**127]
+
+
+@pytest.mark.parametrize("act", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [1, 64])
+def test_e4m3_append_of_every_number(act, rows):
+    """Every 16-bit number, keys and values, by scales with and without an exact reciprocal: the stored code is that of
+    the FP32 quotient rounded to nearest even and saturated; the page's bounds are of the codes stored."""
+    H = len(SCALES)
+    x = torch.arange(-(1 << 15), 1 << 15, dtype=torch.int32).to(torch.int16).view(DT[act]).view(-1, 1, D).expand(-1, H, D)
+    n = x.shape[0]
+    B = n // rows
+    ks, vs = torch.tensor(SCALES), torch.tensor(SCALES[::-1])
+    cache = kvq.PagedCache.empty(B, rows, H, torch.float8_e4m3fn, key_bounds=True, k_scale=ks.cuda(), v_scale=vs.cuda())
+    table = torch.randperm(B, generator=torch.Generator().manual_seed(1)).int()
+    off = None if rows == 1 else torch.arange(0, n + 1, rows, dtype=torch.int32, device="cuda")
+    dev = x.contiguous().cuda()
+    kvq.kvq_paged_append(cache, table.cuda().view(B, 1), torch.zeros(B, dtype=torch.int32, device="cuda"), dev, dev, offsets=off)
+    assert cache.error_word() == 0
+    for pool, s in ((cache.k, ks), (cache.v, vs)):
+        want = (x.float() / s[:, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(B, rows, H, D)
+        got = _raw(pool).cpu()[table.long()].view(torch.float8_e4m3fn)
+        nan = torch.isnan(want.float())
+        assert torch.equal(torch.isnan(got.float()), nan)
+        same = _raw(got) == _raw(want)
+        assert (same | nan).all(), [(SCALES, i) for i in (~(same | nan)).nonzero()[:4].tolist()]
+        if pool is cache.k:
+            lo, hi = cache.key_bounds.float().cpu()[table.long()].unbind(2)
+            w = want.float()
+            assert torch.equal(torch.nan_to_num(lo, 999.0), torch.nan_to_num(w.amin(1), 999.0))
+            assert torch.equal(torch.nan_to_num(hi, 999.0), torch.nan_to_num(w.amax(1), 999.0))
