@@ -609,7 +609,8 @@ kvq_status kvq_paged_append(const kvq_paged_cache* cache, const int32_t* page_ta
                             const kvq_paged_rows* rows, kvq_cuda_stream stream);
 
 /* Workspace bytes that satisfy kvq_paged_decode_attn, kvq_paged_select and
- * kvq_paged_sparse_attn on the current device. 0 for invalid sizes. */
+ * kvq_paged_sparse_attn on the current device. The attention calls take no more
+ * than for max_pages 0, whatever their table's width. 0 for invalid sizes. */
 size_t kvq_paged_workspace_bytes(int n_requests, int n_heads, int n_q_heads, int max_pages);
 
 /*

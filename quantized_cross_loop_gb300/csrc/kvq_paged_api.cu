@@ -132,11 +132,9 @@ kvq_status check_query(const kvq_paged_cache* c, int n_requests, const int32_t* 
   return KVQ_OK;
 }
 
-kvq_status check_workspace(const kvq_paged_cache* c, void* workspace, size_t bytes, int n_requests, int n_q_heads,
-                           int max_pages) {
-  const size_t need = kvq_paged_workspace_bytes(n_requests, c->n_heads, n_q_heads, max_pages);
-  if (need == 0) return fail(KVQ_ERR_CUDA, "no usable CUDA device");
-  if (workspace == nullptr || bytes < need)
+// need: what this call uses of it, no more.
+kvq_status check_workspace(void* workspace, size_t bytes, size_t need) {
+  if (need > 0 && (workspace == nullptr || bytes < need))
     return fail(KVQ_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", workspace ? bytes : size_t(0), need);
   if (!aligned16(workspace)) return fail(KVQ_ERR_MISALIGNED, "workspace must be 16-byte aligned");
   return KVQ_OK;
@@ -157,7 +155,9 @@ kvq_status attend(const kvq_paged_cache* cache, const int32_t* page_table, int m
   if (n_requests == 0) return ok();
   if (out == nullptr) return fail(KVQ_ERR_BAD_ARG, "out is NULL");
   if (!aligned16(out)) return fail(KVQ_ERR_MISALIGNED, "out must be 16-byte aligned");
-  st = check_workspace(cache, workspace, workspace_bytes, n_requests, n_q_heads, max_pages);
+  a.sms = current_sms();
+  if (a.sms == 0) return fail(KVQ_ERR_CUDA, "no usable CUDA device");
+  st = check_workspace(workspace, workspace_bytes, paged::attn_workspace(n_requests, cache->n_heads, n_q_heads, a.sms));
   if (st != KVQ_OK) return st;
   a.table = page_table;
   a.max_pages = max_pages;
@@ -175,7 +175,6 @@ kvq_status attend(const kvq_paged_cache* cache, const int32_t* page_table, int m
   a.out = out;
   a.lse = lse;
   a.ws = static_cast<char*>(workspace);
-  a.sms = current_sms();
   return cuda_status(paged::launch_attn(a, reinterpret_cast<cudaStream_t>(stream)), "paged attention launch");
 }
 
@@ -288,7 +287,9 @@ kvq_status kvq_paged_select(const kvq_paged_cache* cache, const int32_t* page_ta
     return fail(KVQ_ERR_BAD_ARG, "n_select %d n_first %d n_last %d", n_select, n_first, n_last);
   if (n_requests == 0) return ok();
   if (sel == nullptr) return fail(KVQ_ERR_BAD_ARG, "sel is NULL");
-  st = check_workspace(cache, workspace, workspace_bytes, n_requests, n_q_heads, max_pages);
+  a.sms = current_sms();
+  if (a.sms == 0) return fail(KVQ_ERR_CUDA, "no usable CUDA device");
+  st = check_workspace(workspace, workspace_bytes, paged::select_workspace(n_requests, cache->n_heads, max_pages));
   if (st != KVQ_OK) return st;
   a.table = page_table;
   a.max_pages = max_pages;
@@ -304,7 +305,6 @@ kvq_status kvq_paged_select(const kvq_paged_cache* cache, const int32_t* page_ta
   a.n_last = n_last;
   a.sel = sel;
   a.ws = static_cast<char*>(workspace);
-  a.sms = current_sms();
   return cuda_status(paged::launch_select(a, reinterpret_cast<cudaStream_t>(stream)), "page selection launch");
 }
 

@@ -862,7 +862,8 @@ class PagedCache:
         return cls(page_size, n_heads, k, v, bounds, k_scale, v_scale)
 
     def workspace_bytes(self, n_requests: int, n_q_heads: int, max_pages: int) -> int:
-        """Workspace of the attention and selection calls for these sizes (kvq_paged_workspace_bytes)."""
+        """Workspace of the attention and selection calls for these sizes (kvq_paged_workspace_bytes); with max_pages 0
+        that of the attention calls alone, for tables of any width."""
         with torch.cuda.device(self.device):
             return int(lib().kvq_paged_workspace_bytes(n_requests, self.n_heads, n_q_heads, max_pages))
 
@@ -1010,7 +1011,7 @@ def _paged_attend(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, 
     else:
         out_ptr = _ptr(cache, out, "out", torch.float32, (B, Hq, 128))
     lse_ptr = None if lse is None else _ptr(cache, lse, "lse", torch.float32, (B, Hq))
-    ws = _paged_workspace(cache, workspace, B, Hq, W)
+    ws = _paged_workspace(cache, workspace, B, Hq, 0)
     raw = _raw_stream(cache.index)
     if sel is None:
         st = cache.lib.kvq_paged_decode_attn(cache.ref, tab, W, B, lens, q.data_ptr(), qdt, stride, Hq, softmax_scale,

@@ -222,3 +222,29 @@ def test_e4m3_append_of_every_number(act, rows):
             w = want.float()
             assert torch.equal(torch.nan_to_num(lo, 999.0), torch.nan_to_num(w.amin(1), 999.0))
             assert torch.equal(torch.nan_to_num(hi, 999.0), torch.nan_to_num(w.amax(1), 999.0))
+
+
+def test_attention_needs_its_own_workspace_only():
+    """A table of many pages costs the attention nothing: its workspace is that of a table without pages."""
+    b = Batch([300, 40], 16, 2, "bf16")
+    q = _query(2, 8)
+    out, lse = _attend(b, q)
+    small, large = (b.cache.workspace_bytes(2, 8, w) for w in (0, 1 << 20))
+    assert 0 < small < large // 4
+    ws = torch.empty(small, dtype=torch.uint8, device="cuda")
+    wide = torch.full((2, 1 << 16), -5, dtype=torch.int32, device="cuda")
+    wide[:, :b.table.shape[1]] = b.table
+    got = kvq.kvq_paged_decode_attn(b.cache, wide, b.seq, q, workspace=ws)
+    assert torch.equal(got, out)
+    sel = kvq.kvq_paged_select(b.cache, wide, b.seq, q, 5)
+    want = kvq.kvq_paged_sparse_attn(b.cache, b.table, b.seq, q, sel)
+    assert torch.equal(want, kvq.kvq_paged_sparse_attn(b.cache, wide, b.seq, q, sel, workspace=ws))
+    with pytest.raises(kvq.KvqError, match="WORKSPACE"):
+        kvq.kvq_paged_decode_attn(b.cache, wide, b.seq, q, workspace=ws[:small - 16])
+    with pytest.raises(kvq.KvqError, match="WORKSPACE"):
+        kvq.kvq_paged_select(b.cache, wide, b.seq, q, 5, workspace=ws)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    kvq.kvq_paged_decode_attn(b.cache, wide, b.seq, q)
+    assert torch.cuda.max_memory_allocated() - before < small + 4 * out.numel() * 4 + (1 << 16)
