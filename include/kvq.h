@@ -529,7 +529,9 @@ kvq_status kvq_decode_attn_packed_noalloc(const kvq_request* reqs, int n_request
  * beyond its table row, or whose pages are outside the pool, is refused (see
  * each call) and sets an error bit; nothing outside the pool is read or written.
  *
- * head_dim is 128 and Hq / H is 1..16 (any integer). Workspaces may be shared
+ * head_dim is 128 and Hq / H is 1..16 (any integer); a table row holds no more
+ * than 2^31 - 65536 tokens, a selection no more than 2^30 pages, and n_requests *
+ * H is below 2^27. Workspaces may be shared
  * by calls that follow one another on one stream; calls that may overlap need
  * one each. Every call can be captured into a CUDA graph; lengths, tables and
  * offsets are then read at replay.

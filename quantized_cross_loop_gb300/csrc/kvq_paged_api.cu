@@ -105,11 +105,20 @@ kvq_status check_cache(const kvq_paged_cache* c, int need, paged::View* v) {
   return KVQ_OK;
 }
 
+// Token, page and list positions are 32-bit numbers in the kernels, which step beyond the last one by a block's stride
+// (32768 at most).
+constexpr long long kMostTokens = 0x7FFFFFFFLL - 0xFFFF;
+constexpr int kMostSelected = 1 << 30;
+
+bool batch_fits(long long n_requests, int n_heads, long long max_pages) {
+  return n_requests * n_heads * KVQ_PAGED_MAX_G <= 0x7FFFFFFFLL && max_pages <= kMostTokens;
+}
+
 kvq_status check_batch(const kvq_paged_cache* c, const int32_t* page_table, int max_pages, int n_requests) {
   if (n_requests < 0 || max_pages < 0) return fail(KVQ_ERR_BAD_ARG, "n_requests %d max_pages %d", n_requests, max_pages);
-  if ((long long)max_pages * c->page_size > 0x7FFFFFFFLL - KVQ_PAGED_MAX_PAGE)  // token numbers are 32-bit
+  if ((long long)max_pages * c->page_size > kMostTokens)
     return fail(KVQ_ERR_BAD_ARG, "max_pages %d of %d tokens: beyond 2^31 tokens", max_pages, c->page_size);
-  if ((long long)n_requests * c->n_heads * KVQ_PAGED_MAX_G > 0x7FFFFFFFLL)
+  if (!batch_fits(n_requests, c->n_heads, max_pages))
     return fail(KVQ_ERR_BAD_ARG, "n_requests %d x n_heads %d", n_requests, c->n_heads);
   if (n_requests > 0 && max_pages > 0 && page_table == nullptr) return fail(KVQ_ERR_BAD_ARG, "page_table is NULL");
   return KVQ_OK;
@@ -247,7 +256,7 @@ kvq_status kvq_paged_append(const kvq_paged_cache* cache, const int32_t* page_ta
 size_t kvq_paged_workspace_bytes(int n_requests, int n_heads, int n_q_heads, int max_pages) {
   const int sms = current_sms();
   if (n_requests < 0 || n_heads < 1 || n_heads > 1024 || n_q_heads < n_heads || n_q_heads % n_heads != 0 ||
-      n_q_heads / n_heads > KVQ_PAGED_MAX_G || max_pages < 0 || sms == 0)
+      n_q_heads / n_heads > KVQ_PAGED_MAX_G || max_pages < 0 || !batch_fits(n_requests, n_heads, max_pages) || sms == 0)
     return 0;
   const size_t a = paged::attn_workspace(n_requests, n_heads, n_q_heads, sms);
   const size_t b = paged::select_workspace(n_requests, n_heads, max_pages);
@@ -267,7 +276,7 @@ kvq_status kvq_paged_sparse_attn(const kvq_paged_cache* cache, const int32_t* pa
                                  int64_t q_stride, int n_q_heads, const int32_t* sel, int n_select,
                                  float softmax_scale, float* out, float* lse, void* workspace,
                                  size_t workspace_bytes, kvq_cuda_stream stream) {
-  if (n_select < 1) return fail(KVQ_ERR_BAD_ARG, "n_select %d", n_select);
+  if (n_select < 1 || n_select > kMostSelected) return fail(KVQ_ERR_BAD_ARG, "n_select %d", n_select);
   if (sel == nullptr && n_requests > 0) return fail(KVQ_ERR_BAD_ARG, "sel is NULL");
   return attend(cache, page_table, max_pages, n_requests, seq_lens, q, q_dtype, q_stride, n_q_heads, sel, n_select,
                 softmax_scale, out, lse, workspace, workspace_bytes, stream);
@@ -283,7 +292,7 @@ kvq_status kvq_paged_select(const kvq_paged_cache* cache, const int32_t* page_ta
   if (st == KVQ_OK) st = check_batch(cache, page_table, max_pages, n_requests);
   if (st == KVQ_OK) st = check_query(cache, n_requests, seq_lens, q, q_dtype, q_stride, n_q_heads);
   if (st != KVQ_OK) return st;
-  if (n_select < 1 || n_first < 0 || n_last < 0 || (long long)n_first + n_last > n_select)
+  if (n_select < 1 || n_select > kMostSelected || n_first < 0 || n_last < 0 || (long long)n_first + n_last > n_select)
     return fail(KVQ_ERR_BAD_ARG, "n_select %d n_first %d n_last %d", n_select, n_first, n_last);
   if (n_requests == 0) return ok();
   if (sel == nullptr) return fail(KVQ_ERR_BAD_ARG, "sel is NULL");

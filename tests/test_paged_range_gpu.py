@@ -248,3 +248,10 @@ def test_attention_needs_its_own_workspace_only():
     torch.cuda.reset_peak_memory_stats()
     kvq.kvq_paged_decode_attn(b.cache, wide, b.seq, q)
     assert torch.cuda.max_memory_allocated() - before < small + 4 * out.numel() * 4 + (1 << 16)
+
+
+def test_workspace_bytes_of_sizes_beyond_any_call():
+    b = Batch([64, 3], 16, 2, "bf16")
+    assert b.cache.workspace_bytes(2, 8, 2**31 - 65536) > 0
+    for n, hq, width in ((2, 8, 2**31 - 65535), (2, 8, 2**31 - 1), (1 << 26, 8, 0), (2**31 - 1, 2, 0)):
+        assert b.cache.workspace_bytes(n, hq, width) == 0
