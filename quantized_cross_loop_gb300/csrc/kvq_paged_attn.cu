@@ -27,11 +27,13 @@
 // QK^T with the heads as the 16 rows of mma.m16n8k16 and the tokens as columns:
 // its result then is, register for register, the transposed operand of the second
 // product out^T = V^T P^T, so the softmax weights never leave their lane.
-// Exactness: products of 16-bit values are exact; P is split into parts whose sum
-// is P (three of BF16, two of FP16), because one 8- or 11-bit P would cost 2^-9 or
-// 2^-12 of the FP32 result. The tensor cores cut their sums off, so every 16
-// tokens' product starts from zero and is added to the running sum by FP32 FMA,
-// which also applies the rescaling.
+// Exactness: products of 16-bit values are exact; P is split into parts, because one 8-
+// or 11-bit P would cost 2^-9 or 2^-12 of the FP32 result: three of BF16, whose sum is
+// P, or two of FP16, which leave out 2^-23 of a weight or 2^-39 of the unit's largest,
+// whichever is more (of the product alone: the weights' sum is FP32's). A third part of
+// FP16 would be a third more products for less than FP32 sums lose anyway. The tensor
+// cores cut their sums off, so every 16 tokens' product starts from zero and is added to
+// the running sum by FP32 FMA, which also applies the rescaling.
 // E4M3: keys and values become FP16 in registers (exact). A BF16 query becomes FP16 by
 // a power of two per head that brings its largest channel into [2^15, 2^16): exact
 // down to 2^-17, where FP16's step of 2^-24 is the last of eight bits. A head with a
@@ -161,8 +163,8 @@ __device__ __forceinline__ uint32_t pack_half(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// (a, b) as parts whose sum is the value: hi, mid, lo of BF16 by cutting eight
-// bits off at a time (exact), or hi, lo of FP16 (22 bits).
+// (a, b) as parts: hi, mid, lo of BF16 by cutting eight bits off at a time (their sum
+// is the value), or hi, lo of FP16 (22 bits of it).
 template <bool HALF>
 __device__ __forceinline__ void split(float a, float b, uint32_t (&part)[3]) {
   if constexpr (HALF) {

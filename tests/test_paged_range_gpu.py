@@ -255,3 +255,45 @@ def test_workspace_bytes_of_sizes_beyond_any_call():
     assert b.cache.workspace_bytes(2, 8, 2**31 - 65536) > 0
     for n, hq, width in ((2, 8, 2**31 - 65535), (2, 8, 2**31 - 1), (1 << 26, 8, 0), (2**31 - 1, 2, 0)):
         assert b.cache.workspace_bytes(n, hq, width) == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp16", "e4m3"])
+def test_softmax_weights_keep_their_bits(cache):
+    """Two tokens a request, values 0 and 1, logits 0 and s (one channel, exact): out is the second weight.
+
+    Errors, relative to it, s in (-8, 0]: the scale's log2 e and the argument of exp2 (below 16, or 2^4, in FP16's and
+    E4M3's shifted form, half a step of 2^-20 times ln 2): 2^-24 |s| 2 + 2^-21; exp2 itself 2^-22; all that for both
+    weights; the split 2^-22 (FP16, E4M3: two parts of 11 bits) or none (BF16: three of 8); sums of two terms in the
+    tensor cores, cut off by a step of 2^-23 each, the merge of four warps, division and product: 8 * 2^-23 in all.
+    A weight without its last part is off by up to 2^-16 (BF16) or 2^-11."""
+    n = 64
+    g = _gen(9)
+    logit = torch.linspace(-7.9, 0.0, n, device="cuda")
+    act = "fp16" if cache == "fp16" else "bf16"
+    b = Batch([2] * n, 2, 1, cache, seed=1, bounds=False)
+    b.cache.k.copy_(torch.zeros_like(b.cache.k.float()).to(b.dt))
+    if cache == "e4m3":  # few codes: the logits' spread comes from the query
+        b.k_scale.fill_(1.0)
+        b.v_scale.fill_(1.0)
+    pages = b.table[:, 0].long()
+    keys = torch.full((n,), -1.0, device="cuda").to(b.dt)
+    _raw(b.k)[pages, 1, 0, 3] = _raw(keys)
+    one = torch.ones((n, D), device="cuda").to(b.dt)
+    _raw(b.v)[pages, 0, 0] = 0
+    _raw(b.v)[pages, 1, 0] = _raw(one)
+    q = torch.zeros((n, 2, D), device="cuda").to(DT[act])
+    q[:, 0, 3] = (-logit).to(DT[act])
+    q[:, 1, 3] = (-logit * torch.rand(n, generator=g, device="cuda")).to(DT[act])
+    out, lse = _attend(b, q, softmax_scale=1.0)
+    s = -q[..., 3].double()
+    p = s.exp()
+    want = p / (1 + p)
+    tol = 2 * (2.0**-23 * s.abs() + 2.0**-21 + 2.0**-22) + (0 if cache == "bf16" else 2.0**-22) + 8 * 2.0**-23
+    err = (out.double() - want[..., None]).abs() / want[..., None]
+    assert (err <= tol[..., None]).all(), (err / tol[..., None]).max()
+    assert ((lse.double() - torch.log1p(p)).abs() <= tol + 2.0**-22).all()
+    # the tolerance tells a weight whose last part is missing: the definition with such weights is outside of it
+    bits = 16 if cache == "bf16" else 11
+    unit = torch.exp2(torch.floor(torch.log2(p)) + 1 - bits)
+    cut = (torch.floor(p / unit) if cache == "bf16" else torch.round(p / unit)) * unit
+    assert ((cut / (1 + p) - want).abs() / want > tol).sum() > n // 2
