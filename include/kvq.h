@@ -626,8 +626,11 @@ size_t kvq_paged_workspace_bytes(int n_requests, int n_heads, int n_q_heads, int
  * Query head hq reads KV head hq / (Hq/H); softmax and sums are FP32, so that
  * q.k, and |v| summed over the tokens, have to lie within FP32's range; a value
  * that is not finite among those attended to makes its channel NaN or infinite
- * (what lies in other places of a page is not read). A request without tokens, and one whose keys all weigh
- * nothing (q.k = -inf), gets out 0 and lse -inf, a refused one NaN in both.
+ * (what lies in other places of a page is not read). BF16 queries of an E4M3
+ * cache whose channels differ by more than 2^32 within a head are right, but slow
+ * (that head goes without the tensor cores). A request without tokens, and one
+ * whose keys all weigh nothing (q.k = -inf), gets out 0 and lse -inf, a refused
+ * one NaN in both.
  */
 kvq_status kvq_paged_decode_attn(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages,
                                  int n_requests, const int32_t* seq_lens, const void* q, int q_dtype,

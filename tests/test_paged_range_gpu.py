@@ -99,6 +99,35 @@ def test_e4m3_attention_of_far_apart_channels_in_some_heads(g, requests):
     assert torch.isnan(out[0, g:]).all() and torch.isfinite(out[0, :g]).all()
 
 
+def test_captured_e4m3_attention_follows_the_queries():
+    """A captured call replayed with queries that FP16 holds and queries that it does not; two streams at once."""
+    b = Batch([700, 40, 90], 16, 2, "e4m3", seed=1)
+    _raw(b.k)[..., 0] = 0
+    for k in b.K:
+        k[..., 0] = 0
+    q, out, lse = _query(3, 8), torch.empty((3, 8, D), device="cuda"), torch.empty((3, 8), device="cuda")
+    ws = torch.empty(b.cache.workspace_bytes(3, 8, 0), dtype=torch.uint8, device="cuda")
+    kvq.kvq_paged_decode_attn(b.cache, b.table, b.seq, q, out=out, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvq.kvq_paged_decode_attn(b.cache, b.table, b.seq, q, out=out, lse=lse, workspace=ws)
+    seen = []
+    for turn, large in enumerate((1.0, 2.0**70, 1.0, 2.0**40)):
+        q.copy_(_query(3, 8, seed=turn))
+        q[turn % 3, turn::2, 0] = large
+        graph.replay()
+        torch.cuda.synchronize()
+        _compare(b, q, out, lse, 1 / math.sqrt(D))
+        seen.append((q.clone(), out.clone()))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [(want, kvq.kvq_paged_decode_attn(b.cache, b.table, b.seq, x, stream=streams[i % 2]))
+           for i, (x, want) in enumerate(seen * 5)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in got)
+
+
 @pytest.mark.parametrize("gain,k_scale,softmax_scale", [
     (2.0**-115, 2.0**-33, 0.1),      # the scales' product is below FP32's smallest number: all tokens weigh the same
     (2.0**126, 2.0**-78, 2.0**-78),  # ... beside queries of BF16's other end
