@@ -24,7 +24,7 @@
 // 64: 40 us by blocks, 46 by warps; pages of 16: 50 by blocks, 40 by warps), chosen by
 // each unit's own rows, and the ranges are equal in rows, not units: batches mix
 // prompts with requests of one row (a prompt of 2048 and 499 single rows, pages of 256:
-// 26 us; by equal counts of units, each a team's, 849).
+// 24 us; by equal counts of units, each a team's, 849).
 // Rows in flight and resident warps bound these; staging the rotation table in
 // shared memory for eight heads, and fetching the next rows into registers ahead of
 // the arithmetic, were slower (a table's row is in L1 for the heads that follow).
@@ -49,9 +49,10 @@ constexpr int kQueryHeads = 4;     // heads a team has in flight
 constexpr int kWarpRows = 32;      // rows of a unit that a warp takes by itself
 
 // Rows that the beginning and end of a unit count for: pages of up to kWarpRows take
-// a warp much the same time whatever they hold (nine prompts of up to 613 rows, 8-bit
-// pages of 16: 24.2 us with 64, 26.9 with 8), larger ones take a block their rows
-// (499 single rows and 2048, pages of 64: 20.7 us with 8, 29 with 32).
+// a warp much the same time whatever they hold (nine prompts of up to 613 rows, pages
+// of 16, with 64 and with 8: 8-bit 21.9, 24.6 us, 16-bit 21.3, 23.6), larger ones take a
+// block their rows (499 single rows and 2048, with 8 and with 32: pages of 64 21.6, 36.1
+// us, of 256 24.5, 39.8).
 __device__ __forceinline__ int unit_rows(int ps) { return ps <= kWarpRows ? 64 : 8; }
 
 // New rows of request b, or -1 when its start or offsets are outside their range.
@@ -584,8 +585,8 @@ cudaError_t launch_form(const AppendArgs& a, int sms, cudaStream_t stream) {
   }
   // More than two query heads per KV head: half as many blocks of each kernel, so that both fit on an SM and run side
   // by side; else the queries' blocks follow the keys' (4 x 2048 rows, pages of 64, side by side and one after the
-  // other: 8 + 32 heads 38.7, 40.1 us, 8 + 24 35.3, 35.0, 16 + 32 59.2, 52.4, 32 + 32 103, 80; nine prompts of up to
-  // 613 rows into 8-bit pages of 16, 8 + 32 heads 21.1, 24.2).
+  // other: 8 + 32 heads 37.3, 40.7 us, 8 + 24 33.9, 35.7, 16 + 32 55.7, 51.9, 32 + 32 92.6, 76.6; nine prompts of up to
+  // 613 rows into 8-bit pages of 16, 8 + 32 heads 21.9, 24.6; a prompt of 2048 and 499 single rows 24.5, 22.6).
   const int part = Hq > 2 * a.c.H ? 2 : 1;
   // the keys' blocks: eight units each, or (pages of more rows than a warp takes) one unit of 32 rows
   const long long units = (a.n_rows / a.c.ps.d + 2 * (long long)a.B) * a.c.H;  // at most

@@ -40,7 +40,7 @@
 // channel below that, 2^-32 of its largest (beside one that meets zero keys it may be
 // all that counts), is found by the attention kernel (WideHeads) and attended again by
 // FP32 multiply-adds, by the combine kernel: a branch or a call for such heads in the
-// attention kernel's loop cost all others up to 12%, by the registers that it moved.
+// attention kernel's loop cost all others 1 to 30%, by the registers that it moved.
 #include <atomic>
 
 #include "kvq_attn_common.cuh"
@@ -719,8 +719,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) attn_kernel(AttnArgs a
     W = S.prefix.pre[kThreads];
   }
   // The query heads loaded above are looked at here, or, more than eight a group, behind the first copies: ragged 8-bit
-  // requests, 4 heads 92.7 us here, 93.1 there, 12 heads 126.6, 118.4; 16 selected pages, 4 heads 37.5, 38.2, 16 heads
-  // 61.1, 53.6 (without the look 91.5, 125.8; 36.6, 59.7)
+  // requests, 4 heads 92.5 us here, 93.0 there, 12 heads 138.7, 124.2; 16 selected pages, 4 heads 37.8, 38.5, 16 heads
+  // 57.3, 55.6; 512 x 1000, 4 heads 190, 195 (without the look 91.5, 125.8; 36.6, 59.7; 188)
   constexpr bool kLate = NT == 2;
   if (!kLate) look();
   // requests without tokens, and refused ones: no block's range holds them
@@ -1047,8 +1047,8 @@ cudaError_t launch_form(const AttnArgs& a, cudaStream_t stream) {
 
 template <int DT, int QT>
 cudaError_t launch_types(const AttnArgs& a, cudaStream_t stream) {
-  // up to eight heads fill half of a product's rows: the form for 16 would do, but takes 7.9 us instead of 7.1 (one
-  // request of 256 tokens), 324 instead of 312 (512 x 1000) and 119 instead of 92 (64 ragged ones of 8-bit keys)
+  // up to eight heads fill half of a product's rows: the form for 16 would do, but takes 7.4 us instead of 6.7 (one
+  // request of 256 tokens), 322 instead of 312 (512 x 1000) and 116 instead of 92 (64 ragged ones of 8-bit keys)
   if (a.sel != nullptr)
     return a.g <= 8 ? launch_form<DT, QT, 1, true>(a, stream) : launch_form<DT, QT, 2, true>(a, stream);
   return a.g <= 8 ? launch_form<DT, QT, 1, false>(a, stream) : launch_form<DT, QT, 2, false>(a, stream);

@@ -142,10 +142,9 @@ __device__ __forceinline__ void wait_groups() {
 }
 
 // A warp scores a chunk of pages at a time, from a ring of its own that 16-byte
-// asynchronous copies fill (with loads into registers, however many in flight, the
-// bounds came at 5.1 TB/s). A page's bounds are 32 (16-bit) or 16 (E4M3) pieces of
-// 16 bytes; a lane holds the weights of its own 8 or 16 channels of lo or hi and
-// reads only what it copied itself.
+// asynchronous copies fill, so that two chunks are on their way without registers. A
+// page's bounds are 32 (16-bit) or 16 (E4M3) pieces of 16 bytes; a lane holds the
+// weights of its own 8 or 16 channels of lo or hi and reads only what it copied itself.
 template <int DT, int QT>
 struct Scorer {
   static constexpr int kPer = DT == kE4m3 ? 16 : 8;      // channels of a lane
