@@ -178,7 +178,7 @@ __device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) {
 // A head's scale for storing E4M3: the code of the FP32 quotient x / s, rounded to nearest, ties to even. lo and hi are
 // the scale's reciprocal less and more 2^-20, so that x lo and x hi lie on either side of the quotient (all roundings,
 // of a reciprocal below FP32's normal range too, come to less than 2^-20): where both have the same code it is the
-// quotient's, else (one value in some 2^14) the row's values are divided. A power of two has an exact reciprocal: lo and
+// quotient's, else (one value in some 2^15) the row's values are divided. A power of two has an exact reciprocal: lo and
 // hi are that. (8-bit chunks 21.9 us; one product without the check 20.9, which stored ties wrongly; divisions out of
 // line, or a branch for every four values, 22.8.)
 struct Quotient {

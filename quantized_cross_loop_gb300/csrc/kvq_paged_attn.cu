@@ -72,7 +72,8 @@ struct Rec {
 };
 __host__ __device__ constexpr bool rec_per_unit(long long units, int n_ctas) { return units <= n_ctas; }
 
-// Workspace: Rec[n], then 2 n slots of g heads x sum[128] and g x (m, l), then a byte per unit and head (wide_heads).
+// Workspace: Rec[n], then 2 n slots of g heads x sum[128] and g x (m, l), then a byte per unit and head
+// (wide_heads).
 __host__ __device__ constexpr size_t slots_offset(int n) { return (size_t(n) * sizeof(Rec) + 15) / 16 * 16; }
 __host__ __device__ constexpr size_t slot_floats(int g) { return size_t(g) * kD + (size_t(g) + 1) / 2 * 4; }  // (16-byte steps)
 
@@ -268,7 +269,7 @@ __device__ __forceinline__ int query_shift(float top) {
 }
 __device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 
-// Whether FP16 holds the query heads of each unit, a byte per head and kMaxGroup bytes per unit, behind the slots.
+// Query heads that FP16 does not hold: a byte per head that is not 0, kMaxGroup bytes per unit, behind the slots.
 __device__ __forceinline__ uint8_t* wide_heads(const AttnArgs& a, int n) {
   return reinterpret_cast<uint8_t*>(a.ws + slots_offset(n) + 2 * size_t(n) * slot_floats(a.g) * 4);
 }
@@ -366,8 +367,8 @@ struct Block {
       return make_uint2(*reinterpret_cast<const uint32_t*>(p + (16 * j + 2 * q) * 2),
                         *reinterpret_cast<const uint32_t*>(p + (16 * j + 2 * q + 8) * 2));
   }
-  // scale ks 2^shift, whose parts may leave FP32's range where the logits do not (a scale of 0 would make a masked place's
-  // logit NaN; with 2^-149 no logit is off by more than 2^-116).
+  // scale ks 2^shift, whose parts may leave FP32's range where the logits do not (a scale of 0 would make a masked
+  // place's logit NaN; with 2^-149 no logit is off by more than 2^-116).
   __device__ __forceinline__ static float scaled(float scale, float ks, int shift) {
     const uint32_t k = __float_as_uint(ks);
     const float x = ldexpf(scale * __uint_as_float((k & 0x7FFFFFu) | 0x3F800000u), int(k >> 23) - 127 + shift);
@@ -606,7 +607,8 @@ struct Block {
       return fmaxf(fmaxf(S.m[0][head], S.m[1][head]), fmaxf(S.m[2][head], S.m[3][head]));
     };
     float* mine = S.buf + (warp & 1) * 8 * kBufStride;
-    // (a slot's sums stay as they are: times the weights' 2^14, scaled values may leave FP32's range where the mean does not)
+    // (a slot's sums stay as they are: times the weights' 2^14, scaled values may leave FP32's range where the mean does
+    // not)
     const float vs = DT == kE4m3 && slot == nullptr && a.c.v_scale != nullptr ? a.c.v_scale[h] : 1.0f;
     if (threadIdx.x < a.g) {
       const float mx = top(threadIdx.x), base = mx == -INFINITY ? 0.0f : mx;
@@ -828,7 +830,7 @@ struct Joint {  // shared memory of the combine kernel
   alignas(16) float q[kD];
 };
 
-// Sum, maximum and sum of exponentials of `per` warps from `warp` on, in log2 units; every lane has its four channels of x.
+// Maximum (in log2 units), sum of weights and weighted sum of `per` warps from `warp` on; a lane has four channels of x.
 __device__ __forceinline__ void join_warps(const Joint& S, int warp, int per, int lane, float& top, float& l, float4& x) {
   top = S.m[warp];
   for (int w = 1; w < per; ++w) top = fmaxf(top, S.m[warp + w]);
@@ -953,7 +955,8 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(AttnArgs a, in
   auto look = [&](int u0) {
     const long long u = u0 + (long long)lane * gridDim.x;
     const uint64_t among = (~0ull >> (64 - 8 * heads)) << (8 * (j0 & 7));  // the block's heads
-    return __ballot_sync(0xFFFFFFFFu, u < units && (*reinterpret_cast<const uint64_t*>(wide + u * kMaxGroup + (j0 & 8)) & among) != 0);
+    const auto word = [&] { return *reinterpret_cast<const uint64_t*>(wide + u * kMaxGroup + (j0 & 8)); };
+    return __ballot_sync(0xFFFFFFFFu, u < units && (word() & among) != 0);
   };
   uint32_t again = 0u;
   if constexpr (NARROW) again = look(x0);
@@ -1041,8 +1044,8 @@ cudaError_t launch_form(const AttnArgs& a, cudaStream_t stream) {
   int most = 1;
   while (most < 8 && (long long)recs * ((a.g + most - 1) / most) > a.sms) most *= 2;
   count_launch();
-  return launch_dependent(combine_kernel<kNarrow<DT, QT>, kNarrow<DT, QT> && SEL>, dim3(recs, (a.g + most - 1) / most), dim3(kCombineThreads), 0, stream, a, n,
-                          lanes, most);
+  return launch_dependent(combine_kernel<kNarrow<DT, QT>, kNarrow<DT, QT> && SEL>,
+                          dim3(recs, (a.g + most - 1) / most), dim3(kCombineThreads), 0, stream, a, n, lanes, most);
 }
 
 template <int DT, int QT>

@@ -36,7 +36,7 @@ def test_positions_reach_no_kernel_without_a_rotation(tmp_path):
 
 
 def test_sizes_at_which_32_bit_positions_end_are_refused():
-    """Tables of nearly 2^31 tokens and lists of nearly 2^31 pages: a kernel's step beyond the last position would wrap."""
+    """Tables of nearly 2^31 tokens, lists of nearly 2^31 pages: a kernel's step beyond the last position would wrap."""
     kbuild.build()
     L = kvq.lib()
     c = kvq.kvq_paged_cache()

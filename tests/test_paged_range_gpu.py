@@ -159,7 +159,8 @@ def test_e4m3_attention_of_large_and_small_value_scales(v_scale):
 @pytest.mark.parametrize("cache,act", [("bf16", "bf16"), ("fp16", "fp16"), ("e4m3", "bf16"), ("e4m3", "fp16")])
 @pytest.mark.parametrize("channel", [7, 23])
 def test_infinite_queries_beside_masked_places(cache, act, channel):
-    """A query whose products with all keys are -inf finds nothing, also where the last tile has places without a token."""
+    """A query whose products with all keys are -inf finds nothing, also where the last tile has places without a
+    token."""
     b = Batch([16, 40, 3, 70], 16, 1, cache)
     _raw(b.k)[..., channel] = _raw(torch.full((1,), -2.0, device="cuda").to(b.dt))
     q = _query(4, 4, act)
@@ -173,7 +174,8 @@ def test_infinite_queries_beside_masked_places(cache, act, channel):
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
 @pytest.mark.parametrize("size", [-130, -142, -147])
 def test_selection_of_scores_below_fp32s_normal_range(lens, H, cache, size):
-    """Products that FP32 rounds to a few bits or to nothing (FP16's have none such): the order is that of the exact scores all the same."""
+    """Products that FP32 rounds to a few bits or to nothing (those of FP16 numbers are never that small): the order is
+    that of the exact scores all the same."""
     b = _bounds_only(lens, 1, H, "bf16", seed=-size)
     g = _gen(-size)
     n = b.bounds.shape[0]
@@ -237,7 +239,8 @@ def test_e4m3_append_of_every_number(act, rows):
     table = torch.randperm(B, generator=torch.Generator().manual_seed(1)).int()
     off = None if rows == 1 else torch.arange(0, n + 1, rows, dtype=torch.int32, device="cuda")
     dev = x.contiguous().cuda()
-    kvq.kvq_paged_append(cache, table.cuda().view(B, 1), torch.zeros(B, dtype=torch.int32, device="cuda"), dev, dev, offsets=off)
+    start = torch.zeros(B, dtype=torch.int32, device="cuda")
+    kvq.kvq_paged_append(cache, table.cuda().view(B, 1), start, dev, dev, offsets=off)
     assert cache.error_word() == 0
     for pool, s in ((cache.k, ks), (cache.v, vs)):
         want = (x.float() / s[:, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(B, rows, H, D)
