@@ -507,8 +507,10 @@ kvq_status kvq_decode_attn_packed_noalloc(const kvq_request* reqs, int n_request
  * kvq_append_tile_batch read ([64][H][D]) and what the BF16 tail of a request
  * points at.
  *
- *   dtype  of the stored keys, values and bounds: BF16, FP16, or E4M3 with one
- *          FP32 scale per KV head (value = stored * scale[h]).
+ *   dtype  of the stored keys, values and bounds: BF16, FP16, E4M3 with one
+ *          FP32 scale per KV head (value = stored * scale[h]), or E4M3 with one
+ *          FP32 scale per token and KV head, which kvq_paged_append makes from
+ *          the token's own largest magnitude (KVQ_DT_E4M3_TOKEN).
  *   k, v   element (page p, place s, head h, channel d) at
  *          p * page_stride + s * token_stride + h * head_stride + d, in
  *          elements; the strides are multiples of 16 bytes and describe places
@@ -519,6 +521,11 @@ kvq_status kvq_decode_attn_packed_noalloc(const kvq_request* reqs, int n_request
  *          and largest (1) stored key of a page per head and channel, kept by
  *          kvq_paged_append; NULL: none are kept (kvq_paged_select needs them).
  *   k_scale, v_scale  FP32 [n_heads], positive normal numbers, E4M3 only (NULL: 1).
+ *          KVQ_DT_E4M3_TOKEN: FP32 [n_pages][n_heads][page_size], written by
+ *          kvq_paged_append with the rows, neither NULL; such a cache keeps no
+ *          key bounds, and kvq_paged_tree_attn is what attends to it
+ *          (kvq_paged_decode_attn, kvq_paged_select and kvq_paged_sparse_attn
+ *          refuse it).
  *   error  DEVICE int32 or NULL: KVQ_PAGED_ERR_* bits are OR-ed in by the
  *          kernels and never cleared; the caller zeroes it.
  *
@@ -539,14 +546,18 @@ kvq_status kvq_decode_attn_packed_noalloc(const kvq_request* reqs, int n_request
 #define KVQ_DT_BF16 0
 #define KVQ_DT_FP16 1
 #define KVQ_DT_E4M3 2
+#define KVQ_DT_E4M3_TOKEN 4 /* E4M3, a scale per token and KV head (caches only) */
 
 #define KVQ_PAGED_ERR_LENGTH 1     /* a length, start or offset outside its range */
-#define KVQ_PAGED_ERR_SELECTION 32 /* a selection that is not ascending page numbers of its request */
+#define KVQ_PAGED_ERR_WAIT 8       /* a pipeline wait of kvq_paged_tree_attn that ran out (2 s): its output is not to be used */
+#define KVQ_PAGED_ERR_SELECTION 32 /* a selection that is not ascending page numbers of its request, or accepted tokens
+                                      that are not ascending */
 #define KVQ_PAGED_ERR_PAGE 128     /* a page number outside the pool */
 #define KVQ_PAGED_ERR_POSITION 256 /* a position outside the rotation table */
 
 #define KVQ_PAGED_MAX_PAGE 1024 /* largest page_size */
 #define KVQ_PAGED_MAX_G 16      /* query heads per KV head */
+#define KVQ_PAGED_MAX_DRAFT 1024 /* drafted tokens (rows) of a request in kvq_paged_tree_attn */
 
 typedef struct kvq_paged_cache {
   uint32_t version;   /* KVQ_FORMAT_VERSION */
@@ -597,7 +608,10 @@ typedef struct kvq_paged_rows {
  * Append: row i of request b is token start[b] + i. Its key is rotated (x' =
  * x cos - y sin, y' = y cos + x sin in FP32, one rounding at the end), its value
  * copied, both stored on the token's page (E4M3: divided by the head's scale in
- * FP32, rounded to nearest, ties to even, saturated at 448); the page's key bounds take in the new
+ * FP32, rounded to nearest, ties to even, saturated at 448; with a scale per token
+ * that is max(a / 448, 2^-126) of the rotated key's, or the value's, largest
+ * magnitude a, stored beside it: a row with a value that is not finite gets a scale
+ * that is not, and reads back as NaN throughout); the page's key bounds take in the new
  * keys, and start afresh on a page whose first place is written. Queries are
  * rotated the same way into q_out. start is not changed.
  * No page may take rows of two requests, or from two table entries, in one call.
@@ -669,6 +683,79 @@ kvq_status kvq_paged_sparse_attn(const kvq_paged_cache* cache, const int32_t* pa
                                  int64_t q_stride, int n_q_heads, const int32_t* sel, int n_select,
                                  float softmax_scale, float* out, float* lse, void* workspace,
                                  size_t workspace_bytes, kvq_cuda_stream stream);
+
+/*
+ * Rows back out of the cache: row i of request b is token start[b] + i, its key
+ * and value, times their scale in FP32 where the cache has one, rounded to
+ * out_dtype (BF16 or FP16). 64 tokens of a request read to BF16 rows without a gap
+ * ([64][H][128]) are a tile for kvq_append_tile and kvq_append_tile_batch, whatever
+ * the cache's own type and layout.
+ *   offsets  int32 [n_requests + 1] (device): rows offsets[b] .. offsets[b+1]-1 of
+ *            k_out and v_out belong to request b, ascending; NULL: one row per
+ *            request (n_rows == n_requests). Rows behind offsets[n_requests] are
+ *            left alone.
+ *   k_out, v_out  row r at r * k_stride (v_stride) elements, [H][D] within a row;
+ *            16-byte aligned, strides multiples of 8 elements.
+ * Rows of a request whose start or length its table row does not hold, and rows on
+ * a page outside the pool, become NaN.
+ */
+kvq_status kvq_paged_read(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages, int n_requests,
+                          const int32_t* start, const int32_t* offsets, int n_rows, int out_dtype, void* k_out,
+                          void* v_out, int64_t k_stride, int64_t v_stride, kvq_cuda_stream stream);
+
+/* Workspace bytes of kvq_paged_tree_attn on the current device. 0 for invalid sizes. */
+size_t kvq_paged_tree_workspace_bytes(int n_requests, int n_heads, int n_q_heads, int n_rows);
+
+/*
+ * Attention of several queries per request: of a tree of drafted tokens that a
+ * model verifies in one pass, of a chunk of a prompt, or (one row) of a decode step.
+ * Request b has seq_lens[b] tokens in the cache and behind them, at the places
+ * seq_lens[b] + i, its drafted tokens i = 0 .. n_b - 1, appended before the call
+ * (kvq_paged_append; the positions of a tree's tokens are its `positions`). Query
+ * row i of the request attends to all seq_lens[b] cached tokens and to those drafted
+ * tokens j that the mask allows.
+ *   offsets  int32 [n_requests + 1] (device): rows offsets[b] .. offsets[b+1]-1 are
+ *            request b's, ascending; NULL: one row per request (n_rows ==
+ *            n_requests). Rows behind offsets[n_requests] are padding: their out
+ *            and lse are left alone. At most KVQ_PAGED_MAX_DRAFT rows per request.
+ *   mask     uint32 [n_rows][mask_words] (device): bit j % 32 of word j / 32 of a row
+ *            allows drafted token j; a request has at most 32 mask_words rows. NULL
+ *            (mask_words 0): row i attends to the drafted tokens 0 .. i.
+ *   q        BF16 or FP16 (the cache's type unless it is E4M3), row r at r * q_stride
+ *            elements, [Hq][D] within; 16-byte aligned, q_stride a multiple of 8.
+ *   out      q's type, [n_rows][Hq][D], 16-byte aligned. (Not FP32, as of
+ *            kvq_paged_decode_attn: a softmax weight is one 16-bit number here.)
+ *   lse      FP32 [n_rows][Hq] or NULL: ln of the sum of exp(scale q.k).
+ * Query head hq reads KV head hq / (Hq/H). Softmax and sums are FP32; q.k and |v|
+ * summed over the tokens have to lie within FP32's range. Weights are rounded to
+ * BF16 (FP16 caches: to FP16), out once more to its type. A value that is not finite
+ * counts where a row attends to it, and nowhere else; what lies in other places of a
+ * page is not read. A row that attends to nothing, or whose keys all weigh nothing,
+ * gets out 0 and lse -inf; the rows of a request whose length, row count or pages
+ * are outside their range NaN in both.
+ */
+kvq_status kvq_paged_tree_attn(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages, int n_requests,
+                               const int32_t* seq_lens, const int32_t* offsets, int n_rows, const uint32_t* mask,
+                               int mask_words, const void* q, int q_dtype, int64_t q_stride, int n_q_heads,
+                               float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                               kvq_cuda_stream stream);
+
+/*
+ * The accepted ones among the drafted tokens become cached tokens: accepted
+ * (device, int32 [n_accepted]) holds for request b, at offsets[b] ..
+ * offsets[b+1]-1 (int32 [n_requests + 1], device, ascending), the numbers of its
+ * accepted drafted tokens, ascending; the k-th moves from place seq_lens[b] +
+ * accepted[k] to place seq_lens[b] + k: keys, values and their scales, all heads.
+ * Then the request has seq_lens[b] + offsets[b+1] - offsets[b] tokens (seq_lens is
+ * not changed). The key bounds of the pages from that of place seq_lens[b] on are
+ * taken anew from the keys that are there now, so that rejected tokens leave them.
+ * The pages written (from that of place seq_lens[b] on) belong to one request only.
+ * A request whose length, offsets or list is outside its range, or whose accepted
+ * tokens or their places are on a page outside the pool, is left as it is.
+ */
+kvq_status kvq_paged_tree_commit(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages,
+                                 int n_requests, const int32_t* seq_lens, const int32_t* accepted,
+                                 const int32_t* offsets, int n_accepted, kvq_cuda_stream stream);
 
 /* Human-readable name of a status code. */
 const char* kvq_status_string(kvq_status s);

@@ -42,6 +42,8 @@ struct View {
   const float* k_scale;
   const float* v_scale;
   char* bounds;  // [n_pages][H][2][128] elements, or nullptr
+  // 1: E4M3 whose scales are [n_pages][H][page_size] (KVQ_DT_E4M3_TOKEN; the dtype that goes with a View is then kE4m3)
+  int32_t token_scales;
 };
 
 __device__ __forceinline__ void flag(const View& c, int bits) {
@@ -176,6 +178,40 @@ __device__ __forceinline__ void divide(long long x, int d, int& q, int& r) {
   }
 }
 
+// Rows of request b and the first of them, or -1 when its offsets are outside their range (no offsets: one row each).
+__device__ __forceinline__ int row_range(const int32_t* offsets, int n_rows, int b, int& row0) {
+  row0 = b;
+  if (offsets == nullptr) return 1;
+  row0 = offsets[b];
+  const int row1 = offsets[b + 1];
+  return row0 < 0 || row1 < row0 || row1 > n_rows ? -1 : row1 - row0;
+}
+
+// Smaller and larger ones of pairs of 16-bit numbers (BF16, or FP16, which E4M3 values
+// become exactly); NaN stays.
+template <int DT>
+__device__ __forceinline__ uint32_t smaller(uint32_t x, uint32_t y) {
+  if constexpr (DT == kBf16) {
+    const __nv_bfloat162 r =
+        __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 r = __hmin2_nan(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+template <int DT>
+__device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) {
+  if constexpr (DT == kBf16) {
+    const __nv_bfloat162 r =
+        __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  } else {
+    const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
 struct AppendArgs {
   View c;
   const int32_t* table;
@@ -268,6 +304,61 @@ struct SelectArgs {
   char* ws;
   int32_t sms;
 };
+
+struct ReadArgs {
+  View c;
+  const int32_t* table;
+  int32_t max_pages;
+  int32_t B;
+  const int32_t* start;
+  const int32_t* offsets;
+  int32_t n_rows;
+  int32_t dtype;
+  int32_t out_dtype;
+  char* k;
+  char* v;
+  long long k_stride, v_stride;  // bytes
+};
+
+struct CommitArgs {
+  View c;
+  const int32_t* table;
+  int32_t max_pages;
+  int32_t B;
+  const int32_t* lens;
+  const int32_t* accepted;
+  const int32_t* offsets;
+  int32_t n_accepted;
+  int32_t dtype;
+};
+
+struct TreeArgs {
+  View c;
+  const int32_t* table;
+  int32_t max_pages;
+  int32_t B;
+  const int32_t* lens;
+  const int32_t* offsets;
+  int32_t n_rows;
+  const uint32_t* mask;  // [n_rows][mask_words], or nullptr: row i sees the drafted tokens 0 .. i
+  int32_t mask_words;
+  int32_t g;
+  int32_t Hq;
+  const char* q;
+  long long q_stride;  // bytes
+  int32_t q_dtype;
+  int32_t dtype;
+  float scale;
+  char* out;
+  float* lse;
+  char* ws;
+  int32_t sms;
+};
+
+size_t tree_workspace(int B, int H, int Hq, int n_rows, int sms);
+cudaError_t launch_read(const ReadArgs& a, int sms, cudaStream_t stream);
+cudaError_t launch_commit(const CommitArgs& a, cudaStream_t stream);
+cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);
 
 size_t attn_workspace(int B, int H, int Hq, int sms);
 size_t select_workspace(int B, int H, int max_pages);

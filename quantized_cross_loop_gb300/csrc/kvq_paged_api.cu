@@ -52,16 +52,30 @@ int current_sms() {
 }
 
 // The format, sizes, strides and pointers of a cache; need: which pointers the call reads.
-enum { kNeedKv = 1, kNeedBounds = 2 };
+enum { kNeedKv = 1, kNeedBounds = 2, kHeadScales = 4 };  // kHeadScales: the call reads no scales per token
+
+bool known_dtype(int dtype) {
+  return dtype == KVQ_DT_BF16 || dtype == KVQ_DT_FP16 || dtype == KVQ_DT_E4M3 || dtype == KVQ_DT_E4M3_TOKEN;
+}
+bool is_e4m3(int dtype) { return dtype == KVQ_DT_E4M3 || dtype == KVQ_DT_E4M3_TOKEN; }
+// The type that the kernels see: where the scales lie is in the View.
+int kernel_dtype(int dtype) { return is_e4m3(dtype) ? KVQ_DT_E4M3 : dtype; }
 
 kvq_status check_cache(const kvq_paged_cache* c, int need, paged::View* v) {
   if (c == nullptr) return fail(KVQ_ERR_BAD_ARG, "cache is NULL");
   if (c->version != KVQ_FORMAT_VERSION) return fail(KVQ_ERR_UNSUPPORTED, "cache: format version %u", c->version);
-  if (c->dtype < KVQ_DT_BF16 || c->dtype > KVQ_DT_E4M3) return fail(KVQ_ERR_BAD_ARG, "cache: dtype %d", c->dtype);
+  if (!known_dtype(c->dtype)) return fail(KVQ_ERR_BAD_ARG, "cache: dtype %d", c->dtype);
   if (c->head_dim != kD) return fail(KVQ_ERR_UNSUPPORTED, "cache: head_dim %d (kernels support 128)", c->head_dim);
   if (c->n_pages < 1 || c->n_heads < 1 || c->n_heads > 1024 || c->page_size < 1 || c->page_size > KVQ_PAGED_MAX_PAGE)
     return fail(KVQ_ERR_BAD_ARG, "cache: n_pages %d page_size %d n_heads %d", c->n_pages, c->page_size, c->n_heads);
-  const int es = c->dtype == KVQ_DT_E4M3 ? 1 : 2;
+  const int es = is_e4m3(c->dtype) ? 1 : 2;
+  if (c->dtype == KVQ_DT_E4M3_TOKEN) {
+    if (need & kHeadScales)
+      return fail(KVQ_ERR_UNSUPPORTED, "cache: one with a scale per token is attended to by kvq_paged_tree_attn");
+    if (c->k_scale == nullptr || c->v_scale == nullptr)
+      return fail(KVQ_ERR_BAD_ARG, "cache: scales per token without k_scale or v_scale");
+    if (c->key_bounds != nullptr) return fail(KVQ_ERR_BAD_ARG, "cache: key_bounds beside scales per token");
+  }
   if (need & kNeedKv) {
     if (c->k == nullptr || c->v == nullptr) return fail(KVQ_ERR_BAD_ARG, "cache: k or v is NULL");
     if (!aligned16(c->k) || !aligned16(c->v)) return fail(KVQ_ERR_MISALIGNED, "cache: k and v must be 16-byte aligned");
@@ -87,7 +101,7 @@ kvq_status check_cache(const kvq_paged_cache* c, int need, paged::View* v) {
   }
   if (c->key_bounds != nullptr && !aligned16(c->key_bounds))
     return fail(KVQ_ERR_MISALIGNED, "cache: key_bounds must be 16-byte aligned");
-  if (c->dtype != KVQ_DT_E4M3 && (c->k_scale != nullptr || c->v_scale != nullptr))
+  if (!is_e4m3(c->dtype) && (c->k_scale != nullptr || c->v_scale != nullptr))
     return fail(KVQ_ERR_BAD_ARG, "cache: scales belong to an E4M3 cache");
   memset(v, 0, sizeof *v);
   v->k = static_cast<char*>(c->k);
@@ -102,6 +116,7 @@ kvq_status check_cache(const kvq_paged_cache* c, int need, paged::View* v) {
   v->n_pages = c->n_pages;
   v->H = c->n_heads;
   v->ps = paged::fast_div(c->page_size);
+  v->token_scales = c->dtype == KVQ_DT_E4M3_TOKEN;
   return KVQ_OK;
 }
 
@@ -132,12 +147,22 @@ kvq_status check_query(const kvq_paged_cache* c, int n_requests, const int32_t* 
   if (n_q_heads / c->n_heads > KVQ_PAGED_MAX_G)
     return fail(KVQ_ERR_UNSUPPORTED, "%d query heads per KV head (at most %d)", n_q_heads / c->n_heads, KVQ_PAGED_MAX_G);
   if (q_dtype != KVQ_DT_BF16 && q_dtype != KVQ_DT_FP16) return fail(KVQ_ERR_BAD_ARG, "q_dtype %d", q_dtype);
-  if (c->dtype != KVQ_DT_E4M3 && q_dtype != c->dtype)
+  if (!is_e4m3(c->dtype) && q_dtype != c->dtype)
     return fail(KVQ_ERR_UNSUPPORTED, "q_dtype %d on a cache of dtype %d", q_dtype, c->dtype);
   if (n_requests > 0 && (q == nullptr || seq_lens == nullptr)) return fail(KVQ_ERR_BAD_ARG, "q or seq_lens is NULL");
   if (!aligned16(q) || q_stride % 8 != 0) return fail(KVQ_ERR_MISALIGNED, "q must be 16-byte aligned, q_stride a multiple of 8");
   if (n_requests > 1 && (q_stride < 0 || q_stride > (int64_t(1) << 40)))
     return fail(KVQ_ERR_BAD_ARG, "q_stride %lld", (long long)q_stride);
+  return KVQ_OK;
+}
+
+// Rows of a ragged batch, `stride` elements apart: as far as memory could reach.
+bool rows_fit(int n_rows, int64_t stride) {
+  return stride >= 0 && (n_rows < 2 || stride <= (int64_t(1) << 46) / n_rows);
+}
+kvq_status check_rows(int n_requests, const int32_t* offsets, int n_rows) {
+  if (n_rows < 0 || (offsets == nullptr && n_rows != n_requests))
+    return fail(KVQ_ERR_BAD_ARG, "n_rows %d for n_requests %d%s", n_rows, n_requests, offsets ? "" : " without offsets");
   return KVQ_OK;
 }
 
@@ -156,7 +181,7 @@ kvq_status attend(const kvq_paged_cache* cache, const int32_t* page_table, int m
                   size_t workspace_bytes, kvq_cuda_stream stream) {
   paged::AttnArgs a;
   memset(&a, 0, sizeof a);
-  kvq_status st = check_cache(cache, kNeedKv, &a.c);
+  kvq_status st = check_cache(cache, kNeedKv | kHeadScales, &a.c);
   if (st == KVQ_OK) st = check_batch(cache, page_table, max_pages, n_requests);
   if (st == KVQ_OK) st = check_query(cache, n_requests, seq_lens, q, q_dtype, q_stride, n_q_heads);
   if (st != KVQ_OK) return st;
@@ -200,7 +225,7 @@ kvq_status kvq_paged_cache_init(kvq_paged_cache* c, int dtype, int n_pages, int 
   c->page_size = page_size;
   c->n_heads = n_heads;
   c->head_dim = head_dim;
-  if (dtype < KVQ_DT_BF16 || dtype > KVQ_DT_E4M3) return fail(KVQ_ERR_BAD_ARG, "dtype %d", dtype);
+  if (!known_dtype(dtype)) return fail(KVQ_ERR_BAD_ARG, "dtype %d", dtype);
   if (n_pages < 1 || page_size < 1 || page_size > KVQ_PAGED_MAX_PAGE || n_heads < 1 || n_heads > 1024 || head_dim < 1)
     return fail(KVQ_ERR_BAD_ARG, "sizes n_pages %d page_size %d n_heads %d head_dim %d", n_pages, page_size, n_heads,
                 head_dim);
@@ -220,7 +245,7 @@ kvq_status kvq_paged_append(const kvq_paged_cache* cache, const int32_t* page_ta
   if (r->n_rows < 0 || (r->offsets == nullptr && r->n_rows != n_requests))
     return fail(KVQ_ERR_BAD_ARG, "n_rows %d for n_requests %d%s", r->n_rows, n_requests, r->offsets ? "" : " without offsets");
   if (r->dtype != KVQ_DT_BF16 && r->dtype != KVQ_DT_FP16) return fail(KVQ_ERR_BAD_ARG, "rows: dtype %d", r->dtype);
-  if (cache->dtype != KVQ_DT_E4M3 && r->dtype != cache->dtype)
+  if (!is_e4m3(cache->dtype) && r->dtype != cache->dtype)
     return fail(KVQ_ERR_UNSUPPORTED, "rows of dtype %d into a cache of dtype %d", r->dtype, cache->dtype);
   if (r->rotary_dim < 0 || r->rotary_dim > kD || r->rotary_dim % 8 != 0)
     return fail(KVQ_ERR_BAD_ARG, "rotary_dim %d", r->rotary_dim);
@@ -249,7 +274,7 @@ kvq_status kvq_paged_append(const kvq_paged_cache* cache, const int32_t* page_ta
     return fail(KVQ_ERR_BAD_ARG, "q_out_stride %lld: rows overlap", (long long)r->q_out_stride);
   const int sms = current_sms();
   if (sms == 0) return fail(KVQ_ERR_CUDA, "no usable CUDA device");
-  const paged::AppendArgs a = paged::append_args(view, cache->dtype, page_table, max_pages, n_requests, *r);
+  const paged::AppendArgs a = paged::append_args(view, kernel_dtype(cache->dtype), page_table, max_pages, n_requests, *r);
   return cuda_status(paged::launch_append(a, sms, reinterpret_cast<cudaStream_t>(stream)), "paged append launch");
 }
 
@@ -288,7 +313,7 @@ kvq_status kvq_paged_select(const kvq_paged_cache* cache, const int32_t* page_ta
                             size_t workspace_bytes, kvq_cuda_stream stream) {
   paged::SelectArgs a;
   memset(&a, 0, sizeof a);
-  kvq_status st = check_cache(cache, kNeedBounds, &a.c);
+  kvq_status st = check_cache(cache, kNeedBounds | kHeadScales, &a.c);
   if (st == KVQ_OK) st = check_batch(cache, page_table, max_pages, n_requests);
   if (st == KVQ_OK) st = check_query(cache, n_requests, seq_lens, q, q_dtype, q_stride, n_q_heads);
   if (st != KVQ_OK) return st;
@@ -315,6 +340,118 @@ kvq_status kvq_paged_select(const kvq_paged_cache* cache, const int32_t* page_ta
   a.sel = sel;
   a.ws = static_cast<char*>(workspace);
   return cuda_status(paged::launch_select(a, reinterpret_cast<cudaStream_t>(stream)), "page selection launch");
+}
+
+kvq_status kvq_paged_read(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages, int n_requests,
+                          const int32_t* start, const int32_t* offsets, int n_rows, int out_dtype, void* k_out,
+                          void* v_out, int64_t k_stride, int64_t v_stride, kvq_cuda_stream stream) {
+  paged::ReadArgs a;
+  memset(&a, 0, sizeof a);
+  kvq_status st = check_cache(cache, kNeedKv, &a.c);
+  if (st == KVQ_OK) st = check_batch(cache, page_table, max_pages, n_requests);
+  if (st == KVQ_OK) st = check_rows(n_requests, offsets, n_rows);
+  if (st != KVQ_OK) return st;
+  if (out_dtype != KVQ_DT_BF16 && out_dtype != KVQ_DT_FP16) return fail(KVQ_ERR_BAD_ARG, "out_dtype %d", out_dtype);
+  if (n_requests == 0 || n_rows == 0) return ok();
+  if (start == nullptr || k_out == nullptr || v_out == nullptr) return fail(KVQ_ERR_BAD_ARG, "start, k_out or v_out is NULL");
+  if (!aligned16(k_out) || !aligned16(v_out) || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return fail(KVQ_ERR_MISALIGNED, "k_out and v_out must be 16-byte aligned, their strides multiples of 8");
+  const int64_t row = int64_t(cache->n_heads) * kD;
+  for (const int64_t s : {k_stride, v_stride})
+    if (!rows_fit(n_rows, s) || (n_rows > 1 && s < row))
+      return fail(KVQ_ERR_BAD_ARG, "row stride %lld: rows overlap or are out of range", (long long)s);
+  const int sms = current_sms();
+  if (sms == 0) return fail(KVQ_ERR_CUDA, "no usable CUDA device");
+  a.table = page_table;
+  a.max_pages = max_pages;
+  a.B = n_requests;
+  a.start = start;
+  a.offsets = offsets;
+  a.n_rows = n_rows;
+  a.dtype = kernel_dtype(cache->dtype);
+  a.out_dtype = out_dtype;
+  a.k = static_cast<char*>(k_out);
+  a.v = static_cast<char*>(v_out);
+  a.k_stride = k_stride * 2;
+  a.v_stride = v_stride * 2;
+  return cuda_status(paged::launch_read(a, sms, reinterpret_cast<cudaStream_t>(stream)), "paged read launch");
+}
+
+size_t kvq_paged_tree_workspace_bytes(int n_requests, int n_heads, int n_q_heads, int n_rows) {
+  const int sms = current_sms();
+  if (n_requests < 0 || n_heads < 1 || n_heads > 1024 || n_q_heads < n_heads || n_q_heads % n_heads != 0 ||
+      n_q_heads / n_heads > KVQ_PAGED_MAX_G || n_rows < 0 || !batch_fits(n_requests, n_heads, 0) || sms == 0)
+    return 0;
+  return paged::tree_workspace(n_requests, n_heads, n_q_heads, n_rows, sms);
+}
+
+kvq_status kvq_paged_tree_attn(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages, int n_requests,
+                               const int32_t* seq_lens, const int32_t* offsets, int n_rows, const uint32_t* mask,
+                               int mask_words, const void* q, int q_dtype, int64_t q_stride, int n_q_heads,
+                               float softmax_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                               kvq_cuda_stream stream) {
+  paged::TreeArgs a;
+  memset(&a, 0, sizeof a);
+  kvq_status st = check_cache(cache, kNeedKv, &a.c);
+  if (st == KVQ_OK) st = check_batch(cache, page_table, max_pages, n_requests);
+  if (st == KVQ_OK) st = check_rows(n_requests, offsets, n_rows);
+  if (st == KVQ_OK) st = check_query(cache, n_requests > 0 && n_rows > 0 ? (n_rows > 1 ? 2 : 1) : 0, seq_lens, q, q_dtype, q_stride, n_q_heads);
+  if (st != KVQ_OK) return st;
+  if (!(softmax_scale > 0.0f) || softmax_scale > 1e30f) return fail(KVQ_ERR_BAD_ARG, "softmax_scale");
+  if (!rows_fit(n_rows, q_stride)) return fail(KVQ_ERR_BAD_ARG, "q_stride %lld", (long long)q_stride);
+  if (mask_words < 0 || mask_words > KVQ_PAGED_MAX_DRAFT / 32 || (mask == nullptr) != (mask_words == 0))
+    return fail(KVQ_ERR_BAD_ARG, "mask %s mask_words %d", mask == nullptr ? "NULL" : "of", mask_words);
+  if (n_requests == 0 || n_rows == 0) return ok();
+  if (out == nullptr) return fail(KVQ_ERR_BAD_ARG, "out is NULL");
+  if (!aligned16(out)) return fail(KVQ_ERR_MISALIGNED, "out must be 16-byte aligned");
+  a.sms = current_sms();
+  if (a.sms == 0) return fail(KVQ_ERR_CUDA, "no usable CUDA device");
+  st = check_workspace(workspace, workspace_bytes,
+                       paged::tree_workspace(n_requests, cache->n_heads, n_q_heads, n_rows, a.sms));
+  if (st != KVQ_OK) return st;
+  a.table = page_table;
+  a.max_pages = max_pages;
+  a.B = n_requests;
+  a.lens = seq_lens;
+  a.offsets = offsets;
+  a.n_rows = n_rows;
+  a.mask = mask;
+  a.mask_words = mask_words;
+  a.g = n_q_heads / cache->n_heads;
+  a.Hq = n_q_heads;
+  a.q = static_cast<const char*>(q);
+  a.q_stride = q_stride * 2;
+  a.q_dtype = q_dtype;
+  a.dtype = kernel_dtype(cache->dtype);
+  a.scale = softmax_scale;
+  a.out = static_cast<char*>(out);
+  a.lse = lse;
+  a.ws = static_cast<char*>(workspace);
+  return cuda_status(paged::launch_tree(a, reinterpret_cast<cudaStream_t>(stream)), "tree attention launch");
+}
+
+kvq_status kvq_paged_tree_commit(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages,
+                                 int n_requests, const int32_t* seq_lens, const int32_t* accepted,
+                                 const int32_t* offsets, int n_accepted, kvq_cuda_stream stream) {
+  paged::CommitArgs a;
+  memset(&a, 0, sizeof a);
+  kvq_status st = check_cache(cache, kNeedKv, &a.c);
+  if (st == KVQ_OK) st = check_batch(cache, page_table, max_pages, n_requests);
+  if (st != KVQ_OK) return st;
+  if (n_accepted < 0) return fail(KVQ_ERR_BAD_ARG, "n_accepted %d", n_accepted);
+  if (n_requests == 0) return ok();
+  if (seq_lens == nullptr || offsets == nullptr || (n_accepted > 0 && accepted == nullptr))
+    return fail(KVQ_ERR_BAD_ARG, "seq_lens, offsets or accepted is NULL");
+  if (current_sms() == 0) return fail(KVQ_ERR_CUDA, "no usable CUDA device");
+  a.table = page_table;
+  a.max_pages = max_pages;
+  a.B = n_requests;
+  a.lens = seq_lens;
+  a.accepted = accepted;
+  a.offsets = offsets;
+  a.n_accepted = n_accepted;
+  a.dtype = kernel_dtype(cache->dtype);
+  return cuda_status(paged::launch_commit(a, reinterpret_cast<cudaStream_t>(stream)), "paged commit launch");
 }
 
 }  // extern "C"

@@ -136,8 +136,7 @@ __device__ __forceinline__ Wide rotate(const Lane& L, const Angles& t, const Raw
   return x;
 }
 
-// Four stored keys as two words of 16-bit pairs (E4M3 as FP16, exact), and their
-// smaller and larger ones; NaN stays.
+// Four stored keys as two words of 16-bit pairs (E4M3 as FP16, exact).
 template <int DT>
 __device__ __forceinline__ uint2 pairs_of(const char* p) {
   if constexpr (DT == kE4m3) {
@@ -152,29 +151,6 @@ __device__ __forceinline__ void put_pairs(char* p, uint2 x) {
   if constexpr (DT == kE4m3) store4<kE4m3>(p, load4<kFp16>(&x));
   else *reinterpret_cast<uint2*>(p) = x;
 }
-template <int DT>
-__device__ __forceinline__ uint32_t smaller(uint32_t x, uint32_t y) {
-  if constexpr (DT == kBf16) {
-    const __nv_bfloat162 r =
-        __hmin2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  } else {
-    const __half2 r = __hmin2_nan(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-}
-template <int DT>
-__device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) {
-  if constexpr (DT == kBf16) {
-    const __nv_bfloat162 r =
-        __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&y));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  } else {
-    const __half2 r = __hmax2_nan(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
-    return *reinterpret_cast<const uint32_t*>(&r);
-  }
-}
-
 // A head's scale for storing E4M3: the code of the FP32 quotient x / s, rounded to nearest, ties to even. lo and hi are
 // the scale's reciprocal less and more 2^-20, so that x lo and x hi lie on either side of the quotient (all roundings,
 // of a reciprocal below FP32's normal range too, come to less than 2^-20): where both have the same code it is the
@@ -183,8 +159,9 @@ __device__ __forceinline__ uint32_t larger(uint32_t x, uint32_t y) {
 // line, or a branch for every four values, 22.8.)
 struct Quotient {
   float lo, hi, s;
-  __device__ __forceinline__ void open(const float* scale, int h) {
-    s = scale != nullptr ? scale[h] : 1.0f;
+  __device__ __forceinline__ void open(const float* scale, int h) { set(scale != nullptr ? scale[h] : 1.0f); }
+  __device__ __forceinline__ void set(float scale) {
+    s = scale;
     const float r = __frcp_rn(s);
     const bool exact = fmaf(r, s, -1.0f) == 0.0f;
     lo = exact ? r : r * (1.0f - 0x1p-20f);
@@ -202,12 +179,30 @@ __device__ __forceinline__ uint32_t divided(const float4& x, float s) {
   return c;
 }
 
-// What a team does to one (page, head): where rows come from and go to.
-template <int DT, int IN>
+// The scale of a token's row of a head, of which the lanes of a team hold eight channels each: its largest magnitude
+// goes to 448, E4M3's largest number. (Magnitudes are compared as whole numbers: NaN is above infinity. Below 2^-126
+// a scale's own rounding would show; codes of smaller rows are smaller.)
+__device__ __forceinline__ float token_scale(const Wide& x) {
+  uint32_t top = 0u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top = max(top, __float_as_uint((&x.a.x)[i]) & 0x7FFFFFFFu);
+    top = max(top, __float_as_uint((&x.b.x)[i]) & 0x7FFFFFFFu);
+  }
+  const uint32_t team = 0xFFFFu << (threadIdx.x & 16);
+#pragma unroll
+  for (int o = 1; o < kTeam; o <<= 1) top = max(top, __shfl_xor_sync(team, top, o));
+  const float s = __fdiv_rn(__uint_as_float(top), 448.0f);
+  return s < 0x1p-126f ? 0x1p-126f : s;
+}
+
+// What a team does to one (page, head): where rows come from and go to. TS: E4M3 with a scale per token.
+template <int DT, int IN, bool TS>
 struct Unit {
   using Word = std::conditional_t<DT == kE4m3, uint32_t, uint2>;  // four stored channels
   struct Stored {
     Word k[2], v[2];
+    float ks, vs;  // TS
   };
   bool is_q, live;  // live: the page is in the pool
   bool any;
@@ -225,7 +220,7 @@ struct Unit {
     page = a.table[(long long)b * a.max_pages + page_of_request];
     is_q = hh >= a.c.H;
     h = is_q ? hh - a.c.H : hh;
-    if constexpr (DT == kE4m3)
+    if constexpr (DT == kE4m3 && !TS)
       if (!is_q) {
         ks.open(a.c.k_scale, h);
         vs.open(a.c.v_scale, h);
@@ -262,10 +257,16 @@ struct Unit {
     store4<IN>(p + 2 * L.b, x.b);
   }
   // A row as it is stored.
-  __device__ __forceinline__ Stored stored(const Wide& x, const Raw& v) const {
+  __device__ __forceinline__ Stored stored(const Wide& x, const Raw& v) {
     Stored r;
     if constexpr (DT == kE4m3) {
       const Wide y{load4<IN>(&v.a), load4<IN>(&v.b)};
+      if constexpr (TS) {
+        r.ks = token_scale(x);
+        r.vs = token_scale(y);
+        ks.set(r.ks);
+        vs.set(r.vs);
+      }
       r.k[0] = Quotient::codes(x.a, ks.lo);
       r.k[1] = Quotient::codes(x.b, ks.lo);
       r.v[0] = Quotient::codes(y.a, vs.lo);
@@ -285,13 +286,22 @@ struct Unit {
     }
     return r;
   }
-  __device__ __forceinline__ void put(const Lane& L, char* k, char* w, const Stored& r) {
+  __device__ __forceinline__ void put(const AppendArgs& a, const Lane& L, int t, const Stored& r) {
     constexpr int kE = elem_bytes<DT>();
+    char* const k = a.c.k + place(a, t);
+    char* const w = a.c.v + place(a, t);
+    if constexpr (TS)
+      if (threadIdx.x % kTeam == 0) {
+        const long long at = ((long long)page * a.c.H + h) * int(a.c.ps.d) + (t - place0);
+        const_cast<float*>(a.c.k_scale)[at] = r.ks;
+        const_cast<float*>(a.c.v_scale)[at] = r.vs;
+      }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int at = kE * (i == 0 ? L.a : L.b);
       *reinterpret_cast<Word*>(w + at) = r.v[i];
       *reinterpret_cast<Word*>(k + at) = r.k[i];
+      if constexpr (TS) continue;  // (such a cache keeps no bounds)
       const uint2 y = pairs_of<DT>(reinterpret_cast<const char*>(&r.k[i]));
       lo[2 * i] = smaller<DT>(lo[2 * i], y.x);
       lo[2 * i + 1] = smaller<DT>(lo[2 * i + 1], y.y);
@@ -345,7 +355,7 @@ __device__ __forceinline__ void flag_lengths(const AppendArgs& a) {
 }
 
 // One row per request, keys, values and queries: a unit is a request's head.
-template <int DT, int IN, bool INTER>
+template <int DT, int IN, bool INTER, bool TS>
 __global__ void __launch_bounds__(kStepThreads, kStepBlocksPerSm) append_step_kernel(AppendArgs a) {
   wait_prior_grid();
   allow_dependents();
@@ -362,7 +372,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocksPerSm) append_step_ke
   for (long long w = u0; w < u1; ++w) {
     int start, row0;
     if (rows_of(a, b, start, row0) > 0) {
-      Unit<DT, IN> u;
+      Unit<DT, IN, TS> u;
       u.open(a, b, a.c.ps.div(start), hh, start, row0, 1);
       const Raw x = load_raw(u.source(a, start), L);
       Raw v{};
@@ -377,8 +387,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocksPerSm) append_step_ke
         if (u.is_q) {
           u.put_query(L, u.query_out(a, start), y);
         } else {
-          const long long place = u.place(a, start);
-          u.put(L, a.c.k + place, a.c.v + place, u.stored(y, v));
+          u.put(a, L, start, u.stored(y, v));
           u.close(a, L);
         }
       }
@@ -393,7 +402,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepBlocksPerSm) append_step_ke
 // Keys and values of any rows: a block takes the units that start in its range of the
 // work, a row counting one and a unit unit_rows() more. Its warps take the units of up
 // to kWarpRows rows in turn, all of them together the others.
-template <int DT, int IN, bool INTER>
+template <int DT, int IN, bool INTER, bool TS>
 __global__ void __launch_bounds__(kManyThreads, kKeyBlocksPerSm) append_keys_kernel(AppendArgs a) {
   __shared__ Prefix<kManyThreads> S;
   __shared__ uint32_t s_bound[kManyWarps][8][kTeam];
@@ -454,7 +463,7 @@ __global__ void __launch_bounds__(kManyThreads, kKeyBlocksPerSm) append_keys_ker
       if (!mine) continue;
     }
     const int team = all ? threadIdx.x / kTeam : (threadIdx.x / kTeam) & 1, step = all ? kManyThreads / kTeam : 2;
-    Unit<DT, IN> u;
+    Unit<DT, IN, TS> u;
     u.open(a, b, p, h, start, row0, n);
     u.check(a);
     for (int t0 = u.live ? u.first + team : u.last; t0 < u.last; t0 += step * kKeyRows) {
@@ -476,8 +485,7 @@ __global__ void __launch_bounds__(kManyThreads, kKeyBlocksPerSm) append_keys_ker
 #pragma unroll
       for (int i = 0; i < kKeyRows; ++i) {
         if (!ok[i]) continue;
-        const long long place = u.place(a, t0 + i * step);
-        u.put(L, a.c.k + place, a.c.v + place, u.stored(rotate<IN, INTER>(L, g[i], x[i]), y[i]));
+        u.put(a, L, t0 + i * step, u.stored(rotate<IN, INTER>(L, g[i], x[i]), y[i]));
       }
     }
     if (a.c.bounds == nullptr) continue;
@@ -573,14 +581,14 @@ __global__ void __launch_bounds__(kManyThreads, kQueryBlocksPerSm) append_querie
   wait_prior_grid();
 }
 
-template <int DT, int IN, bool INTER>
+template <int DT, int IN, bool INTER, bool TS>
 cudaError_t launch_form(const AppendArgs& a, int sms, cudaStream_t stream) {
   const int Hq = a.q != nullptr ? a.Hq : 0;
   count_launch();
   if (a.offsets == nullptr) {
     const long long need = ((long long)a.B * (a.c.H + Hq) * kTeam + kStepThreads - 1) / kStepThreads;
     const long long fit = (long long)kStepBlocksPerSm * sms;
-    return launch_dependent(append_step_kernel<DT, IN, INTER>, dim3(int(need < fit ? need : fit)),
+    return launch_dependent(append_step_kernel<DT, IN, INTER, TS>, dim3(int(need < fit ? need : fit)),
                             dim3(kStepThreads), 0, stream, a);
   }
   // More than two query heads per KV head: half as many blocks of each kernel, so that both fit on an SM and run side
@@ -593,7 +601,7 @@ cudaError_t launch_form(const AppendArgs& a, int sms, cudaStream_t stream) {
   const long long by_units = (units + kManyWarps - 1) / kManyWarps;
   const long long by_rows = a.c.ps.d > kWarpRows ? (long long)a.n_rows * a.c.H / 32 : 0;
   const long long need = by_units > by_rows ? by_units : by_rows, fit = (long long)kKeyBlocksPerSm * sms / part;
-  const cudaError_t e = launch_dependent(append_keys_kernel<DT, IN, INTER>, dim3(int(need < fit ? need : fit)),
+  const cudaError_t e = launch_dependent(append_keys_kernel<DT, IN, INTER, TS>, dim3(int(need < fit ? need : fit)),
                                          dim3(kManyThreads), 0, stream, a);
   if (e != cudaSuccess || Hq == 0) return e;
   count_launch();
@@ -603,15 +611,16 @@ cudaError_t launch_form(const AppendArgs& a, int sms, cudaStream_t stream) {
                           dim3(kManyThreads), 0, stream, a);
 }
 
-template <int DT, int IN>
+template <int DT, int IN, bool TS = false>
 cudaError_t launch_types(const AppendArgs& a, int sms, cudaStream_t stream) {
-  return a.interleaved ? launch_form<DT, IN, true>(a, sms, stream) : launch_form<DT, IN, false>(a, sms, stream);
+  return a.interleaved ? launch_form<DT, IN, true, TS>(a, sms, stream) : launch_form<DT, IN, false, TS>(a, sms, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs& a, int sms, cudaStream_t stream) {
   const bool bf = a.in_dtype == kBf16;
+  if (a.c.token_scales) return bf ? launch_types<kE4m3, kBf16, true>(a, sms, stream) : launch_types<kE4m3, kFp16, true>(a, sms, stream);
   switch (a.dtype) {
     case kBf16: return launch_types<kBf16, kBf16>(a, sms, stream);
     case kFp16: return launch_types<kFp16, kFp16>(a, sms, stream);

@@ -31,6 +31,8 @@ ATTN_NVFP4 = 8  # OR-ed into algo: the table may hold NVFP4 residual loops
 KVQ_KGROUP_COMPACT, KVQ_KGROUP_TILE = 0, 1  # K groups: 64 stored rows / the stored rows of one 64-token tile
 KVQ_LOOP_K_TILE, KVQ_LOOP_K_NVFP4, KVQ_LOOP_V_NVFP4 = 1, 2, 4
 PAGED_ERR_LENGTH, PAGED_ERR_SELECTION, PAGED_ERR_PAGE, PAGED_ERR_POSITION = 1, 32, 128, 256
+PAGED_ERR_WAIT = 8
+PAGED_MAX_DRAFT = 1024  # rows of a request in kvq_paged_tree_attn
 KVQ_FMT_INT4, KVQ_FMT_NVFP4 = 0, 1  # residual formats: affine INT4 / E2M1 + E4M3 per 16 + FP32 per stream
 
 EXPORTED = (
@@ -43,7 +45,8 @@ EXPORTED = (
     "kvq_reconstruct_batch_ex", "kvq_stream_set_capacity", "kvq_append_workspace_bytes", "kvq_append_tile",
     "kvq_append_batch_workspace_bytes", "kvq_append_tile_batch", "kvq_sparse_decode_workspace_bytes",
     "kvq_sparse_decode_attn_ex", "kvq_paged_cache_init", "kvq_paged_append", "kvq_paged_workspace_bytes",
-    "kvq_paged_decode_attn", "kvq_paged_select", "kvq_paged_sparse_attn",
+    "kvq_paged_decode_attn", "kvq_paged_select", "kvq_paged_sparse_attn", "kvq_paged_read",
+    "kvq_paged_tree_workspace_bytes", "kvq_paged_tree_attn", "kvq_paged_tree_commit",
 )
 
 
@@ -218,6 +221,12 @@ def lib():
                                                 vp, sz, vp]
             L.kvq_paged_select.argtypes = [P(kvq_paged_cache), vp, i32, i32, vp, vp, i32, i64, i32, i32, i32, i32, vp,
                                            vp, sz, vp]
+            L.kvq_paged_read.argtypes = [P(kvq_paged_cache), vp, i32, i32, vp, vp, i32, i32, vp, vp, i64, i64, vp]
+            L.kvq_paged_tree_workspace_bytes.argtypes = [i32, i32, i32, i32]
+            L.kvq_paged_tree_workspace_bytes.restype = sz
+            L.kvq_paged_tree_attn.argtypes = [P(kvq_paged_cache), vp, i32, i32, vp, vp, i32, vp, i32, vp, i32, i64, i32,
+                                              f32, vp, vp, vp, sz, vp]
+            L.kvq_paged_tree_commit.argtypes = [P(kvq_paged_cache), vp, i32, i32, vp, vp, vp, i32, vp]
             L.kvq_paged_sparse_attn.argtypes = [P(kvq_paged_cache), vp, i32, i32, vp, vp, i32, i64, i32, vp, i32, f32,
                                                 vp, vp, vp, sz, vp]
             for name in ("kvq_stream_init", "kvq_encode_base", "kvq_encode_residual", "kvq_build_tile_dir",
@@ -226,7 +235,7 @@ def lib():
                          "kvq_stream_set_format", "kvq_encode_batch_ex", "kvq_reconstruct_batch_ex",
                          "kvq_stream_set_capacity", "kvq_append_tile", "kvq_append_tile_batch",
                          "kvq_paged_cache_init", "kvq_paged_append", "kvq_paged_decode_attn", "kvq_paged_select",
-                         "kvq_paged_sparse_attn"):
+                         "kvq_paged_sparse_attn", "kvq_paged_read", "kvq_paged_tree_attn", "kvq_paged_tree_commit"):
                 getattr(L, name).restype = ctypes.c_int32
             _lib = L
     return _lib
@@ -790,6 +799,7 @@ def kvq_sparse_decode_attn(table: RequestTable, q: torch.Tensor, depth: int, n_h
 # --------------------------------------------------------------------------- paged cache
 
 _PAGED_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float8_e4m3fn: 2}
+_E4M3_TOKEN = 4  # E4M3 with a scale per token and head
 _SCALE_128 = 1.0 / math.sqrt(128)
 
 
@@ -804,7 +814,11 @@ class PagedCache:
     key_bounds  [n_pages, n_heads, 2, 128], contiguous, of the same type: smallest
                 and largest key per page, head and channel, kept by
                 kvq_paged_append and read by kvq_paged_select; None: none.
-    k_scale, v_scale  FP32 [n_heads], positive, for E4M3: value = stored * scale.
+    k_scale, v_scale  for E4M3, value = stored * scale: FP32 [n_heads], positive; or
+                FP32 [n_pages, n_heads, page_size], contiguous, one per token and
+                head, which kvq_paged_append makes from the rows it stores. A cache
+                of such scales has no key bounds and is attended to by
+                kvq_paged_tree_attn.
 
     The kernels OR what they refuse into an error word of the cache
     (PAGED_ERR_*): error_word() reads it, clear_error() zeroes it. A page of 64
@@ -836,14 +850,22 @@ class PagedCache:
             elif name == "key_bounds":
                 if tuple(t.shape) != (n_pages, n_heads, 2, 128) or t.dtype != first.dtype or not t.is_contiguous():
                     raise KvqError(f"key_bounds must be contiguous {first.dtype} [{n_pages}, {n_heads}, 2, 128]")
-            elif t.dtype != torch.float32 or tuple(t.shape) != (n_heads,) or not t.is_contiguous():
-                raise KvqError(f"{name} must be contiguous float32 [{n_heads}]")
+            elif (t.dtype != torch.float32 or not t.is_contiguous()
+                  or tuple(t.shape) not in ((n_heads,), (n_pages, n_heads, page_size))):
+                raise KvqError(f"{name} must be contiguous float32 [{n_heads}] or [{n_pages}, {n_heads}, {page_size}]")
+        self.token_scales = any(t is not None and t.dim() == 3 for t in (k_scale, v_scale))
+        if self.token_scales:
+            if first.dtype != torch.float8_e4m3fn or key_bounds is not None:
+                raise KvqError("scales per token belong to a float8_e4m3fn cache without key_bounds")
+            if k_scale is None or v_scale is None or k_scale.shape != v_scale.shape:
+                raise KvqError("scales per token: k_scale and v_scale come together")
         self.page_size, self.n_heads, self.n_pages = page_size, n_heads, n_pages
         self.dtype, self.device, self.index = first.dtype, first.device, first.get_device()
         self.k, self.v, self.key_bounds, self.k_scale, self.v_scale = k, v, key_bounds, k_scale, v_scale
         self.desc = kvq_paged_cache()
-        _check(lib().kvq_paged_cache_init(ctypes.byref(self.desc), _PAGED_DTYPES[self.dtype], n_pages, page_size,
-                                          n_heads, 128), "kvq_paged_cache_init")
+        dtype = _E4M3_TOKEN if self.token_scales else _PAGED_DTYPES[self.dtype]
+        _check(lib().kvq_paged_cache_init(ctypes.byref(self.desc), dtype, n_pages, page_size, n_heads, 128),
+               "kvq_paged_cache_init")
         if k is not None:
             self.desc.page_stride, self.desc.token_stride, self.desc.head_stride = k.stride()[:3]
         self._error = torch.zeros(4, dtype=torch.int32, device=self.device)
@@ -855,11 +877,22 @@ class PagedCache:
 
     @classmethod
     def empty(cls, n_pages: int, page_size: int, n_heads: int, dtype=torch.bfloat16, device="cuda",
-              key_bounds: bool = False, k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):
-        """A token-major cache with storage of its own."""
+              key_bounds: bool = False, k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None,
+              token_scales: bool = False):
+        """A token-major cache with storage of its own (token_scales: also for a scale per token and head)."""
         k, v = (torch.empty((n_pages, page_size, n_heads, 128), dtype=dtype, device=device) for _ in range(2))
         bounds = torch.empty((n_pages, n_heads, 2, 128), dtype=dtype, device=device) if key_bounds else None
+        if token_scales:
+            if k_scale is not None or v_scale is not None:
+                raise KvqError("token_scales beside k_scale or v_scale")
+            k_scale, v_scale = (torch.empty((n_pages, n_heads, page_size), dtype=torch.float32, device=device)
+                                for _ in range(2))
         return cls(page_size, n_heads, k, v, bounds, k_scale, v_scale)
+
+    def tree_workspace_bytes(self, n_requests: int, n_q_heads: int, n_rows: int) -> int:
+        """Workspace of kvq_paged_tree_attn for these sizes (kvq_paged_tree_workspace_bytes)."""
+        with torch.cuda.device(self.device):
+            return int(lib().kvq_paged_tree_workspace_bytes(n_requests, self.n_heads, n_q_heads, n_rows))
 
     def workspace_bytes(self, n_requests: int, n_q_heads: int, max_pages: int) -> int:
         """Workspace of the attention and selection calls for these sizes (kvq_paged_workspace_bytes); with max_pages 0
@@ -987,9 +1020,9 @@ def _query_type(q: torch.Tensor) -> int:
     return _PAGED_DTYPES[q.dtype]
 
 
-def _paged_workspace(cache: PagedCache, workspace, B, Hq, W):
+def _paged_workspace(cache: PagedCache, workspace, B, Hq, W, bytes_of="kvq_paged_workspace_bytes"):
     if workspace is None:
-        need = int(cache.lib.kvq_paged_workspace_bytes(B, cache.n_heads, Hq, W))
+        need = int(getattr(cache.lib, bytes_of)(B, cache.n_heads, Hq, W))
         return torch.empty(max(need, 16), dtype=torch.uint8, device=cache.device)
     if workspace.get_device() != cache.index or workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise KvqError(f"workspace must be contiguous uint8 on {cache.device}")
@@ -1082,3 +1115,113 @@ def kvq_paged_sparse_attn(cache: PagedCache, page_table: torch.Tensor, seq_lens:
             return kvq_paged_sparse_attn(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, workspace)
     return _paged_attend(cache, page_table, seq_lens, q, sel, softmax_scale, out, lse, workspace,
                          "kvq_paged_sparse_attn")
+
+
+def kvq_paged_read(cache: PagedCache, page_table: torch.Tensor, start: torch.Tensor, k_out: torch.Tensor,
+                   v_out: torch.Tensor, offsets: torch.Tensor | None = None, stream=None):
+    """Rows back out of the cache, into k_out and v_out, BF16 or FP16 [n, H, 128]
+    (rows may be strided): row i of request b is token start[b] + i, rows
+    offsets[b] .. offsets[b + 1] - 1 (None: one row per request); rows behind
+    offsets[B] are left alone. 8-bit values come times their scale. 64 rows of a
+    request in a contiguous BF16 buffer are a tile for kvq_append_tile. Returns
+    (k_out, v_out)."""
+    if _elsewhere(cache, stream):
+        with _made_current(cache, stream):
+            return kvq_paged_read(cache, page_table, start, k_out, v_out, offsets)
+    if cache.k is None:
+        raise KvqError("a cache of key bounds alone cannot be read")
+    shape = _table_shape(page_table)
+    B, W = shape
+    tab = _ptr(cache, page_table, "page_table", torch.int32, shape)
+    dtype = k_out.dtype
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise KvqError(f"k_out must be bfloat16 or float16, got {dtype}")
+    n = k_out.shape[0]
+    ks = _head_rows(cache, k_out, "k_out", dtype, n, cache.n_heads)[1]
+    vs = _head_rows(cache, v_out, "v_out", dtype, n, cache.n_heads)[1]
+    at = _ptr(cache, start, "start", torch.int32, (B,))
+    off = None if offsets is None else _ptr(cache, offsets, "offsets", torch.int32, (B + 1,))
+    st = cache.lib.kvq_paged_read(cache.ref, tab, W, B, at, off, n, _PAGED_DTYPES[dtype], k_out.data_ptr(),
+                                  v_out.data_ptr(), ks, vs, _raw_stream(cache.index))
+    if st:
+        _check(st, "kvq_paged_read")
+    return k_out, v_out
+
+
+def kvq_paged_tree_attn(cache: PagedCache, page_table: torch.Tensor, seq_lens: torch.Tensor, q: torch.Tensor,
+                        offsets: torch.Tensor | None = None, mask: torch.Tensor | None = None,
+                        softmax_scale: float | None = None, out: torch.Tensor | None = None,
+                        lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """Attention of several queries per request over its seq_lens[b] cached tokens
+    and its drafted tokens, which lie at the places behind them (kvq_paged_append
+    puts them there, with `positions` for a tree's). q [n, Hq, 128] (rows may be
+    strided): rows offsets[b] .. offsets[b + 1] - 1 belong to request b (None: one
+    row per request), at most PAGED_MAX_DRAFT each. mask int32 [n, W]: bit j % 32 of
+    word j / 32 lets a row attend to drafted token j (W = ceil(rows of the longest
+    request / 32)); None: row i attends to the drafted tokens 0 .. i, as the tokens
+    of a chunk do. Returns out [n, Hq, 128] of q's type; lse, FP32 [n, Hq], takes the
+    natural log of the softmax's sum. Rows behind offsets[B] are left alone.
+    workspace: cache.tree_workspace_bytes(...) bytes, allocated when None; calls
+    that may overlap need one each."""
+    if _elsewhere(cache, stream):
+        with _made_current(cache, stream):
+            return kvq_paged_tree_attn(cache, page_table, seq_lens, q, offsets, mask, softmax_scale, out, lse, workspace)
+    if cache.k is None:
+        raise KvqError("a cache of key bounds alone cannot be attended to")
+    shape = _table_shape(page_table)
+    B, W = shape
+    tab = _ptr(cache, page_table, "page_table", torch.int32, shape)
+    qdt = _query_type(q)
+    n = q.shape[0]
+    Hq, stride = _head_rows(cache, q, "q", q.dtype, n)
+    lens = _ptr(cache, seq_lens, "seq_lens", torch.int32, (B,))
+    off = None if offsets is None else _ptr(cache, offsets, "offsets", torch.int32, (B + 1,))
+    words, mask_ptr = 0, None
+    if mask is not None:
+        if mask.dim() != 2 or mask.shape[1] < 1:
+            raise KvqError("mask must be [rows, words]")
+        words = mask.shape[1]
+        mask_ptr = _ptr(cache, mask, "mask", torch.int32, (n, words))
+    if softmax_scale is None:
+        softmax_scale = _SCALE_128
+    if out is None:
+        out = torch.empty((n, Hq, 128), dtype=q.dtype, device=cache.device)
+        out_ptr = out.data_ptr()
+    else:
+        out_ptr = _ptr(cache, out, "out", q.dtype, (n, Hq, 128))
+    lse_ptr = None if lse is None else _ptr(cache, lse, "lse", torch.float32, (n, Hq))
+    ws = _paged_workspace(cache, workspace, B, Hq, n, "kvq_paged_tree_workspace_bytes")
+    st = cache.lib.kvq_paged_tree_attn(cache.ref, tab, W, B, lens, off, n, mask_ptr, words, q.data_ptr(), qdt, stride,
+                                       Hq, softmax_scale, out_ptr, lse_ptr, ws.data_ptr(), ws.numel(),
+                                       _raw_stream(cache.index))
+    if st:
+        _check(st, "kvq_paged_tree_attn")
+    return out
+
+
+def kvq_paged_tree_commit(cache: PagedCache, page_table: torch.Tensor, seq_lens: torch.Tensor, accepted: torch.Tensor,
+                          offsets: torch.Tensor, stream=None):
+    """The accepted drafted tokens move to the places behind the cached ones:
+    accepted int32 [n], the numbers of request b's, ascending, at offsets[b] ..
+    offsets[b + 1] - 1 (int32 [B + 1]); the k-th goes from place seq_lens[b] +
+    accepted[k] to seq_lens[b] + k. The key bounds of the pages from there on are
+    taken anew, without the rejected tokens. seq_lens is not changed: the request's
+    new length is seq_lens[b] + offsets[b + 1] - offsets[b]."""
+    if _elsewhere(cache, stream):
+        with _made_current(cache, stream):
+            return kvq_paged_tree_commit(cache, page_table, seq_lens, accepted, offsets)
+    if cache.k is None:
+        raise KvqError("a cache of key bounds alone has no tokens")
+    shape = _table_shape(page_table)
+    B, W = shape
+    tab = _ptr(cache, page_table, "page_table", torch.int32, shape)
+    if accepted.dim() != 1:
+        raise KvqError("accepted must be [n]")
+    n = accepted.shape[0]
+    acc = _ptr(cache, accepted, "accepted", torch.int32, (n,))
+    lens = _ptr(cache, seq_lens, "seq_lens", torch.int32, (B,))
+    off = _ptr(cache, offsets, "offsets", torch.int32, (B + 1,))
+    st = cache.lib.kvq_paged_tree_commit(cache.ref, tab, W, B, lens, acc, off, n, _raw_stream(cache.index))
+    if st:
+        _check(st, "kvq_paged_tree_commit")
