@@ -66,10 +66,14 @@ struct Form {
   static constexpr int kRows = kTile * TILES;
   static constexpr int kSoftmaxWarps = 4 * TILES;
   static constexpr int kMmaWarp = kSoftmaxWarps + kProducers / 32;
-  static constexpr int kThreads = (kMmaWarp + 1) * 32;
+  static constexpr int kThreads = (kMmaWarp + 4) * 32;  // (three idle warps: registers are shared out by four)
+  // registers of the softmax, producer and MMA warps; 504 = 3 x 168 and 512 = 4 x 128 of the launch
+  static constexpr int kSoftmaxRegs = TILES == 1 ? 224 : 144, kProducerRegs = TILES == 1 ? 152 : 112,
+                       kMmaRegs = TILES == 1 ? 128 : 112;
   static constexpr int kSlots = kNarrow ? 3 : (TILES == 1 ? 6 : 5);
   static constexpr int kStages = kNarrow ? (TILES == 1 ? 5 : 3) : 0;  // of raw 8-bit rows
-  static constexpr int kLag = kNarrow ? kStages - 1 : kSlots - 2;     // copies in flight, in slots
+  // slots between a copy and the look at it: 8-bit rows are all converted, of 16-bit ones the drafted values checked
+  static constexpr int kLag = kNarrow ? kStages - 1 : 2;
 };
 
 template <class F>
@@ -111,7 +115,7 @@ __device__ __forceinline__ long long global_ns() {
   return t;
 }
 // Waits for the phase of this parity; false when it took kWaitNs, or another wait of the block did.
-__device__ __noinline__ bool mbar_wait_long(unsigned long long* bar, uint32_t parity, volatile int* abort) {
+__device__ __forceinline__ bool mbar_wait_long(unsigned long long* bar, uint32_t parity, volatile int* abort) {
   const long long t0 = global_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (*abort) return false;
@@ -157,6 +161,12 @@ __device__ __forceinline__ void mma_commit(unsigned long long* bar) {
                : "memory");
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // A thread's row: 32 columns of tensor memory. The registers are read only behind tmem_wait_ld.
 __device__ __forceinline__ void tmem_ld(uint32_t at, uint32_t (&r)[32]) {
   asm volatile(
@@ -177,14 +187,21 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                  "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
-__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[32]) {
+// Registers of further loads that a tmem_wait_ld has waited for, too.
+__device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                      "+r"(r[i + 6]), "+r"(r[i + 7])::"memory");
+}
+// 16 columns, at once and waited for.
+__device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
@@ -205,6 +222,18 @@ __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;"
 template <int N>
 __device__ __forceinline__ void wait_groups() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// The barrier counts this thread once its copies so far have landed.
+__device__ __forceinline__ void arrive_landed(unsigned long long* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 __device__ __forceinline__ uint4 lds16(uint32_t a) {
   uint4 v;
@@ -349,7 +378,7 @@ __device__ __forceinline__ uint32_t seen_bits(const uint32_t* mask, int words, i
 
 // Sum of the values that are not finite in channel c of the drafted tokens that row i sees (0: none).
 template <int DT>
-__device__ __noinline__ float loose(const TreeArgs& a, const Request& r, int b, int h, int i, int c) {
+__device__ __forceinline__ float loose(const TreeArgs& a, const Request& r, int b, int h, int i, int c) {
   const uint32_t* mask = a.mask != nullptr ? a.mask + (long long)(r.row0 + i) * a.mask_words : nullptr;
   float sum = 0.0f;
   for (int j = 0; j < r.n; ++j) {
@@ -452,7 +481,6 @@ struct Softmax {
       float m = -INFINITY, l = 0.0f;
       const int i = r / a.g;
       const uint32_t* mask = a.mask != nullptr && r < M ? a.mask + (long long)(w.r.row0 + i) * a.mask_words : nullptr;
-      const bool chain = a.mask == nullptr;
       float sc = a.scale * kLog2e;
       if constexpr (DT == kE4m3 && !TS)
         if (a.c.k_scale != nullptr) sc = scaled(sc, a.c.k_scale[w.h]);
@@ -488,39 +516,48 @@ struct Softmax {
         if (!mbar_wait(&S.s_full[buf], phase, &S.abort)) return;
         tc_fence_after();
         if (rows) {
-          const bool whole = t0 + kTile <= w.r.P;
-          uint32_t see[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-          if (!whole) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              see[c] = r < M ? seen_bits(chain ? nullptr : mask, a.mask_words, w.r.n, i, t0 + 32 * c - w.r.P) : 0u;
-          }
-          auto logits = [&](int c, uint32_t (&x)[32]) {  // TS: in log2 units, else in the product's
+          // Scores 64 columns at a time, twice: for their maximum, and for the weights (held in between they would take
+          // 128 registers). TS: in log2 units, else the products' own.
+          const bool drafted = t0 + kTile > w.r.P;
+          uint32_t x[2][32];
+          auto pair = [&](int c, int e) { return make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])); };
+          auto load = [&](int half) {
+            tmem_ld(s_at + 64 * half, x[0]);
+            tmem_ld(s_at + 64 * half + 32, x[1]);
+            tmem_wait_ld(x[0]);
+            tmem_landed(x[1]);
             if constexpr (TS) {
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(&kf[32 * c + e]);
-                x[e] = __float_as_uint(__uint_as_float(x[e]) * f.x);
-                x[e + 1] = __float_as_uint(__uint_as_float(x[e + 1]) * f.y);
-                x[e + 2] = __float_as_uint(__uint_as_float(x[e + 2]) * f.z);
-                x[e + 3] = __float_as_uint(__uint_as_float(x[e + 3]) * f.w);
-              }
-            }
-            if (!whole) {
+              for (int c = 0; c < 2; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!((see[c] >> e) & 1)) x[e] = 0xFF800000u;
+                for (int e = 0; e < 32; e += 4) {
+                  const float4 f = *reinterpret_cast<const float4*>(&kf[64 * half + 32 * c + e]);
+                  const float2 y = __fmul2_rn(pair(c, e), make_float2(f.x, f.y));
+                  const float2 z = __fmul2_rn(pair(c, e + 2), make_float2(f.z, f.w));
+                  x[c][e] = __float_as_uint(y.x);
+                  x[c][e + 1] = __float_as_uint(y.y);
+                  x[c][e + 2] = __float_as_uint(z.x);
+                  x[c][e + 3] = __float_as_uint(z.y);
+                }
+            }
+            if (drafted) {
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t see = r < M ? seen_bits(mask, a.mask_words, w.r.n, i, t0 + 64 * half + 32 * c - w.r.P) : 0u;
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  if (!((see >> e) & 1)) x[c][e] = 0xFF800000u;
+              }
             }
           };
           float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tmem_ld(s_at + 32 * c, x);
-            tmem_wait_ld(x);
-            logits(c, x);
+          for (int half = 0; half < 2; ++half) {
+            load(half);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(x[e]));
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
           }
           if constexpr (!TS) mx *= sc;
           if (k == w.begin) {
@@ -532,47 +569,38 @@ struct Softmax {
             // the sums are at rest behind the product before
             if (!mbar_wait(&S.pv_done[TILES == 1 ? 0 : tile], (count - 1) & 1u, &S.abort)) return;
             tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t y[16];
+              tmem_ld16(o_at + 16 * c, y);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t x[32];
-              tmem_ld(o_at + 32 * c, x);
-              tmem_wait_ld(x);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * alpha);
-              tmem_st(o_at + 32 * c, x);
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+              tmem_st16(o_at + 16 * c, y);
             }
             tmem_wait_st();
           }
           const float base = F::kShift - (m == -INFINITY ? 0.0f : m);
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32], p[16];
-            tmem_ld(s_at + 32 * c, x);
-            tmem_wait_ld(x);
-            logits(c, x);
-            float s0 = 0.0f, s1 = 0.0f;
+          for (int half = 0; half < 2; ++half) {
+            load(half);
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              float p0, p1;
-              if constexpr (TS) {
-                p0 = exp2_ftz(__uint_as_float(x[e]) + base);
-                p1 = exp2_ftz(__uint_as_float(x[e + 1]) + base);
-              } else {
-                p0 = exp2_ftz(fmaf(__uint_as_float(x[e]), sc, base));
-                p1 = exp2_ftz(fmaf(__uint_as_float(x[e + 1]), sc, base));
+            for (int c = 0; c < 2; ++c) {
+              uint32_t p[16];
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                float2 y;
+                if constexpr (TS) y = __fadd2_rn(pair(c, e), make_float2(base, base));
+                else y = __ffma2_rn(pair(c, e), make_float2(sc, sc), make_float2(base, base));
+                y = make_float2(exp2_ftz(y.x), exp2_ftz(y.y));
+                sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], y);
+                if constexpr (TS) y = __fmul2_rn(y, *reinterpret_cast<const float2*>(&vf[64 * half + 32 * c + e]));
+                p[e / 2] = pack<F::kValBf>(y.x, y.y);
               }
-              s0 += p0;
-              s1 += p1;
-              if constexpr (TS) {
-                const float2 f = *reinterpret_cast<const float2*>(&vf[32 * c + e]);
-                p0 *= f.x;
-                p1 *= f.y;
-              }
-              p[e / 2] = pack<F::kValBf>(p0, p1);
+              tmem_st16(s_at + 32 * half + 16 * c, p);  // (in the place of scores that are read)
             }
-            l += s0 + s1;
-            tmem_st16(s_at + 16 * c, p);
           }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -666,36 +694,41 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
   for (int i = 0; i <= F::kLag; ++i) past[i] = Past{kTile, 0};
   constexpr int kChunks = kD * elem_bytes<DT>() / 16, kQuads = kChunks / 4;
 
-  // Copy number x (K of a tile, then V) has landed: makes it an operand.
+  // Copy number x (K of a tile, then V) has landed: makes it an operand. (Of 16-bit rows only the drafted values come
+  // here; the others arrive by themselves.)
   auto land = [&](uint32_t x, const Past& p, bool value) -> bool {
     const uint32_t slot = x % F::kSlots;
     const uint32_t to = slots + slot * kSlotBytes;
     if constexpr (F::kNarrow) {
       if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return false;
       const uint32_t from = raws + (x % F::kStages) * kRawBytes;
+      uint4 y[4 * kQuads];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int i = 0; i < 4 * kQuads; ++i) y[i] = lds16(from + i * (kProducers * 16));
+      if (value && p.from < kTile) {  // drafted tokens: NaN is replaced by 0
+        uint32_t any = 0u;
 #pragma unroll
-        for (int f = 0; f < kQuads; ++f) {
-          uint4 y = lds16(from + (e * kQuads + f) * (kProducers * 16));
-          const int token = 32 * warp + 8 * e + (lane & 7), chunk = 4 * f + (lane >> 3);
-          if (value && token >= p.from) {
-            uint32_t any = 0u;
+        for (int i = 0; i < 4 * kQuads; ++i) {
+          if (32 * warp + 8 * (i / kQuads) + (lane & 7) < p.from) continue;
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              const uint32_t nan = (((&y.x)[d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes of 0x7F or 0xFF
-              (&y.x)[d] &= ~((nan >> 7) * 255u);
-              any |= nan;
-            }
-            if (any != 0u) atomicOr(&S.flags[p.number & 7], kLoose);
+          for (int d = 0; d < 4; ++d) {
+            const uint32_t nan = (((&y[i].x)[d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes of 0x7F or 0xFF
+            (&y[i].x)[d] &= ~((nan >> 7) * 255u);
+            any |= nan;
           }
-          uint2 z[4];
-#pragma unroll
-          for (int d = 0; d < 4; ++d) z[d] = value ? widen<F::kValBf>((&y.x)[d]) : widen<F::kKeyBf>((&y.x)[d]);
-          sts16(to + chunk_at(token, 2 * chunk), make_uint4(z[0].x, z[0].y, z[1].x, z[1].y));
-          sts16(to + chunk_at(token, 2 * chunk + 1), make_uint4(z[2].x, z[2].y, z[3].x, z[3].y));
         }
-    } else if (value && p.from < kTile) {
+        if (any != 0u) atomicOr(&S.flags[p.number & 7], kLoose);
+      }
+#pragma unroll
+      for (int i = 0; i < 4 * kQuads; ++i) {
+        const uint32_t at = to + chunk_at(32 * warp + 8 * (i / kQuads) + (lane & 7), 8 * (i % kQuads) + 2 * (lane >> 3));
+        uint2 z[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) z[d] = value ? widen<F::kValBf>((&y[i].x)[d]) : widen<F::kKeyBf>((&y[i].x)[d]);
+        sts16(at, make_uint4(z[0].x, z[0].y, z[1].x, z[1].y));
+        sts16(at + 128, make_uint4(z[2].x, z[2].y, z[3].x, z[3].y));
+      }
+    } else {  // drafted values
       constexpr uint32_t kInf = DT == kBf16 ? 0x7F80u : 0x7C00u;
 #pragma unroll 1
       for (int e = 0; e < 16; ++e) {
@@ -772,8 +805,15 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
 #pragma unroll
         for (int i = F::kLag; i > 0; --i) past[i] = past[i - 1];
         past[0] = now;
-        wait_groups<F::kLag>();
-        if (x >= uint32_t(F::kLag) && !land(x - F::kLag, past[F::kLag], ((x - F::kLag) & 1u) != 0u)) return;
+        if constexpr (!F::kNarrow)
+          if (half == 0 || now.from == kTile) {
+            arrive_landed(&S.full[x % F::kSlots]);
+            past[0].from = kTile;
+          }
+        if (F::kNarrow ? x >= uint32_t(F::kLag) : past[F::kLag].from < kTile) {
+          wait_groups<F::kLag>();
+          if (!land(x - F::kLag, past[F::kLag], ((x - F::kLag) & 1u) != 0u)) return;
+        }
       }
     }
     more = w.next(a, s0, e0);
@@ -782,7 +822,7 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
   wait_groups<0>();
 #pragma unroll
   for (int i = F::kLag - 1; i >= 0; --i)
-    if (x >= uint32_t(i + 1) && !land(x - 1 - i, past[i], ((x - 1 - i) & 1u) != 0u)) return;
+    if ((F::kNarrow ? x >= uint32_t(i + 1) : past[i].from < kTile) && !land(x - 1 - i, past[i], ((x - 1 - i) & 1u) != 0u)) return;
 }
 
 // ---------------------------------------------------------------- products
@@ -812,6 +852,7 @@ __device__ __forceinline__ bool multiply(const TreeArgs& a, Smem<Form<DT, QT, TI
   };
   auto filled = [&](uint32_t x) {
     if (!mbar_wait(&S.full[x % F::kSlots], (x / F::kSlots) & 1u, &S.abort)) return false;
+    if constexpr (!F::kNarrow) fence_async_smem();  // (copies that arrive by themselves have no fence behind them)
     tc_fence_after();
     return true;
   };
@@ -936,17 +977,22 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
   tc_fence_after();
 
   if (warp < F::kSoftmaxWarps) {
+    more_registers<F::kSoftmaxRegs>();
     Softmax<DT, QT, TILES, TS> K(a, S);
     K.run(w, s0, e0, W, C);
   } else if (warp < F::kMmaWarp) {
+    fewer_registers<F::kProducerRegs>();
     produce<DT, QT, TILES, TS>(a, S, w, s0, e0);
     wait_groups<0>();
-  } else if ((threadIdx.x & 31) == 0) {
-    multiply<DT, QT, TILES, TS>(a, S, w, s0, e0);
-    // the products in flight end before the tensor memory is freed
-    mma_commit(&S.drain);
-    int never = 0;
-    mbar_wait(&S.drain, 0, &never);
+  } else {
+    fewer_registers<F::kMmaRegs>();
+    if (threadIdx.x == F::kMmaWarp * 32) {
+      multiply<DT, QT, TILES, TS>(a, S, w, s0, e0);
+      // the products in flight end before the tensor memory is freed
+      mma_commit(&S.drain);
+      int never = 0;
+      mbar_wait(&S.drain, 0, &never);
+    }
   }
   __syncwarp();
   tc_fence_before();
