@@ -134,10 +134,11 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Shared-memory matrix descriptor without swizzle: start, leading (along K) and stride
-// (along M or N) byte offsets between core matrices.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(lbo >> 4) << 16) | (uint64_t(sbo >> 4) << 32) | (1ull << 46);
+// Shared-memory matrix descriptor of operands with a 128-byte swizzle: 1024 bytes from eight rows (tokens) to the next
+// eight; in an MN-major operand `lbo` bytes from 64 channels to the next 64.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(lbo >> 4) << 16) | (uint64_t(1024 >> 4) << 32) | (1ull << 46) |
+         (2ull << 61);
 }
 // Instruction descriptor of kind::f16: A and B of one type, FP32 D, 128 x 128; b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t instr_desc(bool bf16, bool b_mn) {
@@ -397,10 +398,12 @@ __device__ __forceinline__ float loose(const TreeArgs& a, const Request& r, int 
   return sum;
 }
 
-// Where in an operand slot a 16-byte chunk (eight channels) of a token lies: core matrices of 8 tokens x 16 bytes, the
-// same for a K-major (keys) and an MN-major operand (values).
+// Where in an operand slot a 16-byte chunk (eight channels) of a token (or row) lies: 64 channels of all 128 tokens, then
+// the other 64, a token's 128 bytes with its chunks swizzled by the token's number. The same for a K-major operand (keys,
+// queries) and an MN-major one (values). (Core matrices of 8 x 16 bytes without a swizzle take each of a row's chunks to
+// another line of shared memory: the copies' writes then took the products half of their rate.)
 __device__ __forceinline__ uint32_t chunk_at(int token, int chunk) {
-  return uint32_t((token >> 3) * 2048 + chunk * 128 + (token & 7) * 16);
+  return uint32_t((chunk >> 3) * (kSlotBytes / 2) + token * 128 + (((chunk ^ token) & 7) << 4));
 }
 
 struct Rec {  // a unit that begins in a block's range and goes on behind it (parts 0: none)
@@ -443,12 +446,12 @@ struct Softmax {
     }
     const uint32_t to = smem_addr(S.q) + tile * kSlotBytes;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const long long x = __shfl_sync(0xFFFFFFFFu, off, 8 * e + (lane & 7));
+    for (int e = 0; e < 8; ++e) {
+      const long long x = __shfl_sync(0xFFFFFFFFu, off, 4 * e + (lane >> 3));
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        const int chunk = 4 * f + (lane >> 3);
-        copy16(to + chunk_at(32 * warp + 8 * e + (lane & 7), chunk), a.q + (x < 0 ? 0 : x) + chunk * 16, x >= 0);
+      for (int f = 0; f < 2; ++f) {
+        const int chunk = 8 * f + (lane & 7);
+        copy16(to + chunk_at(32 * warp + 4 * e + (lane >> 3), chunk), a.q + (x < 0 ? 0 : x) + chunk * 16, x >= 0);
       }
     }
     commit();
@@ -692,7 +695,7 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
   } past[F::kLag + 1];
 #pragma unroll
   for (int i = 0; i <= F::kLag; ++i) past[i] = Past{kTile, 0};
-  constexpr int kChunks = kD * elem_bytes<DT>() / 16, kQuads = kChunks / 4;
+  constexpr int kHalves = kD * elem_bytes<DT>() / 128;  // 128-byte pieces of a row
 
   // Copy number x (K of a tile, then V) has landed: makes it an operand. (Of 16-bit rows only the drafted values come
   // here; the others arrive by themselves.)
@@ -702,14 +705,14 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
     if constexpr (F::kNarrow) {
       if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return false;
       const uint32_t from = raws + (x % F::kStages) * kRawBytes;
-      uint4 y[4 * kQuads];
+      uint4 y[8];  // 16 channels of eight tokens
 #pragma unroll
-      for (int i = 0; i < 4 * kQuads; ++i) y[i] = lds16(from + i * (kProducers * 16));
+      for (int i = 0; i < 8; ++i) y[i] = lds16(from + i * (kProducers * 16));
       if (value && p.from < kTile) {  // drafted tokens: NaN is replaced by 0
         uint32_t any = 0u;
 #pragma unroll
-        for (int i = 0; i < 4 * kQuads; ++i) {
-          if (32 * warp + 8 * (i / kQuads) + (lane & 7) < p.from) continue;
+        for (int i = 0; i < 8; ++i) {
+          if (32 * warp + 4 * i + (lane >> 3) < p.from) continue;
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
             const uint32_t nan = (((&y[i].x)[d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes of 0x7F or 0xFF
@@ -720,19 +723,19 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
         if (any != 0u) atomicOr(&S.flags[p.number & 7], kLoose);
       }
 #pragma unroll
-      for (int i = 0; i < 4 * kQuads; ++i) {
-        const uint32_t at = to + chunk_at(32 * warp + 8 * (i / kQuads) + (lane & 7), 8 * (i % kQuads) + 2 * (lane >> 3));
+      for (int i = 0; i < 8; ++i) {
+        const int token = 32 * warp + 4 * i + (lane >> 3), chunk = 2 * (lane & 7);
         uint2 z[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d) z[d] = value ? widen<F::kValBf>((&y[i].x)[d]) : widen<F::kKeyBf>((&y[i].x)[d]);
-        sts16(at, make_uint4(z[0].x, z[0].y, z[1].x, z[1].y));
-        sts16(at + 128, make_uint4(z[2].x, z[2].y, z[3].x, z[3].y));
+        sts16(to + chunk_at(token, chunk), make_uint4(z[0].x, z[0].y, z[1].x, z[1].y));
+        sts16(to + chunk_at(token, chunk + 1), make_uint4(z[2].x, z[2].y, z[3].x, z[3].y));
       }
     } else {  // drafted values
       constexpr uint32_t kInf = DT == kBf16 ? 0x7F80u : 0x7C00u;
 #pragma unroll 1
       for (int e = 0; e < 16; ++e) {
-        const int token = 32 * warp + 8 * (e >> 2) + (lane & 7), chunk = 4 * (e & 3) + (lane >> 3);
+        const int token = 32 * warp + 4 * (e >> 1) + (lane >> 3), chunk = 8 * (e & 1) + (lane & 7);
         if (token < p.from) continue;
         const uint32_t at = to + chunk_at(token, chunk);
         uint4 y = lds16(at);
@@ -791,13 +794,13 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
           to = raws + (x % F::kStages) * kRawBytes;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const long long y = __shfl_sync(0xFFFFFFFFu, off, 8 * e + (lane & 7));
+        for (int e = 0; e < 8; ++e) {
+          const long long y = __shfl_sync(0xFFFFFFFFu, off, 4 * e + (lane >> 3));
 #pragma unroll
-          for (int f = 0; f < kQuads; ++f) {
-            const int chunk = 4 * f + (lane >> 3);
-            const uint32_t at = F::kNarrow ? to + (e * kQuads + f) * (kProducers * 16)
-                                           : to + chunk_at(32 * warp + 8 * e + (lane & 7), chunk);
+          for (int f = 0; f < kHalves; ++f) {
+            const int chunk = 8 * f + (lane & 7);
+            const uint32_t at = F::kNarrow ? to + e * (kProducers * 16)
+                                           : to + chunk_at(32 * warp + 4 * e + (lane >> 3), chunk);
             copy16(at, pool + (y < 0 ? 0 : y) + chunk * 16, y >= 0);
           }
         }
@@ -836,17 +839,19 @@ __device__ __forceinline__ bool multiply(const TreeArgs& a, Smem<Form<DT, QT, TI
   uint32_t count[2] = {0, 0};  // products of each row tile so far
   uint32_t units = 0;
   auto keys = [&](int tile, uint32_t x, uint32_t buf) {
-    const uint64_t qa = smem_desc(q + tile * kSlotBytes, 128, 2048), kb = smem_desc(slots + (x % F::kSlots) * kSlotBytes, 128, 2048);
+    const uint64_t qa = smem_desc(q + tile * kSlotBytes, 16), kb = smem_desc(slots + (x % F::kSlots) * kSlotBytes, 16);
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-      mma_ss(tmem + 256u + 128u * buf, qa + 16u * k, kb + 16u * k, instr_desc(F::kKeyBf, false), k > 0);
+    for (uint32_t k = 0; k < 8; ++k) {  // 16 channels: 32 bytes on, four times in each half
+      const uint32_t on = 2u * (k & 3u) + (kSlotBytes / 32) * (k >> 2);
+      mma_ss(tmem + 256u + 128u * buf, qa + on, kb + on, instr_desc(F::kKeyBf, false), k > 0);
+    }
     mma_commit(&S.s_full[buf]);
   };
   auto values = [&](int tile, uint32_t x, uint32_t buf, bool first) {
-    const uint64_t vb = smem_desc(slots + (x % F::kSlots) * kSlotBytes, 2048, 128);
+    const uint64_t vb = smem_desc(slots + (x % F::kSlots) * kSlotBytes, kSlotBytes / 2);
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-      mma_ts(tmem + 128u * tile, tmem + 256u + 128u * buf + 8u * k, vb + 256u * k, instr_desc(F::kValBf, true),
+    for (uint32_t k = 0; k < 8; ++k)  // 16 tokens: 2048 bytes on
+      mma_ts(tmem + 128u * tile, tmem + 256u + 128u * buf + 8u * k, vb + 128u * k, instr_desc(F::kValBf, true),
              !first || k > 0);
     mma_commit(&S.pv_done[tile]);
   };
@@ -915,7 +920,7 @@ template <int DT, int QT, int TILES, bool TS>
 __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_kernel(const __grid_constant__ TreeArgs a) {
   using F = Form<DT, QT, TILES, TS>;
   constexpr int R = F::kRows;
-  extern __shared__ __align__(128) char smem[];
+  extern __shared__ __align__(1024) char smem[];
   Smem<F>& S = *reinterpret_cast<Smem<F>*>(smem);
   wait_prior_grid();
   allow_dependents();
