@@ -36,6 +36,7 @@
 // Every wait is bounded (2 s): a wait that runs out sets an error bit and the block
 // leaves, after its products in flight.
 #include <atomic>
+#include <type_traits>
 
 #include "kvq_attn_common.cuh"
 #include "kvq_paged.cuh"
@@ -695,11 +696,13 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
   } past[F::kLag + 1];
 #pragma unroll
   for (int i = 0; i <= F::kLag; ++i) past[i] = Past{kTile, 0};
+  constexpr int kFirst = F::kLag % 2;  // the half of a tile in which a copy of keys is looked at
   constexpr int kHalves = kD * elem_bytes<DT>() / 128;  // 128-byte pieces of a row
 
   // Copy number x (K of a tile, then V) has landed: makes it an operand. (Of 16-bit rows only the drafted values come
   // here; the others arrive by themselves.)
-  auto land = [&](uint32_t x, const Past& p, bool value) -> bool {
+  auto land = [&](uint32_t x, const Past& p, auto is_value) -> bool {
+    constexpr bool value = decltype(is_value)::value;
     const uint32_t slot = x % F::kSlots;
     const uint32_t to = slots + slot * kSlotBytes;
     if constexpr (F::kNarrow) {
@@ -727,11 +730,11 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
         const int token = 32 * warp + 4 * i + (lane >> 3), chunk = 2 * (lane & 7);
         uint2 z[4];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) z[d] = value ? widen<F::kValBf>((&y[i].x)[d]) : widen<F::kKeyBf>((&y[i].x)[d]);
+        for (int d = 0; d < 4; ++d) z[d] = widen<value ? F::kValBf : F::kKeyBf>((&y[i].x)[d]);
         sts16(to + chunk_at(token, chunk), make_uint4(z[0].x, z[0].y, z[1].x, z[1].y));
         sts16(to + chunk_at(token, chunk + 1), make_uint4(z[2].x, z[2].y, z[3].x, z[3].y));
       }
-    } else {  // drafted values
+    } else if constexpr (value) {  // drafted ones
       constexpr uint32_t kInf = DT == kBf16 ? 0x7F80u : 0x7C00u;
 #pragma unroll 1
       for (int e = 0; e < 16; ++e) {
@@ -815,7 +818,9 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
           }
         if (F::kNarrow ? x >= uint32_t(F::kLag) : past[F::kLag].from < kTile) {
           wait_groups<F::kLag>();
-          if (!land(x - F::kLag, past[F::kLag], ((x - F::kLag) & 1u) != 0u)) return;
+          if (half == kFirst ? !land(x - F::kLag, past[F::kLag], std::false_type{})
+                             : !land(x - F::kLag, past[F::kLag], std::true_type{}))
+            return;
         }
       }
     }
@@ -824,8 +829,9 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
   }
   wait_groups<0>();
 #pragma unroll
-  for (int i = F::kLag - 1; i >= 0; --i)
-    if ((F::kNarrow ? x >= uint32_t(i + 1) : past[i].from < kTile) && !land(x - 1 - i, past[i], ((x - 1 - i) & 1u) != 0u)) return;
+  for (int i = F::kLag - 1; i >= 0; --i)  // (the last one was of values)
+    if (F::kNarrow ? x >= uint32_t(i + 1) : past[i].from < kTile)
+      if (i % 2 ? !land(x - 1 - i, past[i], std::false_type{}) : !land(x - 1 - i, past[i], std::true_type{})) return;
 }
 
 // ---------------------------------------------------------------- products
