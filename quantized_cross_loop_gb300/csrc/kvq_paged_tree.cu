@@ -528,21 +528,30 @@ struct Softmax {
           auto load = [&](int half) {
             tmem_ld(s_at + 64 * half, x[0]);
             tmem_ld(s_at + 64 * half + 32, x[1]);
-            tmem_wait_ld(x[0]);
-            tmem_landed(x[1]);
             if constexpr (TS) {
+              // (a row's scales are the same for all lanes: read while the scores are on their way)
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
+              for (int c = 0; c < 2; ++c) {
+                float4 f[8];
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                  const float4 f = *reinterpret_cast<const float4*>(&kf[64 * half + 32 * c + e]);
-                  const float2 y = __fmul2_rn(pair(c, e), make_float2(f.x, f.y));
-                  const float2 z = __fmul2_rn(pair(c, e + 2), make_float2(f.z, f.w));
-                  x[c][e] = __float_as_uint(y.x);
-                  x[c][e + 1] = __float_as_uint(y.y);
-                  x[c][e + 2] = __float_as_uint(z.x);
-                  x[c][e + 3] = __float_as_uint(z.y);
+                for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float4*>(&kf[64 * half + 32 * c + 4 * e]);
+                if (c == 0) {
+                  tmem_wait_ld(x[0]);
+                  tmem_landed(x[1]);
                 }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const float2 y = __fmul2_rn(pair(c, 4 * e), make_float2(f[e].x, f[e].y));
+                  const float2 z = __fmul2_rn(pair(c, 4 * e + 2), make_float2(f[e].z, f[e].w));
+                  x[c][4 * e] = __float_as_uint(y.x);
+                  x[c][4 * e + 1] = __float_as_uint(y.y);
+                  x[c][4 * e + 2] = __float_as_uint(z.x);
+                  x[c][4 * e + 3] = __float_as_uint(z.y);
+                }
+              }
+            } else {
+              tmem_wait_ld(x[0]);
+              tmem_landed(x[1]);
             }
             if (drafted) {
 #pragma unroll
@@ -591,6 +600,11 @@ struct Softmax {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               uint32_t p[16];
+              [[maybe_unused]] float4 f[8];
+              if constexpr (TS) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float4*>(&vf[64 * half + 32 * c + 4 * e]);
+              }
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 float2 y;
@@ -598,7 +612,7 @@ struct Softmax {
                 else y = __ffma2_rn(pair(c, e), make_float2(sc, sc), make_float2(base, base));
                 y = make_float2(exp2_ftz(y.x), exp2_ftz(y.y));
                 sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], y);
-                if constexpr (TS) y = __fmul2_rn(y, *reinterpret_cast<const float2*>(&vf[64 * half + 32 * c + e]));
+                if constexpr (TS) y = __fmul2_rn(y, e & 2 ? make_float2(f[e / 4].z, f[e / 4].w) : make_float2(f[e / 4].x, f[e / 4].y));
                 p[e / 2] = pack<F::kValBf>(y.x, y.y);
               }
               tmem_st16(s_at + 32 * half + 16 * c, p);  // (in the place of scores that are read)
