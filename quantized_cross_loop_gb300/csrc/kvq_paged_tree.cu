@@ -46,11 +46,12 @@ namespace paged {
 namespace {
 
 constexpr int kTile = 128;       // tokens of a tile, rows of a row tile
-constexpr int kProducers = 128;  // threads
 constexpr int kUnitCost = 1;     // tiles that the end of a unit takes as long as
 constexpr int kSlotBytes = kTile * kD * 2;
 constexpr int kRawBytes = kTile * kD;
 constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColS = 256;  // scores and weights: two buffers of 128 columns; the sums are at 0 (and 128: second row tile)
+constexpr uint32_t kColQ = 128;  // one row tile: queries, two buffers of 64
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;   // log2 of what a row's weights may exceed 1 by before its sums are rescaled
 constexpr long long kWaitNs = 2000000000LL;
@@ -62,34 +63,46 @@ template <int DT, int QT, int TILES, bool TS>
 struct Form {
   static constexpr bool kNarrow = DT == kE4m3;
   static constexpr bool kKeyBf = DT == kBf16 || (kNarrow && QT == kBf16);  // type of Q and K operands
-  static constexpr bool kValBf = DT != kFp16;                              // type of P and V operands
+  static constexpr bool kValBf = DT == kBf16;                              // type of P and V operands
   static constexpr float kShift = kValBf ? -kSlack : 15.0f - kSlack;
   static constexpr int kRows = kTile * TILES;
   static constexpr int kSoftmaxWarps = 4 * TILES;
-  static constexpr int kMmaWarp = kSoftmaxWarps + kProducers / 32;
+  // (8-bit rows: the conversion is what bounds one row tile)
+  static constexpr int kProducerWarps = kNarrow && TILES == 1 ? 8 : 4;
+  static constexpr int kProducers = 32 * kProducerWarps;
+  static constexpr int kTokens = kTile / kProducerWarps;  // of a tile, a producer warp's
+  static constexpr int kMmaWarp = kSoftmaxWarps + kProducerWarps;
   static constexpr int kThreads = (kMmaWarp + 4) * 32;  // (three idle warps: registers are shared out by four)
-  // registers of the softmax, producer and MMA warps; 504 = 3 x 168 and 512 = 4 x 128 of the launch
-  static constexpr int kSoftmaxRegs = TILES == 1 ? 224 : 144, kProducerRegs = TILES == 1 ? 152 : 112,
-                       kMmaRegs = TILES == 1 ? 128 : 112;
+  // registers of the softmax, producer and MMA warps, by four of which they come to 3 x 168 or 4 x 128 of the launch
+  static constexpr int kSoftmaxRegs = kThreads == 384 ? 224 : TILES == 1 ? 168 : 144;
+  static constexpr int kProducerRegs = kThreads == 384 ? 152 : TILES == 1 ? 120 : 112;
+  static constexpr int kMmaRegs = kThreads == 384 ? 128 : TILES == 1 ? 104 : 112;
+  static_assert(kSoftmaxRegs * TILES + kProducerRegs * kProducerWarps / 4 + kMmaRegs == (kThreads == 384 ? 504 : 512));
+  // One row tile: the queries are in tensor memory, two units' (A of the products); two fill it with sums and scores.
+  static constexpr int kQueries = TILES == 1 ? 0 : kRows;
   static constexpr int kSlots = kNarrow ? 3 : (TILES == 1 ? 6 : 5);
-  static constexpr int kStages = kNarrow ? (TILES == 1 ? 5 : 3) : 0;  // of raw 8-bit rows
+  static constexpr int kStages = kNarrow ? (TILES == 1 ? 6 : 3) : 0;  // of raw 8-bit rows
   // slots between a copy and the look at it: 8-bit rows are all converted, of 16-bit ones the drafted values checked
   static constexpr int kLag = kNarrow ? kStages - 1 : 2;
 };
 
 template <class F>
 struct Smem {
-  char q[F::kRows * kD * 2];
   union {
     char slot[F::kSlots][kSlotBytes];
     Prefix<F::kThreads> prefix;  // before the first copy
   };
+  char q[F::kQueries > 0 ? F::kQueries * kD * 2 : 16];
   char raw[F::kStages > 0 ? F::kStages : 1][F::kStages > 0 ? kRawBytes : 16];
-  float scales[F::kSoftmaxWarps / 4][2][2][F::kNarrow ? kTile : 4];  // row tile, parity, K and V, token
+  float scales[F::kSoftmaxWarps / 4][2][3][F::kNarrow ? kTile : 4];  // row tile, parity, (keys', log2 of and values'), token
+  float2 range[F::kSoftmaxWarps / 4][2][4];  // of the values' scales' logarithms: by a warp's 32 tokens
+  // one row tile: what its copies of the rows are joined by
+  float part[F::kQueries > 0 ? 1 : kTile][33];
+  float part_ml[3][F::kQueries > 0 ? 1 : kTile];
   unsigned long long full[F::kSlots], empty[F::kSlots];
-  unsigned long long s_full[2], p_ready[2], pv_done[2], q_full, drain;
+  unsigned long long s_full[2], p_ready[2], pv_done[2], q_full[2], q_free[2], o_free, drain;
   uint32_t tmem;
-  int flags[8];  // of the unit by its number's last bits
+  int flags[16];  // of the unit by its number's last bits
   volatile int abort;
 };
 
@@ -196,6 +209,16 @@ __device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
     asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
                       "+r"(r[i + 6]), "+r"(r[i + 7])::"memory");
 }
+__device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(at),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
 // 16 columns, at once and waited for.
 __device__ __forceinline__ void tmem_ld16(uint32_t at, uint32_t (&r)[16]) {
   asm volatile(
@@ -279,8 +302,8 @@ struct Request {
   int P, n, row0;
   bool refused;
   __device__ __forceinline__ void load(const TreeArgs& a, int b) {
+    P = checked_len(a.lens, b, a.max_pages, a.c.ps);
     n = row_range(a.offsets, a.n_rows, b, row0);
-    P = n > 0 ? checked_len(a.lens, b, a.max_pages, a.c.ps) : 0;
     refused = n < 0 || (n > 0 && (P < 0 || P + (long long)n > (long long)a.max_pages * a.c.ps.d ||
                                   n > KVQ_PAGED_MAX_DRAFT || (a.mask != nullptr && n > 32 * a.mask_words)));
     if (refused) n = 0;
@@ -362,6 +385,10 @@ struct Walk {
   }
 };
 
+// A unit of few rows has them in the row tile several times, each copy for its own share of a tile's tokens, so that all
+// softmax warps have work (the products take 128 rows in any case): the copies of M rows in all.
+__device__ __forceinline__ int copies(int M) { return M <= kTile / 4 ? 4 : M <= kTile / 2 ? 2 : 1; }
+
 // 32 bits of what row i of a request sees, from its drafted token j0 (which may be negative: cached tokens) on.
 __device__ __forceinline__ uint32_t seen_word(const uint32_t* mask, int words, int n, int i, int k) {
   if (k < 0) return 0xFFFFFFFFu;
@@ -411,8 +438,8 @@ struct Rec {  // a unit that begins in a block's range and goes on behind it (pa
   int32_t b, h, rb, parts;
 };
 __host__ __device__ constexpr size_t slots_offset(int n) { return size_t(n) * sizeof(Rec); }
-// sums [32][rows][4], then m and l by row, then flags
-__host__ __device__ constexpr size_t slot_floats(int rows) { return size_t(rows) * (kD + 2) + 4; }
+// sums [32][rows][4], then by row the weights' maximum and sum and (scales per token) what the sums are to, then flags
+__host__ __device__ constexpr size_t slot_floats(int rows) { return size_t(rows) * (kD + 3) + 4; }
 
 // ---------------------------------------------------------------- softmax warps
 
@@ -420,6 +447,14 @@ __host__ __device__ constexpr size_t slot_floats(int rows) { return size_t(rows)
 __device__ __forceinline__ float scaled(float scale, float ks) {
   const float x = scale * ks;
   return isfinite(ks) ? fminf(fmaxf(x, 0x1p-149f), 3.402823466e38f) : ks;
+}
+
+// 2^x / l as two factors f and g (l or a scale may take either out of FP32's range where the product with a sum stays
+// in it): f comes in as 1 / l.
+__device__ __forceinline__ void between(float x, float& f, float& g) {
+  const float half = rintf(0.5f * x);
+  f *= exp2f(fminf(fmaxf(half, -126.0f), 127.0f));
+  g = exp2f(fminf(fmaxf(x - half, -126.0f), 127.0f));
 }
 
 template <int DT, int QT, int TILES, bool TS>
@@ -437,7 +472,7 @@ struct Softmax {
 
   __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, 128;" ::"r"(tile + 1) : "memory"); }
 
-  // The unit's queries of this tile as an operand; the warp's own 32 rows.
+  // Two row tiles: the unit's queries of this tile as an operand; the warp's own 32 rows.
   __device__ __forceinline__ void load_queries(const Walk<F::kRows>& w) {
     const int M = w.r.n * a.g, r = w.rb * F::kRows + threadIdx.x;
     long long off = -1;
@@ -459,227 +494,387 @@ struct Softmax {
     wait_groups<0>();
     fence_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&S.q_full);
+    if (lane == 0) mbar_arrive(&S.q_full[0]);
   }
 
-  // Where token thread's scales of a tile are, or -1.
-  __device__ __forceinline__ long long scale_at(const Walk<F::kRows>& w, int t) const {
-    if (t >= w.tokens) return -1;
-    const int e = a.c.ps.div(t), page = a.table[(long long)w.b * a.max_pages + e];
-    if (page < 0 || page >= a.c.n_pages) return -1;
-    return ((long long)page * a.c.H + w.h) * int(a.c.ps.d) + (t - e * int(a.c.ps.d));
+  // Scales of this thread's token of a tile, in two steps: the page of the pool (-1: none), the scales.
+  struct Token {
+    int page, t, h;
+  };
+  __device__ __forceinline__ Token look_up(const Walk<F::kRows>& w, int k) const {
+    const int t = k * kTile + thread;
+    return Token{t < w.tokens ? a.table[(long long)w.b * a.max_pages + a.c.ps.div(t)] : -1, t, w.h};
+  }
+  __device__ __forceinline__ void fetch(const Token& n, float& ks, float& vs) const {
+    ks = vs = 0.0f;
+    if (n.page < 0 || n.page >= a.c.n_pages) return;
+    const long long at = ((long long)n.page * a.c.H + n.h) * int(a.c.ps.d) + (n.t - a.c.ps.div(n.t) * int(a.c.ps.d));
+    ks = a.c.k_scale[at];
+    vs = a.c.v_scale[at];
+  }
+
+  // Waits for the sums of the row tile's c-th product. (One row tile: that and the one before it may both be under way,
+  // and a wait tells only odd phases from even ones: they take turns at two barriers.)
+  __device__ __forceinline__ bool summed(uint32_t c) const {
+    if (!mbar_wait(&S.pv_done[TILES == 1 ? c & 1u : tile], (TILES == 1 ? c >> 1 : c) & 1u, &S.abort)) return false;
+    tc_fence_after();
+    return true;
+  }
+
+  struct Row {
+    int P, n, i;           // the request's cached and drafted tokens, the row's drafted token
+    bool live;
+    const uint32_t* mask;  // (nullptr: tokens 0 .. i)
+    // the weights' running maximum (log2) and sum, times 2^kShift; TS: not shifted, and `to` is the maximum of the weights
+    // times the values' scales, to which the sums of values are (else to m)
+    float m, l, to;
+  };
+
+  // The scores of tile k in NC x 32 columns, from copy x NC x 32 on, become weights in the place of the first half of
+  // them (for the other columns 0), the row's sums follow. Scores of up to 64 columns are held in registers; of 128 they
+  // are read twice, for their maximum and for the weights, scaled ones (TS) from where the first reading left them.
+  template <int NC>
+  __device__ __forceinline__ bool weigh(Row& row, int k, int begin, uint32_t count, uint32_t s_at, int copy, float sc) {
+    constexpr int kC = NC > 2 ? 2 : NC, kReads = NC / kC;
+    const bool drafted = (k + 1) * kTile > row.P;
+    [[maybe_unused]] const float* kf = S.scales[tile][count & 1u][0] + 32 * NC * copy;
+    [[maybe_unused]] const float* lv = S.scales[tile][count & 1u][1] + 32 * NC * copy;
+    [[maybe_unused]] const float* vf = S.scales[tile][count & 1u][2] + 32 * NC * copy;
+    const uint32_t x_at = s_at + 32u * NC * copy, p_at = s_at + 16u * NC * copy;
+    uint32_t x[kC][32];
+    auto pair = [&](int c, int e) { return make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])); };
+    auto put = [&](int c, int e, float2 y) {
+      x[c][e] = __float_as_uint(y.x);
+      x[c][e + 1] = __float_as_uint(y.y);
+    };
+    auto read = [&](int part) {
+#pragma unroll
+      for (int c = 0; c < kC; ++c) tmem_ld(x_at + 32 * (kC * part + c), x[c]);
+    };
+    auto landed = [&]() {
+      tmem_wait_ld(x[0]);
+#pragma unroll
+      for (int c = 1; c < kC; ++c) tmem_landed(x[c]);
+    };
+    auto mask = [&](int part) {
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        const int j0 = k * kTile + 32 * (NC * copy + kC * part + c) - row.P;
+        const uint32_t see = row.live ? seen_bits(row.mask, a.mask_words, row.n, row.i, j0) : 0u;
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          if (!((see >> e) & 1)) x[c][e] = 0xFF800000u;
+      }
+    };
+    float mx = -INFINITY, nx = -INFINITY;
+    // TS: the largest product of a weight and its scale: no more than the largest of each, which will do while the
+    // scales are within 2^8 of one another (FP16 weights reach down to 2^-21 with all their bits)
+    bool far = false;
+    float high = -INFINITY;
+    if constexpr (TS) {
+      float low = INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = S.range[tile][count & 1u][i];
+        low = fminf(low, y.x);
+        high = fmaxf(high, y.y);
+      }
+      far = high - low > 8.0f;
+    }
+#pragma unroll
+    for (int part = 0; part < kReads; ++part) {
+      read(part);
+      if constexpr (TS) {  // into log2 units
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          float4 f[8];  // (a token's scale is the same for all lanes; read while the scores are on their way)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float4*>(&kf[64 * part + 32 * c + 4 * e]);
+          if (c == 0) landed();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            put(c, 4 * e, __fmul2_rn(pair(c, 4 * e), make_float2(f[e].x, f[e].y)));
+            put(c, 4 * e + 2, __fmul2_rn(pair(c, 4 * e + 2), make_float2(f[e].z, f[e].w)));
+          }
+        }
+      } else {
+        landed();
+      }
+      if (drafted) mask(part);
+#pragma unroll
+      for (int c = 0; c < kC; ++c)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+      if constexpr (TS) {
+        if (far)
+#pragma unroll
+          for (int c = 0; c < kC; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(&lv[64 * part + 32 * c + e]);
+              const float2 y = __fadd2_rn(pair(c, e), make_float2(f.x, f.y));
+              const float2 z = __fadd2_rn(pair(c, e + 2), make_float2(f.z, f.w));
+              nx = max3(max3(nx, y.x, y.y), z.x, z.y);
+            }
+        if constexpr (kReads > 1) {
+#pragma unroll
+          for (int c = 0; c < kC; ++c) tmem_st(x_at + 32 * (kC * part + c), x[c]);
+        }
+      }
+    }
+    if constexpr (TS) {
+      if (!far) nx = mx + high;
+      if constexpr (kReads > 1) tmem_wait_st();
+    } else {
+      nx = mx *= sc;
+    }
+    float& top = TS ? row.to : row.m;  // what the sums are to
+    if (k == begin) {
+      row.m = mx;
+      row.to = nx;
+    } else {
+      if (TS && mx > row.m + kSlack) {
+        row.l *= exp2_ftz(row.m - mx);
+        row.m = mx;
+      }
+      if (__any_sync(0xFFFFFFFFu, nx > top + kSlack)) {
+        const float to = fmaxf(top, nx), alpha = exp2_ftz(top - (to == -INFINITY ? 0.0f : to));
+        top = to;
+        if constexpr (!TS) row.l *= alpha;
+        // the sums are at rest behind the product before
+        if (!summed(count - 1)) return false;
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t y[16];
+          tmem_ld16(o_at + 16 * c, y);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
+          tmem_st16(o_at + 16 * c, y);
+        }
+      }
+    }
+    // TS: weights are taken to m for their own sum, and times their values' scales and `rel` to `to`, so that FP16 holds
+    // the largest of them whatever the scales are (their product stays in FP32's range: what `rel` cannot hold goes to
+    // the weights)
+    [[maybe_unused]] const float on = row.m - row.to + F::kShift, over = TS && on > 127.0f ? on - 127.0f : 0.0f;
+    [[maybe_unused]] const float rel = row.to == -INFINITY ? 0.0f : exp2_ftz(on - over);
+    const float base = (TS ? over : F::kShift) - (row.m == -INFINITY ? 0.0f : row.m);
+    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+    for (int part = 0; part < kReads; ++part) {
+      if constexpr (kReads > 1) {
+        read(part);
+        landed();
+        if (!TS && drafted) mask(part);
+      }
+#pragma unroll
+      for (int c = 0; c < kC; ++c) {
+        uint32_t p[16];
+        [[maybe_unused]] float4 f[8];
+        if constexpr (TS) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float4*>(&vf[64 * part + 32 * c + 4 * e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          float2 y;
+          if constexpr (TS) y = __fadd2_rn(pair(c, e), make_float2(base, base));
+          else y = __ffma2_rn(pair(c, e), make_float2(sc, sc), make_float2(base, base));
+          y = make_float2(exp2_ftz(y.x), exp2_ftz(y.y));
+          sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], y);
+          if constexpr (TS) {
+            const float2 v = e & 2 ? make_float2(f[e / 4].z, f[e / 4].w) : make_float2(f[e / 4].x, f[e / 4].y);
+            y = __fmul2_rn(y, __fmul2_rn(v, make_float2(rel, rel)));
+          }
+          p[e / 2] = pack<F::kValBf>(y.x, y.y);
+        }
+        tmem_st16(p_at + 16 * (kC * part + c), p);
+      }
+    }
+    if constexpr (NC < 4) {
+      uint32_t none[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) none[e] = 0u;
+#pragma unroll
+      for (int c = NC; c < 4; ++c) tmem_st16(s_at + 16 * ((NC * copy + c) & 3), none);
+    }
+    sum[0] = __fadd2_rn(sum[0], sum[1]);
+    row.l += TS ? (sum[0].x + sum[0].y) * exp2_ftz(-over) : sum[0].x + sum[0].y;
+    tmem_wait_st();
+    return true;
   }
 
   __device__ __forceinline__ void run(Walk<F::kRows> w, long long s0, long long e0, long long W, int C) {
     uint32_t count = 0;  // tiles of this thread's row tile so far
     uint32_t units = 0;
+    [[maybe_unused]] Token ahead{-1, 0, 0};  // of the tile after the next one
+    [[maybe_unused]] float ks = 0.0f, vs = 0.0f;
+    [[maybe_unused]] bool fetched = false, looked = false;  // the next tile's scales, and the page of the one behind
     bool more = true;
     while (more) {
-      load_queries(w);
-      const int M = w.r.n * a.g, r = w.rb * F::kRows + threadIdx.x;
+      if constexpr (TILES == 2) load_queries(w);
+      Walk<F::kRows> next = w;  // (one row tile: looked up while there is work to do)
+      if constexpr (TILES == 1) more = next.next(a, s0, e0);
+      const int M = w.r.n * a.g, same = TILES == 1 ? copies(M) : 1;
+      const int copy = thread / (kTile / same), r = w.rb * F::kRows + tile * kTile + thread % (kTile / same);
       const bool active = w.rb * F::kRows + tile * kTile < M;  // the row tile has rows
       // (a row tile without work must not arrive for the next unit in the same phase)
-      if (!active && !mbar_wait(&S.q_full, units & 1u, &S.abort)) return;
+      if (TILES == 2 && !active && !mbar_wait(&S.q_full[0], units & 1u, &S.abort)) return;
       ++units;
-      const bool rows = w.rb * F::kRows + tile * kTile + warp * 32 < M;  // the warp has
-      float m = -INFINITY, l = 0.0f;
-      const int i = r / a.g;
-      const uint32_t* mask = a.mask != nullptr && r < M ? a.mask + (long long)(w.r.row0 + i) * a.mask_words : nullptr;
+      const bool rows = same > 1 || w.rb * F::kRows + tile * kTile + warp * 32 < M;  // the warp has
+      Row row{w.r.P, w.r.n, r / a.g, r < M, nullptr, -INFINITY, 0.0f, -INFINITY};
+      if (a.mask != nullptr && r < M) row.mask = a.mask + (long long)(w.r.row0 + row.i) * a.mask_words;
       float sc = a.scale * kLog2e;
       if constexpr (DT == kE4m3 && !TS)
         if (a.c.k_scale != nullptr) sc = scaled(sc, a.c.k_scale[w.h]);
-      long long at_next = -1;
-      float ks_next = 0.0f, vs_next = 0.0f;
-      [[maybe_unused]] auto fetch = [&](long long at) {
-        ks_next = at >= 0 ? a.c.k_scale[at] : 0.0f;
-        vs_next = at >= 0 ? a.c.v_scale[at] : 0.0f;
-      };
       if constexpr (TS)
-        if (active) {
-          fetch(scale_at(w, w.begin * kTile + thread));
-          at_next = scale_at(w, (w.begin + 1) * kTile + thread);
+        if (active && !fetched) {
+          fetch(look_up(w, w.begin), ks, vs);
+          looked = false;
         }
       for (int k = w.begin; active && k < w.end; ++k, ++count) {
         const int t0 = k * kTile;
         const uint32_t buf = TILES == 1 ? count & 1u : uint32_t(tile), phase = TILES == 1 ? (count >> 1) & 1u : count & 1u;
-        const uint32_t s_at = lanes + 256u + 128u * buf;
-        const float* kf = S.scales[tile][k & 1][0];
-        const float* vf = S.scales[tile][k & 1][1];
+        const uint32_t s_at = lanes + kColS + 128u * buf;
         if constexpr (TS) {
-          float vs = vs_next;
-          if (t0 + thread >= w.r.P && !isfinite(vs)) {
-            atomicOr(&S.flags[w.number & 7], kLoose);
-            vs = 0.0f;
+          float v = vs;
+          if (t0 + thread >= w.r.P && !isfinite(v)) {
+            atomicOr(&S.flags[w.number & 15], kLoose);
+            v = 0.0f;
           }
-          S.scales[tile][k & 1][0][thread] = scaled(sc, ks_next);
-          S.scales[tile][k & 1][1][thread] = vs;
+          S.scales[tile][count & 1u][0][thread] = scaled(sc, ks);
+          const float lv = log2f(v);
+          S.scales[tile][count & 1u][1][thread] = lv;
+          S.scales[tile][count & 1u][2][thread] = v;
+          // a scale of 0 (no token) does not count; one that is not finite makes the range so
+          float2 range = make_float2(v == 0.0f ? INFINITY : lv, lv != lv ? INFINITY : lv);
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            range.x = fminf(range.x, __shfl_xor_sync(0xFFFFFFFFu, range.x, o));
+            range.y = fmaxf(range.y, __shfl_xor_sync(0xFFFFFFFFu, range.y, o));
+          }
+          if (lane == 0) S.range[tile][count & 1u][warp] = range;
           sync();
-          fetch(at_next);
-          at_next = k + 2 < w.end ? scale_at(w, t0 + 2 * kTile + thread) : -1;
+          // the scales of the next tile, the page of the one behind it (of the next unit, where that is known)
+          const bool here = k + 1 < w.end, any = here || (TILES == 1 && more);
+          fetched = any;
+          if (any) {
+            if (!looked) ahead = here ? look_up(w, k + 1) : look_up(next, next.begin);
+            fetch(ahead, ks, vs);
+          }
+          const int on = k + 2 - w.end;  // tiles into the next unit
+          looked = on < 0 || (TILES == 1 && more && next.begin + on < next.end);
+          if (looked) ahead = on < 0 ? look_up(w, k + 2) : look_up(next, next.begin + on);
         }
         if (!mbar_wait(&S.s_full[buf], phase, &S.abort)) return;
         tc_fence_after();
         if (rows) {
-          // Scores 64 columns at a time, twice: for their maximum, and for the weights (held in between they would take
-          // 128 registers). TS: in log2 units, else the products' own.
-          const bool drafted = t0 + kTile > w.r.P;
-          uint32_t x[2][32];
-          auto pair = [&](int c, int e) { return make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])); };
-          auto load = [&](int half) {
-            tmem_ld(s_at + 64 * half, x[0]);
-            tmem_ld(s_at + 64 * half + 32, x[1]);
-            if constexpr (TS) {
-              // (a row's scales are the same for all lanes: read while the scores are on their way)
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                float4 f[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float4*>(&kf[64 * half + 32 * c + 4 * e]);
-                if (c == 0) {
-                  tmem_wait_ld(x[0]);
-                  tmem_landed(x[1]);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const float2 y = __fmul2_rn(pair(c, 4 * e), make_float2(f[e].x, f[e].y));
-                  const float2 z = __fmul2_rn(pair(c, 4 * e + 2), make_float2(f[e].z, f[e].w));
-                  x[c][4 * e] = __float_as_uint(y.x);
-                  x[c][4 * e + 1] = __float_as_uint(y.y);
-                  x[c][4 * e + 2] = __float_as_uint(z.x);
-                  x[c][4 * e + 3] = __float_as_uint(z.y);
-                }
-              }
-            } else {
-              tmem_wait_ld(x[0]);
-              tmem_landed(x[1]);
-            }
-            if (drafted) {
-#pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint32_t see = r < M ? seen_bits(mask, a.mask_words, w.r.n, i, t0 + 64 * half + 32 * c - w.r.P) : 0u;
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                  if (!((see >> e) & 1)) x[c][e] = 0xFF800000u;
-              }
-            }
-          };
-          float mx = -INFINITY;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            load(half);
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-          }
-          if constexpr (!TS) mx *= sc;
-          if (k == w.begin) {
-            m = mx;
-          } else if (__any_sync(0xFFFFFFFFu, mx > m + kSlack)) {
-            const float top = fmaxf(m, mx), alpha = exp2_ftz(m - (top == -INFINITY ? 0.0f : top));
-            m = top;
-            l *= alpha;
-            // the sums are at rest behind the product before
-            if (!mbar_wait(&S.pv_done[TILES == 1 ? 0 : tile], (count - 1) & 1u, &S.abort)) return;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t y[16];
-              tmem_ld16(o_at + 16 * c, y);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * alpha);
-              tmem_st16(o_at + 16 * c, y);
-            }
-            tmem_wait_st();
-          }
-          const float base = F::kShift - (m == -INFINITY ? 0.0f : m);
-          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            load(half);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t p[16];
-              [[maybe_unused]] float4 f[8];
-              if constexpr (TS) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float4*>(&vf[64 * half + 32 * c + 4 * e]);
-              }
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                float2 y;
-                if constexpr (TS) y = __fadd2_rn(pair(c, e), make_float2(base, base));
-                else y = __ffma2_rn(pair(c, e), make_float2(sc, sc), make_float2(base, base));
-                y = make_float2(exp2_ftz(y.x), exp2_ftz(y.y));
-                sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], y);
-                if constexpr (TS) y = __fmul2_rn(y, e & 2 ? make_float2(f[e / 4].z, f[e / 4].w) : make_float2(f[e / 4].x, f[e / 4].y));
-                p[e / 2] = pack<F::kValBf>(y.x, y.y);
-              }
-              tmem_st16(s_at + 32 * half + 16 * c, p);  // (in the place of scores that are read)
-            }
-          }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          tmem_wait_st();
+          bool ok;
+          if (same == 4) ok = weigh<1>(row, k, w.begin, count, s_at, copy, sc);
+          else if (same == 2) ok = weigh<2>(row, k, w.begin, count, s_at, copy, sc);
+          else ok = weigh<4>(row, k, w.begin, count, s_at, 0, sc);
+          if (!ok) return;
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.p_ready[buf]);
       }
       if (active) {
-        if (!mbar_wait(&S.pv_done[TILES == 1 ? 0 : tile], (count - 1) & 1u, &S.abort)) return;
-        tc_fence_after();
+        if (!summed(count - 1)) return;
       }
-      if (threadIdx.x == 0) S.flags[(w.number + 4) & 7] = 0;  // (the producers are at most three units ahead)
-      if (active && rows) finish(w, s0, W, C, r, M, i, m, l);
+      if (threadIdx.x == 0) S.flags[(w.number + 8) & 15] = 0;  // (the producers are at most four units ahead)
+      if (active) {
+        if (same > 1) finish_copies(w, row, r, same, copy);
+        else if (rows) finish(w, row, r, M);
+      }
       if (threadIdx.x == 0 && w.begin == 0 && w.end < w.tiles) {
         const long long last = w.pos + w.tiles - 1;
         reinterpret_cast<Rec*>(a.ws)[blockIdx.x] = Rec{w.b, w.h, w.rb, cta_of(last, W, C) - int(blockIdx.x) + 1};
       }
       tc_fence_before();
-      more = w.next(a, s0, e0);
+      if constexpr (TILES == 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.o_free);
+        w = next;
+      } else {
+        more = w.next(a, s0, e0);
+      }
     }
   }
 
+  // What a whole unit's sums are multiplied by, in two factors (their product may be in FP32's range where one is not).
+  __device__ __forceinline__ float2 factors(const Walk<F::kRows>& w, const Row& row) const {
+    float2 f = make_float2(row.l == 0.0f ? 0.0f : 1.0f / row.l, 1.0f);
+    if (DT == kE4m3 && !TS && a.c.v_scale != nullptr) f.x *= a.c.v_scale[w.h];
+    if constexpr (TS) between(row.to - F::kShift - row.m, f.x, f.y);
+    return f;
+  }
+  __device__ __forceinline__ bool is_whole(const Walk<F::kRows>& w) const { return w.begin == 0 && w.end == w.tiles; }
+  __device__ __forceinline__ int flags_of(const Walk<F::kRows>& w) const {
+    return *reinterpret_cast<volatile int*>(&S.flags[w.number & 15]);
+  }
+  // Where a whole unit's row goes, in query heads.
+  __device__ __forceinline__ long long head_of(const Walk<F::kRows>& w, const Row& row, int r) const {
+    return (long long)(w.r.row0 + row.i) * a.Hq + w.h * a.g + (r - row.i * a.g);
+  }
+  __device__ __forceinline__ float* slot_of(const Walk<F::kRows>& w) const {
+    return reinterpret_cast<float*>(a.ws + slots_offset(gridDim.x)) +
+           size_t(2 * blockIdx.x + (w.begin > 0 ? 0 : 1)) * slot_floats(F::kRows);
+  }
+  __device__ __forceinline__ void put_lse(long long head, const Row& row) const {
+    if (a.lse != nullptr) a.lse[head] = (row.m - (TS ? 0.0f : F::kShift) + log2f(row.l)) * kLn2;
+  }
+  __device__ __forceinline__ void put_slot(float* slot, int at, const Row& row, int flags) const {
+    slot[size_t(F::kRows) * kD + at] = TS ? row.m : row.m - F::kShift;
+    slot[size_t(F::kRows) * (kD + 1) + at] = row.l;
+    slot[size_t(F::kRows) * (kD + 2) + at] = (TS ? row.to : row.m) - F::kShift;
+    if (at == 0) slot[size_t(F::kRows) * (kD + 3)] = __int_as_float(flags);
+  }
+  // N channels of a whole unit's row from c on, scaled, with what is not finite, rounded, to out.
+  template <int N>
+  __device__ __forceinline__ void put_out(const Walk<F::kRows>& w, const Row& row, long long head, int c, float (&x)[N],
+                                          float2 f, int flags) const {
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = row.l == 0.0f ? 0.0f : (TS ? x[e] * f.x * f.y : x[e] * f.x);
+    if ((flags & kLoose) && row.l != 0.0f) {
+#pragma unroll 1
+      for (int e = 0; e < N; ++e) {
+        const float y = loose<DT>(a, w.r, w.b, w.h, row.i, c + e);
+#pragma unroll
+        for (int d = 0; d < N; ++d)
+          if (d == e) x[d] += y;
+      }
+    }
+    char* to = a.out + head * (kD * 2) + c * 2;
+#pragma unroll
+    for (int e = 0; e < N; e += 8)
+      *reinterpret_cast<uint4*>(to + 2 * e) =
+          make_uint4(pack<QT == kBf16>(x[e], x[e + 1]), pack<QT == kBf16>(x[e + 2], x[e + 3]),
+                     pack<QT == kBf16>(x[e + 4], x[e + 5]), pack<QT == kBf16>(x[e + 6], x[e + 7]));
+  }
+
   // The unit's rows, or this part of it, to out and lse or to a slot.
-  __device__ __forceinline__ void finish(const Walk<F::kRows>& w, long long s0, long long W, int C, int r, int M, int i, float m,
-                                         float l) {
-    const bool whole = w.begin == 0 && w.end == w.tiles;
-    const int flags = *reinterpret_cast<volatile int*>(&S.flags[w.number & 7]);
-    if (flags & kBadPage) l = NAN;
-    if (whole) {
-      float f = l == 0.0f ? 0.0f : 1.0f / l;
-      if (DT == kE4m3 && !TS && a.c.v_scale != nullptr) f *= a.c.v_scale[w.h];
-      const long long head = (long long)(w.r.row0 + i) * a.Hq + w.h * a.g + (r - i * a.g);
-      char* to = a.out + head * (kD * 2);
-      if (r < M && a.lse != nullptr) a.lse[head] = (m - F::kShift + log2f(l)) * kLn2;
+  __device__ __forceinline__ void finish(const Walk<F::kRows>& w, Row& row, int r, int M) {
+    const int flags = flags_of(w);
+    if (flags & kBadPage) row.l = NAN;
+    if (is_whole(w)) {
+      const float2 f = factors(w, row);
+      const long long head = head_of(w, row, r);
+      if (r < M) put_lse(head, row);
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32];
         tmem_ld(o_at + 32 * c, x);
         tmem_wait_ld(x);
         if (r >= M) continue;
+        float y[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(x[e]) * f);
-        if ((flags & kLoose) && l != 0.0f)
-          for (int e = 0; e < 32; ++e) {
-            const float y = loose<DT>(a, w.r, w.b, w.h, i, 32 * c + e);
-#pragma unroll
-            for (int d = 0; d < 32; ++d)
-              if (d == e) x[d] = __float_as_uint(__uint_as_float(x[d]) + y);
-          }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 y;
-#pragma unroll
-          for (int d = 0; d < 4; ++d)
-            (&y.x)[d] = pack<QT == kBf16>(__uint_as_float(x[8 * e + 2 * d]), __uint_as_float(x[8 * e + 2 * d + 1]));
-          *reinterpret_cast<uint4*>(to + 64 * c + 16 * e) = y;
-        }
+        for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(x[e]);
+        put_out<32>(w, row, head, 32 * c, y, f, flags);
       }
     } else {
-      float* slot = reinterpret_cast<float*>(a.ws + slots_offset(gridDim.x)) +
-                    size_t(2 * blockIdx.x + (w.begin > 0 ? 0 : 1)) * slot_floats(F::kRows);
-      const int row = threadIdx.x;
+      float* slot = slot_of(w);
+      const int at = threadIdx.x;
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32];
@@ -687,12 +882,64 @@ struct Softmax {
         tmem_wait_ld(x);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<uint4*>(slot + (size_t(8 * c + e) * F::kRows + row) * 4) =
+          *reinterpret_cast<uint4*>(slot + (size_t(8 * c + e) * F::kRows + at) * 4) =
               make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
       }
-      slot[size_t(F::kRows) * kD + row] = m - F::kShift;
-      slot[size_t(F::kRows) * (kD + 1) + row] = l;
-      if (row == 0) slot[size_t(F::kRows) * (kD + 2)] = __int_as_float(flags);
+      put_slot(slot, at, row, flags);
+    }
+  }
+
+  // The same for rows in several copies, joined first: a thread's share is 32 / same channels of each 32 of its row.
+  __device__ __forceinline__ void finish_copies(const Walk<F::kRows>& w, Row& row, int r, int same, int copy) {
+    const int flags = flags_of(w), each = kTile / same, at = thread % each, M = w.r.n * a.g;
+    S.part_ml[0][thread] = row.m;
+    S.part_ml[1][thread] = row.l;
+    S.part_ml[2][thread] = TS ? row.to : row.m;
+    sync();
+    const float mine = TS ? row.to : row.m;
+    float m = -INFINITY, to = -INFINITY, l = 0.0f;
+    for (int i = 0; i < same; ++i) {
+      m = fmaxf(m, S.part_ml[0][i * each + at]);
+      to = fmaxf(to, S.part_ml[2][i * each + at]);
+    }
+    for (int i = 0; i < same; ++i) l += S.part_ml[1][i * each + at] * exp2f(S.part_ml[0][i * each + at] - (m == -INFINITY ? 0.0f : m));
+    row.m = m;
+    row.to = to;
+    row.l = flags & kBadPage ? NAN : l;
+    const float own = exp2f(mine - (to == -INFINITY ? 0.0f : to));
+    const bool whole = is_whole(w), live = r < M;
+    const float2 f = factors(w, row);
+    const long long head = head_of(w, row, r);
+    float* slot = slot_of(w);
+    if (copy == 0 && live) {
+      if (whole) put_lse(head, row);
+      else put_slot(slot, at, row, flags);
+    }
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t x[32];
+      tmem_ld(o_at + 32 * c, x);
+      tmem_wait_ld(x);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) S.part[thread][e] = __uint_as_float(x[e]) * own;
+      sync();
+      for (int e = copy * (32 / same); live && e < (copy + 1) * (32 / same); e += 8) {
+        float y[8];
+#pragma unroll
+        for (int d = 0; d < 8; ++d) y[d] = S.part[at][e + d];
+        for (int i = 1; i < same; ++i)
+#pragma unroll
+          for (int d = 0; d < 8; ++d) y[d] += S.part[i * each + at][e + d];
+        if (whole) {
+          put_out<8>(w, row, head, 32 * c + e, y, f, flags);
+        } else {
+#pragma unroll
+          for (int d = 0; d < 8; d += 4)
+            *reinterpret_cast<float4*>(slot + (size_t((32 * c + e + d) / 4) * F::kRows + at) * 4) =
+                make_float4(y[d], y[d + 1], y[d + 2], y[d + 3]);
+        }
+      }
+      sync();
     }
   }
 };
@@ -703,15 +950,19 @@ template <int DT, int QT, int TILES, bool TS>
 __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TILES, TS>>& S,
                                         Walk<Form<DT, QT, TILES, TS>::kRows> w, long long s0, long long e0) {
   using F = Form<DT, QT, TILES, TS>;
+  constexpr int kN = F::kTokens;  // of a tile, this warp's
   const int thread = int(threadIdx.x) - F::kSoftmaxWarps * 32, warp = thread >> 5, lane = thread & 31;
   const uint32_t slots = smem_addr(S.slot), raws = smem_addr(S.raw) + thread * 16;
-  struct Past {  // a copy in flight: from which of the tile's tokens on values may be replaced, and the unit
-    int from, number;
+  constexpr int kHalves = kD * elem_bytes<DT>() / 128;  // 128-byte pieces of a row
+  constexpr int kCopies = kN / 4;                       // of a piece of four tokens
+  struct Past {  // a copy not looked at yet: from which of the tile's tokens on values may be replaced, and the unit
+    int word;
+    __device__ __forceinline__ int from() const { return word & 0xFF; }
+    __device__ __forceinline__ int number() const { return word >> 8; }
   } past[F::kLag + 1];
 #pragma unroll
-  for (int i = 0; i <= F::kLag; ++i) past[i] = Past{kTile, 0};
-  constexpr int kFirst = F::kLag % 2;  // the half of a tile in which a copy of keys is looked at
-  constexpr int kHalves = kD * elem_bytes<DT>() / 128;  // 128-byte pieces of a row
+  for (int i = 0; i <= F::kLag; ++i) past[i] = Past{kTile};
+  int pending = 0;  // 8-bit rows: copies not converted yet
 
   // Copy number x (K of a tile, then V) has landed: makes it an operand. (Of 16-bit rows only the drafted values come
   // here; the others arrive by themselves.)
@@ -722,14 +973,14 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
     if constexpr (F::kNarrow) {
       if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return false;
       const uint32_t from = raws + (x % F::kStages) * kRawBytes;
-      uint4 y[8];  // 16 channels of eight tokens
+      uint4 y[kCopies];  // 16 channels of a token each
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = lds16(from + i * (kProducers * 16));
-      if (value && p.from < kTile) {  // drafted tokens: NaN is replaced by 0
+      for (int i = 0; i < kCopies; ++i) y[i] = lds16(from + i * (F::kProducers * 16));
+      if (value && p.from() < kTile) {  // drafted tokens: NaN is replaced by 0
         uint32_t any = 0u;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (32 * warp + 4 * i + (lane >> 3) < p.from) continue;
+        for (int i = 0; i < kCopies; ++i) {
+          if (kN * warp + 4 * i + (lane >> 3) < p.from()) continue;
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
             const uint32_t nan = (((&y[i].x)[d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes of 0x7F or 0xFF
@@ -737,11 +988,11 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
             any |= nan;
           }
         }
-        if (any != 0u) atomicOr(&S.flags[p.number & 7], kLoose);
+        if (any != 0u) atomicOr(&S.flags[p.number() & 15], kLoose);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int token = 32 * warp + 4 * i + (lane >> 3), chunk = 2 * (lane & 7);
+      for (int i = 0; i < kCopies; ++i) {
+        const int token = kN * warp + 4 * i + (lane >> 3), chunk = 2 * (lane & 7);
         uint2 z[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d) z[d] = widen<value ? F::kValBf : F::kKeyBf>((&y[i].x)[d]);
@@ -751,9 +1002,9 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
     } else if constexpr (value) {  // drafted ones
       constexpr uint32_t kInf = DT == kBf16 ? 0x7F80u : 0x7C00u;
 #pragma unroll 1
-      for (int e = 0; e < 16; ++e) {
-        const int token = 32 * warp + 4 * (e >> 1) + (lane >> 3), chunk = 8 * (e & 1) + (lane & 7);
-        if (token < p.from) continue;
+      for (int e = 0; e < 2 * kCopies; ++e) {
+        const int token = kN * warp + 4 * (e >> 1) + (lane >> 3), chunk = 8 * (e & 1) + (lane & 7);
+        if (token < p.from()) continue;
         const uint32_t at = to + chunk_at(token, chunk);
         uint4 y = lds16(at);
         bool any = false;
@@ -771,7 +1022,7 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
         }
         if (any) {
           sts16(at, y);
-          atomicOr(&S.flags[p.number & 7], kLoose);
+          atomicOr(&S.flags[p.number() & 15], kLoose);
         }
       }
     }
@@ -779,27 +1030,60 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
     mbar_arrive(&S.full[slot]);
     return true;
   };
+  uint32_t x = 0;  // copies so far
+  // All but the last LEFT copies so far; an even number of them, as LEFT.
+  auto land_all = [&](auto left) -> bool {
+    constexpr int kLeft = decltype(left)::value;
+    wait_groups<kLeft>();
+#pragma unroll
+    for (int i = F::kLag - 1; i >= kLeft; --i)
+      if (F::kNarrow ? i < pending : past[i].from() < kTile) {
+        if (i % 2 ? !land(x - 1 - i, past[i], std::false_type{}) : !land(x - 1 - i, past[i], std::true_type{})) return false;
+        past[i] = Past{kTile};
+      }
+    pending = min(pending, kLeft);
+    return true;
+  };
 
-  // The pool's row of this lane's token (32 warp + lane) of a tile: page of the pool (looked up a tile ahead)
+  // The pool's row of this lane's token of a tile: page of the pool (looked up a tile ahead)
   auto page_of = [&](const Walk<F::kRows>& u, int k) {
-    const int t = k * kTile + 32 * warp + lane;
+    const int t = k * kTile + kN * warp + (lane & (kN - 1));
     return t < u.tokens ? a.table[(long long)u.b * a.max_pages + a.c.ps.div(t)] : -2;  // -2: no token
   };
-  uint32_t x = 0;
   int page = page_of(w, w.begin);
-  for (bool more = true; more;) {
+  uint32_t units = 0;
+  int last = 0;  // tiles of the unit before
+  for (bool more = true; more; ++units) {
+    // one row tile: the unit's queries to tensor memory, a row by a thread of the first four warps; on their way while
+    // the first tile's copies are issued
+    [[maybe_unused]] uint32_t q[2][32];
+    if constexpr (TILES == 1) {
+      const int M = w.r.n * a.g, r = w.rb * F::kRows + thread % (kTile / copies(M));
+      const bool live = thread < kTile && r < M;
+      const int i = r / a.g;
+      const char* from = a.q + (live ? (w.r.row0 + i) * a.q_stride + (long long)(w.h * a.g + (r - i * a.g)) * (kD * 2) : 0);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        uint4 y = make_uint4(0u, 0u, 0u, 0u);
+        if (live) y = *reinterpret_cast<const uint4*>(from + 16 * e);
+        q[e >> 3][4 * (e & 7)] = y.x;
+        q[e >> 3][4 * (e & 7) + 1] = y.y;
+        q[e >> 3][4 * (e & 7) + 2] = y.z;
+        q[e >> 3][4 * (e & 7) + 3] = y.w;
+      }
+    }
     for (int k = w.begin; k < w.end; ++k) {
-      const int t = k * kTile + 32 * warp + lane;
+      const int t = k * kTile + kN * warp + (lane & (kN - 1));
       long long off = -1;
       if (page >= 0 && page < a.c.n_pages) {
         const int place = t - a.c.ps.div(t) * int(a.c.ps.d);
         off = (long long)page * a.c.page_stride + (long long)place * a.c.token_stride + (long long)w.h * a.c.head_stride;
       } else if (page != -2 || t < w.tokens) {
         flag(a.c, KVQ_PAGED_ERR_PAGE);
-        atomicOr(&S.flags[w.number & 7], kBadPage);
+        atomicOr(&S.flags[w.number & 15], kBadPage);
       }
       if (k + 1 < w.end) page = page_of(w, k + 1);
-      const Past now{max(0, min(kTile, w.r.P - k * kTile)), w.number};
+      const int drafts = max(0, min(kTile, w.r.P - k * kTile));  // the first drafted token of the tile
 #pragma unroll
       for (int half = 0; half < 2; ++half, ++x) {
         const char* pool = half == 0 ? a.c.k : a.c.v;
@@ -811,41 +1095,55 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
           to = raws + (x % F::kStages) * kRawBytes;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kCopies; ++e) {
           const long long y = __shfl_sync(0xFFFFFFFFu, off, 4 * e + (lane >> 3));
 #pragma unroll
           for (int f = 0; f < kHalves; ++f) {
             const int chunk = 8 * f + (lane & 7);
-            const uint32_t at = F::kNarrow ? to + e * (kProducers * 16)
-                                           : to + chunk_at(32 * warp + 4 * e + (lane >> 3), chunk);
+            const uint32_t at = F::kNarrow ? to + e * (F::kProducers * 16)
+                                           : to + chunk_at(kN * warp + 4 * e + (lane >> 3), chunk);
             copy16(at, pool + (y < 0 ? 0 : y) + chunk * 16, y >= 0);
           }
         }
         commit();
 #pragma unroll
         for (int i = F::kLag; i > 0; --i) past[i] = past[i - 1];
-        past[0] = now;
+        past[0] = Past{drafts | (w.number & 15) << 8};
         if constexpr (!F::kNarrow)
-          if (half == 0 || now.from == kTile) {
+          if (half == 0 || drafts == kTile) {
             arrive_landed(&S.full[x % F::kSlots]);
-            past[0].from = kTile;
+            past[0] = Past{kTile};
           }
-        if (F::kNarrow ? x >= uint32_t(F::kLag) : past[F::kLag].from < kTile) {
+        if (F::kNarrow ? ++pending > F::kLag : past[F::kLag].from() < kTile) {
           wait_groups<F::kLag>();
-          if (half == kFirst ? !land(x - F::kLag, past[F::kLag], std::false_type{})
-                             : !land(x - F::kLag, past[F::kLag], std::true_type{}))
+          --pending;
+          if (half == F::kLag % 2 ? !land(x - F::kLag, past[F::kLag], std::false_type{})
+                                  : !land(x - F::kLag, past[F::kLag], std::true_type{}))
             return;
         }
       }
+      if constexpr (TILES == 1)
+        if (k == w.begin) {
+          // the buffer's last queries are those of the unit before the last one: multiplied once all its keys are there
+          if (F::kNarrow && pending > 4 && last == 1 && !land_all(std::integral_constant<int, 4>{})) return;
+          if (!mbar_wait(&S.q_free[units & 1u], ((units >> 1) + 1) & 1u, &S.abort)) return;
+          if (thread < kTile) {
+            tc_fence_after();
+            const uint32_t at = S.tmem + (uint32_t(warp) << 21) + kColQ + 64u * (units & 1u);
+            tmem_st(at, q[0]);
+            tmem_st(at + 32, q[1]);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.q_full[units & 1u]);
+          }
+        }
     }
+    last = w.end - w.begin;
     more = w.next(a, s0, e0);
     if (more) page = page_of(w, w.begin);
   }
-  wait_groups<0>();
-#pragma unroll
-  for (int i = F::kLag - 1; i >= 0; --i)  // (the last one was of values)
-    if (F::kNarrow ? x >= uint32_t(i + 1) : past[i].from < kTile)
-      if (i % 2 ? !land(x - 1 - i, past[i], std::false_type{}) : !land(x - 1 - i, past[i], std::true_type{})) return;
+  land_all(std::integral_constant<int, 0>{});
 }
 
 // ---------------------------------------------------------------- products
@@ -859,11 +1157,16 @@ __device__ __forceinline__ bool multiply(const TreeArgs& a, Smem<Form<DT, QT, TI
   uint32_t count[2] = {0, 0};  // products of each row tile so far
   uint32_t units = 0;
   auto keys = [&](int tile, uint32_t x, uint32_t buf) {
-    const uint64_t qa = smem_desc(q + tile * kSlotBytes, 16), kb = smem_desc(slots + (x % F::kSlots) * kSlotBytes, 16);
+    const uint64_t kb = smem_desc(slots + (x % F::kSlots) * kSlotBytes, 16);
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {  // 16 channels: 32 bytes on, four times in each half
       const uint32_t on = 2u * (k & 3u) + (kSlotBytes / 32) * (k >> 2);
-      mma_ss(tmem + 256u + 128u * buf, qa + on, kb + on, instr_desc(F::kKeyBf, false), k > 0);
+      if constexpr (TILES == 1)
+        mma_ts(tmem + kColS + 128u * buf, tmem + kColQ + 64u * (units & 1u) + 8u * k, kb + on, instr_desc(F::kKeyBf, false),
+               k > 0);
+      else
+        mma_ss(tmem + kColS + 128u * buf, smem_desc(q + tile * kSlotBytes, 16) + on, kb + on,
+               instr_desc(F::kKeyBf, false), k > 0);
     }
     mma_commit(&S.s_full[buf]);
   };
@@ -871,9 +1174,14 @@ __device__ __forceinline__ bool multiply(const TreeArgs& a, Smem<Form<DT, QT, TI
     const uint64_t vb = smem_desc(slots + (x % F::kSlots) * kSlotBytes, kSlotBytes / 2);
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k)  // 16 tokens: 2048 bytes on
-      mma_ts(tmem + 128u * tile, tmem + 256u + 128u * buf + 8u * k, vb + 128u * k, instr_desc(F::kValBf, true),
+      mma_ts(tmem + 128u * tile, tmem + kColS + 128u * buf + 8u * k, vb + 128u * k, instr_desc(F::kValBf, true),
              !first || k > 0);
-    mma_commit(&S.pv_done[tile]);
+    mma_commit(&S.pv_done[TILES == 1 ? buf : tile]);
+  };
+  auto wait = [&](unsigned long long* bar, uint32_t phase) {
+    if (!mbar_wait(bar, phase & 1u, &S.abort)) return false;
+    tc_fence_after();
+    return true;
   };
   auto filled = [&](uint32_t x) {
     if (!mbar_wait(&S.full[x % F::kSlots], (x / F::kSlots) & 1u, &S.abort)) return false;
@@ -881,32 +1189,29 @@ __device__ __forceinline__ bool multiply(const TreeArgs& a, Smem<Form<DT, QT, TI
     tc_fence_after();
     return true;
   };
-  auto weights = [&](uint32_t buf, uint32_t phase) {
-    if (!mbar_wait(&S.p_ready[buf], phase & 1u, &S.abort)) return false;
-    tc_fence_after();
-    return true;
-  };
-  for (bool more = true; more; more = w.next(a, s0, e0)) {
-    if (!mbar_wait(&S.q_full, units++ & 1u, &S.abort)) return false;
-    tc_fence_after();
+  for (bool more = true; more; more = w.next(a, s0, e0), ++units) {
     const int n = w.end - w.begin;
     if constexpr (TILES == 1) {
+      if (!wait(&S.q_full[units & 1u], units >> 1)) return false;
       // scores of tile k + 1 are under way while the softmax warps work on tile k's
       for (int k = 0; k <= n; ++k) {
         if (k < n) {
           if (!filled(x + 2 * k)) return false;
           keys(0, x + 2 * k, (count[0] + k) & 1u);
           mma_commit(&S.empty[(x + 2 * k) % F::kSlots]);
+          if (k + 1 == n) mma_commit(&S.q_free[units & 1u]);
         }
         if (k > 0) {
           const uint32_t c = count[0] + k - 1, y = x + 2 * (k - 1) + 1;
-          if (!filled(y) || !weights(c & 1u, c >> 1)) return false;
+          if (!filled(y) || !wait(&S.p_ready[c & 1u], c >> 1)) return false;
+          if (k == 1 && units > 0 && !wait(&S.o_free, units - 1)) return false;  // the unit's sums before are read
           values(0, y, c & 1u, k == 1);
           mma_commit(&S.empty[y % F::kSlots]);
         }
       }
       count[0] += n;
     } else {
+      if (!wait(&S.q_full[0], units)) return false;
       const bool both = w.rb * F::kRows + kTile < w.r.n * a.g;  // the second row tile has rows
       for (int k = 0; k <= n; ++k)
         for (int tile = 0; tile < 2; ++tile) {  // a row tile's products while the other's softmax runs
@@ -914,7 +1219,7 @@ __device__ __forceinline__ bool multiply(const TreeArgs& a, Smem<Form<DT, QT, TI
           if (k > 0) {
             const uint32_t y = x + 2 * (k - 1) + 1;
             if (on) {
-              if (!filled(y) || !weights(tile, count[tile])) return false;
+              if (!filled(y) || !wait(&S.p_ready[tile], count[tile])) return false;
               values(tile, y, tile, k == 1);
               ++count[tile];
             }
@@ -948,17 +1253,19 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
   if (threadIdx.x == 0) {
     reinterpret_cast<Rec*>(a.ws)[blockIdx.x] = Rec{0, 0, 0, 0};
     for (int i = 0; i < F::kSlots; ++i) {
-      mbar_init(&S.full[i], kProducers);
+      mbar_init(&S.full[i], F::kProducers);
       mbar_init(&S.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.s_full[i], 1);
       mbar_init(&S.p_ready[i], 4);
       mbar_init(&S.pv_done[i], 1);
+      mbar_init(&S.q_full[i], TILES == 1 ? 4 : F::kSoftmaxWarps);
+      mbar_init(&S.q_free[i], 1);
     }
-    mbar_init(&S.q_full, F::kSoftmaxWarps);
+    mbar_init(&S.o_free, 4);
     mbar_init(&S.drain, 1);
-    for (int i = 0; i < 8; ++i) S.flags[i] = 0;
+    for (int i = 0; i < 16; ++i) S.flags[i] = 0;
     S.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -1033,10 +1340,23 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
 // range, its rows 32 y .. 32 y + 31, a lane a row, a warp 16 channels of it (and every other part).
 constexpr int kJoinWarps = 16;
 
+// `top` becomes the larger of top and part; what is to them is to it times f and g.
+__device__ __forceinline__ void share(float& top, float part, float& f, float& g) {
+  const float to = fmaxf(top, part), base = to == -INFINITY ? 0.0f : to;
+  f = exp2f(top - base);
+  g = exp2f(part - base);
+  top = to;
+}
+__device__ __forceinline__ void join(float& m, float& l, float pm, float pl) {
+  float f, g;
+  share(m, pm, f, g);
+  l = l * f + pl * g;
+}
+
 template <int DT, int QT, int TILES>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int R = kTile * TILES;
-  __shared__ float s_ml[2][32];
+  __shared__ float s_ml[3][32];
   __shared__ float4 s_x[8][4][32];
   wait_prior_grid();
   allow_dependents();
@@ -1053,21 +1373,21 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   const int M = r.n * a.g, row = 32 * blockIdx.y + lane, at = rec.rb * R + row;
   if (rec.rb * R + 32 * int(blockIdx.y) >= M) return;
   const float* slots = reinterpret_cast<const float*>(a.ws + slots_offset(n));
-  float m = -INFINITY, l = 0.0f;
+  float m = -INFINITY, l = 0.0f, to = -INFINITY;  // (to: what the sums are to)
   float4 x[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   int flags = 0;
   for (int i = odd; i < rec.parts; i += 2) {
     const float* p = slots + size_t(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * slot_floats(R);
-    const float pm = p[size_t(R) * kD + row], pl = p[size_t(R) * (kD + 1) + row];
-    flags |= __float_as_int(p[size_t(R) * (kD + 2)]);
+    const float pm = p[size_t(R) * kD + row], pl = p[size_t(R) * (kD + 1) + row], pn = p[size_t(R) * (kD + 2) + row];
+    flags |= __float_as_int(p[size_t(R) * (kD + 3)]);
     float4 y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const float4*>(p + (size_t(4 * group + e) * R + row) * 4);
-    const float top = fmaxf(m, pm), base = top == -INFINITY ? 0.0f : top, f = exp2f(m - base), g = exp2f(pm - base);
-    m = top;
-    l = l * f + pl * g;
+    join(m, l, pm, pl);
+    float f, g;
+    share(to, pn, f, g);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       x[e] = make_float4(fmaf(g, y[e].x, x[e].x * f), fmaf(g, y[e].y, x[e].y * f), fmaf(g, y[e].z, x[e].z * f),
@@ -1079,24 +1399,26 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     if (group == 0) {
       s_ml[0][lane] = m;
       s_ml[1][lane] = l;
+      s_ml[2][lane] = to;
     }
   }
   flags = __syncthreads_or(flags & kLoose);
   if (odd || at >= M) return;
-  const float pm = s_ml[0][lane], top = fmaxf(m, pm), base = top == -INFINITY ? 0.0f : top, f = exp2f(m - base),
-              g = exp2f(pm - base);
-  l = l * f + s_ml[1][lane] * g;
+  join(m, l, s_ml[0][lane], s_ml[1][lane]);
+  float f, g;
+  share(to, s_ml[2][lane], f, g);
   const int i = at / a.g;
   const long long head = (long long)(r.row0 + i) * a.Hq + rec.h * a.g + (at - i * a.g);
-  float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (DT == kE4m3 && !a.c.token_scales && a.c.v_scale != nullptr) inv *= a.c.v_scale[rec.h];
+  float inv = l == 0.0f ? 0.0f : 1.0f / l, inv2 = 1.0f;
+  if (DT == kE4m3 && a.c.token_scales) between(to - m, inv, inv2);
+  else if (DT == kE4m3 && a.c.v_scale != nullptr) inv *= a.c.v_scale[rec.h];
   uint32_t y[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const float4 z = s_x[group][e][lane];
     float4 v = make_float4(fmaf(g, z.x, x[e].x * f), fmaf(g, z.y, x[e].y * f), fmaf(g, z.z, x[e].z * f),
                            fmaf(g, z.w, x[e].w * f));
-    v = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : times(v, inv);
+    v = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : times(times(v, inv), inv2);
     if (flags && l != 0.0f) {
       v.x += loose<DT>(a, r, rec.b, rec.h, i, 16 * group + 4 * e);
       v.y += loose<DT>(a, r, rec.b, rec.h, i, 16 * group + 4 * e + 1);
@@ -1106,10 +1428,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     y[2 * e] = pack<QT == kBf16>(v.x, v.y);
     y[2 * e + 1] = pack<QT == kBf16>(v.z, v.w);
   }
-  uint4* to = reinterpret_cast<uint4*>(a.out + head * (kD * 2) + group * 32);
-  to[0] = make_uint4(y[0], y[1], y[2], y[3]);
-  to[1] = make_uint4(y[4], y[5], y[6], y[7]);
-  if (a.lse != nullptr && group == 0) a.lse[head] = (top + log2f(l)) * kLn2;
+  uint4* out = reinterpret_cast<uint4*>(a.out + head * (kD * 2) + group * 32);
+  out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+  out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  if (a.lse != nullptr && group == 0) a.lse[head] = (m + log2f(l)) * kLn2;
 }
 
 template <int DT, int QT, int TILES, bool TS>

@@ -94,6 +94,13 @@ class Cache:
             r.append(x)
         return r
 
+    def value_scales(self, b, h, T):
+        """The scales that are not the same for all of a head's values."""
+        if self.dtype != "e4m3t":
+            return torch.ones(T, dtype=torch.float64, device="cuda")
+        page, place = self.where(b, torch.arange(T, device="cuda"))
+        return self.v_scale[page, h, place].double()
+
 
 def _tree(rows, seed, holes=0.0, words=None):
     """Visibility [n, n] of each request's drafted tokens, and the mask's words."""
@@ -119,10 +126,12 @@ def _chain(rows):
     return [torch.ones((n, n), device="cuda").tril() > 0 for n in rows]
 
 
-def _exact(q, K, V, seen, scale, cache, act):
+def _exact(q, K, V, seen, scale, cache, act, vs):
     """out, lse of rows q [n, D] in 64 bits, and their tolerances. A product of 128 channels summed in FP32 is off by
-    `delta`, which moves a logarithmic weight by as much (twice: also the sum's); a weight is rounded to 16 bits (FP16: to
-    no less than 2^-32 of the largest one's unit); tensor-core sums cut off up to 2^-23 per 16 tokens; out is rounded once."""
+    `delta`, which moves a logarithmic weight by as much (twice: also the sum's); a weight (times vs [T], its value's
+    scale, where tokens have one) is rounded to 16 bits: BF16 by 2^-8 of it, FP16 by 2^-11, or half of FP16's smallest
+    step, 2^-25, where the largest weight is at least 2^7: 2^-32 of that one; tensor-core sums cut off up to 2^-23 per 16
+    tokens; out is rounded once."""
     q = q.double()
     s = (q @ K.T * scale).masked_fill(~seen, -math.inf)
     none = (s == -math.inf).all(1)
@@ -131,12 +140,14 @@ def _exact(q, K, V, seen, scale, cache, act):
     Kf, Vf = K.nan_to_num(0, 0, 0), V.nan_to_num(0, 0, 0)
     delta = 136 * 2.0**-23 * scale * (q.abs() @ Kf.abs().T).masked_fill(~seen, 0).amax(1) + 2.0**-20
     seq = (K.shape[0] / 16 + 64) * 2.0**-23
-    half = cache == "fp16"
+    half = cache != "bf16"
     pv = torch.where(seen[..., None] & (p[..., None] >= 0), p[..., None] * V, 0.0).sum(1)
     pa = p.nan_to_num(0) @ Vf.abs()
     tol = (2 * delta + 2 * seq)[:, None] * pa + (2.0**-11 if half else 2.0**-8) * pa
     if half:
-        tol = tol + 2.0**-31 * Vf.abs().amax()
+        vs = vs.nan_to_num(0, 0, 0)
+        codes = (Vf / torch.where(vs == 0, 1.0, vs)[:, None]).abs()
+        tol = tol + 2.0**-32 * (p.nan_to_num(0) * vs).amax(1)[:, None] * codes.sum(0)
     u = 2.0**-11 if act == "fp16" else 2.0**-8
     tol = tol + u * (pv.abs() + tol) + (2.0**-24 if act == "fp16" else 0)
     return pv, lse, tol, delta + seq + 2.0**-21 * lse.abs()
@@ -164,7 +175,7 @@ def _compare(c, q, out, lse, seen, scale=1 / math.sqrt(D), refused=()):
         see = torch.cat([torch.ones((n, T), dtype=torch.bool, device="cuda"), seen[b]], 1)
         for h in range(H):
             for j in range(h * g, h * g + g):
-                o, l, to, tl = _exact(q[r, j], K[:, h], V[:, h], see, scale, c.dtype, act)
+                o, l, to, tl = _exact(q[r, j], K[:, h], V[:, h], see, scale, c.dtype, act, c.value_scales(b, h, T + n))
                 x, y = out[r, j].double(), lse[r, j].double()
                 fine = torch.isfinite(o)
                 assert ((x == o) | (x.isnan() & o.isnan()) | fine).all(), (b, h, j, "not finite")
@@ -297,6 +308,33 @@ def test_values_that_are_not_finite(cache, act, what):
                     assert ((x - o)[ok].abs() <= 0.05).all(), (b, i, j)
         at += n
     assert torch.isfinite(out[:, :4]).all()  # the other KV head
+
+
+@pytest.mark.parametrize("act", ["bf16", "fp16"])
+@pytest.mark.parametrize("low,high", [(-126, -100), (-60, 60), (-110, 0), (30, 100)])
+def test_scales_far_apart(act, low, high):
+    """Values' scales over many powers of two, against the keys' order: the tokens that weigh most have the smallest."""
+    c = Cache([700, 90], [9, 130], 16, 2, "e4m3t", seed=3)
+    for b, T in enumerate([709, 220]):
+        page, place = c.where(b, torch.arange(T, device="cuda"))
+        e = torch.linspace(high, low, T, device="cuda").round()
+        c.v_scale[page, :, place] = torch.exp2(e)[:, None]
+    q = _query(139, 8, act)
+    seen, mask = _tree([9, 130], 6)
+    out, lse = _attend(c, q, _offsets([9, 130]), mask)
+    if act == "bf16" or high < 0:
+        _compare(c, q, out, lse, seen)
+    else:  # (FP16 cannot hold such results: infinite, but the sums are right)
+        fine = torch.full_like(lse, 0.0)
+        at = 0
+        for b, n in enumerate(c.rows):
+            K, _ = c.values(b, 0, c.lens[b] + n)
+            see = torch.cat([torch.ones((n, c.lens[b]), dtype=torch.bool, device="cuda"), seen[b]], 1)
+            for j in range(8):
+                s = (q[at:at + n, j].double() @ K[:, j // 4].T / math.sqrt(D)).masked_fill(~see, -math.inf)
+                fine[at:at + n, j] = torch.logsumexp(s, 1)
+            at += n
+        assert (lse - fine).abs().max() < 1e-4
 
 
 def test_keys_of_minus_infinite_score_weigh_nothing():
