@@ -55,7 +55,6 @@ constexpr uint32_t kColQ = 128;  // one row tile: queries, two buffers of 64
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;   // log2 of what a row's weights may exceed 1 by before its sums are rescaled
 constexpr long long kWaitNs = 2000000000LL;
-enum { kBadPage = 1, kLoose = 2 };  // of a unit
 
 // ---------------------------------------------------------------- forms
 
@@ -102,7 +101,8 @@ struct Smem {
   unsigned long long full[F::kSlots], empty[F::kSlots];
   unsigned long long s_full[2], p_ready[2], pv_done[2], q_full[2], q_free[2], o_free, drain;
   uint32_t tmem;
-  int flags[16];  // of the unit by its number's last bits
+  int bad_page[16];  // of the unit by its number's last bits
+  int loose;         // some drafted value was replaced
   volatile int abort;
 };
 
@@ -319,6 +319,7 @@ struct Request {
     const int nb = blocks(a, R);
     if (a.mask != nullptr) return (long long)nb * (tiles(P + n) + kUnitCost);
     long long w = 0;
+#pragma unroll 1
     for (int rb = 0; rb < nb; ++rb) w += tiles(tokens(a, rb, R)) + kUnitCost;
     return w;
   }
@@ -354,6 +355,7 @@ struct Walk {
     }
     pos = s0 - at + h * head;
     unit(a);
+#pragma unroll 1
     while (pos + tiles + kUnitCost <= s0 && rb + 1 < r.blocks(a, R)) {
       pos += tiles + kUnitCost;
       ++rb;
@@ -373,6 +375,7 @@ struct Walk {
       rb = 0;
       if (++h == a.c.H) {
         h = 0;
+#pragma unroll 1
         do {
           if (++b >= a.B) return false;
           r.load(a, b);
@@ -405,27 +408,6 @@ __device__ __forceinline__ uint32_t seen_bits(const uint32_t* mask, int words, i
   return __funnelshift_r(lo, seen_word(mask, words, n, i, k + 1), j0 & 31);
 }
 
-// Sum of the values that are not finite in channel c of the drafted tokens that row i sees (0: none).
-template <int DT>
-__device__ __forceinline__ float loose(const TreeArgs& a, const Request& r, int b, int h, int i, int c) {
-  const uint32_t* mask = a.mask != nullptr ? a.mask + (long long)(r.row0 + i) * a.mask_words : nullptr;
-  float sum = 0.0f;
-  for (int j = 0; j < r.n; ++j) {
-    if (!((seen_word(mask, a.mask_words, r.n, i, j >> 5) >> (j & 31)) & 1)) continue;
-    const int t = r.P + j, e = a.c.ps.div(t), page = a.table[(long long)b * a.max_pages + e];
-    const int place = t - e * int(a.c.ps.d);
-    if (page < 0 || page >= a.c.n_pages) continue;
-    const char* p = a.c.v + (long long)page * a.c.page_stride + (long long)place * a.c.token_stride +
-                    (long long)h * a.c.head_stride + (c & ~3) * elem_bytes<DT>();
-    const float4 x = load4<DT>(p);
-    float v = (&x.x)[c & 3];
-    if (DT == kE4m3 && a.c.v_scale != nullptr)
-      v *= a.c.v_scale[a.c.token_scales ? ((long long)page * a.c.H + h) * int(a.c.ps.d) + place : h];
-    if (!isfinite(v)) sum += v;
-  }
-  return sum;
-}
-
 // Where in an operand slot a 16-byte chunk (eight channels) of a token (or row) lies: 64 channels of all 128 tokens, then
 // the other 64, a token's 128 bytes with its chunks swizzled by the token's number. The same for a K-major operand (keys,
 // queries) and an MN-major one (values). (Core matrices of 8 x 16 bytes without a swizzle take each of a row's chunks to
@@ -437,9 +419,11 @@ __device__ __forceinline__ uint32_t chunk_at(int token, int chunk) {
 struct Rec {  // a unit that begins in a block's range and goes on behind it (parts 0: none)
   int32_t b, h, rb, parts;
 };
-__host__ __device__ constexpr size_t slots_offset(int n) { return size_t(n) * sizeof(Rec); }
-// sums [32][rows][4], then by row the weights' maximum and sum and (scales per token) what the sums are to, then flags
-__host__ __device__ constexpr size_t slot_floats(int rows) { return size_t(rows) * (kD + 3) + 4; }
+// Workspace: Rec[n], int[n] (a block replaced some drafted value), 2 n slots: sums [32][rows][4], then by row the
+// weights' maximum and sum and what the sums are to.
+__host__ __device__ constexpr size_t loose_offset(int n) { return size_t(n) * sizeof(Rec); }
+__host__ __device__ constexpr size_t slots_offset(int n) { return loose_offset(n) + (size_t(n) * 4 + 15) / 16 * 16; }
+__host__ __device__ constexpr size_t slot_floats(int rows) { return size_t(rows) * (kD + 3); }
 
 // ---------------------------------------------------------------- softmax warps
 
@@ -739,7 +723,7 @@ struct Softmax {
         if constexpr (TS) {
           float v = vs;
           if (t0 + thread >= w.r.P && !isfinite(v)) {
-            atomicOr(&S.flags[w.number & 15], kLoose);
+            S.loose = 1;
             v = 0.0f;
           }
           S.scales[tile][count & 1u][0][thread] = scaled(sc, ks);
@@ -782,7 +766,7 @@ struct Softmax {
       if (active) {
         if (!summed(count - 1)) return;
       }
-      if (threadIdx.x == 0) S.flags[(w.number + 8) & 15] = 0;  // (the producers are at most four units ahead)
+      if (threadIdx.x == 0) S.bad_page[(w.number + 8) & 15] = 0;  // (the producers are at most four units ahead)
       if (active) {
         if (same > 1) finish_copies(w, row, r, same, copy);
         else if (rows) finish(w, row, r, M);
@@ -810,8 +794,8 @@ struct Softmax {
     return f;
   }
   __device__ __forceinline__ bool is_whole(const Walk<F::kRows>& w) const { return w.begin == 0 && w.end == w.tiles; }
-  __device__ __forceinline__ int flags_of(const Walk<F::kRows>& w) const {
-    return *reinterpret_cast<volatile int*>(&S.flags[w.number & 15]);
+  __device__ __forceinline__ bool bad_page(const Walk<F::kRows>& w) const {
+    return *reinterpret_cast<volatile int*>(&S.bad_page[w.number & 15]) != 0;
   }
   // Where a whole unit's row goes, in query heads.
   __device__ __forceinline__ long long head_of(const Walk<F::kRows>& w, const Row& row, int r) const {
@@ -824,27 +808,16 @@ struct Softmax {
   __device__ __forceinline__ void put_lse(long long head, const Row& row) const {
     if (a.lse != nullptr) a.lse[head] = (row.m - (TS ? 0.0f : F::kShift) + log2f(row.l)) * kLn2;
   }
-  __device__ __forceinline__ void put_slot(float* slot, int at, const Row& row, int flags) const {
+  __device__ __forceinline__ void put_slot(float* slot, int at, const Row& row) const {
     slot[size_t(F::kRows) * kD + at] = TS ? row.m : row.m - F::kShift;
     slot[size_t(F::kRows) * (kD + 1) + at] = row.l;
     slot[size_t(F::kRows) * (kD + 2) + at] = (TS ? row.to : row.m) - F::kShift;
-    if (at == 0) slot[size_t(F::kRows) * (kD + 3)] = __int_as_float(flags);
   }
-  // N channels of a whole unit's row from c on, scaled, with what is not finite, rounded, to out.
+  // N channels of a whole unit's row from c on, scaled and rounded, to out.
   template <int N>
-  __device__ __forceinline__ void put_out(const Walk<F::kRows>& w, const Row& row, long long head, int c, float (&x)[N],
-                                          float2 f, int flags) const {
+  __device__ __forceinline__ void put_out(const Row& row, long long head, int c, float (&x)[N], float2 f) const {
 #pragma unroll
     for (int e = 0; e < N; ++e) x[e] = row.l == 0.0f ? 0.0f : (TS ? x[e] * f.x * f.y : x[e] * f.x);
-    if ((flags & kLoose) && row.l != 0.0f) {
-#pragma unroll 1
-      for (int e = 0; e < N; ++e) {
-        const float y = loose<DT>(a, w.r, w.b, w.h, row.i, c + e);
-#pragma unroll
-        for (int d = 0; d < N; ++d)
-          if (d == e) x[d] += y;
-      }
-    }
     char* to = a.out + head * (kD * 2) + c * 2;
 #pragma unroll
     for (int e = 0; e < N; e += 8)
@@ -855,8 +828,7 @@ struct Softmax {
 
   // The unit's rows, or this part of it, to out and lse or to a slot.
   __device__ __forceinline__ void finish(const Walk<F::kRows>& w, Row& row, int r, int M) {
-    const int flags = flags_of(w);
-    if (flags & kBadPage) row.l = NAN;
+    if (bad_page(w)) row.l = NAN;
     if (is_whole(w)) {
       const float2 f = factors(w, row);
       const long long head = head_of(w, row, r);
@@ -870,7 +842,7 @@ struct Softmax {
         float y[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(x[e]);
-        put_out<32>(w, row, head, 32 * c, y, f, flags);
+        put_out<32>(row, head, 32 * c, y, f);
       }
     } else {
       float* slot = slot_of(w);
@@ -885,13 +857,13 @@ struct Softmax {
           *reinterpret_cast<uint4*>(slot + (size_t(8 * c + e) * F::kRows + at) * 4) =
               make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
       }
-      put_slot(slot, at, row, flags);
+      put_slot(slot, at, row);
     }
   }
 
   // The same for rows in several copies, joined first: a thread's share is 32 / same channels of each 32 of its row.
   __device__ __forceinline__ void finish_copies(const Walk<F::kRows>& w, Row& row, int r, int same, int copy) {
-    const int flags = flags_of(w), each = kTile / same, at = thread % each, M = w.r.n * a.g;
+    const int each = kTile / same, at = thread % each, M = w.r.n * a.g;
     S.part_ml[0][thread] = row.m;
     S.part_ml[1][thread] = row.l;
     S.part_ml[2][thread] = TS ? row.to : row.m;
@@ -905,7 +877,7 @@ struct Softmax {
     for (int i = 0; i < same; ++i) l += S.part_ml[1][i * each + at] * exp2f(S.part_ml[0][i * each + at] - (m == -INFINITY ? 0.0f : m));
     row.m = m;
     row.to = to;
-    row.l = flags & kBadPage ? NAN : l;
+    row.l = bad_page(w) ? NAN : l;
     const float own = exp2f(mine - (to == -INFINITY ? 0.0f : to));
     const bool whole = is_whole(w), live = r < M;
     const float2 f = factors(w, row);
@@ -913,7 +885,7 @@ struct Softmax {
     float* slot = slot_of(w);
     if (copy == 0 && live) {
       if (whole) put_lse(head, row);
-      else put_slot(slot, at, row, flags);
+      else put_slot(slot, at, row);
     }
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
@@ -931,7 +903,7 @@ struct Softmax {
 #pragma unroll
           for (int d = 0; d < 8; ++d) y[d] += S.part[i * each + at][e + d];
         if (whole) {
-          put_out<8>(w, row, head, 32 * c + e, y, f, flags);
+          put_out<8>(row, head, 32 * c + e, y, f);
         } else {
 #pragma unroll
           for (int d = 0; d < 8; d += 4)
@@ -955,62 +927,66 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
   const uint32_t slots = smem_addr(S.slot), raws = smem_addr(S.raw) + thread * 16;
   constexpr int kHalves = kD * elem_bytes<DT>() / 128;  // 128-byte pieces of a row
   constexpr int kCopies = kN / 4;                       // of a piece of four tokens
-  struct Past {  // a copy not looked at yet: from which of the tile's tokens on values may be replaced, and the unit
-    int word;
-    __device__ __forceinline__ int from() const { return word & 0xFF; }
-    __device__ __forceinline__ int number() const { return word >> 8; }
-  } past[F::kLag + 1];
-#pragma unroll
-  for (int i = 0; i <= F::kLag; ++i) past[i] = Past{kTile};
-  int pending = 0;  // 8-bit rows: copies not converted yet
+  // Copies not looked at yet, the newest one in the lowest bits: for each the first of the tile's tokens whose value may
+  // be replaced (kTile: none, as for all keys).
+  static_assert(F::kLag <= 7);
+  uint64_t past = 0;
+  int pending = 0;
+  uint32_t x = 0;  // copies so far
 
-  // Copy number x (K of a tile, then V) has landed: makes it an operand. (Of 16-bit rows only the drafted values come
-  // here; the others arrive by themselves.)
-  auto land = [&](uint32_t x, const Past& p, auto is_value) -> bool {
-    constexpr bool value = decltype(is_value)::value;
-    const uint32_t slot = x % F::kSlots;
-    const uint32_t to = slots + slot * kSlotBytes;
+  // The oldest of them has landed and becomes an operand. (Of 16-bit rows only the drafted values are looked at here;
+  // the others arrive by themselves.)
+  auto land = [&](int from, bool value) -> bool {
+    const uint32_t y = x - pending, slot = y % F::kSlots, to = slots + slot * kSlotBytes;
     if constexpr (F::kNarrow) {
-      if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return false;
-      const uint32_t from = raws + (x % F::kStages) * kRawBytes;
-      uint4 y[kCopies];  // 16 channels of a token each
+      if (!mbar_wait(&S.empty[slot], (y / F::kSlots + 1) & 1u, &S.abort)) return false;
+      const uint32_t raw = raws + (y % F::kStages) * kRawBytes;
+      uint4 z[kCopies];  // 16 channels of a token each
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) y[i] = lds16(from + i * (F::kProducers * 16));
-      if (value && p.from() < kTile) {  // drafted tokens: NaN is replaced by 0
+      for (int i = 0; i < kCopies; ++i) z[i] = lds16(raw + i * (F::kProducers * 16));
+      if (from < kTile) {  // drafted tokens: NaN is replaced by 0
         uint32_t any = 0u;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) {
-          if (kN * warp + 4 * i + (lane >> 3) < p.from()) continue;
+          if (kN * warp + 4 * i + (lane >> 3) < from) continue;
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
-            const uint32_t nan = (((&y[i].x)[d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes of 0x7F or 0xFF
-            (&y[i].x)[d] &= ~((nan >> 7) * 255u);
+            const uint32_t nan = (((&z[i].x)[d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes of 0x7F or 0xFF
+            (&z[i].x)[d] &= ~((nan >> 7) * 255u);
             any |= nan;
           }
         }
-        if (any != 0u) atomicOr(&S.flags[p.number() & 15], kLoose);
+        if (any != 0u) S.loose = 1;
       }
+      auto convert = [&](auto bf) {
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) {
-        const int token = kN * warp + 4 * i + (lane >> 3), chunk = 2 * (lane & 7);
-        uint2 z[4];
+        for (int i = 0; i < kCopies; ++i) {
+          const int token = kN * warp + 4 * i + (lane >> 3), chunk = 2 * (lane & 7);
+          uint2 v[4];
 #pragma unroll
-        for (int d = 0; d < 4; ++d) z[d] = widen<value ? F::kValBf : F::kKeyBf>((&y[i].x)[d]);
-        sts16(to + chunk_at(token, chunk), make_uint4(z[0].x, z[0].y, z[1].x, z[1].y));
-        sts16(to + chunk_at(token, chunk + 1), make_uint4(z[2].x, z[2].y, z[3].x, z[3].y));
+          for (int d = 0; d < 4; ++d) v[d] = widen<decltype(bf)::value>((&z[i].x)[d]);
+          sts16(to + chunk_at(token, chunk), make_uint4(v[0].x, v[0].y, v[1].x, v[1].y));
+          sts16(to + chunk_at(token, chunk + 1), make_uint4(v[2].x, v[2].y, v[3].x, v[3].y));
+        }
+      };
+      if constexpr (F::kKeyBf) {
+        if (value) convert(std::bool_constant<F::kValBf>{});
+        else convert(std::bool_constant<F::kKeyBf>{});
+      } else {
+        convert(std::false_type{});
       }
-    } else if constexpr (value) {  // drafted ones
+    } else {
       constexpr uint32_t kInf = DT == kBf16 ? 0x7F80u : 0x7C00u;
 #pragma unroll 1
       for (int e = 0; e < 2 * kCopies; ++e) {
         const int token = kN * warp + 4 * (e >> 1) + (lane >> 3), chunk = 8 * (e & 1) + (lane & 7);
-        if (token < p.from()) continue;
+        if (token < from) continue;
         const uint32_t at = to + chunk_at(token, chunk);
-        uint4 y = lds16(at);
+        uint4 z = lds16(at);
         bool any = false;
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          uint32_t& v = (&y.x)[d];
+          uint32_t& v = (&z.x)[d];
           if ((v & kInf) == kInf) {
             v &= 0xFFFF0000u;
             any = true;
@@ -1021,27 +997,13 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
           }
         }
         if (any) {
-          sts16(at, y);
-          atomicOr(&S.flags[p.number() & 15], kLoose);
+          sts16(at, z);
+          S.loose = 1;
         }
       }
     }
     fence_async_smem();
     mbar_arrive(&S.full[slot]);
-    return true;
-  };
-  uint32_t x = 0;  // copies so far
-  // All but the last LEFT copies so far; an even number of them, as LEFT.
-  auto land_all = [&](auto left) -> bool {
-    constexpr int kLeft = decltype(left)::value;
-    wait_groups<kLeft>();
-#pragma unroll
-    for (int i = F::kLag - 1; i >= kLeft; --i)
-      if (F::kNarrow ? i < pending : past[i].from() < kTile) {
-        if (i % 2 ? !land(x - 1 - i, past[i], std::false_type{}) : !land(x - 1 - i, past[i], std::true_type{})) return false;
-        past[i] = Past{kTile};
-      }
-    pending = min(pending, kLeft);
     return true;
   };
 
@@ -1053,97 +1015,112 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
   int page = page_of(w, w.begin);
   uint32_t units = 0;
   int last = 0;  // tiles of the unit before
-  for (bool more = true; more; ++units) {
-    // one row tile: the unit's queries to tensor memory, a row by a thread of the first four warps; on their way while
-    // the first tile's copies are issued
-    [[maybe_unused]] uint32_t q[2][32];
-    if constexpr (TILES == 1) {
-      const int M = w.r.n * a.g, r = w.rb * F::kRows + thread % (kTile / copies(M));
-      const bool live = thread < kTile && r < M;
-      const int i = r / a.g;
-      const char* from = a.q + (live ? (w.r.row0 + i) * a.q_stride + (long long)(w.h * a.g + (r - i * a.g)) * (kD * 2) : 0);
+  int k = w.begin;
+  bool more = true;
+  long long off = -1;
+  int drafts = kTile;
+  [[maybe_unused]] uint32_t q[2][32];
+#pragma unroll 1
+  for (;;) {  // a copy each: keys and values of a tile in turn; then what is left to be looked at
+    const int half = int(x & 1u);
+    if (more && half == 0) {
+      // one row tile: the unit's queries to tensor memory, a row by a thread of the first four warps; on their way while
+      // the first tile's copies are issued
+      if constexpr (TILES == 1)
+        if (k == w.begin) {
+          const int M = w.r.n * a.g, r = w.rb * F::kRows + thread % (kTile / copies(M));
+          const bool live = thread < kTile && r < M;
+          const int i = r / a.g;
+          const char* from =
+              a.q + (live ? (w.r.row0 + i) * a.q_stride + (long long)(w.h * a.g + (r - i * a.g)) * (kD * 2) : 0);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        uint4 y = make_uint4(0u, 0u, 0u, 0u);
-        if (live) y = *reinterpret_cast<const uint4*>(from + 16 * e);
-        q[e >> 3][4 * (e & 7)] = y.x;
-        q[e >> 3][4 * (e & 7) + 1] = y.y;
-        q[e >> 3][4 * (e & 7) + 2] = y.z;
-        q[e >> 3][4 * (e & 7) + 3] = y.w;
-      }
-    }
-    for (int k = w.begin; k < w.end; ++k) {
+          for (int e = 0; e < 16; ++e) {
+            uint4 y = make_uint4(0u, 0u, 0u, 0u);
+            if (live) y = *reinterpret_cast<const uint4*>(from + 16 * e);
+            q[e >> 3][4 * (e & 7)] = y.x;
+            q[e >> 3][4 * (e & 7) + 1] = y.y;
+            q[e >> 3][4 * (e & 7) + 2] = y.z;
+            q[e >> 3][4 * (e & 7) + 3] = y.w;
+          }
+        }
       const int t = k * kTile + kN * warp + (lane & (kN - 1));
-      long long off = -1;
+      off = -1;
       if (page >= 0 && page < a.c.n_pages) {
         const int place = t - a.c.ps.div(t) * int(a.c.ps.d);
         off = (long long)page * a.c.page_stride + (long long)place * a.c.token_stride + (long long)w.h * a.c.head_stride;
       } else if (page != -2 || t < w.tokens) {
         flag(a.c, KVQ_PAGED_ERR_PAGE);
-        atomicOr(&S.flags[w.number & 15], kBadPage);
+        S.bad_page[w.number & 15] = 1;
       }
       if (k + 1 < w.end) page = page_of(w, k + 1);
-      const int drafts = max(0, min(kTile, w.r.P - k * kTile));  // the first drafted token of the tile
+      drafts = max(0, min(kTile, w.r.P - k * kTile));
+    }
+    if (more) {
+      const char* pool = half == 0 ? a.c.k : a.c.v;
+      uint32_t to = 0;
+      if constexpr (!F::kNarrow) {
+        if (!mbar_wait(&S.empty[x % F::kSlots], (x / F::kSlots + 1) & 1u, &S.abort)) return;
+        to = slots + (x % F::kSlots) * kSlotBytes;
+      } else {
+        to = raws + (x % F::kStages) * kRawBytes;
+      }
 #pragma unroll
-      for (int half = 0; half < 2; ++half, ++x) {
-        const char* pool = half == 0 ? a.c.k : a.c.v;
-        uint32_t to = 0;
-        if constexpr (!F::kNarrow) {
-          if (!mbar_wait(&S.empty[x % F::kSlots], (x / F::kSlots + 1) & 1u, &S.abort)) return;
-          to = slots + (x % F::kSlots) * kSlotBytes;
-        } else {
-          to = raws + (x % F::kStages) * kRawBytes;
-        }
+      for (int e = 0; e < kCopies; ++e) {
+        const long long y = __shfl_sync(0xFFFFFFFFu, off, 4 * e + (lane >> 3));
 #pragma unroll
-        for (int e = 0; e < kCopies; ++e) {
-          const long long y = __shfl_sync(0xFFFFFFFFu, off, 4 * e + (lane >> 3));
-#pragma unroll
-          for (int f = 0; f < kHalves; ++f) {
-            const int chunk = 8 * f + (lane & 7);
-            const uint32_t at = F::kNarrow ? to + e * (F::kProducers * 16)
-                                           : to + chunk_at(kN * warp + 4 * e + (lane >> 3), chunk);
-            copy16(at, pool + (y < 0 ? 0 : y) + chunk * 16, y >= 0);
-          }
-        }
-        commit();
-#pragma unroll
-        for (int i = F::kLag; i > 0; --i) past[i] = past[i - 1];
-        past[0] = Past{drafts | (w.number & 15) << 8};
-        if constexpr (!F::kNarrow)
-          if (half == 0 || drafts == kTile) {
-            arrive_landed(&S.full[x % F::kSlots]);
-            past[0] = Past{kTile};
-          }
-        if (F::kNarrow ? ++pending > F::kLag : past[F::kLag].from() < kTile) {
-          wait_groups<F::kLag>();
-          --pending;
-          if (half == F::kLag % 2 ? !land(x - F::kLag, past[F::kLag], std::false_type{})
-                                  : !land(x - F::kLag, past[F::kLag], std::true_type{}))
-            return;
+        for (int f = 0; f < kHalves; ++f) {
+          const int chunk = 8 * f + (lane & 7);
+          const uint32_t at =
+              F::kNarrow ? to + e * (F::kProducers * 16) : to + chunk_at(kN * warp + 4 * e + (lane >> 3), chunk);
+          copy16(at, pool + (y < 0 ? 0 : y) + chunk * 16, y >= 0);
         }
       }
-      if constexpr (TILES == 1)
-        if (k == w.begin) {
-          // the buffer's last queries are those of the unit before the last one: multiplied once all its keys are there
-          if (F::kNarrow && pending > 4 && last == 1 && !land_all(std::integral_constant<int, 4>{})) return;
-          if (!mbar_wait(&S.q_free[units & 1u], ((units >> 1) + 1) & 1u, &S.abort)) return;
-          if (thread < kTile) {
-            tc_fence_after();
-            const uint32_t at = S.tmem + (uint32_t(warp) << 21) + kColQ + 64u * (units & 1u);
-            tmem_st(at, q[0]);
-            tmem_st(at + 32, q[1]);
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.q_full[units & 1u]);
-          }
-        }
+      commit();
+      if (!F::kNarrow && (half == 0 || drafts == kTile)) arrive_landed(&S.full[x % F::kSlots]);
+      past = past << 8 | uint32_t(half == 0 ? kTile : drafts);
+      ++x;
+      ++pending;
     }
-    last = w.end - w.begin;
-    more = w.next(a, s0, e0);
-    if (more) page = page_of(w, w.begin);
+    // one row tile: the buffer's last queries are those of the unit before the last one, multiplied once all its keys
+    // are there: no more than the last unit's and these copies may be left
+    const bool first = TILES == 1 && more && half == 1 && k == w.begin;
+    const int most = !more ? 0 : first && last == 1 ? min(F::kLag, 4) : F::kLag;
+#pragma unroll 1
+    while (pending > most) {
+      const int from = int(past >> (8 * (pending - 1))) & 0xFF;
+      if (F::kNarrow || from < kTile) {
+        if (most == F::kLag) wait_groups<F::kLag>();
+        else if (most == 4) wait_groups<4>();
+        else wait_groups<0>();
+        if (!land(from, ((x - pending) & 1u) != 0u)) return;
+      }
+      --pending;
+    }
+    if (!more) break;
+    if constexpr (TILES == 1)
+      if (first) {
+        if (!mbar_wait(&S.q_free[units & 1u], ((units >> 1) + 1) & 1u, &S.abort)) return;
+        if (thread < kTile) {
+          tc_fence_after();
+          const uint32_t at = S.tmem + (uint32_t(warp) << 21) + kColQ + 64u * (units & 1u);
+          tmem_st(at, q[0]);
+          tmem_st(at + 32, q[1]);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.q_full[units & 1u]);
+        }
+      }
+    if (half == 1 && ++k == w.end) {
+      last = w.end - w.begin;
+      ++units;
+      more = w.next(a, s0, e0);
+      if (more) {
+        k = w.begin;
+        page = page_of(w, k);
+      }
+    }
   }
-  land_all(std::integral_constant<int, 0>{});
 }
 
 // ---------------------------------------------------------------- products
@@ -1252,6 +1229,7 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     reinterpret_cast<Rec*>(a.ws)[blockIdx.x] = Rec{0, 0, 0, 0};
+    reinterpret_cast<int*>(a.ws + loose_offset(gridDim.x))[blockIdx.x] = 0;
     for (int i = 0; i < F::kSlots; ++i) {
       mbar_init(&S.full[i], F::kProducers);
       mbar_init(&S.empty[i], 1);
@@ -1265,11 +1243,13 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
     }
     mbar_init(&S.o_free, 4);
     mbar_init(&S.drain, 1);
-    for (int i = 0; i < 16; ++i) S.flags[i] = 0;
+    for (int i = 0; i < 16; ++i) S.bad_page[i] = 0;
+    S.loose = 0;
     S.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // requests that are refused: no block's range holds them
+#pragma unroll 1
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     Request r;
     r.load(a, b);
@@ -1277,9 +1257,11 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
     if (threadIdx.x == 0) flag(a.c, KVQ_PAGED_ERR_LENGTH);
     const int n = row_range(a.offsets, a.n_rows, b, r.row0);
     const uint32_t nan = QT == kBf16 ? 0x7FC07FC0u : 0x7E007E00u;
+#pragma unroll 1
     for (long long i = threadIdx.x; i < (long long)max(n, 0) * a.Hq * (kD / 2); i += F::kThreads)
       reinterpret_cast<uint32_t*>(a.out)[(long long)r.row0 * a.Hq * (kD / 2) + i] = nan;
     if (a.lse != nullptr)
+#pragma unroll 1
       for (long long i = threadIdx.x; i < (long long)max(n, 0) * a.Hq; i += F::kThreads)
         a.lse[(long long)r.row0 * a.Hq + i] = NAN;
   }
@@ -1329,7 +1311,10 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0 && S.abort) flag(a.c, KVQ_PAGED_ERR_WAIT);
+  if (threadIdx.x == 0) {
+    if (S.abort) flag(a.c, KVQ_PAGED_ERR_WAIT);
+    if (S.loose) reinterpret_cast<int*>(a.ws + loose_offset(gridDim.x))[blockIdx.x] = 1;
+  }
   if (warp == F::kMmaWarp) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "n"(kTmemCols) : "memory");
@@ -1337,7 +1322,9 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
 }
 
 // Joins the parts of a unit that several blocks' ranges share: block (c, y) those of the unit that begins in block c's
-// range, its rows 32 y .. 32 y + 31, a lane a row, a warp 16 channels of it (and every other part).
+// range, its rows 32 y .. 32 y + 31, a lane a row, a warp 16 channels of it (and every other part). Where some drafted
+// value was replaced by 0 (loose), the blocks add what is not finite to the rows that see it: to those of shared units
+// here, to the others behind them.
 constexpr int kJoinWarps = 16;
 
 // `top` becomes the larger of top and part; what is to them is to it times f and g.
@@ -1353,6 +1340,27 @@ __device__ __forceinline__ void join(float& m, float& l, float pm, float pl) {
   l = l * f + pl * g;
 }
 
+// Sum of the values that are not finite in channels c .. c + 3 of the drafted tokens that row i sees (0: none).
+template <int DT>
+__device__ __noinline__ float4 loose(const TreeArgs& a, const Request& r, int b, int h, int i, int c) {
+  const uint32_t* mask = a.mask != nullptr ? a.mask + (long long)(r.row0 + i) * a.mask_words : nullptr;
+  float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int j = 0; j < r.n; ++j) {
+    if (!((seen_word(mask, a.mask_words, r.n, i, j >> 5) >> (j & 31)) & 1)) continue;
+    const int t = r.P + j, e = a.c.ps.div(t), page = a.table[(long long)b * a.max_pages + e];
+    const int place = t - e * int(a.c.ps.d);
+    if (page < 0 || page >= a.c.n_pages) continue;
+    float4 x = load4<DT>(a.c.v + (long long)page * a.c.page_stride + (long long)place * a.c.token_stride +
+                         (long long)h * a.c.head_stride + c * elem_bytes<DT>());
+    if (DT == kE4m3 && a.c.v_scale != nullptr)
+      x = times(x, a.c.v_scale[a.c.token_scales ? ((long long)page * a.c.H + h) * int(a.c.ps.d) + place : h]);
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      if (!isfinite((&x.x)[d])) (&sum.x)[d] += (&x.x)[d];
+  }
+  return sum;
+}
+
 template <int DT, int QT, int TILES>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ TreeArgs a) {
   constexpr int R = kTile * TILES;
@@ -1360,28 +1368,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
   __shared__ float4 s_x[8][4][32];
   wait_prior_grid();
   allow_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp & 7, odd = warp >> 3;
-  const Rec rec = reinterpret_cast<const Rec*>(a.ws)[blockIdx.x];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = warp & 7, odd = warp >> 3, n = gridDim.x;
+  const Rec* recs = reinterpret_cast<const Rec*>(a.ws);
+  const Rec rec = recs[blockIdx.x];
+  int some = 0;
+  for (int i = threadIdx.x; i < n; i += kJoinWarps * 32) some |= reinterpret_cast<const int*>(a.ws + loose_offset(n))[i];
   // (the bounds hold for every record of the attention kernel; a workspace that something else writes meanwhile must
   // not lead outside of it)
-  const int n = gridDim.x;
-  if (rec.parts < 2 || rec.parts > n - int(blockIdx.x) || rec.b < 0 || rec.b >= a.B || rec.h < 0 || rec.h >= a.c.H ||
-      rec.rb < 0)
-    return;
+  auto shared = [&](const Rec& x, int c) {
+    return x.parts >= 2 && x.parts <= n - c && x.b >= 0 && x.b < a.B && x.h >= 0 && x.h < a.c.H && x.rb >= 0;
+  };
+  const bool mine = shared(rec, blockIdx.x);
   Request r;
-  r.load(a, rec.b);
-  const int M = r.n * a.g, row = 32 * blockIdx.y + lane, at = rec.rb * R + row;
-  if (rec.rb * R + 32 * int(blockIdx.y) >= M) return;
+  r.load(a, mine ? rec.b : 0);
+  const int row = 32 * blockIdx.y + lane, at = rec.rb * R + row, parts = mine && at - lane < r.n * a.g ? rec.parts : 0;
   const float* slots = reinterpret_cast<const float*>(a.ws + slots_offset(n));
   float m = -INFINITY, l = 0.0f, to = -INFINITY;  // (to: what the sums are to)
   float4 x[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  int flags = 0;
-  for (int i = odd; i < rec.parts; i += 2) {
+  for (int i = odd; i < parts; i += 2) {
     const float* p = slots + size_t(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * slot_floats(R);
     const float pm = p[size_t(R) * kD + row], pl = p[size_t(R) * (kD + 1) + row], pn = p[size_t(R) * (kD + 2) + row];
-    flags |= __float_as_int(p[size_t(R) * (kD + 3)]);
     float4 y[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = *reinterpret_cast<const float4*>(p + (size_t(4 * group + e) * R + row) * 4);
@@ -1402,36 +1410,52 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
       s_ml[2][lane] = to;
     }
   }
-  flags = __syncthreads_or(flags & kLoose);
-  if (odd || at >= M) return;
-  join(m, l, s_ml[0][lane], s_ml[1][lane]);
-  float f, g;
-  share(to, s_ml[2][lane], f, g);
-  const int i = at / a.g;
-  const long long head = (long long)(r.row0 + i) * a.Hq + rec.h * a.g + (at - i * a.g);
-  float inv = l == 0.0f ? 0.0f : 1.0f / l, inv2 = 1.0f;
-  if (DT == kE4m3 && a.c.token_scales) between(to - m, inv, inv2);
-  else if (DT == kE4m3 && a.c.v_scale != nullptr) inv *= a.c.v_scale[rec.h];
-  uint32_t y[8];
+  some = __syncthreads_or(some);
+  if (!odd && parts > 0 && at < r.n * a.g) {
+    join(m, l, s_ml[0][lane], s_ml[1][lane]);
+    float f, g;
+    share(to, s_ml[2][lane], f, g);
+    const int i = at / a.g;
+    const long long head = (long long)(r.row0 + i) * a.Hq + rec.h * a.g + (at - i * a.g);
+    float inv = l == 0.0f ? 0.0f : 1.0f / l, inv2 = 1.0f;
+    if (DT == kE4m3 && a.c.token_scales) between(to - m, inv, inv2);
+    else if (DT == kE4m3 && a.c.v_scale != nullptr) inv *= a.c.v_scale[rec.h];
+    uint4* out = reinterpret_cast<uint4*>(a.out + head * (kD * 2) + group * 32);
+    uint32_t y[8];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float4 z = s_x[group][e][lane];
-    float4 v = make_float4(fmaf(g, z.x, x[e].x * f), fmaf(g, z.y, x[e].y * f), fmaf(g, z.z, x[e].z * f),
-                           fmaf(g, z.w, x[e].w * f));
-    v = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : times(times(v, inv), inv2);
-    if (flags && l != 0.0f) {
-      v.x += loose<DT>(a, r, rec.b, rec.h, i, 16 * group + 4 * e);
-      v.y += loose<DT>(a, r, rec.b, rec.h, i, 16 * group + 4 * e + 1);
-      v.z += loose<DT>(a, r, rec.b, rec.h, i, 16 * group + 4 * e + 2);
-      v.w += loose<DT>(a, r, rec.b, rec.h, i, 16 * group + 4 * e + 3);
+    for (int e = 0; e < 4; ++e) {
+      const float4 z = s_x[group][e][lane];
+      float4 v = make_float4(fmaf(g, z.x, x[e].x * f), fmaf(g, z.y, x[e].y * f), fmaf(g, z.z, x[e].z * f),
+                             fmaf(g, z.w, x[e].w * f));
+      v = l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f) : times(times(v, inv), inv2);
+      if (some) {
+        const float4 u = loose<DT>(a, r, rec.b, rec.h, i, 16 * group + 4 * e);
+        v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+      }
+      y[2 * e] = pack<QT == kBf16>(v.x, v.y);
+      y[2 * e + 1] = pack<QT == kBf16>(v.z, v.w);
     }
-    y[2 * e] = pack<QT == kBf16>(v.x, v.y);
-    y[2 * e + 1] = pack<QT == kBf16>(v.z, v.w);
+    out[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    out[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    if (a.lse != nullptr && group == 0) a.lse[head] = (m + log2f(l)) * kLn2;
   }
-  uint4* out = reinterpret_cast<uint4*>(a.out + head * (kD * 2) + group * 32);
-  out[0] = make_uint4(y[0], y[1], y[2], y[3]);
-  out[1] = make_uint4(y[4], y[5], y[6], y[7]);
-  if (a.lse != nullptr && group == 0) a.lse[head] = (m + log2f(l)) * kLn2;
+  if (!some) return;
+  // rows of units that are not shared: a warp a query head, a lane four channels
+  const int warps = n * gridDim.y * kJoinWarps, me = (blockIdx.y * n + blockIdx.x) * kJoinWarps + warp;
+  for (int b = 0; b < a.B; ++b) {
+    r.load(a, b);
+    for (long long u = me; u < (long long)r.n * a.Hq; u += warps) {
+      const int i = int(u / a.Hq), hq = int(u - (long long)i * a.Hq), h = hq / a.g, rb = (i * a.g + hq - h * a.g) / R;
+      bool joined = false;
+      for (int c = lane; c < n; c += 32) joined |= shared(recs[c], c) && recs[c].b == b && recs[c].h == h && recs[c].rb == rb;
+      if (__any_sync(0xFFFFFFFFu, joined)) continue;
+      const float4 y = loose<DT>(a, r, b, h, i, 4 * lane);
+      if (y.x == 0.0f && y.y == 0.0f && y.z == 0.0f && y.w == 0.0f) continue;
+      char* p = a.out + ((long long)(r.row0 + i) * a.Hq + hq) * (kD * 2) + 8 * lane;
+      const float4 x = load4<QT>(p);
+      store4<QT>(p, make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w));
+    }
+  }
 }
 
 template <int DT, int QT, int TILES, bool TS>
