@@ -22,6 +22,7 @@
 //   producers four: 16-byte asynchronous copies of K and V rows into a ring of
 //             operand slots; 8-bit rows by way of a staging ring and a conversion
 //   MMA       one, a lane of which issues all products
+//   checkers  two, for drafted values of 16-bit rows (below)
 // Exactness: products of 16-bit values are exact, sums FP32. 8-bit keys become 16-bit
 // of the queries' type (exact), 8-bit values BF16 (exact). A weight is one 16-bit
 // number (times its value's scale, where tokens have one): BF16, whose range holds
@@ -71,7 +72,7 @@ struct Form {
   static constexpr int kProducers = 32 * kProducerWarps;
   static constexpr int kTokens = kTile / kProducerWarps;  // of a tile, a producer warp's
   static constexpr int kMmaWarp = kSoftmaxWarps + kProducerWarps;
-  static constexpr int kThreads = (kMmaWarp + 4) * 32;  // (three idle warps: registers are shared out by four)
+  static constexpr int kThreads = (kMmaWarp + 4) * 32;  // (registers are shared out by four warps)
   // registers of the softmax, producer and MMA warps, by four of which they come to 3 x 168 or 4 x 128 of the launch
   static constexpr int kSoftmaxRegs = kThreads == 384 ? 224 : TILES == 1 ? 168 : 144;
   static constexpr int kProducerRegs = kThreads == 384 ? 152 : TILES == 1 ? 120 : 112;
@@ -81,8 +82,8 @@ struct Form {
   static constexpr int kQueries = TILES == 1 ? 0 : kRows;
   static constexpr int kSlots = kNarrow ? 3 : (TILES == 1 ? 6 : 5);
   static constexpr int kStages = kNarrow ? (TILES == 1 ? 6 : 3) : 0;  // of raw 8-bit rows
-  // slots between a copy and the look at it: 8-bit rows are all converted, of 16-bit ones the drafted values checked
-  static constexpr int kLag = kNarrow ? kStages - 1 : 2;
+  static constexpr int kLag = kNarrow ? kStages - 1 : 0;  // 8-bit rows: slots between a copy and its conversion
+  static constexpr int kCheckers = kNarrow ? 0 : 64;      // threads (two warps behind the MMA warp) that check drafted values
 };
 
 template <class F>
@@ -99,6 +100,7 @@ struct Smem {
   float part[F::kQueries > 0 ? 1 : kTile][33];
   float part_ml[3][F::kQueries > 0 ? 1 : kTile];
   unsigned long long full[F::kSlots], empty[F::kSlots];
+  unsigned long long raw_full[F::kSlots];  // 16-bit drafted values, before they are checked
   unsigned long long s_full[2], p_ready[2], pv_done[2], q_full[2], q_free[2], o_free, drain;
   uint32_t tmem;
   int bad_page[16];  // of the unit by its number's last bits
@@ -433,6 +435,13 @@ __device__ __forceinline__ float scaled(float scale, float ks) {
   return isfinite(ks) ? fminf(fmaxf(x, 0x1p-149f), 3.402823466e38f) : ks;
 }
 
+// FP32 numbers as whole numbers in the same order, and back.
+__device__ __forceinline__ int in_order(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float in_order(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7FFFFFFF)); }
+
 // 2^x / l as two factors f and g (l or a scale may take either out of FP32's range where the product with a sum stays
 // in it): f comes in as 1 / l.
 __device__ __forceinline__ void between(float x, float& f, float& g) {
@@ -637,12 +646,16 @@ struct Softmax {
         }
       }
     }
-    // TS: weights are taken to m for their own sum, and times their values' scales and `rel` to `to`, so that FP16 holds
-    // the largest of them whatever the scales are (their product stays in FP32's range: what `rel` cannot hold goes to
-    // the weights)
-    [[maybe_unused]] const float on = row.m - row.to + F::kShift, over = TS && on > 127.0f ? on - 127.0f : 0.0f;
-    [[maybe_unused]] const float rel = row.to == -INFINITY ? 0.0f : exp2_ftz(on - over);
-    const float base = (TS ? over : F::kShift) - (row.m == -INFINITY ? 0.0f : row.m);
+    // TS: the weights themselves are to `to` by 2^on, so that FP16 holds the largest product with a scale, and their own
+    // sum is taken back to m; what of `on` might leave FP32's range (scales near its ends) goes to the scales
+    [[maybe_unused]] float on = 0.0f, rest = 0.0f;
+    if constexpr (TS) {
+      const float x = row.to == -INFINITY ? 0.0f : row.m - row.to + F::kShift;
+      on = fminf(fmaxf(x, -60.0f), 60.0f);
+      rest = x - on;
+    }
+    [[maybe_unused]] const bool extreme = TS && __any_sync(0xFFFFFFFFu, rest != 0.0f);
+    const float base = (TS ? on : F::kShift) - (row.m == -INFINITY ? 0.0f : row.m);
     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
     for (int part = 0; part < kReads; ++part) {
@@ -658,6 +671,11 @@ struct Softmax {
         if constexpr (TS) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float4*>(&vf[64 * part + 32 * c + 4 * e]);
+          if (extreme) {
+            const float y = exp2_ftz(rest);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = times(f[e], y);
+          }
         }
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -668,7 +686,7 @@ struct Softmax {
           sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], y);
           if constexpr (TS) {
             const float2 v = e & 2 ? make_float2(f[e / 4].z, f[e / 4].w) : make_float2(f[e / 4].x, f[e / 4].y);
-            y = __fmul2_rn(y, __fmul2_rn(v, make_float2(rel, rel)));
+            y = __fmul2_rn(y, v);
           }
           p[e / 2] = pack<F::kValBf>(y.x, y.y);
         }
@@ -683,7 +701,7 @@ struct Softmax {
       for (int c = NC; c < 4; ++c) tmem_st16(s_at + 16 * ((NC * copy + c) & 3), none);
     }
     sum[0] = __fadd2_rn(sum[0], sum[1]);
-    row.l += TS ? (sum[0].x + sum[0].y) * exp2_ftz(-over) : sum[0].x + sum[0].y;
+    row.l += TS ? (sum[0].x + sum[0].y) * exp2_ftz(-on) : sum[0].x + sum[0].y;
     tmem_wait_st();
     return true;
   }
@@ -727,16 +745,13 @@ struct Softmax {
             v = 0.0f;
           }
           S.scales[tile][count & 1u][0][thread] = scaled(sc, ks);
-          const float lv = log2f(v);
+          const float lv = __log2f(v);  // (decides what the sums are to, not what they are)
           S.scales[tile][count & 1u][1][thread] = lv;
           S.scales[tile][count & 1u][2][thread] = v;
           // a scale of 0 (no token) does not count; one that is not finite makes the range so
-          float2 range = make_float2(v == 0.0f ? INFINITY : lv, lv != lv ? INFINITY : lv);
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            range.x = fminf(range.x, __shfl_xor_sync(0xFFFFFFFFu, range.x, o));
-            range.y = fmaxf(range.y, __shfl_xor_sync(0xFFFFFFFFu, range.y, o));
-          }
+          const int low = __reduce_min_sync(0xFFFFFFFFu, in_order(v == 0.0f ? INFINITY : lv));
+          const int high = __reduce_max_sync(0xFFFFFFFFu, in_order(lv != lv ? INFINITY : lv));
+          const float2 range = make_float2(in_order(low), in_order(high));
           if (lane == 0) S.range[tile][count & 1u][warp] = range;
           sync();
           // the scales of the next tile, the page of the one behind it (of the next unit, where that is known)
@@ -768,7 +783,8 @@ struct Softmax {
       }
       if (threadIdx.x == 0) S.bad_page[(w.number + 8) & 15] = 0;  // (the producers are at most four units ahead)
       if (active) {
-        if (same > 1) finish_copies(w, row, r, same, copy);
+        if (same == 4) finish_copies<4>(w, row, r, copy);
+        else if (same == 2) finish_copies<2>(w, row, r, copy);
         else if (rows) finish(w, row, r, M);
       }
       if (threadIdx.x == 0 && w.begin == 0 && w.end < w.tiles) {
@@ -862,23 +878,31 @@ struct Softmax {
   }
 
   // The same for rows in several copies, joined first: a thread's share is 32 / same channels of each 32 of its row.
-  __device__ __forceinline__ void finish_copies(const Walk<F::kRows>& w, Row& row, int r, int same, int copy) {
-    const int each = kTile / same, at = thread % each, M = w.r.n * a.g;
+  template <int SAME>
+  __device__ __forceinline__ void finish_copies(const Walk<F::kRows>& w, Row& row, int r, int copy) {
+    constexpr int kEach = kTile / SAME, kShare = 32 / SAME;
+    const int at = thread % kEach, M = w.r.n * a.g;
     S.part_ml[0][thread] = row.m;
     S.part_ml[1][thread] = row.l;
-    S.part_ml[2][thread] = TS ? row.to : row.m;
+    if constexpr (TS) S.part_ml[2][thread] = row.to;
     sync();
     const float mine = TS ? row.to : row.m;
-    float m = -INFINITY, to = -INFINITY, l = 0.0f;
-    for (int i = 0; i < same; ++i) {
-      m = fmaxf(m, S.part_ml[0][i * each + at]);
-      to = fmaxf(to, S.part_ml[2][i * each + at]);
+    float m[SAME], l[SAME], top = -INFINITY, to = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < SAME; ++i) {
+      m[i] = S.part_ml[0][i * kEach + at];
+      l[i] = S.part_ml[1][i * kEach + at];
+      top = fmaxf(top, m[i]);
+      if constexpr (TS) to = fmaxf(to, S.part_ml[2][i * kEach + at]);
     }
-    for (int i = 0; i < same; ++i) l += S.part_ml[1][i * each + at] * exp2f(S.part_ml[0][i * each + at] - (m == -INFINITY ? 0.0f : m));
-    row.m = m;
+    row.l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < SAME; ++i) row.l = fmaf(l[i], exp2_ftz(m[i] - (top == -INFINITY ? 0.0f : top)), row.l);
+    row.m = top;
     row.to = to;
-    row.l = bad_page(w) ? NAN : l;
-    const float own = exp2f(mine - (to == -INFINITY ? 0.0f : to));
+    if (!TS) to = top;
+    if (bad_page(w)) row.l = NAN;
+    const float own = exp2_ftz(mine - (to == -INFINITY ? 0.0f : to));
     const bool whole = is_whole(w), live = r < M;
     const float2 f = factors(w, row);
     const long long head = head_of(w, row, r);
@@ -895,23 +919,23 @@ struct Softmax {
 #pragma unroll
       for (int e = 0; e < 32; ++e) S.part[thread][e] = __uint_as_float(x[e]) * own;
       sync();
-      for (int e = copy * (32 / same); live && e < (copy + 1) * (32 / same); e += 8) {
-        float y[8];
+      float y[kShare];
 #pragma unroll
-        for (int d = 0; d < 8; ++d) y[d] = S.part[at][e + d];
-        for (int i = 1; i < same; ++i)
+      for (int d = 0; d < kShare; ++d) y[d] = S.part[at][copy * kShare + d];
 #pragma unroll
-          for (int d = 0; d < 8; ++d) y[d] += S.part[i * each + at][e + d];
-        if (whole) {
-          put_out<8>(row, head, 32 * c + e, y, f);
-        } else {
+      for (int i = 1; i < SAME; ++i)
 #pragma unroll
-          for (int d = 0; d < 8; d += 4)
-            *reinterpret_cast<float4*>(slot + (size_t((32 * c + e + d) / 4) * F::kRows + at) * 4) =
-                make_float4(y[d], y[d + 1], y[d + 2], y[d + 3]);
-        }
+        for (int d = 0; d < kShare; ++d) y[d] += S.part[i * kEach + at][copy * kShare + d];
+      sync();  // the buffer is free again
+      if (!live) continue;
+      if (whole) {
+        put_out<kShare>(row, head, 32 * c + copy * kShare, y, f);
+      } else {
+#pragma unroll
+        for (int d = 0; d < kShare; d += 4)
+          *reinterpret_cast<float4*>(slot + (size_t((32 * c + copy * kShare + d) / 4) * F::kRows + at) * 4) =
+              make_float4(y[d], y[d + 1], y[d + 2], y[d + 3]);
       }
-      sync();
     }
   }
 };
@@ -927,15 +951,14 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
   const uint32_t slots = smem_addr(S.slot), raws = smem_addr(S.raw) + thread * 16;
   constexpr int kHalves = kD * elem_bytes<DT>() / 128;  // 128-byte pieces of a row
   constexpr int kCopies = kN / 4;                       // of a piece of four tokens
-  // Copies not looked at yet, the newest one in the lowest bits: for each the first of the tile's tokens whose value may
-  // be replaced (kTile: none, as for all keys).
+  // 8-bit rows: copies not converted yet, the newest one in the lowest bits: for each the first of the tile's tokens
+  // whose value may be replaced (kTile: none, as for all keys).
   static_assert(F::kLag <= 7);
   uint64_t past = 0;
   int pending = 0;
   uint32_t x = 0;  // copies so far
 
-  // The oldest of them has landed and becomes an operand. (Of 16-bit rows only the drafted values are looked at here;
-  // the others arrive by themselves.)
+  // The oldest of them has landed and becomes an operand.
   auto land = [&](int from, bool value) -> bool {
     const uint32_t y = x - pending, slot = y % F::kSlots, to = slots + slot * kSlotBytes;
     if constexpr (F::kNarrow) {
@@ -975,35 +998,10 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
       } else {
         convert(std::false_type{});
       }
-    } else {
-      constexpr uint32_t kInf = DT == kBf16 ? 0x7F80u : 0x7C00u;
-#pragma unroll 1
-      for (int e = 0; e < 2 * kCopies; ++e) {
-        const int token = kN * warp + 4 * (e >> 1) + (lane >> 3), chunk = 8 * (e & 1) + (lane & 7);
-        if (token < from) continue;
-        const uint32_t at = to + chunk_at(token, chunk);
-        uint4 z = lds16(at);
-        bool any = false;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          uint32_t& v = (&z.x)[d];
-          if ((v & kInf) == kInf) {
-            v &= 0xFFFF0000u;
-            any = true;
-          }
-          if (((v >> 16) & kInf) == kInf) {
-            v &= 0x0000FFFFu;
-            any = true;
-          }
-        }
-        if (any) {
-          sts16(at, z);
-          S.loose = 1;
-        }
-      }
     }
     fence_async_smem();
-    mbar_arrive(&S.full[slot]);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.full[slot]);
     return true;
   };
 
@@ -1021,7 +1019,7 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
   int drafts = kTile;
   [[maybe_unused]] uint32_t q[2][32];
 #pragma unroll 1
-  for (;;) {  // a copy each: keys and values of a tile in turn; then what is left to be looked at
+  for (;;) {  // a copy each: keys and values of a tile in turn; then what is left to be converted
     const int half = int(x & 1u);
     if (more && half == 0) {
       // one row tile: the unit's queries to tensor memory, a row by a thread of the first four warps; on their way while
@@ -1076,25 +1074,27 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
         }
       }
       commit();
-      if (!F::kNarrow && (half == 0 || drafts == kTile)) arrive_landed(&S.full[x % F::kSlots]);
-      past = past << 8 | uint32_t(half == 0 ? kTile : drafts);
+      if constexpr (F::kNarrow) {
+        past = past << 8 | uint32_t(half == 0 ? kTile : drafts);
+        ++pending;
+      } else {
+        arrive_landed(half == 0 || drafts == kTile ? &S.full[x % F::kSlots] : &S.raw_full[x % F::kSlots]);
+      }
       ++x;
-      ++pending;
     }
     // one row tile: the buffer's last queries are those of the unit before the last one, multiplied once all its keys
     // are there: no more than the last unit's and these copies may be left
     const bool first = TILES == 1 && more && half == 1 && k == w.begin;
-    const int most = !more ? 0 : first && last == 1 ? min(F::kLag, 4) : F::kLag;
+    if constexpr (F::kNarrow) {
+      const int most = !more ? 0 : first && last == 1 ? min(F::kLag, 4) : F::kLag;
 #pragma unroll 1
-    while (pending > most) {
-      const int from = int(past >> (8 * (pending - 1))) & 0xFF;
-      if (F::kNarrow || from < kTile) {
+      while (pending > most) {
         if (most == F::kLag) wait_groups<F::kLag>();
         else if (most == 4) wait_groups<4>();
         else wait_groups<0>();
-        if (!land(from, ((x - pending) & 1u) != 0u)) return;
+        if (!land(int(past >> (8 * (pending - 1))) & 0xFF, ((x - pending) & 1u) != 0u)) return;
+        --pending;
       }
-      --pending;
     }
     if (!more) break;
     if constexpr (TILES == 1)
@@ -1120,6 +1120,56 @@ __device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TIL
         page = page_of(w, k);
       }
     }
+  }
+}
+
+// Two warps: drafted values of 16-bit rows that are not finite become 0 before they are multiplied.
+template <int DT, int QT, int TILES, bool TS>
+__device__ __forceinline__ void check_values(const TreeArgs& a, Smem<Form<DT, QT, TILES, TS>>& S,
+                                             Walk<Form<DT, QT, TILES, TS>::kRows> w, long long s0, long long e0) {
+  using F = Form<DT, QT, TILES, TS>;
+  const int thread = int(threadIdx.x) - (F::kMmaWarp + 1) * 32;
+  constexpr uint32_t kInf = DT == kBf16 ? 0x7F80u : 0x7C00u;
+  uint32_t x = 0, phases = 0;  // copies so far; the parity of each slot's next check
+  for (bool more = true; more; more = w.next(a, s0, e0)) {
+    const int k0 = max(w.begin, min(w.end, w.r.P / kTile));  // the first tile with drafted tokens
+    for (int k = k0; k < w.end; ++k) {
+      const uint32_t slot = (x + 2 * (k - w.begin) + 1) % F::kSlots, at = smem_addr(S.slot) + slot * kSlotBytes;
+      const int from = max(0, min(kTile, w.r.P - k * kTile)), to = min(kTile, w.tokens - k * kTile);
+      if (!mbar_wait(&S.raw_full[slot], (phases >> slot) & 1u, &S.abort)) return;
+      phases ^= 1u << slot;
+      // a token's 16 chunks by 16 threads: two of each 128 bytes, in their swizzled order
+#pragma unroll 4
+      for (int token = from + thread / 8; token < to; token += F::kCheckers / 8) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t p = at + half * (kSlotBytes / 2) + token * 128 + (thread & 7) * 16;
+          uint4 z = lds16(p);
+          bool any = false;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            uint32_t& v = (&z.x)[d];
+            if ((v & kInf) == kInf) {
+              v &= 0xFFFF0000u;
+              any = true;
+            }
+            if (((v >> 16) & kInf) == kInf) {
+              v &= 0x0000FFFFu;
+              any = true;
+            }
+          }
+          if (any) {
+            sts16(p, z);
+            S.loose = 1;
+          }
+        }
+      }
+      fence_async_smem();
+      asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(&S.full[slot])),
+                   "r"(F::kProducers / F::kCheckers)
+                   : "memory");
+    }
+    x += 2 * (w.end - w.begin);
   }
 }
 
@@ -1231,7 +1281,8 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
     reinterpret_cast<Rec*>(a.ws)[blockIdx.x] = Rec{0, 0, 0, 0};
     reinterpret_cast<int*>(a.ws + loose_offset(gridDim.x))[blockIdx.x] = 0;
     for (int i = 0; i < F::kSlots; ++i) {
-      mbar_init(&S.full[i], F::kProducers);
+      mbar_init(&S.full[i], F::kNarrow ? F::kProducerWarps : F::kProducers);
+      mbar_init(&S.raw_full[i], F::kProducers);
       mbar_init(&S.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -1307,6 +1358,8 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
       int never = 0;
       mbar_wait(&S.drain, 0, &never);
     }
+    if constexpr (F::kCheckers > 0)
+      if (warp > F::kMmaWarp && warp <= F::kMmaWarp + F::kCheckers / 32) check_values<DT, QT, TILES, TS>(a, S, w, s0, e0);
   }
   __syncwarp();
   tc_fence_before();
