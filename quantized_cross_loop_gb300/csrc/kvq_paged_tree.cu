@@ -20,9 +20,11 @@
 //             rescaled only when its maximum grows by more than 2^8 (its weights then
 //             go to at most 1, or 2^15 for FP16, by kShift)
 //   producers four: 16-byte asynchronous copies of K and V rows into a ring of
-//             operand slots; 8-bit rows by way of a staging ring and a conversion
+//             operand slots; 8-bit rows by way of registers and a conversion (one row
+//             tile: two groups of four, which take the tiles in turn)
 //   MMA       one, a lane of which issues all products
-//   checkers  two, for drafted values of 16-bit rows (below)
+//   checkers  two, for drafted values of 16-bit rows (below); or one that looks up the
+//             scales of a tile's tokens
 // Exactness: products of 16-bit values are exact, sums FP32. 8-bit keys become 16-bit
 // of the queries' type (exact), 8-bit values BF16 (exact). A weight is one 16-bit
 // number (times its value's scale, where tokens have one): BF16, whose range holds
@@ -47,6 +49,7 @@ namespace paged {
 namespace {
 
 constexpr int kTile = 128;       // tokens of a tile, rows of a row tile
+constexpr int kScaleRing = 4;    // tiles whose scales are there at a time
 constexpr int kUnitCost = 1;     // tiles that the end of a unit takes as long as
 constexpr int kSlotBytes = kTile * kD * 2;
 constexpr int kRawBytes = kTile * kD;
@@ -67,22 +70,23 @@ struct Form {
   static constexpr float kShift = kValBf ? -kSlack : 15.0f - kSlack;
   static constexpr int kRows = kTile * TILES;
   static constexpr int kSoftmaxWarps = 4 * TILES;
-  // (8-bit rows: the conversion is what bounds one row tile)
-  static constexpr int kProducerWarps = kNarrow && TILES == 1 ? 8 : 4;
-  static constexpr int kProducers = 32 * kProducerWarps;
-  static constexpr int kTokens = kTile / kProducerWarps;  // of a tile, a producer warp's
+  // groups of four producer warps, which take the tiles in turn: 8-bit rows are copied, converted and stored by the same
+  // threads, one after the other, and two groups do it side by side (64 requests of one token 295 us by eight warps
+  // together)
+  static constexpr int kGroups = kNarrow && TILES == 1 ? 2 : 1;
+  static constexpr int kProducerWarps = 4 * kGroups;
+  static constexpr int kProducers = 128;  // threads of a group
   static constexpr int kMmaWarp = kSoftmaxWarps + kProducerWarps;
   static constexpr int kThreads = (kMmaWarp + 4) * 32;  // (registers are shared out by four warps)
   // registers of the softmax, producer and MMA warps, by four of which they come to 3 x 168 or 4 x 128 of the launch
-  static constexpr int kSoftmaxRegs = kThreads == 384 ? 224 : TILES == 1 ? 168 : 144;
-  static constexpr int kProducerRegs = kThreads == 384 ? 152 : TILES == 1 ? 120 : 112;
-  static constexpr int kMmaRegs = kThreads == 384 ? 128 : TILES == 1 ? 104 : 112;
+  static constexpr int kSoftmaxRegs = kThreads == 384 ? 224 : TILES == 1 ? 176 : 144;
+  static constexpr int kProducerRegs = kThreads == 384 ? 152 : 112;
+  static constexpr int kMmaRegs = kThreads == 384 ? 128 : 112;
   static_assert(kSoftmaxRegs * TILES + kProducerRegs * kProducerWarps / 4 + kMmaRegs == (kThreads == 384 ? 504 : 512));
   // One row tile: the queries are in tensor memory, two units' (A of the products); two fill it with sums and scores.
   static constexpr int kQueries = TILES == 1 ? 0 : kRows;
-  static constexpr int kSlots = kNarrow ? 3 : (TILES == 1 ? 6 : 5);
-  static constexpr int kStages = kNarrow ? (TILES == 1 ? 6 : 3) : 0;  // of raw 8-bit rows
-  static constexpr int kLag = kNarrow ? kStages - 1 : 0;  // 8-bit rows: slots between a copy and its conversion
+  static constexpr int kSlots = kNarrow ? (TILES == 1 ? 4 : 3) : TILES == 1 ? 6 : 5;
+  static constexpr int kStages = kNarrow ? (TILES == 1 ? 2 : 3) : 0;  // a group's 8-bit rows as they come
   static constexpr int kCheckers = kNarrow ? 0 : 64;      // threads (two warps behind the MMA warp) that check drafted values
 };
 
@@ -93,9 +97,12 @@ struct Smem {
     Prefix<F::kThreads> prefix;  // before the first copy
   };
   char q[F::kQueries > 0 ? F::kQueries * kD * 2 : 16];
-  char raw[F::kStages > 0 ? F::kStages : 1][F::kStages > 0 ? kRawBytes : 16];
-  float scales[F::kSoftmaxWarps / 4][2][3][F::kNarrow ? kTile : 4];  // row tile, parity, (keys', log2 of and values'), token
-  float2 range[F::kSoftmaxWarps / 4][2][4];  // of the values' scales' logarithms: by a warp's 32 tokens
+  char raw[F::kStages > 0 ? F::kGroups * F::kStages : 1][F::kStages > 0 ? kRawBytes : 16];
+  // scales of a tile's tokens: the keys' (into log2 units), the logarithms of the values', the values'; and the smallest
+  // and largest of those logarithms
+  float scales[F::kNarrow ? kScaleRing : 1][3][F::kNarrow ? kTile : 4];
+  float2 range[kScaleRing];
+  unsigned long long scales_full[kScaleRing], scales_free[kScaleRing];
   // one row tile: what its copies of the rows are joined by
   float part[F::kQueries > 0 ? 1 : kTile][33];
   float part_ml[3][F::kQueries > 0 ? 1 : kTile];
@@ -490,22 +497,6 @@ struct Softmax {
     if (lane == 0) mbar_arrive(&S.q_full[0]);
   }
 
-  // Scales of this thread's token of a tile, in two steps: the page of the pool (-1: none), the scales.
-  struct Token {
-    int page, t, h;
-  };
-  __device__ __forceinline__ Token look_up(const Walk<F::kRows>& w, int k) const {
-    const int t = k * kTile + thread;
-    return Token{t < w.tokens ? a.table[(long long)w.b * a.max_pages + a.c.ps.div(t)] : -1, t, w.h};
-  }
-  __device__ __forceinline__ void fetch(const Token& n, float& ks, float& vs) const {
-    ks = vs = 0.0f;
-    if (n.page < 0 || n.page >= a.c.n_pages) return;
-    const long long at = ((long long)n.page * a.c.H + n.h) * int(a.c.ps.d) + (n.t - a.c.ps.div(n.t) * int(a.c.ps.d));
-    ks = a.c.k_scale[at];
-    vs = a.c.v_scale[at];
-  }
-
   // Waits for the sums of the row tile's c-th product. (One row tile: that and the one before it may both be under way,
   // and a wait tells only odd phases from even ones: they take turns at two barriers.)
   __device__ __forceinline__ bool summed(uint32_t c) const {
@@ -527,12 +518,13 @@ struct Softmax {
   // them (for the other columns 0), the row's sums follow. Scores of up to 64 columns are held in registers; of 128 they
   // are read twice, for their maximum and for the weights, scaled ones (TS) from where the first reading left them.
   template <int NC>
-  __device__ __forceinline__ bool weigh(Row& row, int k, int begin, uint32_t count, uint32_t s_at, int copy, float sc) {
+  __device__ __forceinline__ bool weigh(Row& row, int k, int begin, uint32_t count, uint32_t all, uint32_t s_at, int copy,
+                                        float sc) {
     constexpr int kC = NC > 2 ? 2 : NC, kReads = NC / kC;
     const bool drafted = (k + 1) * kTile > row.P;
-    [[maybe_unused]] const float* kf = S.scales[tile][count & 1u][0] + 32 * NC * copy;
-    [[maybe_unused]] const float* lv = S.scales[tile][count & 1u][1] + 32 * NC * copy;
-    [[maybe_unused]] const float* vf = S.scales[tile][count & 1u][2] + 32 * NC * copy;
+    [[maybe_unused]] const float* kf = S.scales[all % kScaleRing][0] + 32 * NC * copy;
+    [[maybe_unused]] const float* lv = S.scales[all % kScaleRing][1] + 32 * NC * copy;
+    [[maybe_unused]] const float* vf = S.scales[all % kScaleRing][2] + 32 * NC * copy;
     const uint32_t x_at = s_at + 32u * NC * copy, p_at = s_at + 16u * NC * copy;
     uint32_t x[kC][32];
     auto pair = [&](int c, int e) { return make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])); };
@@ -565,13 +557,9 @@ struct Softmax {
     bool far = false;
     float high = -INFINITY;
     if constexpr (TS) {
-      float low = INFINITY;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 y = S.range[tile][count & 1u][i];
-        low = fminf(low, y.x);
-        high = fmaxf(high, y.y);
-      }
+      const float2 range = S.range[all % kScaleRing];
+      const float low = range.x;
+      high = range.y;
       far = high - low > 8.0f;
     }
 #pragma unroll
@@ -709,9 +697,7 @@ struct Softmax {
   __device__ __forceinline__ void run(Walk<F::kRows> w, long long s0, long long e0, long long W, int C) {
     uint32_t count = 0;  // tiles of this thread's row tile so far
     uint32_t units = 0;
-    [[maybe_unused]] Token ahead{-1, 0, 0};  // of the tile after the next one
-    [[maybe_unused]] float ks = 0.0f, vs = 0.0f;
-    [[maybe_unused]] bool fetched = false, looked = false;  // the next tile's scales, and the page of the one behind
+    [[maybe_unused]] uint32_t all = 0;  // tiles so far, with those of units without rows for this row tile
     bool more = true;
     while (more) {
       if constexpr (TILES == 2) load_queries(w);
@@ -729,55 +715,34 @@ struct Softmax {
       float sc = a.scale * kLog2e;
       if constexpr (DT == kE4m3 && !TS)
         if (a.c.k_scale != nullptr) sc = scaled(sc, a.c.k_scale[w.h]);
-      if constexpr (TS)
-        if (active && !fetched) {
-          fetch(look_up(w, w.begin), ks, vs);
-          looked = false;
-        }
       for (int k = w.begin; active && k < w.end; ++k, ++count) {
-        const int t0 = k * kTile;
         const uint32_t buf = TILES == 1 ? count & 1u : uint32_t(tile), phase = TILES == 1 ? (count >> 1) & 1u : count & 1u;
         const uint32_t s_at = lanes + kColS + 128u * buf;
-        if constexpr (TS) {
-          float v = vs;
-          if (t0 + thread >= w.r.P && !isfinite(v)) {
-            S.loose = 1;
-            v = 0.0f;
-          }
-          S.scales[tile][count & 1u][0][thread] = scaled(sc, ks);
-          const float lv = __log2f(v);  // (decides what the sums are to, not what they are)
-          S.scales[tile][count & 1u][1][thread] = lv;
-          S.scales[tile][count & 1u][2][thread] = v;
-          // a scale of 0 (no token) does not count; one that is not finite makes the range so
-          const int low = __reduce_min_sync(0xFFFFFFFFu, in_order(v == 0.0f ? INFINITY : lv));
-          const int high = __reduce_max_sync(0xFFFFFFFFu, in_order(lv != lv ? INFINITY : lv));
-          const float2 range = make_float2(in_order(low), in_order(high));
-          if (lane == 0) S.range[tile][count & 1u][warp] = range;
-          sync();
-          // the scales of the next tile, the page of the one behind it (of the next unit, where that is known)
-          const bool here = k + 1 < w.end, any = here || (TILES == 1 && more);
-          fetched = any;
-          if (any) {
-            if (!looked) ahead = here ? look_up(w, k + 1) : look_up(next, next.begin);
-            fetch(ahead, ks, vs);
-          }
-          const int on = k + 2 - w.end;  // tiles into the next unit
-          looked = on < 0 || (TILES == 1 && more && next.begin + on < next.end);
-          if (looked) ahead = on < 0 ? look_up(w, k + 2) : look_up(next, next.begin + on);
-        }
+        if constexpr (TS)
+          if (!mbar_wait(&S.scales_full[all % kScaleRing], (all / kScaleRing) & 1u, &S.abort)) return;
         if (!mbar_wait(&S.s_full[buf], phase, &S.abort)) return;
         tc_fence_after();
         if (rows) {
           bool ok;
-          if (same == 4) ok = weigh<1>(row, k, w.begin, count, s_at, copy, sc);
-          else if (same == 2) ok = weigh<2>(row, k, w.begin, count, s_at, copy, sc);
-          else ok = weigh<4>(row, k, w.begin, count, s_at, 0, sc);
+          if (same == 4) ok = weigh<1>(row, k, w.begin, count, all, s_at, copy, sc);
+          else if (same == 2) ok = weigh<2>(row, k, w.begin, count, all, s_at, copy, sc);
+          else ok = weigh<4>(row, k, w.begin, count, all, s_at, 0, sc);
           if (!ok) return;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_ready[buf]);
+        if (lane == 0) {
+          mbar_arrive(&S.p_ready[buf]);
+          if constexpr (TS) mbar_arrive(&S.scales_free[all % kScaleRing]);
+        }
+        if constexpr (TS) ++all;
       }
+      if constexpr (TS && TILES == 2)
+        if (!active)
+          for (int k = w.begin; k < w.end; ++k, ++all) {  // (the ring's places are free when all warps have passed them)
+            if (!mbar_wait(&S.scales_full[all % kScaleRing], (all / kScaleRing) & 1u, &S.abort)) return;
+            if (lane == 0) mbar_arrive(&S.scales_free[all % kScaleRing]);
+          }
       if (active) {
         if (!summed(count - 1)) return;
       }
@@ -942,184 +907,313 @@ struct Softmax {
 
 // ---------------------------------------------------------------- producers
 
-template <int DT, int QT, int TILES, bool TS>
-__device__ __forceinline__ void produce(const TreeArgs& a, Smem<Form<DT, QT, TILES, TS>>& S,
-                                        Walk<Form<DT, QT, TILES, TS>::kRows> w, long long s0, long long e0) {
-  using F = Form<DT, QT, TILES, TS>;
-  constexpr int kN = F::kTokens;  // of a tile, this warp's
-  const int thread = int(threadIdx.x) - F::kSoftmaxWarps * 32, warp = thread >> 5, lane = thread & 31;
-  const uint32_t slots = smem_addr(S.slot), raws = smem_addr(S.raw) + thread * 16;
-  constexpr int kHalves = kD * elem_bytes<DT>() / 128;  // 128-byte pieces of a row
-  constexpr int kCopies = kN / 4;                       // of a piece of four tokens
-  // 8-bit rows: copies not converted yet, the newest one in the lowest bits: for each the first of the tile's tokens
-  // whose value may be replaced (kTile: none, as for all keys).
-  static_assert(F::kLag <= 7);
-  uint64_t past = 0;
-  int pending = 0;
-  uint32_t x = 0;  // copies so far
-
-  // The oldest of them has landed and becomes an operand.
-  auto land = [&](int from, bool value) -> bool {
-    const uint32_t y = x - pending, slot = y % F::kSlots, to = slots + slot * kSlotBytes;
-    if constexpr (F::kNarrow) {
-      if (!mbar_wait(&S.empty[slot], (y / F::kSlots + 1) & 1u, &S.abort)) return false;
-      const uint32_t raw = raws + (y % F::kStages) * kRawBytes;
-      uint4 z[kCopies];  // 16 channels of a token each
-#pragma unroll
-      for (int i = 0; i < kCopies; ++i) z[i] = lds16(raw + i * (F::kProducers * 16));
-      if (from < kTile) {  // drafted tokens: NaN is replaced by 0
-        uint32_t any = 0u;
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-          if (kN * warp + 4 * i + (lane >> 3) < from) continue;
-#pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const uint32_t nan = (((&z[i].x)[d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes of 0x7F or 0xFF
-            (&z[i].x)[d] &= ~((nan >> 7) * 255u);
-            any |= nan;
-          }
-        }
-        if (any != 0u) S.loose = 1;
-      }
-      auto convert = [&](auto bf) {
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-          const int token = kN * warp + 4 * i + (lane >> 3), chunk = 2 * (lane & 7);
-          uint2 v[4];
-#pragma unroll
-          for (int d = 0; d < 4; ++d) v[d] = widen<decltype(bf)::value>((&z[i].x)[d]);
-          sts16(to + chunk_at(token, chunk), make_uint4(v[0].x, v[0].y, v[1].x, v[1].y));
-          sts16(to + chunk_at(token, chunk + 1), make_uint4(v[2].x, v[2].y, v[3].x, v[3].y));
-        }
-      };
-      if constexpr (F::kKeyBf) {
-        if (value) convert(std::bool_constant<F::kValBf>{});
-        else convert(std::bool_constant<F::kKeyBf>{});
-      } else {
-        convert(std::false_type{});
-      }
-    }
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.full[slot]);
-    return true;
-  };
-
-  // The pool's row of this lane's token of a tile: page of the pool (looked up a tile ahead)
-  auto page_of = [&](const Walk<F::kRows>& u, int k) {
-    const int t = k * kTile + kN * warp + (lane & (kN - 1));
-    return t < u.tokens ? a.table[(long long)u.b * a.max_pages + a.c.ps.div(t)] : -2;  // -2: no token
-  };
-  int page = page_of(w, w.begin);
+// What a group of producer warps goes through: every kGroups-th tile of the range.
+template <class F>
+struct Tiles {
+  const TreeArgs& a;
+  Smem<F>& S;
+  const long long s0, e0;
+  Walk<F::kRows> w;
+  const int group, thread, warp, lane;
   uint32_t units = 0;
-  int last = 0;  // tiles of the unit before
-  int k = w.begin;
+  int k;
   bool more = true;
-  long long off = -1;
-  int drafts = kTile;
+  int page;       // of the pool, of the lane's token (32 warp + lane) of the tile (looked up a tile ahead)
+  long long off;  // of that token's row in the pools, or -1
+  int drafts;     // the first drafted token of the tile
+
+  __device__ __forceinline__ Tiles(const TreeArgs& args, Smem<F>& s, const Walk<F::kRows>& walk, long long from, long long to)
+      : a(args), S(s), s0(from), e0(to), w(walk), group((int(threadIdx.x) - F::kSoftmaxWarps * 32) / F::kProducers),
+        thread((int(threadIdx.x) - F::kSoftmaxWarps * 32) % F::kProducers), warp(thread >> 5), lane(thread & 31),
+        k(walk.begin) {
+    if (F::kGroups > 1 && group == 1) step();
+    if (!more) return;
+    page = page_of(k);
+    place();
+  }
+  __device__ __forceinline__ void step() {
+    if (!more || ++k < w.end) return;
+    ++units;
+    more = w.next(a, s0, e0);
+    if (more) k = w.begin;
+  }
+  __device__ __forceinline__ int page_of(int tile) const {
+    const int t = tile * kTile + 32 * warp + lane;
+    return t < w.tokens ? a.table[(long long)w.b * a.max_pages + a.c.ps.div(t)] : -2;  // -2: no token
+  }
+  __device__ __forceinline__ void place() {
+    const int t = k * kTile + 32 * warp + lane;
+    off = -1;
+    if (page >= 0 && page < a.c.n_pages) {
+      const int at = t - a.c.ps.div(t) * int(a.c.ps.d);
+      off = (long long)page * a.c.page_stride + (long long)at * a.c.token_stride + (long long)w.h * a.c.head_stride;
+    } else if (page != -2 || t < w.tokens) {
+      flag(a.c, KVQ_PAGED_ERR_PAGE);
+      S.bad_page[w.number & 15] = 1;
+    }
+    if (k + F::kGroups < w.end) page = page_of(k + F::kGroups);
+    drafts = max(0, min(kTile, w.r.P - k * kTile));
+  }
+  // On to the group's next tile.
+  __device__ __forceinline__ void next() {
+    const uint32_t before = units;
+#pragma unroll 1
+    for (int i = 0; i < F::kGroups; ++i) step();
+    if (!more) return;
+    if (before != units) page = page_of(k);
+    place();
+  }
+  // One row tile: the unit's queries to tensor memory, a row by a thread of the group that has its first tile. N words
+  // of the row from `at` on.
+  template <int N>
+  __device__ __forceinline__ void load_queries(uint32_t (&q)[N], int at) const {
+    const int M = w.r.n * a.g, r = w.rb * F::kRows + thread % (kTile / copies(M));
+    const bool live = r < M;
+    const int i = r / a.g;
+    const char* from =
+        a.q + (live ? (w.r.row0 + i) * a.q_stride + (long long)(w.h * a.g + (r - i * a.g)) * (kD * 2) + 4 * at : 0);
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      uint4 y = make_uint4(0u, 0u, 0u, 0u);
+      if (live) y = *reinterpret_cast<const uint4*>(from + 4 * e);
+      q[e] = y.x;
+      q[e + 1] = y.y;
+      q[e + 2] = y.z;
+      q[e + 3] = y.w;
+    }
+  }
+  // The buffer's last queries are those of the unit before the last one, multiplied once all its keys are there.
+  __device__ __forceinline__ bool wait_queries() const {
+    return mbar_wait(&S.q_free[units & 1u], ((units >> 1) + 1) & 1u, &S.abort);
+  }
+  __device__ __forceinline__ uint32_t queries_at() const {
+    return S.tmem + (uint32_t(warp) << 21) + kColQ + 64u * (units & 1u);
+  }
+  __device__ __forceinline__ void queries_stored() const {
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.q_full[units & 1u]);
+  }
+};
+
+// 16-bit rows: asynchronous copies, which arrive by themselves.
+template <class F, bool QUERIES>
+__device__ __forceinline__ void produce(Tiles<F>& T) {
+  const TreeArgs& a = T.a;
+  Smem<F>& S = T.S;
+  const uint32_t slots = smem_addr(S.slot);
+  uint32_t x = 0;  // copies so far: K and V of a tile, then of the next one
   [[maybe_unused]] uint32_t q[2][32];
 #pragma unroll 1
-  for (;;) {  // a copy each: keys and values of a tile in turn; then what is left to be converted
-    const int half = int(x & 1u);
-    if (more && half == 0) {
-      // one row tile: the unit's queries to tensor memory, a row by a thread of the first four warps; on their way while
-      // the first tile's copies are issued
-      if constexpr (TILES == 1)
-        if (k == w.begin) {
-          const int M = w.r.n * a.g, r = w.rb * F::kRows + thread % (kTile / copies(M));
-          const bool live = thread < kTile && r < M;
-          const int i = r / a.g;
-          const char* from =
-              a.q + (live ? (w.r.row0 + i) * a.q_stride + (long long)(w.h * a.g + (r - i * a.g)) * (kD * 2) : 0);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            uint4 y = make_uint4(0u, 0u, 0u, 0u);
-            if (live) y = *reinterpret_cast<const uint4*>(from + 16 * e);
-            q[e >> 3][4 * (e & 7)] = y.x;
-            q[e >> 3][4 * (e & 7) + 1] = y.y;
-            q[e >> 3][4 * (e & 7) + 2] = y.z;
-            q[e >> 3][4 * (e & 7) + 3] = y.w;
-          }
-        }
-      const int t = k * kTile + kN * warp + (lane & (kN - 1));
-      off = -1;
-      if (page >= 0 && page < a.c.n_pages) {
-        const int place = t - a.c.ps.div(t) * int(a.c.ps.d);
-        off = (long long)page * a.c.page_stride + (long long)place * a.c.token_stride + (long long)w.h * a.c.head_stride;
-      } else if (page != -2 || t < w.tokens) {
-        flag(a.c, KVQ_PAGED_ERR_PAGE);
-        S.bad_page[w.number & 15] = 1;
-      }
-      if (k + 1 < w.end) page = page_of(w, k + 1);
-      drafts = max(0, min(kTile, w.r.P - k * kTile));
-    }
-    if (more) {
-      const char* pool = half == 0 ? a.c.k : a.c.v;
-      uint32_t to = 0;
-      if constexpr (!F::kNarrow) {
-        if (!mbar_wait(&S.empty[x % F::kSlots], (x / F::kSlots + 1) & 1u, &S.abort)) return;
-        to = slots + (x % F::kSlots) * kSlotBytes;
-      } else {
-        to = raws + (x % F::kStages) * kRawBytes;
-      }
-#pragma unroll
-      for (int e = 0; e < kCopies; ++e) {
-        const long long y = __shfl_sync(0xFFFFFFFFu, off, 4 * e + (lane >> 3));
-#pragma unroll
-        for (int f = 0; f < kHalves; ++f) {
-          const int chunk = 8 * f + (lane & 7);
-          const uint32_t at =
-              F::kNarrow ? to + e * (F::kProducers * 16) : to + chunk_at(kN * warp + 4 * e + (lane >> 3), chunk);
-          copy16(at, pool + (y < 0 ? 0 : y) + chunk * 16, y >= 0);
-        }
-      }
-      commit();
-      if constexpr (F::kNarrow) {
-        past = past << 8 | uint32_t(half == 0 ? kTile : drafts);
-        ++pending;
-      } else {
-        arrive_landed(half == 0 || drafts == kTile ? &S.full[x % F::kSlots] : &S.raw_full[x % F::kSlots]);
-      }
-      ++x;
-    }
-    // one row tile: the buffer's last queries are those of the unit before the last one, multiplied once all its keys
-    // are there: no more than the last unit's and these copies may be left
-    const bool first = TILES == 1 && more && half == 1 && k == w.begin;
-    if constexpr (F::kNarrow) {
-      const int most = !more ? 0 : first && last == 1 ? min(F::kLag, 4) : F::kLag;
+  while (T.more) {
+    if constexpr (QUERIES)
+      if (T.k == T.w.begin) {
+        T.load_queries(q[0], 0);
+        T.load_queries(q[1], 32);
+      }  // (on their way while the tile's copies are issued)
 #pragma unroll 1
-      while (pending > most) {
-        if (most == F::kLag) wait_groups<F::kLag>();
-        else if (most == 4) wait_groups<4>();
-        else wait_groups<0>();
-        if (!land(int(past >> (8 * (pending - 1))) & 0xFF, ((x - pending) & 1u) != 0u)) return;
-        --pending;
-      }
-    }
-    if (!more) break;
-    if constexpr (TILES == 1)
-      if (first) {
-        if (!mbar_wait(&S.q_free[units & 1u], ((units >> 1) + 1) & 1u, &S.abort)) return;
-        if (thread < kTile) {
-          tc_fence_after();
-          const uint32_t at = S.tmem + (uint32_t(warp) << 21) + kColQ + 64u * (units & 1u);
-          tmem_st(at, q[0]);
-          tmem_st(at + 32, q[1]);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.q_full[units & 1u]);
+    for (int half = 0; half < 2; ++half, ++x) {
+      const char* pool = half == 0 ? a.c.k : a.c.v;
+      const uint32_t slot = x % F::kSlots, to = slots + slot * kSlotBytes;
+      if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const long long y = __shfl_sync(0xFFFFFFFFu, T.off, 4 * e + (T.lane >> 3));
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int chunk = 8 * f + (T.lane & 7);
+          copy16(to + chunk_at(32 * T.warp + 4 * e + (T.lane >> 3), chunk), pool + (y < 0 ? 0 : y) + chunk * 16, y >= 0);
         }
       }
-    if (half == 1 && ++k == w.end) {
-      last = w.end - w.begin;
-      ++units;
-      more = w.next(a, s0, e0);
-      if (more) {
-        k = w.begin;
-        page = page_of(w, k);
+      arrive_landed(half == 0 || T.drafts == kTile ? &S.full[slot] : &S.raw_full[slot]);
+    }
+    if constexpr (QUERIES)
+      if (T.k == T.w.begin) {
+        if (!T.wait_queries()) return;
+        tc_fence_after();
+        tmem_st(T.queries_at(), q[0]);
+        tmem_st(T.queries_at() + 32, q[1]);
+        T.queries_stored();
+      }
+    T.next();
+  }
+}
+
+// 16 E4M3 channels each of tokens `token`, `token` + 4, ... as two chunks of an operand.
+template <bool BF, int N>
+__device__ __forceinline__ void convert(const uint4 (&z)[N], uint32_t to, int token, int chunk) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint2 v[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) v[d] = widen<BF>((&z[i].x)[d]);
+    sts16(to + chunk_at(token + 4 * i, chunk), make_uint4(v[0].x, v[0].y, v[1].x, v[1].y));
+    sts16(to + chunk_at(token + 4 * i, chunk + 1), make_uint4(v[2].x, v[2].y, v[3].x, v[3].y));
+  }
+}
+
+// 8-bit rows: asynchronous copies into a ring of their own, each thread's to be converted by itself. (Loaded into
+// registers they left room for two slots more, but the fence behind a conversion then waited for the next loads: 64
+// requests of one token with scales per token 308 us.)
+template <class F, bool QUERIES>
+__device__ __forceinline__ void produce_narrow(Tiles<F>& T) {
+  const TreeArgs& a = T.a;
+  Smem<F>& S = T.S;
+  constexpr int kLag = F::kStages - 1;  // copies between a copy and its conversion
+  const uint32_t slots = smem_addr(S.slot), raws = smem_addr(S.raw) + T.group * (F::kStages * kRawBytes) + T.thread * 16;
+  uint32_t mine = 0;  // the group's copies so far: K and V of a tile, then of its next one
+  // Copies not converted yet, the newest one in the lowest bits: for each the first of the tile's tokens whose value may
+  // be replaced (kTile: none, as for all keys).
+  uint32_t past = 0;
+  int pending = 0;
+  // The oldest copy has landed and becomes an operand.
+  auto land = [&]() -> bool {
+    const uint32_t y = mine - pending, x = F::kGroups > 1 ? 4 * (y >> 1) + 2 * T.group + (y & 1u) : y;  // (x: of all)
+    const uint32_t slot = x % F::kSlots, to = slots + slot * kSlotBytes, raw = raws + (y % F::kStages) * kRawBytes;
+    const int from = int(past >> (8 * (pending - 1))) & 0xFF;
+    uint4 z[8];  // 16 channels of a token each
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = lds16(raw + i * (F::kProducers * 16));
+    if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return false;
+    const int token = 32 * T.warp + (T.lane >> 3), chunk = 2 * (T.lane & 7);
+    if (from < kTile) {  // drafted values: NaN becomes 0
+      uint32_t any = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (token + 4 * i < from) continue;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          uint32_t& v = (&z[i].x)[d];
+          const uint32_t nan = ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes of 0x7F or 0xFF
+          v &= ~((nan >> 7) * 255u);
+          any |= nan;
+        }
+      }
+      if (any != 0u) S.loose = 1;
+    }
+    if (F::kKeyBf && (y & 1u) == 0u) convert<true>(z, to, token, chunk);
+    else convert<false>(z, to, token, chunk);
+    fence_async_smem();
+    __syncwarp();
+    if (T.lane == 0) mbar_arrive(&S.full[slot]);
+    --pending;
+    return true;
+  };
+#pragma unroll 1
+  for (;;) {
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      if (T.more) {
+        const char* pool = half == 0 ? a.c.k : a.c.v;
+        const uint32_t to = raws + (mine % F::kStages) * kRawBytes;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const long long y = __shfl_sync(0xFFFFFFFFu, T.off, 4 * e + (T.lane >> 3));
+          copy16(to + e * (F::kProducers * 16), pool + (y < 0 ? 0 : y) + (T.lane & 7) * 16, y >= 0);
+        }
+        commit();
+        past = past << 8 | uint32_t(half == 0 ? kTile : T.drafts);
+        ++mine;
+        ++pending;
+      }
+#pragma unroll 1
+      while (pending > (T.more ? kLag : 0)) {
+        if (T.more) wait_groups<kLag>();
+        else wait_groups<0>();
+        if (!land()) return;
       }
     }
+    if (!T.more) break;
+    if constexpr (QUERIES)
+      if (T.k == T.w.begin) {
+        if (!T.wait_queries()) return;  // (of the copies before it the group has none left)
+        tc_fence_after();
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {  // (not loaded ahead: beside the conversion there are no registers)
+          uint32_t q[16];
+          T.load_queries(q, 16 * i);
+          tmem_st16(T.queries_at() + 16 * i, q);
+        }
+        T.queries_stored();
+      }
+    T.next();
+  }
+}
+
+// One warp: the scales of the tiles' tokens (8-bit rows with a scale per token), four tokens a lane, looked up in two
+// steps one and two tiles ahead.
+template <class F>
+__device__ __forceinline__ void load_scales(const TreeArgs& a, Smem<F>& S, Walk<F::kRows> w, long long s0, long long e0) {
+  const int lane = threadIdx.x & 31;
+  const float sc = a.scale * kLog2e;
+  struct Tile {
+    int t0, P, h;
+    bool there;
+  };
+  int k = w.begin;
+  bool more = true;
+  int page[4];  // of the pool, -1: no token
+  float ks[4], vs[4];
+  auto look_up = [&]() -> Tile {
+    if (!more) return Tile{0, 0, 0, false};
+    const Tile t{k * kTile, w.r.P, w.h, true};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = t.t0 + 4 * lane + i;
+      page[i] = at < w.tokens ? a.table[(long long)w.b * a.max_pages + a.c.ps.div(at)] : -1;
+    }
+    if (++k == w.end) {
+      more = w.next(a, s0, e0);
+      if (more) k = w.begin;
+    }
+    return t;
+  };
+  auto fetch = [&](const Tile& t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ks[i] = vs[i] = 0.0f;
+      if (!t.there || page[i] < 0 || page[i] >= a.c.n_pages) continue;
+      const int at = t.t0 + 4 * lane + i;
+      const long long x = ((long long)page[i] * a.c.H + t.h) * int(a.c.ps.d) + (at - a.c.ps.div(at) * int(a.c.ps.d));
+      ks[i] = a.c.k_scale[x];
+      vs[i] = a.c.v_scale[x];
+    }
+  };
+  Tile now = look_up();
+  fetch(now);
+  Tile next = look_up();
+  for (uint32_t c = 0; now.there; ++c) {
+    const uint32_t at = c % kScaleRing;
+    if (!mbar_wait(&S.scales_free[at], (c / kScaleRing + 1) & 1u, &S.abort)) return;
+    float4 f, l, v;
+    float low = INFINITY, high = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x = vs[i];
+      if (now.t0 + 4 * lane + i >= now.P && !isfinite(x)) {  // a drafted token's: as its values that are not finite
+        S.loose = 1;
+        x = 0.0f;
+      }
+      const float y = __log2f(x);  // (decides what the sums are to, not what they are)
+      (&f.x)[i] = scaled(sc, ks[i]);
+      (&l.x)[i] = y;
+      (&v.x)[i] = x;
+      // a scale of 0 (no token) does not count; one that is not finite makes the range so
+      low = fminf(low, x == 0.0f ? INFINITY : y);
+      high = fmaxf(high, y != y ? INFINITY : y);
+    }
+    *reinterpret_cast<float4*>(&S.scales[at][0][4 * lane]) = f;
+    *reinterpret_cast<float4*>(&S.scales[at][1][4 * lane]) = l;
+    *reinterpret_cast<float4*>(&S.scales[at][2][4 * lane]) = v;
+    low = in_order(__reduce_min_sync(0xFFFFFFFFu, in_order(low)));
+    high = in_order(__reduce_max_sync(0xFFFFFFFFu, in_order(high)));
+    if (lane == 0) S.range[at] = make_float2(low, high);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.scales_full[at]);
+    now = next;
+    fetch(now);
+    next = look_up();
   }
 }
 
@@ -1281,7 +1375,7 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
     reinterpret_cast<Rec*>(a.ws)[blockIdx.x] = Rec{0, 0, 0, 0};
     reinterpret_cast<int*>(a.ws + loose_offset(gridDim.x))[blockIdx.x] = 0;
     for (int i = 0; i < F::kSlots; ++i) {
-      mbar_init(&S.full[i], F::kNarrow ? F::kProducerWarps : F::kProducers);
+      mbar_init(&S.full[i], F::kNarrow ? 4 : F::kProducers);
       mbar_init(&S.raw_full[i], F::kProducers);
       mbar_init(&S.empty[i], 1);
     }
@@ -1291,6 +1385,10 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
       mbar_init(&S.pv_done[i], 1);
       mbar_init(&S.q_full[i], TILES == 1 ? 4 : F::kSoftmaxWarps);
       mbar_init(&S.q_free[i], 1);
+    }
+    for (int i = 0; i < kScaleRing; ++i) {
+      mbar_init(&S.scales_full[i], 1);
+      mbar_init(&S.scales_free[i], F::kSoftmaxWarps);
     }
     mbar_init(&S.o_free, 4);
     mbar_init(&S.drain, 1);
@@ -1347,7 +1445,9 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
     K.run(w, s0, e0, W, C);
   } else if (warp < F::kMmaWarp) {
     fewer_registers<F::kProducerRegs>();
-    produce<DT, QT, TILES, TS>(a, S, w, s0, e0);
+    Tiles<F> T(a, S, w, s0, e0);
+    if constexpr (F::kNarrow) produce_narrow<F, TILES == 1>(T);
+    else produce<F, TILES == 1>(T);
     wait_groups<0>();
   } else {
     fewer_registers<F::kMmaRegs>();
@@ -1358,6 +1458,8 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
       int never = 0;
       mbar_wait(&S.drain, 0, &never);
     }
+    if constexpr (TS)
+      if (warp == F::kMmaWarp + 1) load_scales<F>(a, S, w, s0, e0);
     if constexpr (F::kCheckers > 0)
       if (warp > F::kMmaWarp && warp <= F::kMmaWarp + F::kCheckers / 32) check_values<DT, QT, TILES, TS>(a, S, w, s0, e0);
   }
