@@ -274,6 +274,11 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ float4 lds4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+  return v;
+}
 __device__ __forceinline__ void sts16(uint32_t a, const uint4& v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -522,9 +527,9 @@ struct Softmax {
                                         float sc) {
     constexpr int kC = NC > 2 ? 2 : NC, kReads = NC / kC;
     const bool drafted = (k + 1) * kTile > row.P;
-    [[maybe_unused]] const float* kf = S.scales[all % kScaleRing][0] + 32 * NC * copy;
-    [[maybe_unused]] const float* lv = S.scales[all % kScaleRing][1] + 32 * NC * copy;
-    [[maybe_unused]] const float* vf = S.scales[all % kScaleRing][2] + 32 * NC * copy;
+    // the tile's scales: a token's is the same for all lanes
+    [[maybe_unused]] const uint32_t kf = smem_addr(S.scales[all % kScaleRing][0]) + 128 * NC * copy, lv = kf + 4 * kTile,
+                                    vf = lv + 4 * kTile;
     const uint32_t x_at = s_at + 32u * NC * copy, p_at = s_at + 16u * NC * copy;
     uint32_t x[kC][32];
     auto pair = [&](int c, int e) { return make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])); };
@@ -568,9 +573,9 @@ struct Softmax {
       if constexpr (TS) {  // into log2 units
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
-          float4 f[8];  // (a token's scale is the same for all lanes; read while the scores are on their way)
+          float4 f[8];  // (read while the scores are on their way)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float4*>(&kf[64 * part + 32 * c + 4 * e]);
+          for (int e = 0; e < 8; ++e) f[e] = lds4(kf + 4 * (64 * part + 32 * c + 4 * e));
           if (c == 0) landed();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -592,7 +597,7 @@ struct Softmax {
           for (int c = 0; c < kC; ++c)
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&lv[64 * part + 32 * c + e]);
+              const float4 f = lds4(lv + 4 * (64 * part + 32 * c + e));
               const float2 y = __fadd2_rn(pair(c, e), make_float2(f.x, f.y));
               const float2 z = __fadd2_rn(pair(c, e + 2), make_float2(f.z, f.w));
               nx = max3(max3(nx, y.x, y.y), z.x, z.y);
@@ -658,7 +663,7 @@ struct Softmax {
         [[maybe_unused]] float4 f[8];
         if constexpr (TS) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = *reinterpret_cast<const float4*>(&vf[64 * part + 32 * c + 4 * e]);
+          for (int e = 0; e < 8; ++e) f[e] = lds4(vf + 4 * (64 * part + 32 * c + 4 * e));
           if (extreme) {
             const float y = exp2_ftz(rest);
 #pragma unroll
