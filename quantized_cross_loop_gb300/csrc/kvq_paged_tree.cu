@@ -50,7 +50,7 @@ namespace {
 
 constexpr int kTile = 128;       // tokens of a tile, rows of a row tile
 constexpr int kScaleRing = 4;    // tiles whose scales are there at a time
-constexpr int kUnitCost = 1;     // tiles that the end of a unit takes as long as
+constexpr int kUnitCost = 2;     // tiles that the end of a unit takes as long as (1: 64 requests of one token 176 us, 2: 170, 3: 171)
 constexpr int kSlotBytes = kTile * kD * 2;
 constexpr int kRawBytes = kTile * kD;
 constexpr uint32_t kTmemCols = 512;
