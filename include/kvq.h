@@ -728,11 +728,14 @@ size_t kvq_paged_tree_workspace_bytes(int n_requests, int n_heads, int n_q_heads
  *   lse      FP32 [n_rows][Hq] or NULL: ln of the sum of exp(scale q.k).
  * Query head hq reads KV head hq / (Hq/H). Softmax and sums are FP32; q.k and |v|
  * summed over the tokens have to lie within FP32's range. Weights are rounded to
- * BF16 (FP16 caches: to FP16), out once more to its type. A value that is not finite
- * counts where a row attends to it, and nowhere else; what lies in other places of a
- * page is not read. A row that attends to nothing, or whose keys all weigh nothing,
- * gets out 0 and lse -inf; the rows of a request whose length, row count or pages
- * are outside their range NaN in both.
+ * 16 bits (BF16 of a BF16 cache, else FP16, which leaves out what is below 2^-31 of
+ * the largest), out once more to its type. A value that is not finite makes its
+ * channel NaN or infinite in the rows that attend to its token, and in no others;
+ * what lies in other places of a page is not read. A row that attends to nothing, or
+ * whose keys all weigh nothing, gets out 0 and lse -inf. All rows of a request whose
+ * length or row count is outside its range become NaN in both, and so do rows whose
+ * tokens are on a page outside the pool (possibly others of their request, too);
+ * requests whose offsets are out of order have no rows.
  */
 kvq_status kvq_paged_tree_attn(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages, int n_requests,
                                const int32_t* seq_lens, const int32_t* offsets, int n_rows, const uint32_t* mask,

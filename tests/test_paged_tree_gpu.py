@@ -240,6 +240,46 @@ def test_many_requests_and_a_long_one():
     _compare(c, q, out, lse, seen)
 
 
+@pytest.mark.parametrize("cache,act", ALL)
+@pytest.mark.parametrize("rows", [(1, 3), (20, 33), (30, 70)])
+def test_many_short_units(cache, act, rows):
+    """Units of one or two tiles, many to a block: queries, rings and flags are used anew at every turn."""
+    rng = random.Random(5)
+    B = 700 if rows[1] < 10 else 300
+    lens = [rng.randint(0, 200) for _ in range(B)]
+    n = [rng.randint(*rows) for _ in range(B)]
+    c = Cache(lens, n, 32, 2, cache, seed=2)
+    q = _query(sum(n), 8, act)
+    seen, mask = _tree(n, 4, 0.1)
+    out, lse = _attend(c, q, _offsets(n), mask)
+    for b in range(0, B, 23):  # (a sample, the same of every form)
+        r = slice(sum(n[:b]), sum(n[:b + 1]))
+        K, V = c.values(b, 0, lens[b] + n[b])
+        see = torch.cat([torch.ones((n[b], lens[b]), dtype=torch.bool, device="cuda"), seen[b]], 1)
+        for j in range(8):
+            o, l, to, tl = _exact(q[r, j], K[:, j // 4], V[:, j // 4], see, 1 / math.sqrt(D), cache, act,
+                                  c.value_scales(b, j // 4, lens[b] + n[b]))
+            assert (out[r, j].double() - o).abs().le(to + 1e-30).all(), (b, j)
+            y = lse[r, j].double()
+            assert ((y == l) | (y - l).abs().le(tl)).all(), (b, j)
+    assert c.cache.error_word() == 0
+    again, lse2 = _attend(c, q, _offsets(n), mask)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("cache", ["e4m3", "e4m3t", "bf16"])
+def test_queries_of_channels_far_apart(cache):
+    """The largest channel meets keys of zero there: what the small ones find is all that counts."""
+    c = Cache([300, 70], [5, 40], 16, 2, cache, seed=3)
+    _raw(c.k)[..., 7] = 0
+    q = _query(45, 8, "bf16")
+    q[..., 7] = 2.0**70
+    q[::2] = q[::2] * 2.0**-3
+    seen, mask = _tree([5, 40], 2)
+    out, lse = _attend(c, q, _offsets([5, 40]), mask)
+    _compare(c, q, out, lse, seen)
+
+
 @pytest.mark.parametrize("cache,act", [("bf16", "bf16"), ("e4m3t", "bf16"), ("fp16", "fp16")])
 def test_long_shared_units(cache, act):
     """One request whose units' tokens are cut among all blocks, with two row tiles."""
