@@ -525,7 +525,9 @@ struct Softmax {
   template <int NC>
   __device__ __forceinline__ bool weigh(Row& row, int k, int begin, uint32_t count, uint32_t all, uint32_t s_at, int copy,
                                         float sc) {
-    constexpr int kC = NC > 2 ? 2 : NC, kReads = NC / kC;
+    // (8-bit rows: 32 columns at a time, in a loop: beside the conversion's the code would not stay in the instruction
+    // cache, see the capture)
+    constexpr int kC = NC > 2 ? (F::kNarrow ? 1 : 2) : NC, kReads = NC / kC, kUnroll = F::kNarrow ? 1 : kReads;
     const bool drafted = (k + 1) * kTile > row.P;
     // the tile's scales: a token's is the same for all lanes
     [[maybe_unused]] const uint32_t kf = smem_addr(S.scales[all % kScaleRing][0]) + 128 * NC * copy, lv = kf + 4 * kTile,
@@ -567,7 +569,7 @@ struct Softmax {
       high = range.y;
       far = high - low > 8.0f;
     }
-#pragma unroll
+#pragma unroll kUnroll
     for (int part = 0; part < kReads; ++part) {
       read(part);
       if constexpr (TS) {  // into log2 units
@@ -575,7 +577,7 @@ struct Softmax {
         for (int c = 0; c < kC; ++c) {
           float4 f[8];  // (read while the scores are on their way)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = lds4(kf + 4 * (64 * part + 32 * c + 4 * e));
+          for (int e = 0; e < 8; ++e) f[e] = lds4(kf + 4 * (32 * (kC * part + c) + 4 * e));
           if (c == 0) landed();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -597,7 +599,7 @@ struct Softmax {
           for (int c = 0; c < kC; ++c)
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
-              const float4 f = lds4(lv + 4 * (64 * part + 32 * c + e));
+              const float4 f = lds4(lv + 4 * (32 * (kC * part + c) + e));
               const float2 y = __fadd2_rn(pair(c, e), make_float2(f.x, f.y));
               const float2 z = __fadd2_rn(pair(c, e + 2), make_float2(f.z, f.w));
               nx = max3(max3(nx, y.x, y.y), z.x, z.y);
@@ -650,7 +652,7 @@ struct Softmax {
     [[maybe_unused]] const bool extreme = TS && __any_sync(0xFFFFFFFFu, rest != 0.0f);
     const float base = (TS ? on : F::kShift) - (row.m == -INFINITY ? 0.0f : row.m);
     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
+#pragma unroll kUnroll
     for (int part = 0; part < kReads; ++part) {
       if constexpr (kReads > 1) {
         read(part);
@@ -663,7 +665,7 @@ struct Softmax {
         [[maybe_unused]] float4 f[8];
         if constexpr (TS) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = lds4(vf + 4 * (64 * part + 32 * c + 4 * e));
+          for (int e = 0; e < 8; ++e) f[e] = lds4(vf + 4 * (32 * (kC * part + c) + 4 * e));
           if (extreme) {
             const float y = exp2_ftz(rest);
 #pragma unroll
@@ -1045,16 +1047,22 @@ __device__ __forceinline__ void produce(Tiles<F>& T) {
   }
 }
 
-// 16 E4M3 channels each of tokens `token`, `token` + 4, ... as two chunks of an operand.
-template <bool BF, int N>
-__device__ __forceinline__ void convert(const uint4 (&z)[N], uint32_t to, int token, int chunk) {
+// A lane's share of an 8-bit copy's i-th part: 16 channels of one of eight tokens, the first or the second half of the
+// row's, so that eight lanes write to all banks (a whole row by eight lanes: each bank twice).
+__device__ __forceinline__ int part_token(int lane, int i) { return 8 * (i >> 1) + (lane >> 2); }
+__device__ __forceinline__ int part_chunk(int lane, int i) { return 4 * (i & 1) + (lane & 3); }
+
+// Four parts from the i-th on as chunks of an operand.
+template <bool BF>
+__device__ __forceinline__ void convert(const uint4 (&z)[4], uint32_t to, int token, int lane, int i) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
+  for (int e = 0; e < 4; ++e) {
     uint2 v[4];
 #pragma unroll
-    for (int d = 0; d < 4; ++d) v[d] = widen<BF>((&z[i].x)[d]);
-    sts16(to + chunk_at(token + 4 * i, chunk), make_uint4(v[0].x, v[0].y, v[1].x, v[1].y));
-    sts16(to + chunk_at(token + 4 * i, chunk + 1), make_uint4(v[2].x, v[2].y, v[3].x, v[3].y));
+    for (int d = 0; d < 4; ++d) v[d] = widen<BF>((&z[e].x)[d]);
+    const int t = token + part_token(lane, i + e), c = 2 * part_chunk(lane, i + e);
+    sts16(to + chunk_at(t, c), make_uint4(v[0].x, v[0].y, v[1].x, v[1].y));
+    sts16(to + chunk_at(t, c + 1), make_uint4(v[2].x, v[2].y, v[3].x, v[3].y));
   }
 }
 
@@ -1077,28 +1085,30 @@ __device__ __forceinline__ void produce_narrow(Tiles<F>& T) {
     const uint32_t y = mine - pending, x = F::kGroups > 1 ? 4 * (y >> 1) + 2 * T.group + (y & 1u) : y;  // (x: of all)
     const uint32_t slot = x % F::kSlots, to = slots + slot * kSlotBytes, raw = raws + (y % F::kStages) * kRawBytes;
     const int from = int(past >> (8 * (pending - 1))) & 0xFF;
-    uint4 z[8];  // 16 channels of a token each
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = lds16(raw + i * (F::kProducers * 16));
     if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return false;
-    const int token = 32 * T.warp + (T.lane >> 3), chunk = 2 * (T.lane & 7);
-    if (from < kTile) {  // drafted values: NaN becomes 0
-      uint32_t any = 0u;
+#pragma unroll 1
+    for (int i = 0; i < 8; i += 4) {
+      uint4 z[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (token + 4 * i < from) continue;
+      for (int e = 0; e < 4; ++e) z[e] = lds16(raw + (i + e) * (F::kProducers * 16));
+      if (from < kTile) {  // drafted values: NaN becomes 0
+        uint32_t any = 0u;
 #pragma unroll
-        for (int d = 0; d < 4; ++d) {
-          uint32_t& v = (&z[i].x)[d];
-          const uint32_t nan = ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes of 0x7F or 0xFF
-          v &= ~((nan >> 7) * 255u);
-          any |= nan;
+        for (int e = 0; e < 4; ++e) {
+          if (32 * T.warp + part_token(T.lane, i + e) < from) continue;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            uint32_t& v = (&z[e].x)[d];
+            const uint32_t nan = ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;  // bytes of 0x7F or 0xFF
+            v &= ~((nan >> 7) * 255u);
+            any |= nan;
+          }
         }
+        if (any != 0u) S.loose = 1;
       }
-      if (any != 0u) S.loose = 1;
+      if (F::kKeyBf && (y & 1u) == 0u) convert<true>(z, to, 32 * T.warp, T.lane, i);
+      else convert<false>(z, to, 32 * T.warp, T.lane, i);
     }
-    if (F::kKeyBf && (y & 1u) == 0u) convert<true>(z, to, token, chunk);
-    else convert<false>(z, to, token, chunk);
     fence_async_smem();
     __syncwarp();
     if (T.lane == 0) mbar_arrive(&S.full[slot]);
@@ -1114,8 +1124,8 @@ __device__ __forceinline__ void produce_narrow(Tiles<F>& T) {
         const uint32_t to = raws + (mine % F::kStages) * kRawBytes;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const long long y = __shfl_sync(0xFFFFFFFFu, T.off, 4 * e + (T.lane >> 3));
-          copy16(to + e * (F::kProducers * 16), pool + (y < 0 ? 0 : y) + (T.lane & 7) * 16, y >= 0);
+          const long long y = __shfl_sync(0xFFFFFFFFu, T.off, part_token(T.lane, e));
+          copy16(to + e * (F::kProducers * 16), pool + (y < 0 ? 0 : y) + part_chunk(T.lane, e) * 16, y >= 0);
         }
         commit();
         past = past << 8 | uint32_t(half == 0 ? kTile : T.drafts);
