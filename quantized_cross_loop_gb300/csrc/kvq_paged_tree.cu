@@ -211,13 +211,6 @@ __device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
                  "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
-// Registers of further loads that a tmem_wait_ld has waited for, too.
-__device__ __forceinline__ void tmem_landed(uint32_t (&r)[32]) {
-#pragma unroll
-  for (int i = 0; i < 32; i += 8)
-    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
-                      "+r"(r[i + 6]), "+r"(r[i + 7])::"memory");
-}
 __device__ __forceinline__ void tmem_st(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
@@ -519,44 +512,30 @@ struct Softmax {
     float m, l, to;
   };
 
-  // The scores of tile k in NC x 32 columns, from copy x NC x 32 on, become weights in the place of the first half of
-  // them (for the other columns 0), the row's sums follow. Scores of up to 64 columns are held in registers; of 128 they
-  // are read twice, for their maximum and for the weights, scaled ones (TS) from where the first reading left them.
-  template <int NC>
+  // The scores of tile k in 32 n columns, from 32 n copy on, become weights in the place of the first half of them (for
+  // the other columns 0), the row's sums follow. The scores are read 32 columns at a time, for their maximum and then,
+  // scaled ones (TS) from where the first reading left them, for the weights. (All in loops: unrolled, or with an instance
+  // for each n, the code of a block's roles does not stay in the instruction cache beside one another: 4 x 65535 tokens
+  // of 8-bit rows 198 us, 148 us so.)
   __device__ __forceinline__ bool weigh(Row& row, int k, int begin, uint32_t count, uint32_t all, uint32_t s_at, int copy,
-                                        float sc) {
-    // (8-bit rows: 32 columns at a time, in a loop: beside the conversion's the code would not stay in the instruction
-    // cache, see the capture)
-    constexpr int kC = NC > 2 ? (F::kNarrow ? 1 : 2) : NC, kReads = NC / kC, kUnroll = F::kNarrow ? 1 : kReads;
+                                        int n, float sc) {
     const bool drafted = (k + 1) * kTile > row.P;
     // the tile's scales: a token's is the same for all lanes
-    [[maybe_unused]] const uint32_t kf = smem_addr(S.scales[all % kScaleRing][0]) + 128 * NC * copy, lv = kf + 4 * kTile,
+    [[maybe_unused]] const uint32_t kf = smem_addr(S.scales[all % kScaleRing][0]) + 128 * n * copy, lv = kf + 4 * kTile,
                                     vf = lv + 4 * kTile;
-    const uint32_t x_at = s_at + 32u * NC * copy, p_at = s_at + 16u * NC * copy;
-    uint32_t x[kC][32];
-    auto pair = [&](int c, int e) { return make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])); };
-    auto put = [&](int c, int e, float2 y) {
-      x[c][e] = __float_as_uint(y.x);
-      x[c][e + 1] = __float_as_uint(y.y);
-    };
-    auto read = [&](int part) {
-#pragma unroll
-      for (int c = 0; c < kC; ++c) tmem_ld(x_at + 32 * (kC * part + c), x[c]);
-    };
-    auto landed = [&]() {
-      tmem_wait_ld(x[0]);
-#pragma unroll
-      for (int c = 1; c < kC; ++c) tmem_landed(x[c]);
+    const uint32_t x_at = s_at + 32u * n * copy, p_at = s_at + 16u * n * copy;
+    uint32_t x[32];
+    auto pair = [&](int e) { return make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])); };
+    auto put = [&](int e, float2 y) {
+      x[e] = __float_as_uint(y.x);
+      x[e + 1] = __float_as_uint(y.y);
     };
     auto mask = [&](int part) {
+      const int j0 = k * kTile + 32 * (n * copy + part) - row.P;
+      const uint32_t see = row.live ? seen_bits(row.mask, a.mask_words, row.n, row.i, j0) : 0u;
 #pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        const int j0 = k * kTile + 32 * (NC * copy + kC * part + c) - row.P;
-        const uint32_t see = row.live ? seen_bits(row.mask, a.mask_words, row.n, row.i, j0) : 0u;
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (!((see >> e) & 1)) x[c][e] = 0xFF800000u;
-      }
+      for (int e = 0; e < 32; ++e)
+        if (!((see >> e) & 1)) x[e] = 0xFF800000u;
     };
     float mx = -INFINITY, nx = -INFINITY;
     // TS: the largest product of a weight and its scale: no more than the largest of each, which will do while the
@@ -569,50 +548,44 @@ struct Softmax {
       high = range.y;
       far = high - low > 8.0f;
     }
-#pragma unroll kUnroll
-    for (int part = 0; part < kReads; ++part) {
-      read(part);
+#pragma unroll 1
+    for (int part = 0; part < n; ++part) {
+      tmem_ld(x_at + 32 * part, x);
       if constexpr (TS) {  // into log2 units
 #pragma unroll
-        for (int c = 0; c < kC; ++c) {
-          float4 f[8];  // (read while the scores are on their way)
+        for (int q = 0; q < 2; ++q) {
+          float4 f[4];  // (the first ones are read while the scores are on their way)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = lds4(kf + 4 * (32 * (kC * part + c) + 4 * e));
-          if (c == 0) landed();
+          for (int e = 0; e < 4; ++e) f[e] = lds4(kf + 4 * (32 * part + 16 * q + 4 * e));
+          if (q == 0) tmem_wait_ld(x);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            put(c, 4 * e, __fmul2_rn(pair(c, 4 * e), make_float2(f[e].x, f[e].y)));
-            put(c, 4 * e + 2, __fmul2_rn(pair(c, 4 * e + 2), make_float2(f[e].z, f[e].w)));
+          for (int e = 0; e < 4; ++e) {
+            const int i = 16 * q + 4 * e;
+            put(i, __fmul2_rn(pair(i), make_float2(f[e].x, f[e].y)));
+            put(i + 2, __fmul2_rn(pair(i + 2), make_float2(f[e].z, f[e].w)));
           }
         }
       } else {
-        landed();
+        tmem_wait_ld(x);
       }
       if (drafted) mask(part);
 #pragma unroll
-      for (int c = 0; c < kC; ++c)
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+      for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
       if constexpr (TS) {
         if (far)
 #pragma unroll
-          for (int c = 0; c < kC; ++c)
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 f = lds4(lv + 4 * (32 * (kC * part + c) + e));
-              const float2 y = __fadd2_rn(pair(c, e), make_float2(f.x, f.y));
-              const float2 z = __fadd2_rn(pair(c, e + 2), make_float2(f.z, f.w));
-              nx = max3(max3(nx, y.x, y.y), z.x, z.y);
-            }
-        if constexpr (kReads > 1) {
-#pragma unroll
-          for (int c = 0; c < kC; ++c) tmem_st(x_at + 32 * (kC * part + c), x[c]);
-        }
+          for (int e = 0; e < 32; e += 4) {
+            const float4 f = lds4(lv + 4 * (32 * part + e));
+            const float2 y = __fadd2_rn(pair(e), make_float2(f.x, f.y));
+            const float2 z = __fadd2_rn(pair(e + 2), make_float2(f.z, f.w));
+            nx = max3(max3(nx, y.x, y.y), z.x, z.y);
+          }
+        tmem_st(x_at + 32 * part, x);
       }
     }
     if constexpr (TS) {
       if (!far) nx = mx + high;
-      if constexpr (kReads > 1) tmem_wait_st();
+      tmem_wait_st();
     } else {
       nx = mx *= sc;
     }
@@ -652,48 +625,45 @@ struct Softmax {
     [[maybe_unused]] const bool extreme = TS && __any_sync(0xFFFFFFFFu, rest != 0.0f);
     const float base = (TS ? on : F::kShift) - (row.m == -INFINITY ? 0.0f : row.m);
     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll kUnroll
-    for (int part = 0; part < kReads; ++part) {
-      if constexpr (kReads > 1) {
-        read(part);
-        landed();
-        if (!TS && drafted) mask(part);
-      }
+#pragma unroll 1
+    for (int part = 0; part < n; ++part) {
+      tmem_ld(x_at + 32 * part, x);
+      tmem_wait_ld(x);
+      if (!TS && drafted) mask(part);
+      uint32_t p[16];
 #pragma unroll
-      for (int c = 0; c < kC; ++c) {
-        uint32_t p[16];
-        [[maybe_unused]] float4 f[8];
+      for (int q = 0; q < 2; ++q) {
+        [[maybe_unused]] float4 f[4];
         if constexpr (TS) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] = lds4(vf + 4 * (32 * (kC * part + c) + 4 * e));
+          for (int e = 0; e < 4; ++e) f[e] = lds4(vf + 4 * (32 * part + 16 * q + 4 * e));
           if (extreme) {
             const float y = exp2_ftz(rest);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = times(f[e], y);
+            for (int e = 0; e < 4; ++e) f[e] = times(f[e], y);
           }
         }
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
+        for (int i = 0; i < 16; i += 2) {
+          const int e = 16 * q + i;
           float2 y;
-          if constexpr (TS) y = __fadd2_rn(pair(c, e), make_float2(base, base));
-          else y = __ffma2_rn(pair(c, e), make_float2(sc, sc), make_float2(base, base));
+          if constexpr (TS) y = __fadd2_rn(pair(e), make_float2(base, base));
+          else y = __ffma2_rn(pair(e), make_float2(sc, sc), make_float2(base, base));
           y = make_float2(exp2_ftz(y.x), exp2_ftz(y.y));
-          sum[(e >> 1) & 1] = __fadd2_rn(sum[(e >> 1) & 1], y);
-          if constexpr (TS) {
-            const float2 v = e & 2 ? make_float2(f[e / 4].z, f[e / 4].w) : make_float2(f[e / 4].x, f[e / 4].y);
-            y = __fmul2_rn(y, v);
-          }
+          sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], y);
+          if constexpr (TS)
+            y = __fmul2_rn(y, i & 2 ? make_float2(f[i / 4].z, f[i / 4].w) : make_float2(f[i / 4].x, f[i / 4].y));
           p[e / 2] = pack<F::kValBf>(y.x, y.y);
         }
-        tmem_st16(p_at + 16 * (kC * part + c), p);
       }
+      tmem_st16(p_at + 16 * part, p);
     }
-    if constexpr (NC < 4) {
+    if (n < 4) {
       uint32_t none[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) none[e] = 0u;
-#pragma unroll
-      for (int c = NC; c < 4; ++c) tmem_st16(s_at + 16 * ((NC * copy + c) & 3), none);
+#pragma unroll 1
+      for (int c = n; c < 4; ++c) tmem_st16(s_at + 16 * ((n * copy + c) & 3), none);
     }
     sum[0] = __fadd2_rn(sum[0], sum[1]);
     row.l += TS ? (sum[0].x + sum[0].y) * exp2_ftz(-on) : sum[0].x + sum[0].y;
@@ -730,11 +700,7 @@ struct Softmax {
         if (!mbar_wait(&S.s_full[buf], phase, &S.abort)) return;
         tc_fence_after();
         if (rows) {
-          bool ok;
-          if (same == 4) ok = weigh<1>(row, k, w.begin, count, all, s_at, copy, sc);
-          else if (same == 2) ok = weigh<2>(row, k, w.begin, count, all, s_at, copy, sc);
-          else ok = weigh<4>(row, k, w.begin, count, all, s_at, 0, sc);
-          if (!ok) return;
+          if (!weigh(row, k, w.begin, count, all, s_at, same > 1 ? copy : 0, 4 / same, sc)) return;
         }
         tc_fence_before();
         __syncwarp();
