@@ -23,7 +23,7 @@
 //             operand slots; 8-bit rows by way of registers and a conversion (one row
 //             tile: two groups of four, which take the tiles in turn)
 //   MMA       one, a lane of which issues all products
-//   checkers  two, for drafted values of 16-bit rows (below); or one that looks up the
+//   checkers  two, for drafted values of 16-bit rows (below); or two that look up the
 //             scales of a tile's tokens
 // Exactness: products of 16-bit values are exact, sums FP32. 8-bit keys become 16-bit
 // of the queries' type (exact), 8-bit values BF16 (exact). A weight is one 16-bit
@@ -101,7 +101,7 @@ struct Smem {
   // scales of a tile's tokens: the keys' (into log2 units), the logarithms of the values', the values'; and the smallest
   // and largest of those logarithms
   float scales[F::kNarrow ? kScaleRing : 1][3][F::kNarrow ? kTile : 4];
-  float2 range[kScaleRing];
+  float2 range[kScaleRing][2];
   unsigned long long scales_full[kScaleRing], scales_free[kScaleRing];
   // one row tile: what its copies of the rows are joined by
   float part[F::kQueries > 0 ? 1 : kTile][33];
@@ -543,9 +543,9 @@ struct Softmax {
     bool far = false;
     float high = -INFINITY;
     if constexpr (TS) {
-      const float2 range = S.range[all % kScaleRing];
-      const float low = range.x;
-      high = range.y;
+      const float2 y = S.range[all % kScaleRing][0], z = S.range[all % kScaleRing][1];
+      const float low = fminf(y.x, z.x);
+      high = fmaxf(y.y, z.y);
       far = high - low > 8.0f;
     }
 #pragma unroll 1
@@ -1122,11 +1122,11 @@ __device__ __forceinline__ void produce_narrow(Tiles<F>& T) {
   }
 }
 
-// One warp: the scales of the tiles' tokens (8-bit rows with a scale per token), four tokens a lane, looked up in two
+// Two warps: the scales of the tiles' tokens (8-bit rows with a scale per token), two tokens a lane, looked up in two
 // steps one and two tiles ahead.
 template <class F>
 __device__ __forceinline__ void load_scales(const TreeArgs& a, Smem<F>& S, Walk<F::kRows> w, long long s0, long long e0) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, part = int(threadIdx.x >> 5) - F::kMmaWarp - 1, first = 64 * part + 2 * lane;
   const float sc = a.scale * kLog2e;
   struct Tile {
     int t0, P, h;
@@ -1134,16 +1134,14 @@ __device__ __forceinline__ void load_scales(const TreeArgs& a, Smem<F>& S, Walk<
   };
   int k = w.begin;
   bool more = true;
-  int page[4];  // of the pool, -1: no token
-  float ks[4], vs[4];
+  int page[2];  // of the pool, -1: no token
+  float ks[2], vs[2];
   auto look_up = [&]() -> Tile {
     if (!more) return Tile{0, 0, 0, false};
-    const Tile t{k * kTile, w.r.P, w.h, true};
+    const Tile t{k * kTile + first, w.r.P, w.h, true};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = t.t0 + 4 * lane + i;
-      page[i] = at < w.tokens ? a.table[(long long)w.b * a.max_pages + a.c.ps.div(at)] : -1;
-    }
+    for (int i = 0; i < 2; ++i)
+      page[i] = t.t0 + i < w.tokens ? a.table[(long long)w.b * a.max_pages + a.c.ps.div(t.t0 + i)] : -1;
     if (++k == w.end) {
       more = w.next(a, s0, e0);
       if (more) k = w.begin;
@@ -1152,46 +1150,50 @@ __device__ __forceinline__ void load_scales(const TreeArgs& a, Smem<F>& S, Walk<
   };
   auto fetch = [&](const Tile& t) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       ks[i] = vs[i] = 0.0f;
       if (!t.there || page[i] < 0 || page[i] >= a.c.n_pages) continue;
-      const int at = t.t0 + 4 * lane + i;
+      const int at = t.t0 + i;
       const long long x = ((long long)page[i] * a.c.H + t.h) * int(a.c.ps.d) + (at - a.c.ps.div(at) * int(a.c.ps.d));
       ks[i] = a.c.k_scale[x];
       vs[i] = a.c.v_scale[x];
     }
   };
-  Tile now = look_up();
-  fetch(now);
-  Tile next = look_up();
-  for (uint32_t c = 0; now.there; ++c) {
-    const uint32_t at = c % kScaleRing;
-    if (!mbar_wait(&S.scales_free[at], (c / kScaleRing + 1) & 1u, &S.abort)) return;
-    float4 f, l, v;
-    float low = INFINITY, high = -INFINITY;
+  Tile now{0, 0, 0, false}, next{0, 0, 0, false};
+  uint32_t c = 0;
+#pragma unroll 1
+  for (int turn = 0;; ++turn) {  // (the first two turns only look ahead)
+    if (turn >= 2) {
+      if (!now.there) return;
+      const uint32_t at = c % kScaleRing;
+      if (!mbar_wait(&S.scales_free[at], (c / kScaleRing + 1) & 1u, &S.abort)) return;
+      float2 f, l, v;
+      float low = INFINITY, high = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x = vs[i];
-      if (now.t0 + 4 * lane + i >= now.P && !isfinite(x)) {  // a drafted token's: as its values that are not finite
-        S.loose = 1;
-        x = 0.0f;
+      for (int i = 0; i < 2; ++i) {
+        float x = vs[i];
+        if (now.t0 + i >= now.P && !isfinite(x)) {  // a drafted token's: as its values that are not finite
+          S.loose = 1;
+          x = 0.0f;
+        }
+        const float y = __log2f(x);  // (decides what the sums are to, not what they are)
+        (&f.x)[i] = scaled(sc, ks[i]);
+        (&l.x)[i] = y;
+        (&v.x)[i] = x;
+        // a scale of 0 (no token) does not count; one that is not finite makes the range so
+        low = fminf(low, x == 0.0f ? INFINITY : y);
+        high = fmaxf(high, y != y ? INFINITY : y);
       }
-      const float y = __log2f(x);  // (decides what the sums are to, not what they are)
-      (&f.x)[i] = scaled(sc, ks[i]);
-      (&l.x)[i] = y;
-      (&v.x)[i] = x;
-      // a scale of 0 (no token) does not count; one that is not finite makes the range so
-      low = fminf(low, x == 0.0f ? INFINITY : y);
-      high = fmaxf(high, y != y ? INFINITY : y);
+      *reinterpret_cast<float2*>(&S.scales[at][0][first]) = f;
+      *reinterpret_cast<float2*>(&S.scales[at][1][first]) = l;
+      *reinterpret_cast<float2*>(&S.scales[at][2][first]) = v;
+      low = in_order(__reduce_min_sync(0xFFFFFFFFu, in_order(low)));
+      high = in_order(__reduce_max_sync(0xFFFFFFFFu, in_order(high)));
+      if (lane == 0) S.range[at][part] = make_float2(low, high);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&S.scales_full[at]);
+      ++c;
     }
-    *reinterpret_cast<float4*>(&S.scales[at][0][4 * lane]) = f;
-    *reinterpret_cast<float4*>(&S.scales[at][1][4 * lane]) = l;
-    *reinterpret_cast<float4*>(&S.scales[at][2][4 * lane]) = v;
-    low = in_order(__reduce_min_sync(0xFFFFFFFFu, in_order(low)));
-    high = in_order(__reduce_max_sync(0xFFFFFFFFu, in_order(high)));
-    if (lane == 0) S.range[at] = make_float2(low, high);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&S.scales_full[at]);
     now = next;
     fetch(now);
     next = look_up();
@@ -1368,7 +1370,7 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
       mbar_init(&S.q_free[i], 1);
     }
     for (int i = 0; i < kScaleRing; ++i) {
-      mbar_init(&S.scales_full[i], 1);
+      mbar_init(&S.scales_full[i], 2);
       mbar_init(&S.scales_free[i], F::kSoftmaxWarps);
     }
     mbar_init(&S.o_free, 4);
@@ -1440,7 +1442,7 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
       mbar_wait(&S.drain, 0, &never);
     }
     if constexpr (TS)
-      if (warp == F::kMmaWarp + 1) load_scales<F>(a, S, w, s0, e0);
+      if (warp == F::kMmaWarp + 1 || warp == F::kMmaWarp + 2) load_scales<F>(a, S, w, s0, e0);
     if constexpr (F::kCheckers > 0)
       if (warp > F::kMmaWarp && warp <= F::kMmaWarp + F::kCheckers / 32) check_values<DT, QT, TILES, TS>(a, S, w, s0, e0);
   }
