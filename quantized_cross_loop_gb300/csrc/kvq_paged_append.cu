@@ -25,6 +25,10 @@
 // each unit's own rows, and the ranges are equal in rows, not units: batches mix
 // prompts with requests of one row (a prompt of 2048 and 499 single rows, pages of 256:
 // 24 us; by equal counts of units, each a team's, 849).
+// A scale per token and KV head (8-bit rows) is that of the row's largest magnitude, which
+// a team finds by shuffles; the codes are then found as for a scale per head (64 requests of
+// one row, 8 + 32 heads, 3.3 us; four prompts of 8192 tokens, 8 + 64 heads, 236 us, 5.5
+// TB/s; with a scale per head 3.5 and 202).
 // Rows in flight and resident warps bound these; staging the rotation table in
 // shared memory for eight heads, and fetching the next rows into registers ahead of
 // the arithmetic, were slower (a table's row is in L1 for the heads that follow).

@@ -14,7 +14,11 @@ namespace {
 //
 // Sixteen lanes (a team) hold a row of a head, eight channels each. Work: (row, head)
 // pairs in the rows' order, a block's teams side by side, so that the heads of a row
-// are written together; kReadRows pairs in flight per team.
+// are written together; kReadRows pairs in flight per team. Measured: eight FP16
+// requests of up to 8191 rows to BF16, 8 heads, pages of 16, 138 MB moved: 24.9 us,
+// 5.5 TB/s, 82% of a copy's rate; other blocks per SM x rows in flight: 1 x 8 25.3 us,
+// 2 x 6 25.2, 2 x 8 26.0, 4 x 6 31.5, 4 x 8 35.5, 8 x 2 25.4. 64 tiles of 64 rows, E4M3
+// with scales per token, 25 MB: 7.7 us (launch and the chain offsets -> table -> row).
 
 constexpr int kReadThreads = 256;
 constexpr int kReadTeam = 16;
@@ -159,7 +163,8 @@ __global__ void __launch_bounds__(kReadThreads, kReadBlocksPerSm) read_kernel(Re
 // read before any is written. That is in order, because the list ascends: the k-th
 // accepted token is at place k or behind it, so what a later step reads lies behind
 // what an earlier one wrote. The bounds are then taken from the keys as they are.
-// Bound: latency (a few rows per request).
+// Bound: latency (a few rows per request): 64 requests that keep 5 of 16 BF16 tokens,
+// 8 heads, 4.8 us; 256 that keep up to 32 of 64, E4M3 with scales per token, 8.5 us.
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveWarps = kMoveThreads / 32;

@@ -11,33 +11,50 @@
 // ranges, one per block (one block an SM); lengths are read on the device, so a
 // captured call follows them. A unit that lies in one block's range is finished
 // there; of the others each block leaves (m, l, sum) in one of its two slots, and the
-// combine kernel joins them.
+// joining kernel joins them.
 //
-// Both products run on tcgen05 with 128 rows: S = Q K^T from shared memory, O += P V
-// with P in tensor memory, where the softmax warps leave it in the place of S. A
-// block's warps:
+// Both products run on tcgen05 with 128 rows: S = Q K^T, the queries in tensor memory
+// (one row tile) or in shared memory (two: sums and scores fill tensor memory), and
+// O += P V with P in tensor memory, where the softmax warps leave it in the place of
+// S. A block's warps:
 //   softmax   four per row tile, a thread a row: no shuffles; the sums of a row are
 //             rescaled only when its maximum grows by more than 2^8 (its weights then
-//             go to at most 1, or 2^15 for FP16, by kShift)
+//             go to at most 1, or 2^15 for FP16, by kShift). A unit of up to 64 (32)
+//             rows is in the row tile twice (four times), each copy for its share of
+//             a tile's tokens, else a few rows would leave three warps of four idle
 //   producers four: 16-byte asynchronous copies of K and V rows into a ring of
-//             operand slots; 8-bit rows by way of registers and a conversion (one row
-//             tile: two groups of four, which take the tiles in turn)
+//             operand slots; 8-bit rows into a ring of their own, from which the same
+//             threads convert them (one row tile: two groups of four, which take the
+//             tiles in turn)
 //   MMA       one, a lane of which issues all products
 //   checkers  two, for drafted values of 16-bit rows (below); or two that look up the
 //             scales of a tile's tokens
 // Exactness: products of 16-bit values are exact, sums FP32. 8-bit keys become 16-bit
-// of the queries' type (exact), 8-bit values BF16 (exact). A weight is one 16-bit
-// number (times its value's scale, where tokens have one): BF16, whose range holds
-// any scale's product, or FP16 for FP16 caches, down to 2^-31 of the largest weight.
-// The result is rounded to 16 bits anyway, and three parts would triple the second
-// product, which bounds wide trees.
+// numbers of the queries' type, 8-bit values FP16, both exactly. A weight is one
+// 16-bit number: of BF16 for BF16 caches (its operand's type is the values'), of FP16
+// for the others, there down to 2^-31 of the largest weight with values' scales
+// (where tokens have them) multiplied in before the rounding. The result is rounded
+// to 16 bits anyway, and three parts would triple the second product, which bounds
+// wide trees.
 //
 // A drafted token's value that is not finite must not reach rows that do not see it
-// (0 x infinity): the producers replace it by 0, and the rows that see it get it back
-// at the end (loose).
+// (0 x infinity): the checkers, or the conversion, replace it by 0, and the rows that
+// see it get it back at the end (loose).
 //
 // Every wait is bounded (2 s): a wait that runs out sets an error bit and the block
 // leaves, after its products in flight.
+//
+// Bound: few rows, HBM (each cached row is read once); from about 128 rows a KV head on
+// the tensor cores and the softmax (16 KB of operands a product, 128 x 128 exponentials
+// a tile). Measured, 8 KV heads, BF16 but where said: 64 requests of up to 16383 tokens, one
+// new token each, 173 us, 6.1 TB/s (91% of a copy's rate); 512 x 1000 tokens, four new
+// ones each, 339 us (94%); trees of 16 over 64 requests of up to 4095 tokens 95 us,
+// 5.1 TB/s; trees of 64, 64 heads, over 8 x 16384 tokens 240 us, 1.14 PFLOP/s; E4M3, 64
+// requests of one token with a scale per head 168 us (3.1 TB/s), with one per token
+// 182 us: conversion and the scales' multiplications, not HBM.
+// The block's roles share an instruction cache, and their code is kept in loops for
+// it: unrolled forms stalled on instructions more than on anything else (4 x 65535
+// tokens of E4M3 with a scale per token 330 us, 186 now).
 #include <atomic>
 #include <type_traits>
 
@@ -50,7 +67,7 @@ namespace {
 
 constexpr int kTile = 128;       // tokens of a tile, rows of a row tile
 constexpr int kScaleRing = 4;    // tiles whose scales are there at a time
-constexpr int kUnitCost = 2;     // tiles that the end of a unit takes as long as (1: 64 requests of one token 176 us, 2: 170, 3: 171)
+constexpr int kUnitCost = 2;     // tiles that the end of a unit takes as long as (64 requests of one token: 1 176 us, 2 170, 3 171)
 constexpr int kSlotBytes = kTile * kD * 2;
 constexpr int kRawBytes = kTile * kD;
 constexpr uint32_t kTmemCols = 512;
@@ -71,8 +88,8 @@ struct Form {
   static constexpr int kRows = kTile * TILES;
   static constexpr int kSoftmaxWarps = 4 * TILES;
   // groups of four producer warps, which take the tiles in turn: 8-bit rows are copied, converted and stored by the same
-  // threads, one after the other, and two groups do it side by side (64 requests of one token 295 us by eight warps
-  // together)
+  // threads, one after the other, and two groups do it side by side (eight warps together were slower: 64 requests of
+  // one token, a scale per head, 244 us then, 207 in turn, with a warp of its own for the scales per token)
   static constexpr int kGroups = kNarrow && TILES == 1 ? 2 : 1;
   static constexpr int kProducerWarps = 4 * kGroups;
   static constexpr int kProducers = 128;  // threads of a group
@@ -87,6 +104,10 @@ struct Form {
   static constexpr int kQueries = TILES == 1 ? 0 : kRows;
   static constexpr int kSlots = kNarrow ? (TILES == 1 ? 4 : 3) : TILES == 1 ? 6 : 5;
   static constexpr int kStages = kNarrow ? (TILES == 1 ? 2 : 3) : 0;  // a group's 8-bit rows as they come
+  // of a copy's eight parts those that a thread converts at once: two where the code for BF16 keys and for FP16 values
+  // stands beside that for scales per token, else four (the code's size: 64 requests of one token with BF16 queries and
+  // scales per token 235 us by four, 182 by two; with FP16 queries 177 and 194; with a scale per head 169 and 174)
+  static constexpr int kParts = TS && kKeyBf ? 2 : 4;
   static constexpr int kCheckers = kNarrow ? 0 : 64;      // threads (two warps behind the MMA warp) that check drafted values
 };
 
@@ -1018,11 +1039,11 @@ __device__ __forceinline__ void produce(Tiles<F>& T) {
 __device__ __forceinline__ int part_token(int lane, int i) { return 8 * (i >> 1) + (lane >> 2); }
 __device__ __forceinline__ int part_chunk(int lane, int i) { return 4 * (i & 1) + (lane & 3); }
 
-// Four parts from the i-th on as chunks of an operand.
-template <bool BF>
-__device__ __forceinline__ void convert(const uint4 (&z)[4], uint32_t to, int token, int lane, int i) {
+// N parts from the i-th on as chunks of an operand.
+template <bool BF, int N>
+__device__ __forceinline__ void convert(const uint4 (&z)[N], uint32_t to, int token, int lane, int i) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < N; ++e) {
     uint2 v[4];
 #pragma unroll
     for (int d = 0; d < 4; ++d) v[d] = widen<BF>((&z[e].x)[d]);
@@ -1053,14 +1074,14 @@ __device__ __forceinline__ void produce_narrow(Tiles<F>& T) {
     const int from = int(past >> (8 * (pending - 1))) & 0xFF;
     if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return false;
 #pragma unroll 1
-    for (int i = 0; i < 8; i += 4) {
-      uint4 z[4];
+    for (int i = 0; i < 8; i += F::kParts) {
+      uint4 z[F::kParts];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) z[e] = lds16(raw + (i + e) * (F::kProducers * 16));
+      for (int e = 0; e < F::kParts; ++e) z[e] = lds16(raw + (i + e) * (F::kProducers * 16));
       if (from < kTile) {  // drafted values: NaN becomes 0
         uint32_t any = 0u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < F::kParts; ++e) {
           if (32 * T.warp + part_token(T.lane, i + e) < from) continue;
 #pragma unroll
           for (int d = 0; d < 4; ++d) {

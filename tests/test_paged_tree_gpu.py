@@ -741,7 +741,7 @@ def test_commit_leaves_refused_requests_alone():
 @pytest.mark.parametrize("cache", ["bf16", "e4m3t"])
 def test_a_serving_run(cache):
     """A prompt in two chunks, then steps of drafting, verifying and committing; each attention against the tokens that a
-    plain list of keys and values holds. Captured commits and appends follow the lengths."""
+    plain list of keys and values holds."""
     H, Hq, ps, B = 2, 8, 16, 3
     g = _gen(11)
     W = 20
@@ -801,6 +801,77 @@ def test_a_serving_run(cache):
                     K = pool.k[table[b, p].long(), :min(ps, lens[b] - p * ps)]
                     assert torch.equal(pool.key_bounds[table[b, p].long()], torch.stack([K.amin(0), K.amax(0)], 1))
     assert pool.error_word() == 0
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3t"])
+def test_a_captured_step_follows_its_inputs(cache):
+    """A step of appending, attending, committing and reading back, captured once and replayed with other lengths, rows,
+    trees and paths, leaves in one cache what the same calls leave in another, bit for bit."""
+    H, Hq, ps, B, W, n = 2, 8, 16, 3, 12, 24
+    g = _gen(12)
+
+    def pool():
+        if cache == "e4m3t":
+            p = kvq.PagedCache.empty(B * W + 1, ps, H, dtype=torch.float8_e4m3fn, token_scales=True)
+        else:
+            p = kvq.PagedCache.empty(B * W + 1, ps, H, key_bounds=True)
+        return p
+
+    pools = [pool(), pool()]
+    for p in pools:
+        for t in (p.k, p.v, p.k_scale, p.v_scale, p.key_bounds):
+            if t is not None:
+                t.view(torch.uint8).zero_()
+    table = torch.zeros((B, W), dtype=torch.int32, device="cuda")
+    start = torch.zeros(B, dtype=torch.int32, device="cuda")
+    off, taken_off = (torch.zeros(B + 1, dtype=torch.int32, device="cuda") for _ in range(2))
+    taken = torch.zeros(n, dtype=torch.int32, device="cuda")
+    mask = torch.zeros((n, 1), dtype=torch.int32, device="cuda")
+    k, v = (torch.zeros((n, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros((n, Hq, D), dtype=torch.bfloat16, device="cuda")
+    ws = [torch.empty(p.tree_workspace_bytes(B, Hq, n), dtype=torch.uint8, device="cuda") for p in pools]
+    outs = [[torch.zeros((n, Hq, D), dtype=torch.bfloat16, device="cuda"), torch.zeros((n, Hq), device="cuda"),
+             torch.zeros((n, H, D), dtype=torch.bfloat16, device="cuda"),
+             torch.zeros((n, H, D), dtype=torch.bfloat16, device="cuda")] for _ in pools]
+
+    def step(i):
+        p, (out, lse, rk, rv) = pools[i], outs[i]
+        kvq.kvq_paged_append(p, table, start, k, v, offsets=off)
+        kvq.kvq_paged_tree_attn(p, table, start, q, offsets=off, mask=mask, out=out, lse=lse, workspace=ws[i])
+        kvq.kvq_paged_tree_commit(p, table, start, taken, taken_off)
+        kvq.kvq_paged_read(p, table, start, rk, rv, offsets=taken_off)
+
+    step(0)  # (no rows yet: nothing but the first calls' set-up)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(0)
+    lens = [0, 7, 100]
+    for rows in ([8, 1, 15], [0, 20, 4], [3, 3, 3], [8, 8, 8]):
+        seen, m = _tree(rows, sum(lens))
+        paths = [[j for j in range(r) if seen[b][r // 2, j]] if r else [] for b, r in enumerate(rows)]
+        flat = [x for a in paths for x in a]
+        table.copy_(torch.randperm(B * W, generator=g, device="cuda").view(B, W).to(torch.int32))
+        start.copy_(torch.tensor(lens, dtype=torch.int32))
+        off.copy_(_offsets(rows))
+        taken_off.copy_(_offsets([len(a) for a in paths]))
+        taken[:len(flat)] = torch.tensor(flat, dtype=torch.int32, device="cuda")
+        mask.zero_()
+        mask[:m.shape[0]] = m
+        for t in (k, v, q):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        torch.cuda.synchronize()
+        graph.replay()
+        step(1)
+        torch.cuda.synchronize()
+        for a, b in zip(*outs):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        for name in ("k", "v", "k_scale", "v_scale", "key_bounds"):
+            a, b = (getattr(p, name) for p in pools)
+            assert a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert flat and bool((outs[0][2][:len(flat)] != 0).any())
+        lens = [t + len(a) for t, a in zip(lens, paths)]
+    assert [p.error_word() for p in pools] == [0, 0]
 
 
 def test_arguments_of_the_binding():
