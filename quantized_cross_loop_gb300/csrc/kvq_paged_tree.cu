@@ -206,6 +206,13 @@ __device__ __forceinline__ void mma_commit(unsigned long long* bar) {
                : "memory");
 }
 
+// One lane of a warp that is together.
+__device__ __forceinline__ bool elect() {
+  uint32_t ok;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(ok));
+  return ok != 0;
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -1277,42 +1284,51 @@ template <int DT, int QT, int TILES, bool TS>
 __device__ __forceinline__ bool multiply(const TreeArgs& a, Smem<Form<DT, QT, TILES, TS>>& S,
                                          Walk<Form<DT, QT, TILES, TS>::kRows> w, long long s0, long long e0) {
   using F = Form<DT, QT, TILES, TS>;
-  const uint32_t tmem = S.tmem, q = smem_addr(S.q), slots = smem_addr(S.slot);
+  auto same = [](uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); };
+  const uint32_t tmem = same(S.tmem), q = smem_addr(S.q), slots = smem_addr(S.slot);
   uint32_t x = 0;             // slots so far
   uint32_t count[2] = {0, 0};  // products of each row tile so far
   uint32_t units = 0;
   auto keys = [&](int tile, uint32_t x, uint32_t buf) {
-    const uint64_t kb = smem_desc(slots + (x % F::kSlots) * kSlotBytes, 16);
+    const uint32_t slot = same(x % F::kSlots), to = same(tmem + kColS + 128u * buf);
+    [[maybe_unused]] const uint32_t qa = same(tmem + kColQ + 64u * (units & 1u));
+    const uint64_t kb = smem_desc(slots + slot * kSlotBytes, 16);
+    if (!elect()) return;
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k) {  // 16 channels: 32 bytes on, four times in each half
       const uint32_t on = 2u * (k & 3u) + (kSlotBytes / 32) * (k >> 2);
       if constexpr (TILES == 1)
-        mma_ts(tmem + kColS + 128u * buf, tmem + kColQ + 64u * (units & 1u) + 8u * k, kb + on, instr_desc(F::kKeyBf, false),
+        mma_ts(to, qa + 8u * k, kb + on, instr_desc(F::kKeyBf, false),
                k > 0);
       else
-        mma_ss(tmem + kColS + 128u * buf, smem_desc(q + tile * kSlotBytes, 16) + on, kb + on,
+        mma_ss(to, smem_desc(q + tile * kSlotBytes, 16) + on, kb + on,
                instr_desc(F::kKeyBf, false), k > 0);
     }
     mma_commit(&S.s_full[buf]);
   };
   auto values = [&](int tile, uint32_t x, uint32_t buf, bool first) {
-    const uint64_t vb = smem_desc(slots + (x % F::kSlots) * kSlotBytes, kSlotBytes / 2);
+    const uint32_t slot = same(x % F::kSlots), from = same(tmem + kColS + 128u * buf);
+    const uint64_t vb = smem_desc(slots + slot * kSlotBytes, kSlotBytes / 2);
+    if (!elect()) return;
 #pragma unroll
     for (uint32_t k = 0; k < 8; ++k)  // 16 tokens: 2048 bytes on
-      mma_ts(tmem + 128u * tile, tmem + kColS + 128u * buf + 8u * k, vb + 128u * k, instr_desc(F::kValBf, true),
+      mma_ts(tmem + 128u * tile, from + 8u * k, vb + 128u * k, instr_desc(F::kValBf, true),
              !first || k > 0);
     mma_commit(&S.pv_done[TILES == 1 ? buf : tile]);
   };
   auto wait = [&](unsigned long long* bar, uint32_t phase) {
-    if (!mbar_wait(bar, phase & 1u, &S.abort)) return false;
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1u, &S.abort))) return false;
     tc_fence_after();
     return true;
   };
   auto filled = [&](uint32_t x) {
-    if (!mbar_wait(&S.full[x % F::kSlots], (x / F::kSlots) & 1u, &S.abort)) return false;
+    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S.full[x % F::kSlots], (x / F::kSlots) & 1u, &S.abort))) return false;
     if constexpr (!F::kNarrow) fence_async_smem();  // (copies that arrive by themselves have no fence behind them)
     tc_fence_after();
     return true;
+  };
+  auto done = [&](unsigned long long* bar) {
+    if (elect()) mma_commit(bar);
   };
   for (bool more = true; more; more = w.next(a, s0, e0), ++units) {
     const int n = w.end - w.begin;
@@ -1323,15 +1339,15 @@ __device__ __forceinline__ bool multiply(const TreeArgs& a, Smem<Form<DT, QT, TI
         if (k < n) {
           if (!filled(x + 2 * k)) return false;
           keys(0, x + 2 * k, (count[0] + k) & 1u);
-          mma_commit(&S.empty[(x + 2 * k) % F::kSlots]);
-          if (k + 1 == n) mma_commit(&S.q_free[units & 1u]);
+          done(&S.empty[(x + 2 * k) % F::kSlots]);
+          if (k + 1 == n) done(&S.q_free[units & 1u]);
         }
         if (k > 0) {
           const uint32_t c = count[0] + k - 1, y = x + 2 * (k - 1) + 1;
           if (!filled(y) || !wait(&S.p_ready[c & 1u], c >> 1)) return false;
           if (k == 1 && units > 0 && !wait(&S.o_free, units - 1)) return false;  // the unit's sums before are read
           values(0, y, c & 1u, k == 1);
-          mma_commit(&S.empty[y % F::kSlots]);
+          done(&S.empty[y % F::kSlots]);
         }
       }
       count[0] += n;
@@ -1348,14 +1364,14 @@ __device__ __forceinline__ bool multiply(const TreeArgs& a, Smem<Form<DT, QT, TI
               values(tile, y, tile, k == 1);
               ++count[tile];
             }
-            if (last) mma_commit(&S.empty[y % F::kSlots]);
+            if (last) done(&S.empty[y % F::kSlots]);
           }
           if (k < n) {
             if (on) {
               if (!filled(x + 2 * k)) return false;
               keys(tile, x + 2 * k, tile);
             }
-            if (last) mma_commit(&S.empty[(x + 2 * k) % F::kSlots]);
+            if (last) done(&S.empty[(x + 2 * k) % F::kSlots]);
           }
         }
     }
@@ -1455,10 +1471,10 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
     wait_groups<0>();
   } else {
     fewer_registers<F::kMmaRegs>();
-    if (threadIdx.x == F::kMmaWarp * 32) {
+    if (warp == F::kMmaWarp) {
       multiply<DT, QT, TILES, TS>(a, S, w, s0, e0);
       // the products in flight end before the tensor memory is freed
-      mma_commit(&S.drain);
+      if (elect()) mma_commit(&S.drain);
       int never = 0;
       mbar_wait(&S.drain, 0, &never);
     }
