@@ -26,7 +26,10 @@
 //             operand slots; 8-bit rows into a ring of their own, from which the same
 //             threads convert them (one row tile: two groups of four, which take the
 //             tiles in turn)
-//   MMA       one, a lane of which issues all products
+//   MMA       one, which stays together and elects a lane to issue the products: their
+//             descriptors are then the warp's and computed once (issued by a lone
+//             thread wide trees took 240 us for 235, of E4M3 271 for 251; in a loop that
+//             is not unrolled 278: a product's issue is on the rows' critical path)
 //   checkers  two, for drafted values of 16-bit rows (below); or two that look up the
 //             scales of a tile's tokens
 // Exactness: products of 16-bit values are exact, sums FP32. 8-bit keys become 16-bit
@@ -106,7 +109,7 @@ struct Form {
   static constexpr int kStages = kNarrow ? (TILES == 1 ? 2 : 3) : 0;  // a group's 8-bit rows as they come
   // of a copy's eight parts those that a thread converts at once: two where the code for BF16 keys and for FP16 values
   // stands beside that for scales per token, else four (the code's size: 64 requests of one token with BF16 queries and
-  // scales per token 235 us by four, 182 by two; with FP16 queries 177 and 194; with a scale per head 169 and 174)
+  // scales per token 212 us by four, 176 by two; with FP16 queries 165 and 180; with a scale per head 163 and 167)
   static constexpr int kParts = TS && kKeyBf ? 2 : 4;
   static constexpr int kCheckers = kNarrow ? 0 : 64;      // threads (two warps behind the MMA warp) that check drafted values
 };
@@ -565,6 +568,11 @@ struct Softmax {
       for (int e = 0; e < 32; ++e)
         if (!((see >> e) & 1)) x[e] = 0xFF800000u;
     };
+    // Two row tiles and a tile of cached tokens: for the maximum the next columns are on their way while these are worked
+    // on (wide trees of 16 bits 235 us, 229 so, chunks 244 and 239; the same for the weights 229 and 237, and registers
+    // went to memory).
+    constexpr bool kAhead = TILES == 2 && !TS;
+    [[maybe_unused]] uint32_t y[32];
     float mx = -INFINITY, nx = -INFINITY;
     // TS: the largest product of a weight and its scale: no more than the largest of each, which will do while the
     // scales are within 2^8 of one another (FP16 weights reach down to 2^-21 with all their bits)
@@ -576,6 +584,22 @@ struct Softmax {
       high = fmaxf(y.y, z.y);
       far = high - low > 8.0f;
     }
+    auto highest = [&](const uint32_t (&z)[32]) {
+#pragma unroll
+      for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+    };
+    if (kAhead && !drafted) {
+      tmem_ld(x_at, x);
+#pragma unroll
+      for (int part = 0; part < 4; part += 2) {
+        tmem_wait_ld(x);
+        tmem_ld(x_at + 32 * (part + 1), y);
+        highest(x);
+        tmem_wait_ld(y);
+        if (part == 0) tmem_ld(x_at + 64, x);
+        highest(y);
+      }
+    } else
 #pragma unroll 1
     for (int part = 0; part < n; ++part) {
       tmem_ld(x_at + 32 * part, x);
@@ -597,8 +621,7 @@ struct Softmax {
         tmem_wait_ld(x);
       }
       if (drafted) mask(part);
-#pragma unroll
-      for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+      highest(x);
       if constexpr (TS) {
         if (far)
 #pragma unroll
