@@ -48,16 +48,16 @@
 // leaves, after its products in flight.
 //
 // Bound: few rows, HBM (each cached row is read once); from about 128 rows a KV head on
-// the tensor cores and the softmax (16 KB of operands a product, 128 x 128 exponentials
-// a tile). Measured, 8 KV heads, BF16 but where said: 64 requests of up to 16383 tokens, one
-// new token each, 173 us, 6.1 TB/s (91% of a copy's rate); 512 x 1000 tokens, four new
-// ones each, 339 us (94%); trees of 16 over 64 requests of up to 4095 tokens 95 us,
-// 5.1 TB/s; trees of 64, 64 heads, over 8 x 16384 tokens 240 us, 1.14 PFLOP/s; E4M3, 64
-// requests of one token with a scale per head 168 us (3.1 TB/s), with one per token
-// 182 us: conversion and the scales' multiplications, not HBM.
+// a row tile's chain of product, softmax (128 x 128 exponentials) and product. Measured,
+// 8 KV heads, BF16 but where said: 64 requests of up to 16383 tokens, one new token each,
+// 172 us, 6.1 TB/s (91% of a copy's rate); 512 x 1000 tokens, four new ones each, 339 us
+// (94%); trees of 16 over 64 requests of up to 4095 tokens 95 us, 5.2 TB/s; trees of 64, 64
+// heads, over 8 x 16384 tokens 230 us, 1.20 PFLOP/s; E4M3, 64 requests of one token with a
+// scale per head 163 us (3.2 TB/s), with one per token 176 us (3.1 TB/s): conversion and the
+// scales' multiplications, not HBM.
 // The block's roles share an instruction cache, and their code is kept in loops for
 // it: unrolled forms stalled on instructions more than on anything else (4 x 65535
-// tokens of E4M3 with a scale per token 330 us, 186 now).
+// tokens of E4M3 with a scale per token 330 us, 182 now).
 #include <atomic>
 #include <type_traits>
 
@@ -547,7 +547,7 @@ struct Softmax {
   // the other columns 0), the row's sums follow. The scores are read 32 columns at a time, for their maximum and then,
   // scaled ones (TS) from where the first reading left them, for the weights. (All in loops: unrolled, or with an instance
   // for each n, the code of a block's roles does not stay in the instruction cache beside one another: 4 x 65535 tokens
-  // of 8-bit rows 198 us, 148 us so.)
+  // of 8-bit rows with a scale per head 198 us, 143 us so; 512 x 1000 tokens of 16 bits 353 and 339.)
   __device__ __forceinline__ bool weigh(Row& row, int k, int begin, uint32_t count, uint32_t all, uint32_t s_at, int copy,
                                         int n, float sc) {
     const bool drafted = (k + 1) * kTile > row.P;
