@@ -50,10 +50,10 @@
 // Bound: few rows, HBM (each cached row is read once); from about 128 rows a KV head on
 // a row tile's chain of product, softmax (128 x 128 exponentials) and product. Measured,
 // 8 KV heads, BF16 but where said: 64 requests of up to 16383 tokens, one new token each,
-// 172 us, 6.1 TB/s (91% of a copy's rate); 512 x 1000 tokens, four new ones each, 339 us
-// (94%); trees of 16 over 64 requests of up to 4095 tokens 95 us, 5.2 TB/s; trees of 64, 64
-// heads, over 8 x 16384 tokens 230 us, 1.20 PFLOP/s; E4M3, 64 requests of one token with a
-// scale per head 163 us (3.2 TB/s), with one per token 176 us (3.1 TB/s): conversion and the
+// 168 us, 6.3 TB/s (94% of a copy's rate); 512 x 1000 tokens, four new ones each, 332 us
+// (96%); trees of 16 over 64 requests of up to 4095 tokens 93 us, 5.3 TB/s; trees of 64, 64
+// heads, over 8 x 16384 tokens 222 us, 1.24 PFLOP/s; E4M3, 64 requests of one token with a
+// scale per head 164 us (3.2 TB/s), with one per token 177 us (3.1 TB/s): conversion and the
 // scales' multiplications, not HBM.
 // The block's roles share an instruction cache, and their code is kept in loops for
 // it: unrolled forms stalled on instructions more than on anything else (4 x 65535
@@ -584,9 +584,14 @@ struct Softmax {
       high = fmaxf(y.y, z.y);
       far = high - low > 8.0f;
     }
-    auto highest = [&](const uint32_t (&z)[32]) {
+    auto highest = [&](const uint32_t (&z)[32]) {  // (in two chains: wide trees 230 us by one, 222 so)
+      float top = -INFINITY;
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+      for (int e = 0; e < 32; e += 4) {
+        mx = max3(mx, __uint_as_float(z[e]), __uint_as_float(z[e + 1]));
+        top = max3(top, __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3]));
+      }
+      mx = fmaxf(mx, top);
     };
     if (kAhead && !drafted) {
       tmem_ld(x_at, x);
