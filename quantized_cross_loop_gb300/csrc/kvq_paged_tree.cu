@@ -30,7 +30,7 @@
 //             descriptors are then the warp's and computed once (issued by a lone
 //             thread wide trees took 240 us for 235, of E4M3 271 for 251; in a loop that
 //             is not unrolled 278: a product's issue is on the rows' critical path)
-//   checkers  two, for drafted values of 16-bit rows (below); or two that look up the
+//   screeners two, for drafted values of 16-bit rows (below); or two that look up the
 //             scales of a tile's tokens
 // Exactness: products of 16-bit values are exact, sums FP32. 8-bit keys become 16-bit
 // numbers of the queries' type, 8-bit values FP16, both exactly. A weight is one
@@ -41,7 +41,7 @@
 // wide trees.
 //
 // A drafted token's value that is not finite must not reach rows that do not see it
-// (0 x infinity): the checkers, or the conversion, replace it by 0, and the rows that
+// (0 x infinity): the screeners, or the conversion, replace it by 0, and the rows that
 // see it get it back at the end (loose).
 //
 // Every wait is bounded (2 s): a wait that runs out sets an error bit and the block
@@ -49,12 +49,12 @@
 //
 // Bound: few rows, HBM (each cached row is read once); from about 128 rows a KV head on
 // a row tile's chain of product, softmax (128 x 128 exponentials) and product. Measured,
-// 8 KV heads, BF16 but where said: 64 requests of up to 16383 tokens, one new token each,
-// 168 us, 6.3 TB/s (94% of a copy's rate); 512 x 1000 tokens, four new ones each, 332 us
-// (96%); trees of 16 over 64 requests of up to 4095 tokens 93 us, 5.3 TB/s; trees of 64, 64
-// heads, over 8 x 16384 tokens 222 us, 1.24 PFLOP/s; E4M3, 64 requests of one token with a
-// scale per head 164 us (3.2 TB/s), with one per token 177 us (3.1 TB/s): conversion and the
-// scales' multiplications, not HBM.
+// 8 KV heads, BF16 but where said (from one GPU to another 2-3% less): 64 requests of up
+// to 16383 tokens, one new token each, 172 us, 6.1 TB/s (91% of a copy's rate); 512 x 1000
+// tokens, four new ones each, 338 us (95%); trees of 16 over 64 requests of up to 4095
+// tokens 95 us, 5.2 TB/s; trees of 64, 64 heads, over 8 x 16384 tokens 224 us, 1.23
+// PFLOP/s; E4M3, 64 requests of one token with a scale per head 163 us (3.2 TB/s), with one
+// per token 177 us (3.1 TB/s): conversion and the scales' multiplications, not HBM.
 // The block's roles share an instruction cache, and their code is kept in loops for
 // it: unrolled forms stalled on instructions more than on anything else (4 x 65535
 // tokens of E4M3 with a scale per token 330 us, 182 now).
@@ -107,11 +107,7 @@ struct Form {
   static constexpr int kQueries = TILES == 1 ? 0 : kRows;
   static constexpr int kSlots = kNarrow ? (TILES == 1 ? 4 : 3) : TILES == 1 ? 6 : 5;
   static constexpr int kStages = kNarrow ? (TILES == 1 ? 2 : 3) : 0;  // a group's 8-bit rows as they come
-  // of a copy's eight parts those that a thread converts at once: two where the code for BF16 keys and for FP16 values
-  // stands beside that for scales per token, else four (the code's size: 64 requests of one token with BF16 queries and
-  // scales per token 212 us by four, 176 by two; with FP16 queries 165 and 180; with a scale per head 163 and 167)
-  static constexpr int kParts = TS && kKeyBf ? 2 : 4;
-  static constexpr int kCheckers = kNarrow ? 0 : 64;      // threads (two warps behind the MMA warp) that check drafted values
+  static constexpr int kScreeners = kNarrow ? 0 : 64;  // threads (two warps behind the MMA warp) that check drafted values
 };
 
 template <class F>
@@ -556,7 +552,7 @@ struct Softmax {
                                     vf = lv + 4 * kTile;
     const uint32_t x_at = s_at + 32u * n * copy, p_at = s_at + 16u * n * copy;
     uint32_t x[32];
-    auto pair = [&](int e) { return make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])); };
+    auto pair = [](const uint32_t (&z)[32], int e) { return make_float2(__uint_as_float(z[e]), __uint_as_float(z[e + 1])); };
     auto put = [&](int e, float2 y) {
       x[e] = __float_as_uint(y.x);
       x[e + 1] = __float_as_uint(y.y);
@@ -584,7 +580,7 @@ struct Softmax {
       high = fmaxf(y.y, z.y);
       far = high - low > 8.0f;
     }
-    auto highest = [&](const uint32_t (&z)[32]) {  // (in two chains: wide trees 230 us by one, 222 so)
+    auto highest = [&](const uint32_t (&z)[32]) {  // (in two chains: wide trees 230 us by one, 224 so)
       float top = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 32; e += 4) {
@@ -618,8 +614,8 @@ struct Softmax {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = 16 * q + 4 * e;
-            put(i, __fmul2_rn(pair(i), make_float2(f[e].x, f[e].y)));
-            put(i + 2, __fmul2_rn(pair(i + 2), make_float2(f[e].z, f[e].w)));
+            put(i, __fmul2_rn(pair(x, i), make_float2(f[e].x, f[e].y)));
+            put(i + 2, __fmul2_rn(pair(x, i + 2), make_float2(f[e].z, f[e].w)));
           }
         }
       } else {
@@ -632,8 +628,8 @@ struct Softmax {
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
             const float4 f = lds4(lv + 4 * (32 * part + e));
-            const float2 y = __fadd2_rn(pair(e), make_float2(f.x, f.y));
-            const float2 z = __fadd2_rn(pair(e + 2), make_float2(f.z, f.w));
+            const float2 y = __fadd2_rn(pair(x, e), make_float2(f.x, f.y));
+            const float2 z = __fadd2_rn(pair(x, e + 2), make_float2(f.z, f.w));
             nx = max3(max3(nx, y.x, y.y), z.x, z.y);
           }
         tmem_st(x_at + 32 * part, x);
@@ -703,8 +699,8 @@ struct Softmax {
         for (int i = 0; i < 16; i += 2) {
           const int e = 16 * q + i;
           float2 y;
-          if constexpr (TS) y = __fadd2_rn(pair(e), make_float2(base, base));
-          else y = __ffma2_rn(pair(e), make_float2(sc, sc), make_float2(base, base));
+          if constexpr (TS) y = __fadd2_rn(pair(x, e), make_float2(base, base));
+          else y = __ffma2_rn(pair(x, e), make_float2(sc, sc), make_float2(base, base));
           y = make_float2(exp2_ftz(y.x), exp2_ftz(y.y));
           sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], y);
           if constexpr (TS)
@@ -1091,7 +1087,7 @@ __device__ __forceinline__ void convert(const uint4 (&z)[N], uint32_t to, int to
 // 8-bit rows: asynchronous copies into a ring of their own, each thread's to be converted by itself. (Loaded into
 // registers they left room for two slots more, but the fence behind a conversion then waited for the next loads: 64
 // requests of one token with scales per token 308 us.)
-template <class F, bool QUERIES>
+template <class F, bool QUERIES, int PARTS>
 __device__ __forceinline__ void produce_narrow(Tiles<F>& T) {
   const TreeArgs& a = T.a;
   Smem<F>& S = T.S;
@@ -1109,14 +1105,14 @@ __device__ __forceinline__ void produce_narrow(Tiles<F>& T) {
     const int from = int(past >> (8 * (pending - 1))) & 0xFF;
     if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return false;
 #pragma unroll 1
-    for (int i = 0; i < 8; i += F::kParts) {
-      uint4 z[F::kParts];
+    for (int i = 0; i < 8; i += PARTS) {
+      uint4 z[PARTS];
 #pragma unroll
-      for (int e = 0; e < F::kParts; ++e) z[e] = lds16(raw + (i + e) * (F::kProducers * 16));
+      for (int e = 0; e < PARTS; ++e) z[e] = lds16(raw + (i + e) * (F::kProducers * 16));
       if (from < kTile) {  // drafted values: NaN becomes 0
         uint32_t any = 0u;
 #pragma unroll
-        for (int e = 0; e < F::kParts; ++e) {
+        for (int e = 0; e < PARTS; ++e) {
           if (32 * T.warp + part_token(T.lane, i + e) < from) continue;
 #pragma unroll
           for (int d = 0; d < 4; ++d) {
@@ -1258,7 +1254,7 @@ __device__ __forceinline__ void load_scales(const TreeArgs& a, Smem<F>& S, Walk<
 
 // Two warps: drafted values of 16-bit rows that are not finite become 0 before they are multiplied.
 template <int DT, int QT, int TILES, bool TS>
-__device__ __forceinline__ void check_values(const TreeArgs& a, Smem<Form<DT, QT, TILES, TS>>& S,
+__device__ __forceinline__ void screen_values(const TreeArgs& a, Smem<Form<DT, QT, TILES, TS>>& S,
                                              Walk<Form<DT, QT, TILES, TS>::kRows> w, long long s0, long long e0) {
   using F = Form<DT, QT, TILES, TS>;
   const int thread = int(threadIdx.x) - (F::kMmaWarp + 1) * 32;
@@ -1273,7 +1269,7 @@ __device__ __forceinline__ void check_values(const TreeArgs& a, Smem<Form<DT, QT
       phases ^= 1u << slot;
       // a token's 16 chunks by 16 threads: two of each 128 bytes, in their swizzled order
 #pragma unroll 4
-      for (int token = from + thread / 8; token < to; token += F::kCheckers / 8) {
+      for (int token = from + thread / 8; token < to; token += F::kScreeners / 8) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const uint32_t p = at + half * (kSlotBytes / 2) + token * 128 + (thread & 7) * 16;
@@ -1299,7 +1295,7 @@ __device__ __forceinline__ void check_values(const TreeArgs& a, Smem<Form<DT, QT
       }
       fence_async_smem();
       asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(&S.full[slot])),
-                   "r"(F::kProducers / F::kCheckers)
+                   "r"(F::kProducers / F::kScreeners)
                    : "memory");
     }
     x += 2 * (w.end - w.begin);
@@ -1494,7 +1490,10 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
   } else if (warp < F::kMmaWarp) {
     fewer_registers<F::kProducerRegs>();
     Tiles<F> T(a, S, w, s0, e0);
-    if constexpr (F::kNarrow) produce_narrow<F, TILES == 1>(T);
+    // of a copy's eight parts those that a thread converts at once: two where the code for BF16 keys and for FP16 values
+    // stands beside that for scales per token, else four (the code's size: 64 requests of one token with BF16 queries and
+    // scales per token 212 us by four, 176 by two; with FP16 queries 165 and 180; with a scale per head 163 and 167)
+    if constexpr (F::kNarrow) produce_narrow<F, TILES == 1, TS && F::kKeyBf ? 2 : 4>(T);
     else produce<F, TILES == 1>(T);
     wait_groups<0>();
   } else {
@@ -1508,8 +1507,8 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
     }
     if constexpr (TS)
       if (warp == F::kMmaWarp + 1 || warp == F::kMmaWarp + 2) load_scales<F>(a, S, w, s0, e0);
-    if constexpr (F::kCheckers > 0)
-      if (warp > F::kMmaWarp && warp <= F::kMmaWarp + F::kCheckers / 32) check_values<DT, QT, TILES, TS>(a, S, w, s0, e0);
+    if constexpr (F::kScreeners > 0)
+      if (warp > F::kMmaWarp && warp <= F::kMmaWarp + F::kScreeners / 32) screen_values<DT, QT, TILES, TS>(a, S, w, s0, e0);
   }
   __syncwarp();
   tc_fence_before();
