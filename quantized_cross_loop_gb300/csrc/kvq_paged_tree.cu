@@ -792,10 +792,11 @@ struct Softmax {
     }
   }
 
-  // What a whole unit's sums are multiplied by, in two factors (their product may be in FP32's range where one is not).
+  // What a whole unit's sums are multiplied by, in two factors (their product may leave FP32's range where the sums times
+  // one and then the other do not: 8-bit values' scales are as small as 2^-126).
   __device__ __forceinline__ float2 factors(const Walk<F::kRows>& w, const Row& row) const {
     float2 f = make_float2(row.l == 0.0f ? 0.0f : 1.0f / row.l, 1.0f);
-    if (DT == kE4m3 && !TS && a.c.v_scale != nullptr) f.x *= a.c.v_scale[w.h];
+    if (DT == kE4m3 && !TS && a.c.v_scale != nullptr) f.y = a.c.v_scale[w.h];
     if constexpr (TS) between(row.to - F::kShift - row.m, f.x, f.y);
     return f;
   }
@@ -823,7 +824,7 @@ struct Softmax {
   template <int N>
   __device__ __forceinline__ void put_out(const Row& row, long long head, int c, float (&x)[N], float2 f) const {
 #pragma unroll
-    for (int e = 0; e < N; ++e) x[e] = row.l == 0.0f ? 0.0f : (TS ? x[e] * f.x * f.y : x[e] * f.x);
+    for (int e = 0; e < N; ++e) x[e] = row.l == 0.0f ? 0.0f : (DT == kE4m3 ? x[e] * f.x * f.y : x[e] * f.x);
     char* to = a.out + head * (kD * 2) + c * 2;
 #pragma unroll
     for (int e = 0; e < N; e += 8)
@@ -1621,7 +1622,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_cons
     const long long head = (long long)(r.row0 + i) * a.Hq + rec.h * a.g + (at - i * a.g);
     float inv = l == 0.0f ? 0.0f : 1.0f / l, inv2 = 1.0f;
     if (DT == kE4m3 && a.c.token_scales) between(to - m, inv, inv2);
-    else if (DT == kE4m3 && a.c.v_scale != nullptr) inv *= a.c.v_scale[rec.h];
+    else if (DT == kE4m3 && a.c.v_scale != nullptr) inv2 = a.c.v_scale[rec.h];
     uint4* out = reinterpret_cast<uint4*>(a.out + head * (kD * 2) + group * 32);
     uint32_t y[8];
 #pragma unroll
