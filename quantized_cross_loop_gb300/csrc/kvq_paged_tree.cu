@@ -77,7 +77,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 256;  // scores and weights: two buffers of 128 columns; the sums are at 0 (and 128: second row tile)
 constexpr uint32_t kColQ = 128;  // one row tile: queries, two buffers of 64
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.0f;   // log2 of what a row's weights may exceed 1 by before its sums are rescaled
+constexpr float kSlack = 8.0f;   // log2 of what a row's weights may exceed 1 by before its sums are rescaled (Form::kRise)
 constexpr long long kWaitNs = 2000000000LL;
 
 // ---------------------------------------------------------------- forms
@@ -87,7 +87,13 @@ struct Form {
   static constexpr bool kNarrow = DT == kE4m3;
   static constexpr bool kKeyBf = DT == kBf16 || (kNarrow && QT == kBf16);  // type of Q and K operands
   static constexpr bool kValBf = DT == kBf16;                              // type of P and V operands
-  static constexpr float kShift = kValBf ? -kSlack : 15.0f - kSlack;
+  // With scales per token the sums are to a bound of the products of weights and scales, which is up to 2^kNear above the
+  // largest product: that comes off the slack, so that FP16 holds the largest product at 2^7 or more in any case (its
+  // smallest step is 2^-31 of that) and at 2^15 at most. (Scales within 2^kNear spare the look for the largest product:
+  // wide trees 335 us, with it 379. Two for four leaves more slack, 334, and more tiles without.)
+  static constexpr float kNear = TS ? 4.0f : 0.0f;
+  static constexpr float kRise = kSlack - kNear;  // log2 of what the products may grow by before the sums are rescaled
+  static constexpr float kShift = kValBf ? -kRise : 15.0f - kRise;
   static constexpr int kRows = kTile * TILES;
   static constexpr int kSoftmaxWarps = 4 * TILES;
   // groups of four producer warps, which take the tiles in turn: 8-bit rows are copied, converted and stored by the same
@@ -571,14 +577,14 @@ struct Softmax {
     [[maybe_unused]] uint32_t y[32];
     float mx = -INFINITY, nx = -INFINITY;
     // TS: the largest product of a weight and its scale: no more than the largest of each, which will do while the
-    // scales are within 2^8 of one another (FP16 weights reach down to 2^-21 with all their bits)
+    // scales are within 2^kNear of one another
     bool far = false;
     float high = -INFINITY;
     if constexpr (TS) {
       const float2 y = S.range[all % kScaleRing][0], z = S.range[all % kScaleRing][1];
       const float low = fminf(y.x, z.x);
       high = fmaxf(y.y, z.y);
-      far = high - low > 8.0f;
+      far = high - low > F::kNear;
     }
     auto highest = [&](const uint32_t (&z)[32]) {  // (in two chains: wide trees 230 us by one, 224 so)
       float top = -INFINITY;
@@ -650,7 +656,7 @@ struct Softmax {
         row.l *= exp2_ftz(row.m - mx);
         row.m = mx;
       }
-      if (__any_sync(0xFFFFFFFFu, nx > top + kSlack)) {
+      if (__any_sync(0xFFFFFFFFu, nx > top + F::kRise)) {
         const float to = fmaxf(top, nx), alpha = exp2_ftz(top - (to == -INFINITY ? 0.0f : to));
         top = to;
         if constexpr (!TS) row.l *= alpha;

@@ -8,7 +8,7 @@ import math
 import pytest
 import torch
 
-from tests.test_paged_tree_gpu import D, Cache, _attend, _exact, _gen, _offsets, _query, _tree
+from tests.test_paged_tree_gpu import D, Cache, _attend, _compare, _exact, _gen, _offsets, _query, _raw, _tree
 
 pytestmark = pytest.mark.gpu
 
@@ -41,3 +41,50 @@ def test_value_scales_per_head_to_the_ends_of_their_range(lens, rows, scale):
             assert (out[at:at + r, j].double() - o).abs().le(to + 2.0**-134).all(), (b, j)
             assert (lse[at:at + r, j].double() - l).abs().le(tl).all(), (b, j)
         at += r
+
+
+@pytest.mark.parametrize("act", ["bf16", "fp16"])
+@pytest.mark.parametrize("B,H,n", [(24, 8, 1), (24, 8, 20), (8, 4, 70)])
+def test_many_light_tokens_of_large_scales_beside_a_heavy_one(act, B, H, n):
+    """One token has nearly all of the weight and the smallest scale of its tile, just under 2^8 below the others'. The
+    others' products of weight and scale are 2^-24.6 of its own each: 8000 of them count, and what is left out lies below
+    2^-31 of the largest product, whatever the tile's scales are."""
+    T = 8000
+    c = Cache([T] * B, [n] * B, 64, H, "e4m3t", seed=3)
+    c.k_scale.fill_(1.0)
+    c.v_scale.fill_(1.0)
+    _raw(c.k)[:] = 0
+    light, heavy, one = (_raw(torch.tensor([x], device="cuda").to(c.v.dtype)) for x in (448.0, 1.0, 1.0))
+    _raw(c.v)[:] = light
+    for b in range(B):
+        page, place = c.where(b, torch.tensor([5], device="cuda"))
+        _raw(c.k)[page, place, :, 0] = one
+        _raw(c.v)[page, place] = heavy
+        c.v_scale[page, :, place] = 2.0**-7.9
+    q = _query(n * B, 2 * H, act)
+    q[..., 0] = 22.5  # (2^32.5 in base 2)
+    seen, mask = _tree([n] * B, 2)
+    out, lse = _attend(c, q, _offsets([n] * B), mask, softmax_scale=1.0)
+    _compare(c, q, out, lse, seen, 1.0)
+
+
+@pytest.mark.parametrize("act", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [[1], [9], [50], [140]])
+def test_products_with_scales_rise_and_fall(act, rows):
+    """Tile by tile the heaviest token and the largest scale are others, so that their products, the weights and the scales
+    all have other maxima: nothing overflows FP16, nothing that counts is lost."""
+    T = 128 * 40
+    c = Cache([T], rows, 32, 1, "e4m3t", seed=5)
+    t = torch.arange(T + rows[0], device="cuda")
+    page, place = c.where(0, t)
+    k = torch.zeros((T + rows[0], 1, D), device="cuda")
+    k[:, 0, 0] = (t // 128 * 7 % 16).float() / 2 + (t % 5 == 0) * 3.0 * (t // 128 % 3 == 1)
+    c.k_scale[page, :, place] = 1.0
+    _raw(c.k)[page, place] = _raw(k.to(c.k.dtype))
+    e = (t // 128 * 5 % 9).float() - 4 - torch.where(t % 5 == 0, (t // 128 % 9).float(), 0.0)
+    c.v_scale[page, :, place] = torch.exp2(e)[:, None]
+    q = _query(rows[0], 4, act)
+    q[..., 0] = 1.75
+    seen, mask = _tree(rows, 3)
+    out, lse = _attend(c, q, _offsets(rows), mask, softmax_scale=1.0)
+    _compare(c, q, out, lse, seen, 1.0)
