@@ -399,7 +399,9 @@ kvq_status kvq_paged_tree_attn(const kvq_paged_cache* cache, const int32_t* page
   if (st != KVQ_OK) return st;
   if (!(softmax_scale > 0.0f) || softmax_scale > 1e30f) return fail(KVQ_ERR_BAD_ARG, "softmax_scale");
   if (!rows_fit(n_rows, q_stride)) return fail(KVQ_ERR_BAD_ARG, "q_stride %lld", (long long)q_stride);
-  if (mask_words < 0 || mask_words > KVQ_PAGED_MAX_DRAFT / 32 || (mask == nullptr) != (mask_words == 0))
+  // (a mask of no rows has no address)
+  if (mask_words < 0 || mask_words > KVQ_PAGED_MAX_DRAFT / 32 ||
+      (mask == nullptr ? mask_words > 0 && n_rows > 0 : mask_words == 0))
     return fail(KVQ_ERR_BAD_ARG, "mask %s mask_words %d", mask == nullptr ? "NULL" : "of", mask_words);
   if (n_requests == 0 || n_rows == 0) return ok();
   if (out == nullptr) return fail(KVQ_ERR_BAD_ARG, "out is NULL");

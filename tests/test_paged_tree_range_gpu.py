@@ -88,3 +88,16 @@ def test_products_with_scales_rise_and_fall(act, rows):
     seen, mask = _tree(rows, 3)
     out, lse = _attend(c, q, _offsets(rows), mask, softmax_scale=1.0)
     _compare(c, q, out, lse, seen, 1.0)
+
+
+# ------------------------------------------------------------------ sizes
+
+
+def test_a_step_without_rows():
+    """Nothing is drafted: a mask of no rows is no less valid than none."""
+    c = Cache([20, 30], [0, 0], 16, 2, "bf16", seed=1)
+    q, off = _query(0, 8, "bf16"), _offsets([0, 0])
+    for mask in (None, torch.empty((0, 1), dtype=torch.int32, device="cuda")):
+        out, lse = _attend(c, q, off, mask)
+        assert out.shape == (0, 8, D) and lse.shape == (0, 8)
+    assert c.cache.error_word() == 0
