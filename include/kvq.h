@@ -697,7 +697,9 @@ kvq_status kvq_paged_sparse_attn(const kvq_paged_cache* cache, const int32_t* pa
  *   k_out, v_out  row r at r * k_stride (v_stride) elements, [H][D] within a row;
  *            16-byte aligned, strides multiples of 8 elements.
  * Rows of a request whose start or length its table row does not hold, and rows on
- * a page outside the pool, become NaN.
+ * a page outside the pool, become NaN. Offsets that do not ascend, or lie outside of
+ * 0 .. n_rows, set KVQ_PAGED_ERR_LENGTH: their requests have no rows, and rows of
+ * others may be left alone, too.
  */
 kvq_status kvq_paged_read(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages, int n_requests,
                           const int32_t* start, const int32_t* offsets, int n_rows, int out_dtype, void* k_out,

@@ -76,6 +76,13 @@ __global__ void __launch_bounds__(kReadThreads, kReadBlocksPerSm) read_kernel(Re
   const long long pairs = (long long)a.n_rows * H;
   const long long p1 = part_start(blockIdx.x + 1, pairs, gridDim.x);
   long long p = part_start(blockIdx.x, pairs, gridDim.x) + threadIdx.x / kReadTeam;
+  // requests that have no rows because their offsets are out of order or beyond the rows: no row leads to them
+  if (a.offsets != nullptr)
+#pragma unroll 1
+    for (int i = blockIdx.x * kReadThreads + threadIdx.x; i < a.B; i += gridDim.x * kReadThreads) {
+      int row0;
+      if (row_range(a.offsets, a.n_rows, i, row0) < 0) flag(a.c, KVQ_PAGED_ERR_LENGTH);
+    }
   if (p >= p1) return;
   int row, h;
   divide(p, H, row, h);

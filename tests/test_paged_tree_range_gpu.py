@@ -8,6 +8,7 @@ import math
 import pytest
 import torch
 
+from quantized_cross_loop_gb300 import kvq
 from tests.test_paged_tree_gpu import D, Cache, _attend, _compare, _exact, _gen, _offsets, _query, _raw, _tree
 
 pytestmark = pytest.mark.gpu
@@ -101,3 +102,32 @@ def test_a_step_without_rows():
         out, lse = _attend(c, q, off, mask)
         assert out.shape == (0, 8, D) and lse.shape == (0, 8)
     assert c.cache.error_word() == 0
+
+
+# ------------------------------------------------------------------ offsets out of order
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3t"])
+def test_read_reports_requests_whose_offsets_are_out_of_range(cache):
+    c = Cache([200, 30, 40], [0] * 3, 16, 2, cache, seed=1)
+    zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+
+    def read(B, offsets, n):
+        k, v = (torch.full((n, 2, D), 7.0, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+        c.cache.clear_error()
+        off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        kvq.kvq_paged_read(c.cache, c.table[:B].contiguous(), zero[:B].contiguous(), k, v, offsets=off)
+        return k, v, c.cache.error_word()
+
+    for offsets in ([0, 100], [-1, 64], [5, 4]):  # beyond the rows, in front of them, backwards
+        k, v, error = read(1, offsets, 64)
+        assert (k == 7).all() and (v == 7).all() and error == kvq.PAGED_ERR_LENGTH
+    k, v, error = read(3, [0, 3, 3, 1000], 10)  # the last request's
+    want = [x.float().bfloat16() for x in c.values(0, 0, 3)]
+    assert torch.equal(k[:3], want[0]) and torch.equal(v[:3], want[1])
+    assert (k[3:] == 7).all() and (v[3:] == 7).all() and error == kvq.PAGED_ERR_LENGTH
+    k, v, error = read(3, [0, 3, 2, 2], 10)  # request 1 goes backwards, request 2 has no rows
+    assert torch.equal(k[:3], want[0]) and (k[3:] == 7).all() and error == kvq.PAGED_ERR_LENGTH
+    k, v, error = read(3, [2, 5, 5, 7], 10)  # rows in front of the first and behind the last are nobody's
+    assert torch.equal(k[2:5], want[0]) and (k[:2] == 7).all() and (k[7:] == 7).all() and error == 0
+    assert torch.equal(k[5:7], c.values(2, 0, 2)[0].float().bfloat16())
