@@ -44,8 +44,11 @@
 // (0 x infinity): the screeners, or the conversion, replace it by 0, and the rows that
 // see it get it back at the end (loose).
 //
-// Every wait is bounded (2 s): a wait that runs out sets an error bit and the block
-// leaves, after its products in flight.
+// Every wait is bounded (2 s). When one runs out an error bit is set; producers,
+// products and screeners leave, whole warps at a time; the softmax warps, which meet at
+// barriers of their own, go through their tiles without waiting; products in flight end
+// before the tensor memory is freed. (With waits that have a limit in those barriers'
+// place one token each of E4M3 took 205 us for 176.)
 //
 // Bound: few rows, HBM (each cached row is read once); from about 128 rows a KV head on
 // a row tile's chain of product, softmax (128 x 128 exponentials) and product. Measured,
@@ -78,7 +81,7 @@ constexpr uint32_t kColS = 256;  // scores and weights: two buffers of 128 colum
 constexpr uint32_t kColQ = 128;  // one row tile: queries, two buffers of 64
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;   // log2 of what a row's weights may exceed 1 by before its sums are rescaled (Form::kRise)
-constexpr long long kWaitNs = 2000000000LL;
+constexpr int kWaitTries = 1 << 19;  // of a wait, each of up to 4.1 us: 2 s
 
 // ---------------------------------------------------------------- forms
 
@@ -158,25 +161,23 @@ __device__ __forceinline__ bool mbar_try_wait(unsigned long long* bar, uint32_t 
                : "memory");
   return ok != 0;
 }
-__device__ __forceinline__ long long global_ns() {
-  long long t;
-  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-  return t;
-}
-// Waits for the phase of this parity; false when it took kWaitNs, or another wait of the block did.
+// Waits for the phase of this parity; false when it took kWaitTries, or another wait of the block did. (Tries are counted,
+// not the time, which goes on while a kernel is set aside.)
 __device__ __forceinline__ bool mbar_wait_long(unsigned long long* bar, uint32_t parity, volatile int* abort) {
-  const long long t0 = global_ns();
-  while (!mbar_try_wait(bar, parity)) {
+#pragma unroll 1
+  for (int i = 0; i < kWaitTries; ++i) {
     if (*abort) return false;
-    if (global_ns() - t0 > kWaitNs) {
-      *abort = 1;
-      return false;
-    }
+    if (mbar_try_wait(bar, parity)) return true;
   }
-  return true;
+  *abort = 1;
+  return false;
 }
 __device__ __forceinline__ bool mbar_wait(unsigned long long* bar, uint32_t parity, volatile int* abort) {
   return mbar_try_wait(bar, parity) || mbar_wait_long(bar, parity, abort);
+}
+// The same by a whole warp, with one answer for all lanes: what it does next takes all of them.
+__device__ __forceinline__ bool warp_wait(unsigned long long* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, mbar_try_wait(bar, parity)) || __all_sync(0xFFFFFFFFu, mbar_wait_long(bar, parity, abort));
 }
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -501,6 +502,13 @@ struct Softmax {
       : a(args), S(s), tile(threadIdx.x / kTile), thread(threadIdx.x % kTile), warp((threadIdx.x >> 5) & 3),
         lane(threadIdx.x & 31), lanes(s.tmem + (uint32_t((threadIdx.x >> 5) & 3) << 21)), o_at(lanes + 128u * (threadIdx.x / kTile)) {}
 
+  // A wait that runs out is noted (S.abort), and the warp goes on with what is there: its reads and writes are in bounds
+  // whatever they find, the waits that follow end after a try, and all lanes and warps come to the barriers that they
+  // share. (Warps that left would leave others at finish_copies' barriers, which have no limit.)
+  __device__ __forceinline__ void wait(unsigned long long* bar, uint32_t phase) const {
+    mbar_wait(bar, phase & 1u, &S.abort);
+    tc_fence_after();
+  }
   __device__ __forceinline__ void sync() const { asm volatile("bar.sync %0, 128;" ::"r"(tile + 1) : "memory"); }
 
   // Two row tiles: the unit's queries of this tile as an operand; the warp's own 32 rows.
@@ -530,10 +538,8 @@ struct Softmax {
 
   // Waits for the sums of the row tile's c-th product. (One row tile: that and the one before it may both be under way,
   // and a wait tells only odd phases from even ones: they take turns at two barriers.)
-  __device__ __forceinline__ bool summed(uint32_t c) const {
-    if (!mbar_wait(&S.pv_done[TILES == 1 ? c & 1u : tile], (TILES == 1 ? c >> 1 : c) & 1u, &S.abort)) return false;
-    tc_fence_after();
-    return true;
+  __device__ __forceinline__ void summed(uint32_t c) const {
+    wait(&S.pv_done[TILES == 1 ? c & 1u : tile], TILES == 1 ? c >> 1 : c);
   }
 
   struct Row {
@@ -550,7 +556,7 @@ struct Softmax {
   // scaled ones (TS) from where the first reading left them, for the weights. (All in loops: unrolled, or with an instance
   // for each n, the code of a block's roles does not stay in the instruction cache beside one another: 4 x 65535 tokens
   // of 8-bit rows with a scale per head 198 us, 143 us so; 512 x 1000 tokens of 16 bits 353 and 339.)
-  __device__ __forceinline__ bool weigh(Row& row, int k, int begin, uint32_t count, uint32_t all, uint32_t s_at, int copy,
+  __device__ __forceinline__ void weigh(Row& row, int k, int begin, uint32_t count, uint32_t all, uint32_t s_at, int copy,
                                         int n, float sc) {
     const bool drafted = (k + 1) * kTile > row.P;
     // the tile's scales: a token's is the same for all lanes
@@ -661,7 +667,7 @@ struct Softmax {
         top = to;
         if constexpr (!TS) row.l *= alpha;
         // the sums are at rest behind the product before
-        if (!summed(count - 1)) return false;
+        summed(count - 1);
 #pragma unroll 1
         for (int c = 0; c < 8; ++c) {
           uint32_t y[16];
@@ -726,7 +732,6 @@ struct Softmax {
     sum[0] = __fadd2_rn(sum[0], sum[1]);
     row.l += TS ? (sum[0].x + sum[0].y) * exp2_ftz(-on) : sum[0].x + sum[0].y;
     tmem_wait_st();
-    return true;
   }
 
   __device__ __forceinline__ void run(Walk<F::kRows> w, long long s0, long long e0, long long W, int C) {
@@ -742,7 +747,7 @@ struct Softmax {
       const int copy = thread / (kTile / same), r = w.rb * F::kRows + tile * kTile + thread % (kTile / same);
       const bool active = w.rb * F::kRows + tile * kTile < M;  // the row tile has rows
       // (a row tile without work must not arrive for the next unit in the same phase)
-      if (TILES == 2 && !active && !mbar_wait(&S.q_full[0], units & 1u, &S.abort)) return;
+      if (TILES == 2 && !active) wait(&S.q_full[0], units);
       ++units;
       const bool rows = same > 1 || w.rb * F::kRows + tile * kTile + warp * 32 < M;  // the warp has
       Row row{w.r.P, w.r.n, r / a.g, r < M, nullptr, -INFINITY, 0.0f, -INFINITY};
@@ -753,13 +758,9 @@ struct Softmax {
       for (int k = w.begin; active && k < w.end; ++k, ++count) {
         const uint32_t buf = TILES == 1 ? count & 1u : uint32_t(tile), phase = TILES == 1 ? (count >> 1) & 1u : count & 1u;
         const uint32_t s_at = lanes + kColS + 128u * buf;
-        if constexpr (TS)
-          if (!mbar_wait(&S.scales_full[all % kScaleRing], (all / kScaleRing) & 1u, &S.abort)) return;
-        if (!mbar_wait(&S.s_full[buf], phase, &S.abort)) return;
-        tc_fence_after();
-        if (rows) {
-          if (!weigh(row, k, w.begin, count, all, s_at, same > 1 ? copy : 0, 4 / same, sc)) return;
-        }
+        if constexpr (TS) mbar_wait(&S.scales_full[all % kScaleRing], (all / kScaleRing) & 1u, &S.abort);
+        wait(&S.s_full[buf], phase);
+        if (rows) weigh(row, k, w.begin, count, all, s_at, same > 1 ? copy : 0, 4 / same, sc);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -771,12 +772,11 @@ struct Softmax {
       if constexpr (TS && TILES == 2)
         if (!active)
           for (int k = w.begin; k < w.end; ++k, ++all) {  // (the ring's places are free when all warps have passed them)
-            if (!mbar_wait(&S.scales_full[all % kScaleRing], (all / kScaleRing) & 1u, &S.abort)) return;
+            mbar_wait(&S.scales_full[all % kScaleRing], (all / kScaleRing) & 1u, &S.abort);
+            __syncwarp();
             if (lane == 0) mbar_arrive(&S.scales_free[all % kScaleRing]);
           }
-      if (active) {
-        if (!summed(count - 1)) return;
-      }
+      if (active) summed(count - 1);
       if (threadIdx.x == 0) S.bad_page[(w.number + 8) & 15] = 0;  // (the producers are at most four units ahead)
       if (active) {
         if (same == 4) finish_copies<4>(w, row, r, copy);
@@ -849,6 +849,7 @@ struct Softmax {
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32];
+        __syncwarp();  // (the lanes without a row are back)
         tmem_ld(o_at + 32 * c, x);
         tmem_wait_ld(x);
         if (r >= M) continue;
@@ -911,6 +912,7 @@ struct Softmax {
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t x[32];
+      __syncwarp();  // (the lanes without a row are back)
       tmem_ld(o_at + 32 * c, x);
       tmem_wait_ld(x);
 #pragma unroll
@@ -1016,7 +1018,7 @@ struct Tiles {
   }
   // The buffer's last queries are those of the unit before the last one, multiplied once all its keys are there.
   __device__ __forceinline__ bool wait_queries() const {
-    return mbar_wait(&S.q_free[units & 1u], ((units >> 1) + 1) & 1u, &S.abort);
+    return warp_wait(&S.q_free[units & 1u], ((units >> 1) + 1) & 1u, &S.abort);
   }
   __device__ __forceinline__ uint32_t queries_at() const {
     return S.tmem + (uint32_t(warp) << 21) + kColQ + 64u * (units & 1u);
@@ -1048,7 +1050,7 @@ __device__ __forceinline__ void produce(Tiles<F>& T) {
     for (int half = 0; half < 2; ++half, ++x) {
       const char* pool = half == 0 ? a.c.k : a.c.v;
       const uint32_t slot = x % F::kSlots, to = slots + slot * kSlotBytes;
-      if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return;
+      if (!warp_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const long long y = __shfl_sync(0xFFFFFFFFu, T.off, 4 * e + (T.lane >> 3));
@@ -1110,7 +1112,7 @@ __device__ __forceinline__ void produce_narrow(Tiles<F>& T) {
     const uint32_t y = mine - pending, x = F::kGroups > 1 ? 4 * (y >> 1) + 2 * T.group + (y & 1u) : y;  // (x: of all)
     const uint32_t slot = x % F::kSlots, to = slots + slot * kSlotBytes, raw = raws + (y % F::kStages) * kRawBytes;
     const int from = int(past >> (8 * (pending - 1))) & 0xFF;
-    if (!mbar_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return false;
+    if (!warp_wait(&S.empty[slot], (x / F::kSlots + 1) & 1u, &S.abort)) return false;
 #pragma unroll 1
     for (int i = 0; i < 8; i += PARTS) {
       uint4 z[PARTS];
@@ -1225,7 +1227,7 @@ __device__ __forceinline__ void load_scales(const TreeArgs& a, Smem<F>& S, Walk<
     if (turn >= 2) {
       if (!now.there) return;
       const uint32_t at = c % kScaleRing;
-      if (!mbar_wait(&S.scales_free[at], (c / kScaleRing + 1) & 1u, &S.abort)) return;
+      if (!warp_wait(&S.scales_free[at], (c / kScaleRing + 1) & 1u, &S.abort)) return;
       float2 f, l, v;
       float low = INFINITY, high = -INFINITY;
 #pragma unroll
@@ -1272,7 +1274,7 @@ __device__ __forceinline__ void screen_values(const TreeArgs& a, Smem<Form<DT, Q
     for (int k = k0; k < w.end; ++k) {
       const uint32_t slot = (x + 2 * (k - w.begin) + 1) % F::kSlots, at = smem_addr(S.slot) + slot * kSlotBytes;
       const int from = max(0, min(kTile, w.r.P - k * kTile)), to = min(kTile, w.tokens - k * kTile);
-      if (!mbar_wait(&S.raw_full[slot], (phases >> slot) & 1u, &S.abort)) return;
+      if (!warp_wait(&S.raw_full[slot], (phases >> slot) & 1u, &S.abort)) return;
       phases ^= 1u << slot;
       // a token's 16 chunks by 16 threads: two of each 128 bytes, in their swizzled order
 #pragma unroll 4
@@ -1348,12 +1350,12 @@ __device__ __forceinline__ bool multiply(const TreeArgs& a, Smem<Form<DT, QT, TI
     mma_commit(&S.pv_done[TILES == 1 ? buf : tile]);
   };
   auto wait = [&](unsigned long long* bar, uint32_t phase) {
-    if (!__all_sync(0xFFFFFFFFu, mbar_wait(bar, phase & 1u, &S.abort))) return false;
+    if (!warp_wait(bar, phase & 1u, &S.abort)) return false;
     tc_fence_after();
     return true;
   };
   auto filled = [&](uint32_t x) {
-    if (!__all_sync(0xFFFFFFFFu, mbar_wait(&S.full[x % F::kSlots], (x / F::kSlots) & 1u, &S.abort))) return false;
+    if (!warp_wait(&S.full[x % F::kSlots], (x / F::kSlots) & 1u, &S.abort)) return false;
     if constexpr (!F::kNarrow) fence_async_smem();  // (copies that arrive by themselves have no fence behind them)
     tc_fence_after();
     return true;

@@ -1,6 +1,9 @@
-"""Tree attention without a GPU: calls that have nothing to do."""
+"""Tree attention without a GPU: calls that have nothing to do; what its kernel does when a wait runs out, by its source."""
 
 from __future__ import annotations
+
+import os
+import re
 
 import pytest
 
@@ -22,3 +25,41 @@ def test_a_mask_of_no_rows_needs_no_address(L):
     assert _tree(L, c, n=0, mask=None, words=33) == BAD
     assert _tree(L, c, n=0, mask=P, words=0) == BAD
     assert _tree(L, c, n=9, mask=None, words=1) == BAD
+
+
+def _functions(text):
+    """Bodies of a source file's functions (and of its types' members) by name."""
+    out = {}
+    for m in re.finditer(r"(\w+)\([^;{}]*\)\s*(?:const )?(?::[^{;]*)?\{", text):
+        depth, i = 0, m.end() - 1
+        while True:
+            depth += {"{": 1, "}": -1}.get(text[i], 0)
+            i += 1
+            if depth == 0:
+                break
+        out.setdefault(m.group(1), []).append(text[m.end():i - 1])
+    return out
+
+
+def test_no_wait_of_the_tree_kernel_leaves_another_behind():
+    """A wait that runs out must not keep anybody from a barrier or a collective that others are at: softmax warps, which
+    share a barrier without a limit, have no way out of their tiles; the other roles leave by whole warps and share none."""
+    with open(os.path.join(kbuild.CSRC, "kvq_paged_tree.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    bodies = _functions(text)
+    softmax = text[text.index("struct Softmax"):text.index("struct Tiles")]
+    rest = text.replace(softmax, "")
+    assert softmax.count("bar.sync") == 1 and "bar.sync" not in rest and "barrier.sync" not in text
+    for name in ("run", "weigh", "summed", "finish", "finish_copies", "load_queries"):
+        for body in (b for b in bodies[name] if b in softmax):
+            assert re.search(r"return( true| false)?;", body) is None, name
+    assert "warp_wait" not in softmax  # (nobody votes there: nobody leaves)
+    roles = rest[rest.index("struct Tiles"):rest.index("tree_kernel(")]
+    assert re.search(r"(?<!warp_)\bwait_long|\bmbar_wait\(|mbar_try_wait\(", roles) is None
+    assert "__syncthreads" not in roles and "__syncthreads" not in softmax
+    # the kernel's own: the last one is behind all roles
+    kernel = text[text.index("tree_kernel(const"):text.index("constexpr int kJoinWarps")]
+    assert kernel.rindex("__syncthreads") > kernel.rindex("screen_values") and "return" not in kernel[kernel.index("tcgen05.alloc"):]
+    # and each wait ends: a counted loop around the try
+    (long,) = bodies["mbar_wait_long"]
+    assert re.search(r"for \(int i = 0; i < kWaitTries; \+\+i\)", long) and "while" not in long
