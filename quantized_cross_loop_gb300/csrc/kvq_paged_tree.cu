@@ -284,6 +284,8 @@ template <int N>
 __device__ __forceinline__ void wait_groups() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+// All of this thread's copies, those that are in no group among them.
+__device__ __forceinline__ void wait_copies() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // The barrier counts this thread once its copies so far have landed.
 __device__ __forceinline__ void arrive_landed(unsigned long long* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -1504,7 +1506,7 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
     // scales per token 212 us by four, 176 by two; with FP16 queries 165 and 180; with a scale per head 163 and 167)
     if constexpr (F::kNarrow) produce_narrow<F, TILES == 1, TS && F::kKeyBf ? 2 : 4>(T);
     else produce<F, TILES == 1>(T);
-    wait_groups<0>();
+    wait_copies();  // (where a wait has run out some may be under way)
   } else {
     fewer_registers<F::kMmaRegs>();
     if (warp == F::kMmaWarp) {

@@ -63,3 +63,12 @@ def test_no_wait_of_the_tree_kernel_leaves_another_behind():
     # and each wait ends: a counted loop around the try
     (long,) = bodies["mbar_wait_long"]
     assert re.search(r"for \(int i = 0; i < kWaitTries; \+\+i\)", long) and "while" not in long
+
+
+def test_copies_under_way_land_before_the_tree_kernel_ends():
+    """Those of 16-bit rows are in no group that a wait for groups knows of."""
+    with open(os.path.join(kbuild.CSRC, "kvq_paged_tree.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    kernel = text[text.index("tree_kernel(const"):text.index("constexpr int kJoinWarps")]
+    behind = kernel[kernel.index("produce<F"):]
+    assert "wait_copies();" in behind[:behind.index("} else {")] and _functions(text)["wait_copies"][0].count("cp.async.wait_all")
