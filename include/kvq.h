@@ -705,7 +705,10 @@ kvq_status kvq_paged_read(const kvq_paged_cache* cache, const int32_t* page_tabl
                           const int32_t* start, const int32_t* offsets, int n_rows, int out_dtype, void* k_out,
                           void* v_out, int64_t k_stride, int64_t v_stride, kvq_cuda_stream stream);
 
-/* Workspace bytes of kvq_paged_tree_attn on the current device. 0 for invalid sizes. */
+/*
+ * Workspace bytes of kvq_paged_tree_attn on the current device, for calls of up to
+ * n_requests requests and n_rows rows. 0 for invalid sizes.
+ */
 size_t kvq_paged_tree_workspace_bytes(int n_requests, int n_heads, int n_q_heads, int n_rows);
 
 /*

@@ -355,7 +355,8 @@ struct TreeArgs {
   int32_t sms;
 };
 
-size_t tree_workspace(int B, int H, int Hq, int n_rows, int sms);
+size_t tree_workspace(int B, int H, int Hq, int n_rows, int sms);        // of a call
+size_t tree_workspace_up_to(int B, int H, int Hq, int n_rows, int sms);  // of any call of no more requests and rows
 cudaError_t launch_read(const ReadArgs& a, int sms, cudaStream_t stream);
 cudaError_t launch_commit(const CommitArgs& a, cudaStream_t stream);
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream);

@@ -382,7 +382,7 @@ size_t kvq_paged_tree_workspace_bytes(int n_requests, int n_heads, int n_q_heads
   if (n_requests < 0 || n_heads < 1 || n_heads > 1024 || n_q_heads < n_heads || n_q_heads % n_heads != 0 ||
       n_q_heads / n_heads > KVQ_PAGED_MAX_G || n_rows < 0 || !batch_fits(n_requests, n_heads, 0) || sms == 0)
     return 0;
-  return paged::tree_workspace(n_requests, n_heads, n_q_heads, n_rows, sms);
+  return paged::tree_workspace_up_to(n_requests, n_heads, n_q_heads, n_rows, sms);
 }
 
 kvq_status kvq_paged_tree_attn(const kvq_paged_cache* cache, const int32_t* page_table, int max_pages, int n_requests,

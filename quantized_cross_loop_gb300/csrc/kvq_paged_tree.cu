@@ -1711,6 +1711,10 @@ size_t tree_workspace(int B, int H, int Hq, int n_rows, int sms) {
   return slots_offset(sms) + 2 * size_t(sms) * slot_floats(kTile * row_tiles(B, Hq / H, n_rows)) * 4;
 }
 
+size_t tree_workspace_up_to(int B, int H, int Hq, int n_rows, int sms) {
+  return tree_workspace(min(B, 1), H, Hq, n_rows, sms);  // (the fewer the requests the wider are theirs)
+}
+
 cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   const bool bf = a.q_dtype == kBf16;
   if (a.dtype == kBf16) return launch_types<kBf16, kBf16>(a, stream);

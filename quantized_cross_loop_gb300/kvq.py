@@ -890,7 +890,7 @@ class PagedCache:
         return cls(page_size, n_heads, k, v, bounds, k_scale, v_scale)
 
     def tree_workspace_bytes(self, n_requests: int, n_q_heads: int, n_rows: int) -> int:
-        """Workspace of kvq_paged_tree_attn for these sizes (kvq_paged_tree_workspace_bytes)."""
+        """Workspace of kvq_paged_tree_attn for calls of up to these sizes (kvq_paged_tree_workspace_bytes)."""
         with torch.cuda.device(self.device):
             return int(lib().kvq_paged_tree_workspace_bytes(n_requests, self.n_heads, n_q_heads, n_rows))
 

@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from quantized_cross_loop_gb300 import kvq
-from tests.test_paged_tree_gpu import D, Cache, _attend, _compare, _exact, _gen, _offsets, _query, _raw, _tree
+from tests.test_paged_tree_gpu import D, Cache, _attend, _chain, _compare, _exact, _gen, _offsets, _query, _raw, _tree
 
 pytestmark = pytest.mark.gpu
 
@@ -92,6 +92,26 @@ def test_products_with_scales_rise_and_fall(act, rows):
 
 
 # ------------------------------------------------------------------ sizes
+
+
+@pytest.mark.parametrize("H,Hq", [(8, 32), (1, 16), (2, 2)])
+def test_workspace_of_the_largest_sizes_is_enough(H, Hq):
+    """A workspace for some requests and rows serves every call of no more of either."""
+    cache = kvq.PagedCache.empty(4, 16, H)
+    B, n = [0, 1, 2, 7, 8, 64, 1000], [0, 1, 8, 9, 63, 129, 1024, 5000]
+    size = [[cache.tree_workspace_bytes(b, Hq, r) for r in n] for b in B]
+    for i in range(len(B)):
+        for j in range(len(n)):
+            assert size[i][j] >= max(size[x][y] for x in range(i + 1) for y in range(j + 1)), (B[i], n[j])
+
+
+def test_a_workspace_serves_smaller_batches():
+    rows = [300, 129, 0, 83]
+    c = Cache([40, 0, 7, 1000], rows, 16, 8, "bf16", seed=4)
+    ws = torch.empty(c.cache.tree_workspace_bytes(64, 32, sum(rows)), dtype=torch.uint8, device="cuda")
+    q = _query(sum(rows), 32, "bf16")
+    out, lse = _attend(c, q, _offsets(rows), None, workspace=ws)
+    _compare(c, q, out, lse, _chain(rows))
 
 
 def test_a_step_without_rows():
