@@ -9,7 +9,8 @@ import pytest
 import torch
 
 from quantized_cross_loop_gb300 import kvq
-from tests.test_paged_tree_gpu import D, Cache, _attend, _chain, _compare, _exact, _gen, _offsets, _query, _raw, _tree
+from tests.test_paged_tree_gpu import (D, Cache, _all_bits, _attend, _chain, _compare, _exact, _gen, _offsets,
+                                       _query, _raw, _tree)
 
 pytestmark = pytest.mark.gpu
 
@@ -91,6 +92,27 @@ def test_products_with_scales_rise_and_fall(act, rows):
     _compare(c, q, out, lse, seen, 1.0)
 
 
+# ------------------------------------------------------------------ values that are not finite
+
+
+@pytest.mark.parametrize("cache,act", [("bf16", "bf16"), ("fp16", "fp16"), ("e4m3", "fp16"), ("e4m3t", "bf16"),
+                                       ("e4m3t", "fp16")])
+@pytest.mark.parametrize("rows", [[12, 40], [1, 9], [70, 140]])
+def test_finite_channels_beside_values_that_are_not(cache, act, rows):
+    """The channels that stay finite are as exact as without such values."""
+    c = Cache([70, 129], rows, 16, 2, cache, seed=4)
+    seen, mask = _tree(rows, 6)
+    bad = [math.nan] if cache.startswith("e4m3") else [math.nan, math.inf, -math.inf]
+    for i, (b, t) in enumerate(((0, 70), (0, 70 + rows[0] // 2), (1, 129), (1, 129 + rows[1] - 1))):
+        page, place = c.where(b, torch.tensor([t], device="cuda"))
+        for d in (3 * i, 64 + i):
+            _raw(c.v)[page, place, 1, d] = _raw(torch.tensor([bad[(i + d) % len(bad)]], device="cuda").to(c.v.dtype))
+    q = _query(sum(rows), 8, act)
+    out, lse = _attend(c, q, _offsets(rows), mask)
+    _compare(c, q, out, lse, seen)
+    assert not torch.isfinite(out[:, 4:]).all() and torch.isfinite(out[:, :4]).all()
+
+
 # ------------------------------------------------------------------ sizes
 
 
@@ -151,3 +173,27 @@ def test_read_reports_requests_whose_offsets_are_out_of_range(cache):
     k, v, error = read(3, [2, 5, 5, 7], 10)  # rows in front of the first and behind the last are nobody's
     assert torch.equal(k[2:5], want[0]) and (k[:2] == 7).all() and (k[7:] == 7).all() and error == 0
     assert torch.equal(k[5:7], c.values(2, 0, 2)[0].float().bfloat16())
+
+
+@pytest.mark.parametrize("cache,bounds", [("bf16", True), ("e4m3t", False)])
+def test_commit_leaves_requests_of_such_offsets_alone(cache, bounds):
+    """Requests 1 and 2 have no list, one's beyond the end and one's backwards; request 0's and 3's tokens move."""
+    lens = [20, 20, 20, 20]
+    c = Cache(lens, [10] * 4, 16, 2, cache, seed=4, bounds=bounds)
+    accepted = torch.tensor([2, 5, 1, 4, 7], dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 2, 900, 2, 5], dtype=torch.int32, device="cuda")
+    want = _all_bits(c)
+    for b, a in ((0, [2, 5]), (3, [1, 4, 7])):
+        src, dst = c.where(b, 20 + torch.tensor(a, device="cuda")), c.where(b, 20 + torch.arange(len(a), device="cuda"))
+        for x in want[:2]:
+            x[dst] = x[src].clone()
+        if cache == "e4m3t":
+            for x in want[2:]:
+                x[dst[0], :, dst[1]] = x[src[0], :, src[1]].clone()
+        else:  # (20 tokens and those: the second page)
+            k = want[0].view(c.k.dtype)[c.table[b, 1].long(), :4 + len(a)].float()
+            want[-1][c.table[b, 1].long()] = torch.stack([k.amin(0), k.amax(0)], 1).to(c.bounds.dtype)
+    kvq.kvq_paged_tree_commit(c.cache, c.table, c.seq, accepted, off)
+    for x, y in zip(want, _all_bits(c)):
+        assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+    assert c.cache.error_word() == kvq.PAGED_ERR_LENGTH
