@@ -731,10 +731,13 @@ size_t kvq_paged_tree_workspace_bytes(int n_requests, int n_heads, int n_q_heads
  *   out      q's type, [n_rows][Hq][D], 16-byte aligned. (Not FP32, as of
  *            kvq_paged_decode_attn: a softmax weight is one 16-bit number here.)
  *   lse      FP32 [n_rows][Hq] or NULL: ln of the sum of exp(scale q.k).
- * Query head hq reads KV head hq / (Hq/H). Softmax and sums are FP32; q.k and |v|
- * summed over the tokens have to lie within FP32's range. Weights are rounded to
- * 16 bits (BF16 of a BF16 cache, else FP16, which leaves out what is below 2^-31 of
- * the largest), out once more to its type. A value that is not finite makes its
+ * Query head hq reads KV head hq / (Hq/H). Softmax and sums are FP32; q.k (of E4M3
+ * also with the keys as stored) and |v| summed over the tokens have to lie within
+ * FP32's range. Weights are rounded to 16 bits (BF16 of a BF16 cache, else FP16, which
+ * leaves out what is below 2^-31 of the largest; with a scale per token these are the
+ * products of weights and values' scales, and weights below 2^-186 of the row's largest
+ * count as 0, as do those below 2^-66 under scales above 2^106), out once more to its
+ * type. A value that is not finite makes its
  * channel NaN or infinite in the rows that attend to its token, and in no others;
  * what lies in other places of a page is not read. A row that attends to nothing, or
  * whose keys all weigh nothing, gets out 0 and lse -inf. All rows of a request whose

@@ -681,7 +681,9 @@ struct Softmax {
       }
     }
     // TS: the weights themselves are to `to` by 2^on, so that FP16 holds the largest product with a scale, and their own
-    // sum is taken back to m; what of `on` might leave FP32's range (scales near its ends) goes to the scales
+    // sum is taken back to m; what of `on` might leave FP32's range (scales near its ends) is multiplied in behind the
+    // scales (2^rest times a scale may be infinite, that of a token whose weight is 0 among them). Weights below 2^-186
+    // of m's are 0 then, or below 2^-66 where the products are 2^71 above it.
     [[maybe_unused]] float on = 0.0f, rest = 0.0f;
     if constexpr (TS) {
       const float x = row.to == -INFINITY ? 0.0f : row.m - row.to + F::kShift;
@@ -689,6 +691,7 @@ struct Softmax {
       rest = x - on;
     }
     [[maybe_unused]] const bool extreme = TS && __any_sync(0xFFFFFFFFu, rest != 0.0f);
+    [[maybe_unused]] const float more = exp2f(rest);
     const float base = (TS ? on : F::kShift) - (row.m == -INFINITY ? 0.0f : row.m);
     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll 1
@@ -703,11 +706,6 @@ struct Softmax {
         if constexpr (TS) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) f[e] = lds4(vf + 4 * (32 * part + 16 * q + 4 * e));
-          if (extreme) {
-            const float y = exp2_ftz(rest);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = times(f[e], y);
-          }
         }
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
@@ -717,8 +715,10 @@ struct Softmax {
           else y = __ffma2_rn(pair(x, e), make_float2(sc, sc), make_float2(base, base));
           y = make_float2(exp2_ftz(y.x), exp2_ftz(y.y));
           sum[(i >> 1) & 1] = __fadd2_rn(sum[(i >> 1) & 1], y);
-          if constexpr (TS)
+          if constexpr (TS) {
             y = __fmul2_rn(y, i & 2 ? make_float2(f[i / 4].z, f[i / 4].w) : make_float2(f[i / 4].x, f[i / 4].y));
+            if (extreme) y = __fmul2_rn(y, make_float2(more, more));
+          }
           p[e / 2] = pack<F::kValBf>(y.x, y.y);
         }
       }

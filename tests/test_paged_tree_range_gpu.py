@@ -92,6 +92,40 @@ def test_products_with_scales_rise_and_fall(act, rows):
     _compare(c, q, out, lse, seen, 1.0)
 
 
+@pytest.mark.parametrize("act", ["bf16", "fp16"])
+@pytest.mark.parametrize("rows", [[3], [20], [60], [140], [9, 50]])
+@pytest.mark.parametrize("low,high", [(-126, 100), (-126, 60), (-100, 110)])
+def test_hidden_scales_far_above_those_of_the_tokens_seen(act, rows, low, high):
+    """A drafted token of the largest scales does not reach the rows that do not see it: they see the smallest ones, which
+    the way from weights to products has to bridge (BF16 holds results down to 2^-134, FP16 none of these)."""
+    lens = [70, 0][:len(rows)]
+    c = Cache(lens, rows, 16, 2, "e4m3t", seed=3)
+    for b, T in enumerate(x + y for x, y in zip(lens, rows)):
+        page, place = c.where(b, torch.arange(T, device="cuda"))
+        _raw(c.v)[page, place] = _raw((200 + 50 * torch.randn((T, 2, D), generator=_gen(b), device="cuda")).to(c.v.dtype))
+        c.v_scale[page, :, place] = 2.0**low
+        page, place = c.where(b, torch.tensor([lens[b] + 1], device="cuda"))
+        c.v_scale[page, :, place] = 2.0**high
+    n = sum(rows)
+    q = _query(n, 8, act)
+    seen, mask = _tree(rows, 6)
+    hidden = torch.cat([~s[:, 1] for s in seen])
+    assert hidden.any() and not hidden.all()
+    out, lse = _attend(c, q, _offsets(rows), mask)
+    at = 0
+    for b, (T, r) in enumerate(zip(lens, rows)):
+        K, V = c.values(b, 0, T + r)
+        see = torch.cat([torch.ones((r, T), dtype=torch.bool, device="cuda"), seen[b]], 1)
+        for j in range(8):
+            o, l, to, tl = _exact(q[at:at + r, j], K[:, j // 4], V[:, j // 4], see, 1 / math.sqrt(D), "e4m3t", act,
+                                  c.value_scales(b, j // 4, T + r))
+            x = out[at:at + r, j].double()
+            assert ((x - o).abs().le(to + 2.0**-134) | (x.isinf() if act == "fp16" else torch.zeros_like(x) > 0)).all(), (b, j)
+            assert (lse[at:at + r, j].double() - l).abs().le(tl).all(), (b, j)
+        at += r
+    assert torch.isfinite(out[hidden]).all()
+
+
 # ------------------------------------------------------------------ values that are not finite
 
 
