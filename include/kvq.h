@@ -713,7 +713,8 @@ size_t kvq_paged_tree_workspace_bytes(int n_requests, int n_heads, int n_q_heads
 
 /*
  * Attention of several queries per request: of a tree of drafted tokens that a
- * model verifies in one pass, of a chunk of a prompt, or (one row) of a decode step.
+ * model verifies in one pass, of a chunk of a prompt, or (one row) of a decode step
+ * (over E4M3 with a scale per head kvq_paged_decode_attn is the faster one for that).
  * Request b has seq_lens[b] tokens in the cache and behind them, at the places
  * seq_lens[b] + i, its drafted tokens i = 0 .. n_b - 1, appended before the call
  * (kvq_paged_append; the positions of a tree's tokens are its `positions`). Query

@@ -18,7 +18,8 @@ namespace {
 // requests of up to 8191 rows to BF16, 8 heads, pages of 16, 138 MB moved: 24.9 us,
 // 5.5 TB/s, 82% of a copy's rate; other blocks per SM x rows in flight: 1 x 8 25.3 us,
 // 2 x 6 25.2, 2 x 8 26.0, 4 x 6 31.5, 4 x 8 35.5, 8 x 2 25.4. 64 tiles of 64 rows, E4M3
-// with scales per token, 25 MB: 7.7 us (launch and the chain offsets -> table -> row).
+// with scales per token, 25 MB: 7.6 us (launch, the search for a row's request, which is
+// log2 of the requests dependent loads, and range and start -> table -> row).
 
 constexpr int kReadThreads = 256;
 constexpr int kReadTeam = 16;
@@ -171,7 +172,9 @@ __global__ void __launch_bounds__(kReadThreads, kReadBlocksPerSm) read_kernel(Re
 // accepted token is at place k or behind it, so what a later step reads lies behind
 // what an earlier one wrote. The bounds are then taken from the keys as they are.
 // Bound: latency (a few rows per request): 64 requests that keep 5 of 16 BF16 tokens,
-// 8 heads, 4.8 us; 256 that keep up to 32 of 64, E4M3 with scales per token, 8.5 us.
+// 8 heads, 4.8 us; 256 that keep up to 32 of 64, E4M3 with scales per token, 8.5 us: 2048
+// blocks, five to an SM, are 2.7 waves of the whole chain, which reads list and table
+// twice (to check them, and to move).
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveWarps = kMoveThreads / 32;

@@ -18,8 +18,9 @@
 // O += P V with P in tensor memory, where the softmax warps leave it in the place of
 // S. A block's warps:
 //   softmax   four per row tile, a thread a row: no shuffles; the sums of a row are
-//             rescaled only when its maximum grows by more than 2^8 (its weights then
-//             go to at most 1, or 2^15 for FP16, by kShift). A unit of up to 64 (32)
+//             rescaled only when its maximum grows by more than 2^8, with scales per
+//             token 2^4 (its weights then go to at most 1, or 2^15 for FP16, by
+//             kShift). A unit of up to 64 (32)
 //             rows is in the row tile twice (four times), each copy for its share of
 //             a tile's tokens, else a few rows would leave three warps of four idle
 //   producers four: 16-byte asynchronous copies of K and V rows into a ring of
@@ -36,9 +37,9 @@
 // numbers of the queries' type, 8-bit values FP16, both exactly. A weight is one
 // 16-bit number: of BF16 for BF16 caches (its operand's type is the values'), of FP16
 // for the others, there down to 2^-31 of the largest weight with values' scales
-// (where tokens have them) multiplied in before the rounding. The result is rounded
-// to 16 bits anyway, and three parts would triple the second product, which bounds
-// wide trees.
+// (where tokens have them) multiplied in before the rounding. That adds 4 to 9% to the
+// error that the rounding of the result leaves; three parts would triple the second
+// product, which bounds wide trees.
 //
 // A drafted token's value that is not finite must not reach rows that do not see it
 // (0 x infinity): the screeners, or the conversion, replace it by 0, and the rows that
@@ -55,12 +56,15 @@
 // 8 KV heads, BF16 but where said (from one GPU to another 2-3% less): 64 requests of up
 // to 16383 tokens, one new token each, 172 us, 6.1 TB/s (91% of a copy's rate); 512 x 1000
 // tokens, four new ones each, 338 us (95%); trees of 16 over 64 requests of up to 4095
-// tokens 95 us, 5.2 TB/s; trees of 64, 64 heads, over 8 x 16384 tokens 224 us, 1.23
-// PFLOP/s; E4M3, 64 requests of one token with a scale per head 163 us (3.2 TB/s), with one
-// per token 177 us (3.1 TB/s): conversion and the scales' multiplications, not HBM.
+// tokens 95 us, 5.2 TB/s; trees of 64, 64 heads, over 8 x 16384 tokens 223 us, 1.23
+// PFLOP/s (in a long run of calls 241, 1.14 PFLOP/s); 4 x 65535 tokens of E4M3 with a scale
+// per token 176 us, with one per head 132. One token each over E4M3, 64 requests: with a
+// scale per token 177 us (3.1 TB/s), with one per head 161; every 8-bit row is widened in
+// shared memory for products of 128 rows of which four are real, and
+// kvq_paged_decode_attn, which widens in registers, takes 92.5 for the latter.
 // The block's roles share an instruction cache, and their code is kept in loops for
 // it: unrolled forms stalled on instructions more than on anything else (4 x 65535
-// tokens of E4M3 with a scale per token 330 us, 182 now).
+// tokens of E4M3 with a scale per token 330 us, 176 now).
 #include <atomic>
 #include <type_traits>
 
@@ -93,7 +97,7 @@ struct Form {
   // With scales per token the sums are to a bound of the products of weights and scales, which is up to 2^kNear above the
   // largest product: that comes off the slack, so that FP16 holds the largest product at 2^7 or more in any case (its
   // smallest step is 2^-31 of that) and at 2^15 at most. (Scales within 2^kNear spare the look for the largest product:
-  // wide trees 335 us, with it 379. Two for four leaves more slack, 334, and more tiles without.)
+  // wide trees 324 us, with it 362. Two for four leaves more slack, 323, and more tiles that have to look.)
   static constexpr float kNear = TS ? 4.0f : 0.0f;
   static constexpr float kRise = kSlack - kNear;  // log2 of what the products may grow by before the sums are rescaled
   static constexpr float kShift = kValBf ? -kRise : 15.0f - kRise;
@@ -779,7 +783,7 @@ struct Softmax {
             if (lane == 0) mbar_arrive(&S.scales_free[all % kScaleRing]);
           }
       if (active) summed(count - 1);
-      if (threadIdx.x == 0) S.bad_page[(w.number + 8) & 15] = 0;  // (the producers are at most four units ahead)
+      if (threadIdx.x == 0) S.bad_page[(w.number + 8) & 15] = 0;  // (the producers are less than eight units ahead)
       if (active) {
         if (same == 4) finish_copies<4>(w, row, r, copy);
         else if (same == 2) finish_copies<2>(w, row, r, copy);
@@ -1503,7 +1507,7 @@ __global__ void __launch_bounds__(Form<DT, QT, TILES, TS>::kThreads, 1) tree_ker
     Tiles<F> T(a, S, w, s0, e0);
     // of a copy's eight parts those that a thread converts at once: two where the code for BF16 keys and for FP16 values
     // stands beside that for scales per token, else four (the code's size: 64 requests of one token with BF16 queries and
-    // scales per token 212 us by four, 176 by two; with FP16 queries 165 and 180; with a scale per head 163 and 167)
+    // scales per token 233 us by four, 177 by two; with FP16 queries 173 and 178; with a scale per head 161 and 166)
     if constexpr (F::kNarrow) produce_narrow<F, TILES == 1, TS && F::kKeyBf ? 2 : 4>(T);
     else produce<F, TILES == 1>(T);
     wait_copies();  // (where a wait has run out some may be under way)
@@ -1694,7 +1698,9 @@ cudaError_t launch_form(const TreeArgs& a, cudaStream_t stream) {
                           stream, a);
 }
 
-// Two row tiles per block where the requests' mean rows fill more than one.
+// Two row tiles per block where the requests' mean rows fill more than one. (By the mean, since the host does not see
+// the offsets: a chunk of 1000 rows over 8192 tokens among 63 single rows, which then goes by one, took 319 us, the chunk
+// alone 143 by two and the single rows 170 by one.)
 int row_tiles(int B, int g, int n_rows) { return ((long long)n_rows + B - 1) / (B > 0 ? B : 1) * g > kTile ? 2 : 1; }
 
 template <int DT, int QT>

@@ -1122,7 +1122,8 @@ def kvq_paged_read(cache: PagedCache, page_table: torch.Tensor, start: torch.Ten
     """Rows back out of the cache, into k_out and v_out, BF16 or FP16 [n, H, 128]
     (rows may be strided): row i of request b is token start[b] + i, rows
     offsets[b] .. offsets[b + 1] - 1 (None: one row per request); rows behind
-    offsets[B] are left alone. 8-bit values come times their scale. 64 rows of a
+    offsets[B] are left alone, and so are those of requests whose offsets are out of
+    order (PAGED_ERR_LENGTH). 8-bit values come times their scale. 64 rows of a
     request in a contiguous BF16 buffer are a tile for kvq_append_tile. Returns
     (k_out, v_out)."""
     if _elsewhere(cache, stream):
@@ -1162,8 +1163,8 @@ def kvq_paged_tree_attn(cache: PagedCache, page_table: torch.Tensor, seq_lens: t
     request / 32)); None: row i attends to the drafted tokens 0 .. i, as the tokens
     of a chunk do. Returns out [n, Hq, 128] of q's type; lse, FP32 [n, Hq], takes the
     natural log of the softmax's sum. Rows behind offsets[B] are left alone.
-    workspace: cache.tree_workspace_bytes(...) bytes, allocated when None; calls
-    that may overlap need one each."""
+    workspace: cache.tree_workspace_bytes(...) bytes for these sizes or larger ones,
+    allocated when None; calls that may overlap need one each."""
     if _elsewhere(cache, stream):
         with _made_current(cache, stream):
             return kvq_paged_tree_attn(cache, page_table, seq_lens, q, offsets, mask, softmax_scale, out, lse, workspace)
