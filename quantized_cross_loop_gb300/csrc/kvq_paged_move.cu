@@ -324,7 +324,10 @@ __global__ void __launch_bounds__(kMoveThreads) commit_kernel(CommitArgs a) {
 
 template <int DT, int OUT>
 cudaError_t launch_read_form(const ReadArgs& a, int sms, cudaStream_t stream) {
-  const long long need = ((long long)a.n_rows * a.c.H + kReadTeams - 1) / kReadTeams, fit = (long long)kReadBlocksPerSm * sms;
+  // blocks for the rows, and for the look at every request's offsets
+  const long long rows = ((long long)a.n_rows * a.c.H + kReadTeams - 1) / kReadTeams;
+  const long long requests = ((long long)a.B + kReadThreads - 1) / kReadThreads;
+  const long long need = rows > requests ? rows : requests, fit = (long long)kReadBlocksPerSm * sms;
   count_launch();
   return launch_dependent(read_kernel<DT, OUT>, dim3(int(need < fit ? need : fit)), dim3(kReadThreads), 0, stream, a);
 }

@@ -209,6 +209,28 @@ def test_read_reports_requests_whose_offsets_are_out_of_range(cache):
     assert torch.equal(k[5:7], c.values(2, 0, 2)[0].float().bfloat16())
 
 
+def test_read_of_few_rows_of_many_requests():
+    """The rows of three among 200000 requests; then the last but one's offsets are out of order, too."""
+    B, H = 200000, 2
+    cache = kvq.PagedCache.empty(8, 16, H)
+    cache.k.copy_(torch.arange(8 * 16 * H * D, device="cuda").view(8, 16, H, D) % 251)
+    cache.v.copy_(cache.k + 1)
+    table = torch.full((B, 1), 1 << 30, dtype=torch.int32, device="cuda")
+    rows = torch.zeros(B, dtype=torch.int32)
+    at = {0: (3, 2), 123456: (0, 1), B - 1: (7, 5)}  # page, rows
+    for b, (page, n) in at.items():
+        table[b, 0], rows[b] = page, n
+    off = torch.cat([torch.zeros(1, dtype=torch.int32), rows.cumsum(0).to(torch.int32)]).cuda()
+    start = torch.full((B,), 2, dtype=torch.int32, device="cuda")
+    want = torch.cat([cache.k[page, 2:2 + n] for page, n in at.values()])
+    k, v = (torch.full((9, H, D), 7.0, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    kvq.kvq_paged_read(cache, table, start, k, v, offsets=off)
+    assert torch.equal(k[:8], want) and torch.equal(v[:8], want + 1) and (k[8] == 7).all() and cache.error_word() == 0
+    off[B - 1] = 1
+    kvq.kvq_paged_read(cache, table, start, k, v, offsets=off)
+    assert cache.error_word() == kvq.PAGED_ERR_LENGTH
+
+
 @pytest.mark.parametrize("cache,bounds", [("bf16", True), ("e4m3t", False)])
 def test_commit_leaves_requests_of_such_offsets_alone(cache, bounds):
     """Requests 1 and 2 have no list, one's beyond the end and one's backwards; request 0's and 3's tokens move."""
