@@ -170,6 +170,22 @@ def test_a_workspace_serves_smaller_batches():
     _compare(c, q, out, lse, _chain(rows))
 
 
+@pytest.mark.parametrize("cache,act", [("bf16", "bf16"), ("fp16", "fp16"), ("e4m3", "bf16"), ("e4m3t", "bf16")])
+@pytest.mark.parametrize("mask", [False, True])
+def test_a_long_chunk_among_single_rows(cache, act, mask):
+    """The mean of the rows is small, one request's are many: it goes through many units of the form for few rows."""
+    rows = [1] * 30 + [700] + [1] * 5 + [0, 2]
+    lens = [(37 * b) % 300 for b in range(30)] + [500] + [0, 1, 128, 1000, 63] + [9, 0]
+    c = Cache(lens, rows, 16, 2, cache, seed=6)
+    q = _query(sum(rows) + 1, 8, act)
+    seen, bits = _tree(rows, 5, 0.1) if mask else (_chain(rows), None)
+    if mask:
+        bits = torch.cat([bits, bits[:1]])
+    out, lse = _attend(c, q, _offsets(rows), bits)
+    _compare(c, q, out, lse, seen)
+    assert c.cache.error_word() == 0
+
+
 def test_a_step_without_rows():
     """Nothing is drafted: a mask of no rows is no less valid than none."""
     c = Cache([20, 30], [0, 0], 16, 2, "bf16", seed=1)
